@@ -26,7 +26,9 @@ __all__ = [
     "attn_fwd_splitkv_workspace_size", "attn_bwd", "attn_bwd_phase", "attn_bwd_workspace_size", "attn_bwd_dq_splits",
     "attn_bwd_noalloc", "ATTN_NOALLOC_SCRATCH_BYTES", "attn_online_softmax_step", "attn_device_status",
     "attn_selftest_wait_timeout", "attn_strerror", "attn_last_cuda_error", "attn_version",
-    "forward", "backward",
+    "attn_fwd_scored", "attn_fwd_scored_workspace_size", "attn_bwd_scored", "attn_bwd_scored_workspace_size",
+    "attn_rope_init", "attn_rope", "AttnScore", "AttnRope",
+    "forward", "backward", "forward_scored", "backward_scored", "rope_plan", "rope",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libattn.so")
@@ -36,6 +38,20 @@ ATTN_ERR_CUDA, ATTN_ERR_TIMEOUT, ATTN_ERR_WORKSPACE = 4, 5, 6
 ATTN_F32, ATTN_BF16 = 0, 1
 
 _P, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+
+
+
+class AttnScore(ctypes.Structure):
+    """attn_score_t: how the scored attention changes and masks its scores (device addresses, 0 for none)."""
+    _fields_ = [("softcap", _F), ("causal", _I), ("slopes", _P), ("q_pos", _P), ("key_begin", _P), ("key_end", _P)]
+
+
+class AttnRope(ctypes.Structure):
+    """attn_rope_t: a plan of rotary positions (see rope_plan)."""
+    _fields_ = [("rot", _I), ("interleaved", _I), ("mscale", _F), ("reserved", _I), ("turns", ctypes.c_uint64 * 128)]
+
+
+_STRIDES = ctypes.c_longlong * 12
 
 # name -> (restype, argtypes); must list every function of include/attn.h
 _SIGNATURES = {
@@ -50,6 +66,12 @@ _SIGNATURES = {
     "attn_bwd_phase": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P, _SZ,
                             _I, _P]),
     "attn_bwd_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P]),
+    "attn_fwd_scored": (_I, [_P] * 5 + [_I] * 7 + [_F, ctypes.POINTER(AttnScore), _I, _P, _SZ, _P]),
+    "attn_fwd_scored_workspace_size": (_SZ, [_I] * 8),
+    "attn_bwd_scored": (_I, [_P] * 9 + [_I] * 7 + [_F, ctypes.POINTER(AttnScore), _I, _P, _SZ, _P]),
+    "attn_bwd_scored_workspace_size": (_SZ, [_I] * 8),
+    "attn_rope_init": (_I, [ctypes.POINTER(AttnRope), _I, _I] + [ctypes.c_double] * 6),
+    "attn_rope": (_I, [ctypes.POINTER(AttnRope)] + [_P] * 4 + [ctypes.POINTER(ctypes.c_longlong), _P] + [_I] * 7 + [_P]),
     "attn_online_softmax_step": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P]),
     "attn_device_status": (_I, [_P]),
     "attn_selftest_wait_timeout": (_I, [_I, _P]),
@@ -217,6 +239,52 @@ def attn_bwd_noalloc(Q, K, V, O, LSE, dO, dQ, dK, dV, B, H, Tq, Tk, d, dv, scale
 ATTN_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
+def attn_fwd_scored(Q, K, V, O, LSE, B, H, Hkv, Tq, Tk, d, dv, scale, score, dtype, workspace, workspace_bytes,
+                    stream=None, check=True) -> int:
+    """`score`: an AttnScore, or None for plain scores without a mask."""
+    st = load_library().attn_fwd_scored(_ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(LSE), B, H, Hkv, Tq, Tk, d, dv,
+                                        scale, score, dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+    if check:
+        _check(st, "attn_fwd_scored")
+    return st
+
+
+def attn_fwd_scored_workspace_size(B, H, Hkv, Tq, Tk, d, dv, dtype) -> int:
+    return load_library().attn_fwd_scored_workspace_size(B, H, Hkv, Tq, Tk, d, dv, dtype)
+
+
+def attn_bwd_scored(Q, K, V, O, LSE, dO, dQ, dK, dV, B, H, Hkv, Tq, Tk, d, dv, scale, score, dtype, workspace,
+                    workspace_bytes, stream=None, check=True) -> int:
+    st = load_library().attn_bwd_scored(_ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(LSE), _ptr(dO), _ptr(dQ), _ptr(dK),
+                                        _ptr(dV), B, H, Hkv, Tq, Tk, d, dv, scale, score, dtype, _ptr(workspace),
+                                        workspace_bytes, _stream(stream))
+    if check:
+        _check(st, "attn_bwd_scored")
+    return st
+
+
+def attn_bwd_scored_workspace_size(B, H, Hkv, Tq, Tk, d, dv, dtype) -> int:
+    return load_library().attn_bwd_scored_workspace_size(B, H, Hkv, Tq, Tk, d, dv, dtype)
+
+
+def attn_rope_init(plan, rot, interleaved, theta, factor, original_length, low_turns, high_turns, mscale,
+                   check=True) -> int:
+    st = load_library().attn_rope_init(plan, rot, interleaved, theta, factor, original_length, low_turns, high_turns,
+                                       mscale)
+    if check:
+        _check(st, "attn_rope_init")
+    return st
+
+
+def attn_rope(plan, Q, Qout, K, Kout, strides, pos, B, H, Hkv, T, d, inverse, dtype, stream=None, check=True) -> int:
+    """`strides`: 12 element strides (batch, head, token of Q, Qout, K, Kout)."""
+    st = load_library().attn_rope(plan, _ptr(Q), _ptr(Qout), _ptr(K), _ptr(Kout), _STRIDES(*strides), _ptr(pos), B, H,
+                                  Hkv, T, d, inverse, dtype, _stream(stream))
+    if check:
+        _check(st, "attn_rope")
+    return st
+
+
 def attn_device_status(stream=None) -> int:
     return load_library().attn_device_status(_stream(stream))
 
@@ -276,3 +344,142 @@ def backward(q, k, v, o, lse, do, causal: bool = False, scale: Optional[float] =
     attn_bwd(q, k, v, o, lse, do, dq, dk, dvv, B, H, Tq, Tk, d, dv, scale, causal, dt, int(deterministic),
              workspace, workspace.numel(), stream)
     return dq, dk, dvv
+
+
+def _device_of(t):
+    """The CUDA device index of tensor t."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    return t.device.index
+
+
+class _on:
+    """Makes a tensor's device, and a stream given for the call, current, so that what the call allocates belongs to
+    the stream its kernels run on. Costs nothing where both are current already."""
+
+    def __init__(self, index, stream):
+        self.guards = []
+        if index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(index))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=index)
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _scored_args(q, k, v, causal, scale, softcap, slopes, q_pos, key_begin, key_end):
+    """Checks shapes, types and devices; (B, H, Hkv, Tq, Tk, d, dv, dtype, scale, AttnScore)."""
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("expected [B, H, T, d] tensors")
+    B, H, Tq, d = q.shape
+    Hkv, Tk, dv = k.shape[1], k.shape[2], v.shape[3]
+    if k.shape != (B, Hkv, Tk, d) or v.shape != (B, Hkv, Tk, dv):
+        raise ValueError("Q, K, V shapes disagree")
+    if Hkv == 0 or H % Hkv:
+        raise ValueError("the number of query heads must be a multiple of the number of key heads")
+    dev = q.get_device()
+    for t in (q, k, v):
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        if t.dtype != q.dtype or t.get_device() != dev:
+            raise ValueError("Q, K and V must have one dtype and device")
+    for name, t in (("q_pos", q_pos), ("key_begin", key_begin), ("key_end", key_end)):
+        if t is not None and (t.dtype != torch.int32 or t.shape != (B, Tq) or not t.is_contiguous() or
+                              t.get_device() != dev):
+            raise ValueError(f"{name} must be a contiguous int32 [B, Tq] tensor on Q's device")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (H,) or not slopes.is_contiguous() or
+                               slopes.get_device() != dev):
+        raise ValueError("slopes must be a contiguous fp32 [H] tensor on Q's device")
+    score = AttnScore(softcap, int(causal), _ptr(slopes), _ptr(q_pos), _ptr(key_begin), _ptr(key_end))
+    return B, H, Hkv, Tq, Tk, d, dv, _dtype_code(q), 1.0 / math.sqrt(d) if scale is None else float(scale), score
+
+
+def _workspace(given, nbytes, like):
+    if given is not None:
+        return given
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device)
+
+
+def forward_scored(q, k, v, causal: bool = False, scale: Optional[float] = None, softcap: float = 0.0, slopes=None,
+                   q_pos=None, key_begin=None, key_end=None, stream=None, workspace=None):
+    """O, LSE of the scored attention: q [B, H, Tq, d], k [B, Hkv, Tk, d], v [B, Hkv, Tk, dv].
+
+    Scores scale * q.k are capped by softcap * tanh(. / softcap) where softcap > 0, lowered by slopes[h] *
+    |q_pos - key| where slopes ([H] fp32) is given, and limited to keys [key_begin, key_end) of each query row
+    (int32 [B, Tq], shared by the heads) and, with causal, to keys at or before q_pos (default: the row index).
+    Allocates O, LSE and, unless given, the workspace (uint8, attn_fwd_scored_workspace_size bytes)."""
+    B, H, Hkv, Tq, Tk, d, dv, dt, scale, score = _scored_args(q, k, v, causal, scale, softcap, slopes, q_pos,
+                                                              key_begin, key_end)
+    with _on(_device_of(q), stream):
+        o = torch.empty((B, H, Tq, dv), dtype=q.dtype, device=q.device)
+        lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
+        ws = _workspace(workspace, attn_fwd_scored_workspace_size(B, H, Hkv, Tq, Tk, d, dv, dt), q)
+        attn_fwd_scored(q, k, v, o, lse, B, H, Hkv, Tq, Tk, d, dv, scale, score, dt, ws, ws.numel(), stream)
+    return o, lse
+
+
+def backward_scored(q, k, v, o, lse, do, causal: bool = False, scale: Optional[float] = None, softcap: float = 0.0,
+                    slopes=None, q_pos=None, key_begin=None, key_end=None, stream=None, workspace=None):
+    """dQ, dK, dV of forward_scored's O (same arguments; dK and dV summed over the heads that share them)."""
+    B, H, Hkv, Tq, Tk, d, dv, dt, scale, score = _scored_args(q, k, v, causal, scale, softcap, slopes, q_pos,
+                                                              key_begin, key_end)
+    for name, t, shape, dtype in (("O", o, (B, H, Tq, dv), q.dtype), ("dO", do, (B, H, Tq, dv), q.dtype),
+                                  ("LSE", lse, (B, H, Tq), torch.float32)):
+        if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != q.get_device():
+            raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on Q's device")
+    with _on(_device_of(q), stream):
+        dq, dk, dvv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ws = _workspace(workspace, attn_bwd_scored_workspace_size(B, H, Hkv, Tq, Tk, d, dv, dt), q)
+        attn_bwd_scored(q, k, v, o, lse, do, dq, dk, dvv, B, H, Hkv, Tq, Tk, d, dv, scale, score, dt, ws, ws.numel(),
+                        stream)
+    return dq, dk, dvv
+
+
+def rope_plan(rot: int, interleaved: bool = False, theta: float = 10000.0, factor: float = 1.0,
+              original_length: float = 0.0, low_turns: float = 1.0, high_turns: float = 4.0,
+              mscale: float = 1.0) -> AttnRope:
+    """A plan for rope(): `rot` rotated elements a head, pairs (i, i + rot/2) or, interleaved, (2i, 2i + 1).
+
+    `factor` stretches the context: every frequency is divided by it, or, with original_length > 0, only those
+    of pairs that make fewer than high_turns turns over it (wholly below low_turns)."""
+    plan = AttnRope()
+    attn_rope_init(plan, int(rot), int(interleaved), theta, factor, original_length, low_turns, high_turns, mscale)
+    return plan
+
+
+def rope(q, k, plan: AttnRope, pos=None, inverse: bool = False, out=None, stream=None):
+    """Rotary positions of q [B, H, T, d] and k [B, Hkv, T, d] (any strides, last dimension contiguous).
+
+    pos: int32 [B, T] positions (default: the token index); inverse turns back, which is the gradient. Returns
+    new contiguous tensors, or writes `out` = (q_out, k_out), which may be (q, k) themselves."""
+    if q.dim() != 4 or k.dim() != 4 or q.dtype != k.dtype or q.get_device() != k.get_device():
+        raise ValueError("expected two [B, H, T, d] tensors of one dtype and device")
+    B, H, T, d = q.shape
+    Hkv = k.shape[1]
+    if k.shape != (B, Hkv, T, d):
+        raise ValueError("Q and K shapes disagree")
+    if pos is not None and (pos.dtype != torch.int32 or pos.shape != (B, T) or not pos.is_contiguous() or
+                            pos.get_device() != q.get_device()):
+        raise ValueError("pos must be a contiguous int32 [B, T] tensor on Q's device")
+    with _on(_device_of(q), stream):
+        if out is None:
+            out = (torch.empty((B, H, T, d), dtype=q.dtype, device=q.device),
+                   torch.empty((B, Hkv, T, d), dtype=q.dtype, device=q.device))
+        strides = []
+        for t, shape in ((q, q.shape), (out[0], q.shape), (k, k.shape), (out[1], k.shape)):
+            if t.shape != shape or t.dtype != q.dtype or t.get_device() != q.get_device():
+                raise ValueError("outputs must have the shapes, dtype and device of Q and K")
+            st = t.stride()
+            if st[3] != 1 and d > 1:
+                raise ValueError("the last dimension must be contiguous")
+            strides += st[:3]
+        attn_rope(plan, q, out[0], k, out[1], strides, pos, B, H, Hkv, T, d, int(inverse), _dtype_code(q), stream)
+    return out

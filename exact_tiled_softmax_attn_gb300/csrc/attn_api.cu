@@ -6,10 +6,9 @@
 #include <stdint.h>
 #include <string.h>
 
-#include <mutex>
-
 #include "attn.h"
 #include "common.cuh"
+#include "host.h"
 #include "launch.h"
 #include "simt.h"
 #include "ptx.cuh"
@@ -22,13 +21,6 @@ __device__ uint32_t g_device_status;
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceInfo {
-  std::once_flag once;
-  cudaError_t err = cudaSuccess;
-  int num_sms = 0;
-  int l2_bytes = 0;
-  uint32_t* status = nullptr;
-};
 DeviceInfo g_dev[kMaxDevices];
 
 thread_local int t_last_cuda_error = 0;
@@ -38,6 +30,7 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 std::once_flag g_encode_once;
 EncodeTiledFn g_encode = nullptr;
+}  // namespace
 
 attn_status_t cuda_fail(cudaError_t e) {
   t_last_cuda_error = static_cast<int>(e);
@@ -61,7 +54,7 @@ attn_status_t device_info(DeviceInfo** out) {
   return ATTN_OK;
 }
 
-attn_status_t encoder(EncodeTiledFn* fn) {
+static attn_status_t encoder(EncodeTiledFn* fn) {
   std::call_once(g_encode_once, [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -78,8 +71,8 @@ attn_status_t encoder(EncodeTiledFn* fn) {
 // 3-D map over a [planes, rows, inner] array with 128-byte swizzled boxes of
 // box_rows rows x (128 bytes of elements): 64 bf16 or 32 fp32. Rows past
 // `rows` read as zero within each plane (and are not written by reduces).
-attn_status_t make_map(CUtensorMap* m, const void* base, int inner, int rows, int planes, bool f32 = false,
-                       unsigned box_rows = 128) {
+attn_status_t make_map(CUtensorMap* m, const void* base, int inner, int rows, int planes, bool f32,
+                       unsigned box_rows) {
   EncodeTiledFn enc;
   attn_status_t s = encoder(&enc);
   if (s != ATTN_OK) return s;
@@ -100,16 +93,8 @@ attn_status_t make_map(CUtensorMap* m, const void* base, int inner, int rows, in
   return ATTN_OK;
 }
 
-size_t elem_size(attn_dtype_t dt) { return dt == ATTN_BF16 ? 2 : 4; }
+namespace {
 
-struct Range {
-  uintptr_t lo, hi;
-};
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-Range range(const void* p, size_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, lo + bytes};
-}
 
 // bf16 shapes. The forward takes d and dv in [8, 256], multiples of 8 (a row
 // of Q, K, V or O is then a whole number of 16-byte TMA and store units): the
@@ -144,14 +129,7 @@ attn_status_t check_common(int B, int H, int Tq, int Tk, int d, int dv, float sc
   return ATTN_OK;
 }
 
-attn_status_t check_ptr(const void* p, size_t bytes, size_t align) {
-  if (bytes == 0) return ATTN_OK;  // empty tensors may be NULL
-  if (p == nullptr) return ATTN_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(p) % align) return ATTN_ERR_MISALIGNED;
-  return ATTN_OK;
-}
-
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+}  // namespace
 
 // Key splits for `units` work units of nkb key tiles each, one CTA per unit
 // and key range on `slots` SMs: the time of S splits is taken as the waves of
@@ -171,6 +149,8 @@ int wave_splits(long long units, int nkb, int slots) {
   while (S < smax && cost(S) > 1.05 * best) ++S;
   return S;
 }
+
+namespace {
 
 struct BwdLayout {
   size_t lse2_off, d_off, acc_off, acc_bytes, sched_off, total;

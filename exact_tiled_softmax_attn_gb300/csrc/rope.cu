@@ -1,0 +1,289 @@
+// Rotary positions of queries and keys.
+//
+// Pair (u, v) of a token at position p is turned by p * f_i. The plan holds
+// f_i / (2 pi) as F_i * 2^-64, so that p * F_i modulo 2^64 is the angle as a
+// fraction of a turn, exact at any position: its upper 32 bits, as a signed
+// number, times 2^-31 is the angle in half turns within [-1, 1), which
+// sincospi takes. (An fp32 product p * f_i would be off by 0.03 radians at p
+// = 10^6.) One thread does one chunk of pairs of one token for several heads
+// and so computes each sine and cosine once for all of them; the rest of a
+// head (from rot on) is copied in chunks of its own. Bound by memory: every
+// element is read and written once, in 16-byte accesses where rows, strides
+// and pointers allow.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attn.h"
+#include "host.h"
+
+namespace attn {
+namespace rope {
+
+constexpr int NT = 256;
+
+struct View {   // element strides of batch, head, token
+  long long b, h, t;
+};
+
+struct Params {
+  attn_rope_t plan;
+  const void* x[2];   // Q, K
+  void* y[2];
+  View xs[2], ys[2];
+  const int* pos;
+  int heads[2];       // H, Hkv
+  int B, T, d;
+  int slots;          // threads that share a token's chunk, each with every slots-th head
+  int rot_chunks;     // chunks of V pairs
+  int chunks;         // and of V copied elements behind them
+  int tokens_per_block;
+  float sign;         // -1: inverse
+};
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T e[V];
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// V pairs (or V copied elements) a chunk; INTER: the pairs of a chunk are 2 V
+// adjacent elements, otherwise V elements at i and V at i + rot / 2.
+template <typename T, int V, bool INTER>
+__global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ Params P) {
+  using W = Vec<T, V>;
+  const int per_token = P.slots * P.chunks;
+  const long long tokens = static_cast<long long>(P.B) * P.T;
+  const int n = P.tokens_per_block * per_token;
+  for (int i = threadIdx.x; i < n; i += NT) {
+    const int tok = i / per_token, rest = i - tok * per_token;
+    const int slot = rest / P.chunks, c = rest - slot * P.chunks;
+    const long long bt = static_cast<long long>(blockIdx.x) * P.tokens_per_block + tok;
+    if (bt >= tokens) return;
+    const int b = static_cast<int>(bt / P.T), t = static_cast<int>(bt - static_cast<long long>(b) * P.T);
+    const bool turn = c < P.rot_chunks;
+    int o0, o1;   // the chunk's two places in a row
+    float cs[V], sn[V];
+    if (turn) {
+      const long long pos = P.pos ? P.pos[bt] : t;
+      o0 = INTER ? 2 * V * c : V * c;
+      o1 = INTER ? o0 + V : o0 + P.plan.rot / 2;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const unsigned long long turns = static_cast<unsigned long long>(pos) * P.plan.turns[V * c + e];
+        const float half_turns = static_cast<float>(static_cast<int>(turns >> 32)) * 0x1p-31f;
+        sincospif(half_turns, &sn[e], &cs[e]);
+        sn[e] *= P.sign * P.plan.mscale;
+        cs[e] *= P.plan.mscale;
+      }
+    } else {
+      o0 = o1 = P.plan.rot + V * (c - P.rot_chunks);
+    }
+    const int total = P.heads[0] + P.heads[1];
+#pragma unroll 4
+    for (int h = slot; h < total; h += P.slots) {
+      const int k = h >= P.heads[0] ? 1 : 0;
+      const int hh = h - (k ? P.heads[0] : 0);
+      const T* x = static_cast<const T*>(P.x[k]) + b * P.xs[k].b + hh * P.xs[k].h + t * P.xs[k].t;
+      T* y = static_cast<T*>(P.y[k]) + b * P.ys[k].b + hh * P.ys[k].h + t * P.ys[k].t;
+      W u = *reinterpret_cast<const W*>(x + o0);
+      if (turn) {
+        W v = *reinterpret_cast<const W*>(x + o1);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          // pair e of the chunk: (u_e, v_e), or elements 2e, 2e + 1 of the 2 V adjacent ones
+          T& pu = INTER ? (2 * e < V ? u.e[(2 * e) % V] : v.e[(2 * e) % V]) : u.e[e];
+          T& pv = INTER ? (2 * e + 1 < V ? u.e[(2 * e + 1) % V] : v.e[(2 * e + 1) % V]) : v.e[e];
+          const float a = to_f(pu), w = to_f(pv);
+          pu = from_f<T>(a * cs[e] - w * sn[e]);
+          pv = from_f<T>(w * cs[e] + a * sn[e]);
+        }
+        *reinterpret_cast<W*>(y + o1) = v;
+      }
+      *reinterpret_cast<W*>(y + o0) = u;
+    }
+  }
+}
+
+// Elements past a view's first one to its last one plus one.
+long long extent(const View& s, int B, int H, int T, int d) {
+  return (B - 1) * s.b + (H - 1) * s.h + (T - 1) * s.t + d;
+}
+
+// Whether no two elements of the view share an address: its dimensions, from
+// the smallest stride up, must each step over what lies below.
+bool distinct(const View& s, int B, int H, int T, int d) {
+  long long st[3] = {s.b, s.h, s.t};
+  long long n[3] = {B, H, T};
+  long long span = d;
+  for (int i = 0; i < 3; ++i) {
+    int m = i;
+    for (int j = i + 1; j < 3; ++j)
+      if (st[j] < st[m]) m = j;
+    const long long a = st[m], c = n[m];
+    st[m] = st[i], n[m] = n[i];
+    if (c <= 1) continue;
+    if (a < span) return false;
+    span += (c - 1) * a;
+  }
+  return true;
+}
+
+// Whether two views are known to share no address: their extents are apart,
+// or both step by the same batch and token strides and lie beside each other
+// within a token (the queries and keys of one projection's rows).
+bool apart(const void* pa, const View& a, int Ha, const void* pb, const View& b, int Hb, int B, int T, int d,
+           size_t es) {
+  if (!overlap(range(pa, extent(a, B, Ha, T, d) * es), range(pb, extent(b, B, Hb, T, d) * es))) return true;
+  if (a.t != b.t || a.t <= 0 || (B > 1 && (a.b != b.b || a.b % a.t))) return false;
+  const long long delta = static_cast<long long>(reinterpret_cast<uintptr_t>(pb)) -
+                          static_cast<long long>(reinterpret_cast<uintptr_t>(pa));
+  const long long step = a.t * static_cast<long long>(es);
+  const long long off = ((delta % step) + step) % step;
+  const long long la = ((Ha - 1) * a.h + d) * static_cast<long long>(es),
+                  lb = ((Hb - 1) * b.h + d) * static_cast<long long>(es);
+  return off >= la && off + lb <= step;
+}
+
+template <typename T, int V>
+cudaError_t launch(Params& P, cudaStream_t st, int num_sms) {
+  const long long tokens = static_cast<long long>(P.B) * P.T;
+  P.rot_chunks = P.plan.rot / 2 / V;
+  P.chunks = P.rot_chunks + (P.d - P.plan.rot) / V;
+  const int total = P.heads[0] + P.heads[1];
+  // heads per thread: up to 8, as long as at least 1024 threads an SM are left
+  int per = 8;
+  while (per > 1 && tokens * P.chunks * ((total + per - 1) / per) < num_sms * 1024LL) per /= 2;
+  P.slots = (total + per - 1) / per;
+  const int per_token = P.slots * P.chunks;
+  P.tokens_per_block = per_token >= NT ? 1 : NT / per_token;
+  const long long grid = (tokens + P.tokens_per_block - 1) / P.tokens_per_block;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (P.plan.interleaved)
+    rope_kernel<T, V, true><<<static_cast<unsigned>(grid), NT, 0, st>>>(P);
+  else
+    rope_kernel<T, V, false><<<static_cast<unsigned>(grid), NT, 0, st>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace rope
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" {
+
+attn_status_t attn_rope_init(attn_rope_t* plan, int rot, int interleaved, double theta, double factor,
+                             double original_length, double low_turns, double high_turns, double mscale) {
+  if (plan == nullptr || rot < 2 || rot > 2 * ATTN_ROPE_MAX_PAIRS || rot % 2) return ATTN_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return ATTN_ERR_INVALID_ARG;
+  if (!(theta > 1.0) || !isfinite(theta) || !(factor >= 1.0) || !isfinite(factor)) return ATTN_ERR_INVALID_ARG;
+  if (!(original_length >= 0.0) || !isfinite(original_length)) return ATTN_ERR_INVALID_ARG;
+  if (original_length > 0.0 && !(low_turns >= 0.0 && low_turns < high_turns && isfinite(high_turns)))
+    return ATTN_ERR_INVALID_ARG;
+  if (!(mscale > 0.0) || !isfinite(static_cast<float>(mscale)) || !(static_cast<float>(mscale) > 0.f))
+    return ATTN_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925;
+  *plan = attn_rope_t{};
+  plan->rot = rot;
+  plan->interleaved = interleaved;
+  plan->mscale = static_cast<float>(mscale);
+  for (int i = 0; i < rot / 2; ++i) {
+    const double f = pow(theta, -2.0 * i / rot);
+    double keep = 0.0;   // the share of f that is not divided by the factor
+    if (original_length > 0.0) {
+      keep = (original_length * f / two_pi - low_turns) / (high_turns - low_turns);
+      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+    }
+    const double g = f * keep + f / factor * (1.0 - keep);
+    plan->turns[i] = static_cast<unsigned long long>(rint(ldexp(g / two_pi, 64)));   // g <= 1: below 2^62
+  }
+  return ATTN_OK;
+}
+
+attn_status_t attn_rope(const attn_rope_t* plan, const void* Q, void* Qout, const void* K, void* Kout,
+                        const long long* strides, const int* pos, int B, int H, int Hkv, int T, int d, int inverse,
+                        attn_dtype_t dtype, void* stream) {
+  if (plan == nullptr || strides == nullptr || B < 0 || H < 0 || Hkv < 0 || T < 0 || d <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (inverse != 0 && inverse != 1) return ATTN_ERR_INVALID_ARG;
+  if (dtype != ATTN_F32 && dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  if (plan->rot < 2 || plan->rot % 2 || plan->rot > d || (plan->interleaved != 0 && plan->interleaved != 1))
+    return ATTN_ERR_INVALID_ARG;
+  if (d > 2 * ATTN_ROPE_MAX_PAIRS) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(H) + Hkv > 0x7fffffff / 256) return ATTN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(pos) % 4) return ATTN_ERR_MISALIGNED;
+  const size_t es = elem_size(dtype);
+  const void* in[2] = {Q, K};
+  void* out[2] = {Qout, Kout};
+  const int heads[2] = {H, Hkv};
+  const bool some = B > 0 && T > 0;
+  rope::Params P{};
+  bool wide = true;   // 16-byte accesses everywhere
+  const int V = 16 / static_cast<int>(es);
+  for (int k = 0; k < 2; ++k) {
+    const long long* s = strides + 6 * k;
+    P.xs[k] = rope::View{s[0], s[1], s[2]};
+    P.ys[k] = rope::View{s[3], s[4], s[5]};
+    P.heads[k] = some ? heads[k] : 0;
+    if (P.heads[k] == 0) continue;
+    for (int i = 0; i < 6; ++i) {
+      if (s[i] < 0 || s[i] > (1LL << 50)) return ATTN_ERR_INVALID_ARG;
+      wide = wide && s[i] % V == 0;
+    }
+    for (const void* p : {in[k], static_cast<const void*>(out[k])}) {
+      if (p == nullptr) return ATTN_ERR_INVALID_ARG;
+      if (reinterpret_cast<uintptr_t>(p) % es) return ATTN_ERR_MISALIGNED;
+      wide = wide && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+    }
+    if (static_cast<double>(s[0]) * B + static_cast<double>(s[1]) * heads[k] + static_cast<double>(s[2]) * T > 9e15 ||
+        static_cast<double>(s[3]) * B + static_cast<double>(s[4]) * heads[k] + static_cast<double>(s[5]) * T > 9e15)
+      return ATTN_ERR_INVALID_ARG;
+    if (!rope::distinct(P.ys[k], B, heads[k], T, d)) return ATTN_ERR_INVALID_ARG;
+    P.x[k] = in[k];
+    P.y[k] = out[k];
+  }
+  for (int k = 0; k < 2; ++k) {   // output k against the inputs and the other output
+    if (P.heads[k] == 0) continue;
+    for (int j = 0; j < 2; ++j) {
+      if (P.heads[j] == 0) continue;
+      const rope::View &y = P.ys[k], &x = P.xs[j];
+      const bool in_place = j == k && in[k] == out[k] && y.b == x.b && y.h == x.h && y.t == x.t;
+      if (!in_place && !rope::apart(out[k], y, heads[k], in[j], x, heads[j], B, T, d, es)) return ATTN_ERR_INVALID_ARG;
+      if (j > k && !rope::apart(out[k], y, heads[k], out[j], P.ys[j], heads[j], B, T, d, es))
+        return ATTN_ERR_INVALID_ARG;
+    }
+    if (pos && overlap(range(out[k], rope::extent(P.ys[k], B, heads[k], T, d) * es),
+                       range(pos, static_cast<size_t>(B) * T * 4)))
+      return ATTN_ERR_INVALID_ARG;
+  }
+  if (!some || (H == 0 && Hkv == 0)) return ATTN_OK;
+  DeviceInfo* di;
+  attn_status_t s = device_info(&di);
+  if (s != ATTN_OK) return s;
+  P.plan = *plan;
+  P.pos = pos;
+  P.B = B;
+  P.T = T;
+  P.d = d;
+  P.sign = inverse ? -1.f : 1.f;
+  wide = wide && (plan->rot / 2) % V == 0 && (d - plan->rot) % V == 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dtype == ATTN_BF16)
+    e = wide ? rope::launch<__nv_bfloat16, 8>(P, st, di->num_sms) : rope::launch<__nv_bfloat16, 1>(P, st, di->num_sms);
+  else
+    e = wide ? rope::launch<float, 4>(P, st, di->num_sms) : rope::launch<float, 1>(P, st, di->num_sms);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,95 @@
+// Internal interface of the scored attention (include/attn.h, attn_fwd_scored
+// and attn_bwd_scored) between its C-ABI layer and its kernels.
+//
+// The query heads that share a key head are adjacent in memory, so their rows
+// form one packed list of R = G * Tq rows per key head (G = H / Hkv): Q is
+// [B * Hkv, R, d] and row r belongs to query head hkv * G + r / Tq at token
+// r % Tq. Every kernel works on packed rows. Heads that share keys then also
+// share key tiles, and the sums of dK and dV over a group are sums over rows.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace attn {
+
+constexpr int kScoredTile = 128;   // rows of the plan's row tiles, keys of its key tiles
+
+struct ScoredProblem {
+  int B, Hkv, G, Tq, Tk, d, dv;
+  int R;         // packed query rows of a key head: G * Tq
+  int n_rt;      // 128-row tiles of R
+  int n_kt;      // 128-key tiles of Tk
+  float scale;
+  float softcap;          // 0: none
+  const float* slopes;    // [H] or null
+  __host__ __device__ int rpad() const { return n_rt * kScoredTile; }
+};
+
+// What the plan kernel makes of the ranges of a call (all in the workspace).
+struct ScoredPlan {
+  int4* rows;      // [B][rpad]: {key begin, key end, position, 0}; begin = INT_MAX, end = 0 for rows that see nothing
+  int4* tiles;     // [B][n_rt]: {min begin, max end over the rows that see keys, max begin, min end over all rows}
+  int2* ktiles;    // [B][n_kt]: {first row tile, row tiles} whose hull meets the key tile (backward only), or null
+  float* slope2;   // [Hkv][rpad]: slope * log2(e) of each packed row (backward with a bias only), or null
+  uint32_t* counters;   // two unit counters, zeroed
+};
+
+struct ScoredMask {   // the caller's arrays
+  const int* q_pos;
+  const int* key_begin;
+  const int* key_end;
+  int causal;
+};
+
+cudaError_t launch_scored_plan(const ScoredProblem& p, const ScoredMask& m, const ScoredPlan& plan, cudaStream_t s);
+
+struct ScoredFwd {
+  ScoredProblem p;
+  ScoredPlan plan;
+  ScoredMask mask;
+  const void* Q;
+  const void* K;
+  const void* V;
+  void* O;
+  float* LSE;
+  int n_splits;       // key ranges of split_keys keys (a multiple of 128) each, as units of their own
+  int split_keys;
+  float* Opart;       // [n_splits][B * Hkv * R][dv] fp32, n_splits > 1
+  float* LSEpart;     // [n_splits][B * Hkv * R]
+  const CUtensorMap* tmQ;   // bf16 only
+  const CUtensorMap* tmK;
+  const CUtensorMap* tmV;
+  uint32_t* status;
+  int num_sms;
+  cudaStream_t stream;
+};
+
+struct ScoredBwd {
+  ScoredProblem p;
+  ScoredPlan plan;
+  const void* Q;
+  const void* K;
+  const void* V;
+  const void* O;
+  const float* LSE;
+  const void* dO;
+  void* dQ;
+  void* dK;
+  void* dV;
+  float* D;         // [B * Hkv][rpad]: rowsum(dO o O), 0 behind row R
+  float* NL;        // [B * Hkv][rpad]: -LSE * log2(e), -inf for rows that see nothing and behind row R
+  uint32_t* status;
+  int num_sms;
+  cudaStream_t stream;
+};
+
+// CUDA cores (fp32 problems)
+cudaError_t launch_scored_fwd_simt(const ScoredFwd& a, bool bf16);
+cudaError_t launch_scored_bwd_simt(const ScoredBwd& a, bool bf16);
+
+// O and LSE from the partial results of the key ranges, in range order
+cudaError_t launch_scored_merge(const ScoredFwd& a, bool bf16);
+
+}  // namespace attn

@@ -1,0 +1,281 @@
+// C-ABI layer of the scored attention: argument validation, workspace
+// layout and dispatch.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attn.h"
+#include "host.h"
+#include "launch.h"
+#include "scored.h"
+
+namespace attn {
+namespace {
+
+constexpr int kMaxRows = 1 << 30;
+// Workspace sizes are rules of the shapes alone, so counts that aim at
+// filling the GPU use GB300's SM count.
+constexpr int kSms = 152;
+
+attn_status_t check_scored(int B, int H, int Hkv, int Tq, int Tk, int d, int dv, attn_dtype_t dt) {
+  if (B < 0 || H < 0 || Tq < 0 || Tk < 0 || d <= 0 || dv <= 0) return ATTN_ERR_INVALID_ARG;
+  if (Hkv < 1 || H % Hkv) return ATTN_ERR_INVALID_ARG;
+  if (dt != ATTN_F32 && dt != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  if (Tq > kMaxRows || Tk > kMaxRows || static_cast<long long>(H / Hkv) * Tq > kMaxRows) return ATTN_ERR_INVALID_ARG;
+  // work units (64-row or 64-key tiles of every head) are counted in int
+  const double heads = static_cast<double>(B) * Hkv;
+  const double rows = static_cast<double>(H / Hkv) * Tq;
+  if (heads * ((rows > Tk ? rows : Tk) / 64.0 + 2.0) > 2147483647.0) return ATTN_ERR_INVALID_ARG;
+  if (d > 128 || dv > 128) return ATTN_ERR_UNSUPPORTED;
+  if (dt == ATTN_BF16 && (d % 8 || dv % 8)) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+attn_status_t check_score(const attn_score_t& sc, int B, int H, int Tq, float scale) {
+  if (!(scale > 0.f) || !isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (!(sc.softcap >= 0.f) || !isfinite(sc.softcap)) return ATTN_ERR_INVALID_ARG;
+  if (sc.causal != 0 && sc.causal != 1) return ATTN_ERR_INVALID_ARG;
+  for (const void* x : {static_cast<const void*>(sc.slopes), static_cast<const void*>(sc.q_pos),
+                        static_cast<const void*>(sc.key_begin), static_cast<const void*>(sc.key_end)})
+    if (reinterpret_cast<uintptr_t>(x) % 4) return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+ScoredProblem problem(int B, int H, int Hkv, int Tq, int Tk, int d, int dv) {
+  ScoredProblem p{};
+  p.B = B;
+  p.Hkv = Hkv;
+  p.G = H / Hkv;
+  p.Tq = Tq;
+  p.Tk = Tk;
+  p.d = d;
+  p.dv = dv;
+  p.R = p.G * Tq;
+  p.n_rt = (p.R + kScoredTile - 1) / kScoredTile;
+  p.n_kt = (Tk + kScoredTile - 1) / kScoredTile;
+  return p;
+}
+
+// Key ranges of the forward: the CUDA-core kernel runs two 64-row tiles per
+// SM at a time.
+void fwd_splits(const ScoredProblem& p, attn_dtype_t dt, int* S, int* keys) {
+  const long long units = static_cast<long long>(p.B) * p.Hkv * ((p.R + 63) / 64);
+  const int want = wave_splits(units, p.n_kt, 2 * kSms);
+  const int tiles = want > 1 ? (p.n_kt + want - 1) / want : p.n_kt;
+  *S = want > 1 ? (p.n_kt + tiles - 1) / tiles : 1;
+  *keys = tiles * kScoredTile;
+}
+
+struct Layout {
+  size_t rows, tiles, counters, ktiles, slope2, D, NL, opart, lsepart, total;
+  int n_splits, split_keys;
+};
+
+// Forward: rows | tiles | counters | Opart | LSEpart. Backward: rows | tiles |
+// counters | ktiles | slope2 | D | NL. Each part starts on 256 bytes.
+Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
+  Layout L{};
+  L.n_splits = 1;
+  L.split_keys = p.n_kt * kScoredTile;
+  if (p.B == 0 || p.R == 0 || p.Tk == 0) return L;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = round_up(off + bytes, 256);
+    return at;
+  };
+  const size_t B = p.B, rpad = p.rpad(), heads = B * p.Hkv;
+  L.rows = take(B * rpad * sizeof(int4));
+  L.tiles = take(B * p.n_rt * sizeof(int4));
+  L.counters = take(256);
+  if (bwd) {
+    L.ktiles = take(B * p.n_kt * sizeof(int2));
+    L.slope2 = take(p.Hkv * rpad * sizeof(float));
+    L.D = take(heads * rpad * sizeof(float));
+    L.NL = take(heads * rpad * sizeof(float));
+  } else {
+    fwd_splits(p, dt, &L.n_splits, &L.split_keys);
+    if (L.n_splits > 1) {
+      L.opart = take(L.n_splits * heads * p.R * p.dv * sizeof(float));
+      L.lsepart = take(L.n_splits * heads * p.R * sizeof(float));
+    }
+  }
+  L.total = off;
+  return L;
+}
+
+ScoredPlan plan_at(const Layout& L, void* ws, bool bwd, bool bias) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  ScoredPlan s{};
+  s.rows = reinterpret_cast<int4*>(w + L.rows);
+  s.tiles = reinterpret_cast<int4*>(w + L.tiles);
+  s.counters = reinterpret_cast<uint32_t*>(w + L.counters);
+  if (bwd) s.ktiles = reinterpret_cast<int2*>(w + L.ktiles);
+  if (bwd && bias) s.slope2 = reinterpret_cast<float*>(w + L.slope2);
+  return s;
+}
+
+struct Arrays {   // the caller's device arrays of attn_score_t as ranges
+  Range r[4];
+};
+Arrays arrays(const attn_score_t& sc, int B, int H, int Tq) {
+  const size_t n = static_cast<size_t>(B) * Tq * 4;
+  return {{range(sc.slopes, sc.slopes ? static_cast<size_t>(H) * 4 : 0), range(sc.q_pos, sc.q_pos ? n : 0),
+           range(sc.key_begin, sc.key_begin ? n : 0), range(sc.key_end, sc.key_end ? n : 0)}};
+}
+
+attn_status_t check_ws(const void* ws, size_t bytes, size_t need) {
+  if (need == 0) return ATTN_OK;
+  if (ws == nullptr || bytes < need || reinterpret_cast<uintptr_t>(ws) % 256) return ATTN_ERR_WORKSPACE;
+  return ATTN_OK;
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" {
+
+size_t attn_fwd_scored_workspace_size(int B, int H, int Hkv, int Tq, int Tk, int d, int dv, attn_dtype_t dtype) {
+  if (check_scored(B, H, Hkv, Tq, Tk, d, dv, dtype) != ATTN_OK) return 0;
+  return layout(problem(B, H, Hkv, Tq, Tk, d, dv), dtype, false).total;
+}
+
+size_t attn_bwd_scored_workspace_size(int B, int H, int Hkv, int Tq, int Tk, int d, int dv, attn_dtype_t dtype) {
+  if (check_scored(B, H, Hkv, Tq, Tk, d, dv, dtype) != ATTN_OK) return 0;
+  return layout(problem(B, H, Hkv, Tq, Tk, d, dv), dtype, true).total;
+}
+
+attn_status_t attn_fwd_scored(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int H, int Hkv,
+                              int Tq, int Tk, int d, int dv, float scale, const attn_score_t* score,
+                              attn_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  attn_status_t s = check_scored(B, H, Hkv, Tq, Tk, d, dv, dtype);
+  const attn_score_t sc = score ? *score : attn_score_t{};
+  if (s == ATTN_OK) s = check_score(sc, B, H, Tq, scale);
+  if (s != ATTN_OK) return s;
+  const bool bf16 = dtype == ATTN_BF16;
+  const size_t es = elem_size(dtype), align = bf16 ? 16 : 4;
+  const size_t nq = static_cast<size_t>(B) * H * Tq, nk = static_cast<size_t>(B) * Hkv * Tk;
+  const void* ins[3] = {Q, K, V};
+  const size_t in_bytes[3] = {nq * d * es, nk * d * es, nk * dv * es};
+  for (int i = 0; i < 3; ++i)
+    if ((s = check_ptr(ins[i], in_bytes[i], align)) != ATTN_OK) return s;
+  if ((s = check_ptr(O, nq * dv * es, align)) != ATTN_OK) return s;
+  if ((s = check_ptr(LSE, nq * 4, 4)) != ATTN_OK) return s;
+  ScoredFwd a{};
+  a.p = problem(B, H, Hkv, Tq, Tk, d, dv);
+  a.p.scale = scale;
+  a.p.softcap = sc.softcap;
+  a.p.slopes = sc.slopes;
+  const Layout L = layout(a.p, dtype, false);
+  if ((s = check_ws(workspace, workspace_bytes, L.total)) != ATTN_OK) return s;
+  const Arrays ar = arrays(sc, B, H, Tq);
+  const Range ro = range(O, nq * dv * es), rl = range(LSE, nq * 4), rw = range(workspace, L.total);
+  if (overlap(ro, rl)) return ATTN_ERR_INVALID_ARG;
+  if (overlap(rw, ro) || overlap(rw, rl)) return ATTN_ERR_WORKSPACE;
+  const Range in[7] = {range(Q, in_bytes[0]), range(K, in_bytes[1]), range(V, in_bytes[2]),
+                       ar.r[0], ar.r[1], ar.r[2], ar.r[3]};
+  for (const Range& x : in) {
+    if (overlap(ro, x) || overlap(rl, x)) return ATTN_ERR_INVALID_ARG;
+    if (overlap(rw, x)) return ATTN_ERR_WORKSPACE;
+  }
+  if (nq == 0) return ATTN_OK;
+  DeviceInfo* di;
+  if ((s = device_info(&di)) != ATTN_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (Tk == 0) {
+    e = launch_fill_empty_fwd(Problem{B, H, Tq, Tk, d, dv, scale, 0}, O, LSE, static_cast<int>(es), st);
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+  }
+  a.mask = ScoredMask{sc.q_pos, sc.key_begin, sc.key_end, sc.causal};
+  a.plan = plan_at(L, workspace, false, sc.slopes != nullptr);
+  a.Q = Q;
+  a.K = K;
+  a.V = V;
+  a.O = O;
+  a.LSE = LSE;
+  a.n_splits = L.n_splits;
+  a.split_keys = L.split_keys;
+  a.Opart = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.opart);
+  a.LSEpart = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.lsepart);
+  a.status = di->status;
+  a.num_sms = di->num_sms;
+  a.stream = st;
+  e = launch_scored_plan(a.p, a.mask, a.plan, st);
+  if (e == cudaSuccess) e = launch_scored_fwd_simt(a, bf16);
+  if (e == cudaSuccess && a.n_splits > 1) e = launch_scored_merge(a, bf16);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+attn_status_t attn_bwd_scored(const void* Q, const void* K, const void* V, const void* O, const float* LSE,
+                              const void* dO, void* dQ, void* dK, void* dV, int B, int H, int Hkv, int Tq, int Tk,
+                              int d, int dv, float scale, const attn_score_t* score, attn_dtype_t dtype,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  attn_status_t s = check_scored(B, H, Hkv, Tq, Tk, d, dv, dtype);
+  const attn_score_t sc = score ? *score : attn_score_t{};
+  if (s == ATTN_OK) s = check_score(sc, B, H, Tq, scale);
+  if (s != ATTN_OK) return s;
+  const bool bf16 = dtype == ATTN_BF16;
+  const size_t es = elem_size(dtype), align = bf16 ? 16 : 4;
+  const size_t nq = static_cast<size_t>(B) * H * Tq, nk = static_cast<size_t>(B) * Hkv * Tk;
+  const void* ins[6] = {Q, K, V, O, LSE, dO};
+  const size_t in_bytes[6] = {nq * d * es, nk * d * es, nk * dv * es, nq * dv * es, nq * 4, nq * dv * es};
+  for (int i = 0; i < 6; ++i)
+    if ((s = check_ptr(ins[i], in_bytes[i], i == 4 ? 4 : align)) != ATTN_OK) return s;
+  void* outs[3] = {dQ, dK, dV};
+  const size_t out_bytes[3] = {nq * d * es, nk * d * es, nk * dv * es};
+  for (int i = 0; i < 3; ++i)
+    if ((s = check_ptr(outs[i], out_bytes[i], align)) != ATTN_OK) return s;
+  ScoredBwd a{};
+  a.p = problem(B, H, Hkv, Tq, Tk, d, dv);
+  a.p.scale = scale;
+  a.p.softcap = sc.softcap;
+  a.p.slopes = sc.slopes;
+  const Layout L = layout(a.p, dtype, true);
+  if ((s = check_ws(workspace, workspace_bytes, L.total)) != ATTN_OK) return s;
+  const Arrays ar = arrays(sc, B, H, Tq);
+  const Range ro[4] = {range(dQ, out_bytes[0]), range(dK, out_bytes[1]), range(dV, out_bytes[2]),
+                       range(workspace, L.total)};
+  for (int i = 0; i < 4; ++i) {
+    const attn_status_t bad = i == 3 ? ATTN_ERR_WORKSPACE : ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < 6; ++j)
+      if (overlap(ro[i], range(ins[j], in_bytes[j]))) return bad;
+    for (const Range& x : ar.r)
+      if (overlap(ro[i], x)) return bad;
+    for (int j = 0; j < i; ++j)
+      if (overlap(ro[i], ro[j])) return bad;
+  }
+  if (nq == 0 && nk == 0) return ATTN_OK;
+  DeviceInfo* di;
+  if ((s = device_info(&di)) != ATTN_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (nq == 0 || nk == 0) {   // no query-key pair
+    e = cudaSuccess;
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = launch_zero(outs[i], out_bytes[i], st);
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+  }
+  a.plan = plan_at(L, workspace, true, sc.slopes != nullptr);
+  a.Q = Q;
+  a.K = K;
+  a.V = V;
+  a.O = O;
+  a.LSE = LSE;
+  a.dO = dO;
+  a.dQ = dQ;
+  a.dK = dK;
+  a.dV = dV;
+  a.D = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.D);
+  a.NL = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.NL);
+  a.status = di->status;
+  a.num_sms = di->num_sms;
+  a.stream = st;
+  e = launch_scored_plan(a.p, ScoredMask{sc.q_pos, sc.key_begin, sc.key_end, sc.causal}, a.plan, st);
+  if (e == cudaSuccess) e = launch_scored_bwd_simt(a, bf16);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+}  // extern "C"

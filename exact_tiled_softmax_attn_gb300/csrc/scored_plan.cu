@@ -1,0 +1,141 @@
+// Plan of a scored-attention call: the key range of every packed query row,
+// the hull of the ranges of each 128-row tile, and the row tiles that each
+// 128-key tile meets. Also the merge of partial results over key ranges.
+#include <cuda_bf16.h>
+#include <limits.h>
+#include <math_constants.h>
+
+#include "scored.h"
+
+namespace attn {
+namespace scored {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr int kPosLimit = 1 << 30;
+
+// One block per (row tile, batch entry), one thread per row.
+__global__ void __launch_bounds__(kScoredTile) plan_rows_kernel(const ScoredProblem p, const ScoredMask m,
+                                                                 const ScoredPlan out) {
+  const int b = blockIdx.x / p.n_rt, tile = blockIdx.x - b * p.n_rt;
+  const int row = tile * kScoredTile + threadIdx.x;
+  const bool valid = row < p.R;
+  int lo = INT_MAX, hi = 0, pos = 0;
+  if (valid) {
+    const int t = row % p.Tq;
+    const long long at = static_cast<long long>(b) * p.Tq + t;
+    pos = m.q_pos ? min(max(m.q_pos[at], -kPosLimit), kPosLimit) : t;
+    lo = m.key_begin ? max(m.key_begin[at], 0) : 0;
+    hi = m.key_end ? min(m.key_end[at], p.Tk) : p.Tk;
+    if (m.causal) hi = min(hi, pos + 1);
+    if (lo >= hi) {
+      lo = INT_MAX;
+      hi = 0;
+    }
+  }
+  const long long n = static_cast<long long>(b) * p.rpad() + row;
+  out.rows[n] = make_int4(lo, hi, pos, 0);
+  if (out.slope2 && b == 0)
+    for (int k = 0; k < p.Hkv; ++k)
+      out.slope2[static_cast<long long>(k) * p.rpad() + row] = valid ? p.slopes[k * p.G + row / p.Tq] * LOG2E : 0.f;
+  // hull over the rows that see keys; the keys that every row sees
+  int v[4] = {lo, -hi, valid ? -lo : -INT_MAX, valid ? hi : INT_MAX};   // minima of all four
+  if (!valid) v[2] = INT_MAX;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = min(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
+  __shared__ int s[4][4];
+  if ((threadIdx.x & 31) == 0)
+    for (int i = 0; i < 4; ++i) s[i][threadIdx.x >> 5] = v[i];
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) v[i] = min(min(s[i][0], s[i][1]), min(s[i][2], s[i][3]));
+    const int hull_hi = -v[1];
+    out.tiles[static_cast<long long>(b) * p.n_rt + tile] =
+        make_int4(hull_hi > 0 ? v[0] : 0, hull_hi, -v[2], v[3]);
+    if (tile == 0 && b == 0) out.counters[0] = out.counters[1] = 0u;
+  }
+}
+
+// One warp per (key tile, batch entry).
+__global__ void __launch_bounds__(128) plan_keys_kernel(const ScoredProblem p, const ScoredPlan out) {
+  const long long w = (static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (w >= static_cast<long long>(p.B) * p.n_kt) return;
+  const int b = static_cast<int>(w / p.n_kt), kt = static_cast<int>(w % p.n_kt);
+  const int k0 = kt * kScoredTile, k1 = k0 + kScoredTile;
+  int first = INT_MAX, nlast = INT_MAX;   // nlast: minus the last tile
+  for (int t = lane; t < p.n_rt; t += 32) {
+    const int4 h = out.tiles[static_cast<long long>(b) * p.n_rt + t];
+    if (h.x < k1 && h.y > k0) {
+      first = min(first, t);
+      nlast = min(nlast, -t);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+    nlast = min(nlast, __shfl_xor_sync(0xffffffffu, nlast, o));
+  }
+  if (lane == 0) out.ktiles[w] = first == INT_MAX ? make_int2(0, 0) : make_int2(first, -nlast - first + 1);
+}
+
+// One warp per row; every lane holds the row's weights' sum.
+template <typename T>
+__global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ Opart,
+                                                    const float* __restrict__ LSEpart, T* __restrict__ O,
+                                                    float* __restrict__ LSE, long long rows, int dv, int n_splits) {
+  const int lane = threadIdx.x & 31;
+  const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+  if (r >= rows) return;
+  float mx = -CUDART_INF_F;
+  for (int s = lane; s < n_splits; s += 32) mx = fmaxf(mx, LSEpart[s * rows + r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  float lse = -CUDART_INF_F, wsum = 0.f;
+  if (mx != -CUDART_INF_F) {
+#pragma unroll 4
+    for (int s = 0; s < n_splits; ++s) {
+      const float w = expf(LSEpart[s * rows + r] - mx);   // 0 for a range without keys
+      wsum += w;
+      const float* o = Opart + (s * rows + r) * dv;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (lane + 32 * c < dv && w > 0.f) acc[c] = fmaf(w, o[lane + 32 * c], acc[c]);
+    }
+    const float inv = 1.0f / wsum;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] *= inv;
+    lse = mx + logf(wsum);
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (lane + 32 * c < dv) O[r * dv + lane + 32 * c] = static_cast<T>(acc[c]);
+  if (lane == 0) LSE[r] = lse;
+}
+
+}  // namespace scored
+
+cudaError_t launch_scored_plan(const ScoredProblem& p, const ScoredMask& m, const ScoredPlan& plan, cudaStream_t s) {
+  scored::plan_rows_kernel<<<p.n_rt * p.B, kScoredTile, 0, s>>>(p, m, plan);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || plan.ktiles == nullptr) return e;
+  const long long warps = static_cast<long long>(p.B) * p.n_kt;
+  scored::plan_keys_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, s>>>(p, plan);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_scored_merge(const ScoredFwd& a, bool bf16) {
+  const long long rows = static_cast<long long>(a.p.B) * a.p.Hkv * a.p.R;
+  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+  if (bf16)
+    scored::merge_kernel<<<grid, 256, 0, a.stream>>>(a.Opart, a.LSEpart, static_cast<__nv_bfloat16*>(a.O), a.LSE, rows,
+                                                     a.p.dv, a.n_splits);
+  else
+    scored::merge_kernel<<<grid, 256, 0, a.stream>>>(a.Opart, a.LSEpart, static_cast<float*>(a.O), a.LSE, rows,
+                                                     a.p.dv, a.n_splits);
+  return cudaGetLastError();
+}
+
+}  // namespace attn

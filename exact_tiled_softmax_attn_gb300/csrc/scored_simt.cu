@@ -1,0 +1,456 @@
+// Scored attention on CUDA cores, forward and backward, in fp32 arithmetic.
+//
+// 64-row by 64-key tiles, 256 threads as 16 x 16, each with a 4 x 4 piece of
+// a score tile and 4 rows by 4 columns per 64 of the accumulators. Per 16
+// products a thread reads 8 floats of shared memory as float4 (rows of a tile
+// lie 64 * NC + 4 floats apart, an odd number of float4, so the 16 rows a
+// warp reads at one column fall into different banks). Bound by the FMA rate
+// and those reads. Row tiles visit only the key tiles their ranges' hull
+// meets, and key tiles only the row tiles whose hull meets them.
+#include <cuda_bf16.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "scored.h"
+
+namespace attn {
+namespace scored_simt {
+
+constexpr int BM = 64, BN = 64, NT = 256;
+constexpr int LDP = BN + 4;
+
+template <int NC>
+struct Pitch {
+  static constexpr int v = 64 * NC + 4;
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// 64 rows of `d` elements from row r0 into a tile of pitch 64 * NC + 4, zeros
+// past column d and outside rows [lo, hi).
+template <typename T, int NC>
+__device__ __forceinline__ void load_tile(float* s, const T* g, int r0, int lo, int hi, int d) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = warp; r < 64; r += NT / 32) {
+    const int row = r0 + r;
+    const bool in = row >= lo && row < hi;
+    const T* src = g + static_cast<long long>(in ? row : 0) * d;
+#pragma unroll
+    for (int c = 0; c < 2 * NC; ++c) {
+      const int k = lane + 32 * c;
+      s[r * Pitch<NC>::v + k] = (in && k < d) ? to_f(src[k]) : 0.f;
+    }
+  }
+}
+
+// x[i][j] = row (4 ty + i) of a . row (tx + 16 j) of b over d columns
+template <int NC>
+__device__ __forceinline__ void dot_tile(float (&x)[4][4], const float* a, const float* b, int d) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  constexpr int P = Pitch<NC>::v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+  const float* ar = a + 4 * ty * P;
+  const float* br = b + tx * P;
+  for (int k = 0; k < d; k += 4) {
+    float4 u[4], v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const float4*>(ar + i * P + k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float4*>(br + 16 * j * P + k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[i][j] = fmaf(u[i].x, v[j].x, x[i][j]);
+        x[i][j] = fmaf(u[i].y, v[j].y, x[i][j]);
+        x[i][j] = fmaf(u[i].z, v[j].z, x[i][j]);
+        x[i][j] = fmaf(u[i].w, v[j].w, x[i][j]);
+      }
+  }
+}
+
+// acc[i][4 c + e] += sum_k w[4 ty + i][k] * b[k][4 tx + 64 c + e]   (w row-major, pitch LDP)
+template <int NC>
+__device__ __forceinline__ void acc_rows(float (&acc)[4][4 * NC], const float* w, const float* b) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  constexpr int P = Pitch<NC>::v;
+#pragma unroll 2
+  for (int k = 0; k < BN; k += 4) {
+    float u[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 t = *reinterpret_cast<const float4*>(w + (4 * ty + i) * LDP + k);
+      u[i][0] = t.x, u[i][1] = t.y, u[i][2] = t.z, u[i][3] = t.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const float4 v = *reinterpret_cast<const float4*>(b + (k + e) * P + 4 * tx + 64 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[i][4 * c] = fmaf(u[i][e], v.x, acc[i][4 * c]);
+          acc[i][4 * c + 1] = fmaf(u[i][e], v.y, acc[i][4 * c + 1]);
+          acc[i][4 * c + 2] = fmaf(u[i][e], v.z, acc[i][4 * c + 2]);
+          acc[i][4 * c + 3] = fmaf(u[i][e], v.w, acc[i][4 * c + 3]);
+        }
+      }
+  }
+}
+
+// acc[i][4 c + e] += sum_r w[r][4 ty + i] * b[r][4 tx + 64 c + e]   (the product with w transposed)
+template <int NC>
+__device__ __forceinline__ void acc_cols(float (&acc)[4][4 * NC], const float* w, const float* b) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  constexpr int P = Pitch<NC>::v;
+#pragma unroll 4
+  for (int r = 0; r < BM; ++r) {
+    const float4 t = *reinterpret_cast<const float4*>(w + r * LDP + 4 * ty);
+    const float u[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const float4 v = *reinterpret_cast<const float4*>(b + r * P + 4 * tx + 64 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i][4 * c] = fmaf(u[i], v.x, acc[i][4 * c]);
+        acc[i][4 * c + 1] = fmaf(u[i], v.y, acc[i][4 * c + 1]);
+        acc[i][4 * c + 2] = fmaf(u[i], v.z, acc[i][4 * c + 2]);
+        acc[i][4 * c + 3] = fmaf(u[i], v.w, acc[i][4 * c + 3]);
+      }
+    }
+  }
+}
+
+template <typename T, int NC>
+__device__ __forceinline__ void store_row(T* row, const float (&acc)[4 * NC], float mul, int d) {
+  const int tx = threadIdx.x & 15;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (4 * tx + 64 * c + e < d) row[4 * tx + 64 * c + e] = static_cast<T>(acc[4 * c + e] * mul);
+}
+
+// The changed score of raw product x, and its derivative by scale * x.
+__device__ __forceinline__ float score(float x, const ScoredProblem& p, float slope, int pos, int key, float* grad) {
+  float s = x * p.scale;
+  *grad = 1.f;
+  if (p.softcap > 0.f) {
+    const float t = tanhf(s / p.softcap);
+    s = p.softcap * t;
+    *grad = 1.f - t * t;
+  }
+  if (p.slopes) s -= slope * fabsf(static_cast<float>(pos - key));
+  return s;
+}
+
+struct RowInfo {
+  int lo[4], hi[4], pos[4];
+  float slope[4];
+};
+
+__device__ __forceinline__ RowInfo row_info(const ScoredProblem& p, const ScoredPlan& plan, int bh, int r0) {
+  RowInfo ri;
+  const int b = bh / p.Hkv, kvh = bh - b * p.Hkv, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 4 * ty + i;   // rows up to rpad have entries; BM divides it
+    const int4 w = plan.rows[static_cast<long long>(b) * p.rpad() + r];
+    ri.lo[i] = w.x, ri.hi[i] = w.y, ri.pos[i] = w.z;
+    ri.slope[i] = p.slopes && r < p.R ? p.slopes[kvh * p.G + r / p.Tq] : 0.f;
+  }
+  return ri;
+}
+
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <typename T, int NCK, int NCV>
+__global__ void __launch_bounds__(NT) fwd_kernel(const ScoredProblem p, const ScoredPlan plan, const T* __restrict__ Q,
+                                                  const T* __restrict__ K, const T* __restrict__ V,
+                                                  T* __restrict__ O, float* __restrict__ LSE, int n_splits,
+                                                  int split_keys, float* __restrict__ Opart,
+                                                  float* __restrict__ LSEpart) {
+  extern __shared__ __align__(16) float smem[];
+  float* sQ = smem;
+  float* sK = sQ + BM * Pitch<NCK>::v;
+  float* sV = sK + BN * Pitch<NCK>::v;
+  float* sP = sV + BN * Pitch<NCV>::v;
+  const int nt = (p.R + BM - 1) / BM;
+  const int bh = blockIdx.x / nt, split = blockIdx.y;
+  const int r0 = (nt - 1 - (blockIdx.x - bh * nt)) * BM;   // causal: the longest rows first
+  const int b = bh / p.Hkv;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const RowInfo ri = row_info(p, plan, bh, r0);
+  const int4 hull = plan.tiles[static_cast<long long>(b) * p.n_rt + r0 / kScoredTile];
+  const int k_lo = max(hull.x, split * split_keys), k_hi = min(hull.y, (split + 1) * split_keys);
+  load_tile<T, NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
+  const T* Kh = K + static_cast<long long>(bh) * p.Tk * p.d;
+  const T* Vh = V + static_cast<long long>(bh) * p.Tk * p.dv;
+  float acc[4][4 * NCV], m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -CUDART_INF_F;
+    l[i] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4 * NCV; ++e) acc[i][e] = 0.f;
+  }
+  for (int k0 = k_lo / BN * BN; k0 < k_hi; k0 += BN) {
+    __syncthreads();
+    load_tile<T, NCK>(sK, Kh, k0, k_lo, k_hi, p.d);
+    load_tile<T, NCV>(sV, Vh, k0, k_lo, k_hi, p.dv);
+    __syncthreads();
+    float x[4][4];
+    dot_tile<NCK>(x, sQ, sK, p.d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mx = -CUDART_INF_F, g;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = k0 + tx + 16 * j;
+        const float s = score(x[i][j], p, ri.slope[i], ri.pos[i], key, &g);
+        x[i][j] = key >= max(ri.lo[i], k_lo) && key < min(ri.hi[i], k_hi) ? s : -CUDART_INF_F;
+        mx = fmaxf(mx, x[i][j]);
+      }
+      const float mn = fmaxf(m[i], row_max(mx));
+      const float ref = mn == -CUDART_INF_F ? 0.f : mn;   // no key seen yet: every exponential is exp(-inf)
+      const float corr = expf(m[i] - ref);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = expf(x[i][j] - ref);
+        sum += e;
+        sP[(4 * ty + i) * LDP + tx + 16 * j] = e;
+      }
+      l[i] = l[i] * corr + row_sum(sum);
+      m[i] = mn;
+#pragma unroll
+      for (int e = 0; e < 4 * NCV; ++e) acc[i][e] *= corr;
+    }
+    __syncthreads();
+    acc_rows<NCV>(acc, sP, sV);
+  }
+  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.R;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 4 * ty + i;
+    if (r >= p.R) continue;
+    const long long row = static_cast<long long>(bh) * p.R + r;
+    const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+    const float lse = l[i] > 0.f ? m[i] + logf(l[i]) : -CUDART_INF_F;
+    if (n_splits > 1) {
+      store_row<float, NCV>(Opart + (split * rows + row) * p.dv, acc[i], inv, p.dv);
+      if (tx == 0) LSEpart[split * rows + row] = lse;
+    } else {
+      store_row<T, NCV>(O + row * p.dv, acc[i], inv, p.dv);
+      if (tx == 0) LSE[row] = lse;
+    }
+  }
+}
+
+// dQ of a 64-row tile, and D = rowsum(dO o O) of its rows for the dK/dV kernel.
+template <typename T, int NCK, int NCV>
+__global__ void __launch_bounds__(NT) dq_kernel(const ScoredProblem p, const ScoredPlan plan, const T* __restrict__ Q,
+                                                 const T* __restrict__ K, const T* __restrict__ V,
+                                                 const T* __restrict__ O, const float* __restrict__ LSE,
+                                                 const T* __restrict__ dO, T* __restrict__ dQ,
+                                                 float* __restrict__ D) {
+  extern __shared__ __align__(16) float smem[];
+  float* sQ = smem;
+  float* sK = sQ + BM * Pitch<NCK>::v;
+  float* sdO = sK + BN * Pitch<NCK>::v;
+  float* sV = sdO + BM * Pitch<NCV>::v;
+  float* sW = sV + BN * Pitch<NCV>::v;
+  const int nt = (p.R + BM - 1) / BM;
+  const int bh = blockIdx.x / nt;
+  const int r0 = (nt - 1 - (blockIdx.x - bh * nt)) * BM;
+  const int b = bh / p.Hkv;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const RowInfo ri = row_info(p, plan, bh, r0);
+  const int4 hull = plan.tiles[static_cast<long long>(b) * p.n_rt + r0 / kScoredTile];
+  load_tile<T, NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
+  load_tile<T, NCV>(sdO, dO + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);
+  load_tile<T, NCV>(sV, O + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);   // O, until the loop
+  __syncthreads();
+  float lse[4], dd[4], acc[4][4 * NCK];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 4 * ty + i;
+    lse[i] = r < p.R ? LSE[static_cast<long long>(bh) * p.R + r] : -CUDART_INF_F;
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4 * NCV; ++c)
+      s = fmaf(sdO[(4 * ty + i) * Pitch<NCV>::v + tx + 16 * c], sV[(4 * ty + i) * Pitch<NCV>::v + tx + 16 * c], s);
+    dd[i] = row_sum(s);
+    if (tx == 0) D[static_cast<long long>(bh) * p.rpad() + r] = dd[i];
+#pragma unroll
+    for (int e = 0; e < 4 * NCK; ++e) acc[i][e] = 0.f;
+  }
+  const T* Kh = K + static_cast<long long>(bh) * p.Tk * p.d;
+  const T* Vh = V + static_cast<long long>(bh) * p.Tk * p.dv;
+  for (int k0 = hull.x / BN * BN; k0 < hull.y; k0 += BN) {
+    __syncthreads();
+    load_tile<T, NCK>(sK, Kh, k0, hull.x, hull.y, p.d);
+    load_tile<T, NCV>(sV, Vh, k0, hull.x, hull.y, p.dv);
+    __syncthreads();
+    float x[4][4], y[4][4];
+    dot_tile<NCK>(x, sQ, sK, p.d);
+    dot_tile<NCV>(y, sdO, sV, p.dv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = k0 + tx + 16 * j;
+        float g;
+        const float s = score(x[i][j], p, ri.slope[i], ri.pos[i], key, &g);
+        const bool in = key >= ri.lo[i] && key < ri.hi[i];
+        sW[(4 * ty + i) * LDP + tx + 16 * j] = in ? expf(s - lse[i]) * (y[i][j] - dd[i]) * g : 0.f;
+      }
+    __syncthreads();
+    acc_rows<NCK>(acc, sW, sK);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 4 * ty + i;
+    if (r < p.R)
+      store_row<T, NCK>(dQ + (static_cast<long long>(bh) * p.R + r) * p.d, acc[i], p.scale, p.d);
+  }
+}
+
+template <typename T, int NCK, int NCV>
+__global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const ScoredPlan plan,
+                                                   const T* __restrict__ Q, const T* __restrict__ K,
+                                                   const T* __restrict__ V, const float* __restrict__ LSE,
+                                                   const T* __restrict__ dO, const float* __restrict__ D,
+                                                   T* __restrict__ dK, T* __restrict__ dV) {
+  extern __shared__ __align__(16) float smem[];
+  float* sQ = smem;
+  float* sK = sQ + BM * Pitch<NCK>::v;
+  float* sdO = sK + BN * Pitch<NCK>::v;
+  float* sV = sdO + BM * Pitch<NCV>::v;
+  float* sP = sV + BN * Pitch<NCV>::v;
+  float* sW = sP + BM * LDP;
+  const int nt = (p.Tk + BN - 1) / BN;
+  const int bh = blockIdx.x / nt, k0 = (blockIdx.x - bh * nt) * BN;
+  const int b = bh / p.Hkv;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  load_tile<T, NCK>(sK, K + static_cast<long long>(bh) * p.Tk * p.d, k0, 0, p.Tk, p.d);
+  load_tile<T, NCV>(sV, V + static_cast<long long>(bh) * p.Tk * p.dv, k0, 0, p.Tk, p.dv);
+  float ak[4][4 * NCK], av[4][4 * NCV];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4 * NCK; ++e) ak[i][e] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4 * NCV; ++e) av[i][e] = 0.f;
+  }
+  const int2 list = plan.ktiles[static_cast<long long>(b) * p.n_kt + k0 / kScoredTile];
+  for (int r0 = list.x * kScoredTile; r0 < min(p.R, (list.x + list.y) * kScoredTile); r0 += BM) {
+    const int4 hull = plan.tiles[static_cast<long long>(b) * p.n_rt + r0 / kScoredTile];
+    if (hull.x >= k0 + BN || hull.y <= k0) continue;
+    __syncthreads();
+    load_tile<T, NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
+    load_tile<T, NCV>(sdO, dO + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);
+    const RowInfo ri = row_info(p, plan, bh, r0);
+    __syncthreads();
+    float x[4][4], y[4][4];
+    dot_tile<NCK>(x, sQ, sK, p.d);
+    dot_tile<NCV>(y, sdO, sV, p.dv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + 4 * ty + i;
+      const float lse = r < p.R ? LSE[static_cast<long long>(bh) * p.R + r] : 0.f;
+      const float dd = D[static_cast<long long>(bh) * p.rpad() + r];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = k0 + tx + 16 * j;
+        float g;
+        const float s = score(x[i][j], p, ri.slope[i], ri.pos[i], key, &g);
+        const bool in = key >= ri.lo[i] && key < ri.hi[i];
+        const float e = in ? expf(s - lse) : 0.f;
+        sP[(4 * ty + i) * LDP + tx + 16 * j] = e;
+        sW[(4 * ty + i) * LDP + tx + 16 * j] = in ? e * (y[i][j] - dd) * g : 0.f;
+      }
+    }
+    __syncthreads();
+    acc_cols<NCV>(av, sP, sdO);
+    acc_cols<NCK>(ak, sW, sQ);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int key = k0 + 4 * ty + i;
+    if (key < p.Tk) {
+      store_row<T, NCK>(dK + (static_cast<long long>(bh) * p.Tk + key) * p.d, ak[i], p.scale, p.d);
+      store_row<T, NCV>(dV + (static_cast<long long>(bh) * p.Tk + key) * p.dv, av[i], 1.f, p.dv);
+    }
+  }
+}
+
+template <typename T, int NCK, int NCV>
+cudaError_t fwd(const ScoredFwd& a) {
+  const ScoredProblem& p = a.p;
+  const int smem = (BM * Pitch<NCK>::v + BN * Pitch<NCK>::v + BN * Pitch<NCV>::v + BM * LDP) * 4;
+  auto kern = fwd_kernel<T, NCK, NCV>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((p.R + BM - 1) / BM * p.B * p.Hkv, a.n_splits);
+  kern<<<grid, NT, smem, a.stream>>>(p, a.plan, static_cast<const T*>(a.Q), static_cast<const T*>(a.K),
+                                     static_cast<const T*>(a.V), static_cast<T*>(a.O), a.LSE, a.n_splits,
+                                     a.split_keys, a.Opart, a.LSEpart);
+  return cudaGetLastError();
+}
+
+template <typename T, int NCK, int NCV>
+cudaError_t bwd(const ScoredBwd& a) {
+  const ScoredProblem& p = a.p;
+  const int tiles = 2 * BM * (Pitch<NCK>::v + Pitch<NCV>::v);
+  const int smem_q = (tiles + BM * LDP) * 4, smem_kv = (tiles + 2 * BM * LDP) * 4;
+  auto kq = dq_kernel<T, NCK, NCV>;
+  auto kk = dkdv_kernel<T, NCK, NCV>;
+  cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv)) != cudaSuccess) return e;
+  const T *Q = static_cast<const T*>(a.Q), *K = static_cast<const T*>(a.K), *V = static_cast<const T*>(a.V),
+          *dO = static_cast<const T*>(a.dO);
+  kq<<<(p.R + BM - 1) / BM * p.B * p.Hkv, NT, smem_q, a.stream>>>(p, a.plan, Q, K, V, static_cast<const T*>(a.O),
+                                                                        a.LSE, dO, static_cast<T*>(a.dQ), a.D);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  kk<<<(p.Tk + BN - 1) / BN * p.B * p.Hkv, NT, smem_kv, a.stream>>>(p, a.plan, Q, K, V, a.LSE, dO, a.D,
+                                                                          static_cast<T*>(a.dK),
+                                                                          static_cast<T*>(a.dV));
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t fwd_t(const ScoredFwd& a) {
+  if (a.p.d <= 64) return a.p.dv <= 64 ? fwd<T, 1, 1>(a) : fwd<T, 1, 2>(a);
+  return a.p.dv <= 64 ? fwd<T, 2, 1>(a) : fwd<T, 2, 2>(a);
+}
+template <typename T>
+cudaError_t bwd_t(const ScoredBwd& a) {
+  if (a.p.d <= 64) return a.p.dv <= 64 ? bwd<T, 1, 1>(a) : bwd<T, 1, 2>(a);
+  return a.p.dv <= 64 ? bwd<T, 2, 1>(a) : bwd<T, 2, 2>(a);
+}
+
+}  // namespace scored_simt
+
+cudaError_t launch_scored_fwd_simt(const ScoredFwd& a, bool bf16) {
+  return bf16 ? scored_simt::fwd_t<__nv_bfloat16>(a) : scored_simt::fwd_t<float>(a);
+}
+cudaError_t launch_scored_bwd_simt(const ScoredBwd& a, bool bf16) {
+  return bf16 ? scored_simt::bwd_t<__nv_bfloat16>(a) : scored_simt::bwd_t<float>(a);
+}
+
+}  // namespace attn

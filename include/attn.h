@@ -289,6 +289,129 @@ ATTN_API attn_status_t attn_bwd_noalloc(const void* Q, const void* K, const void
                                         attn_dtype_t dtype, int deterministic, void* stream);
 
 /*
+ * Scored attention: softmax attention whose scores are changed before the
+ * softmax and whose mask is one range of keys per query row, with query heads
+ * that share key heads. With x = scale * q_i . k_j, for query row i of query
+ * head h and key j of key head h / (H / Hkv):
+ *   t    = softcap * tanh(x / softcap)            (x itself when softcap == 0)
+ *   S_ij = t - slopes[h] * |q_pos[b,i] - j|       (t itself when slopes == NULL)
+ *   S_ij = -inf unless key_begin[b,i] <= j < key_end[b,i], and, with
+ *          causal = 1, j <= q_pos[b,i]
+ * and O, LSE as above. Causal, document (rows see their own document's keys),
+ * prefix (rows see a prefix and what precedes them), sliding-window and
+ * padding masks are all of this form. A row whose range is empty gives O = 0,
+ * LSE = -inf and zero gradients. The three arrays are shared by the heads of
+ * a batch entry; ranges are clamped to [0, Tk] and positions to +-2^30 on the
+ * device, so any values are safe. The struct is read during the call; the
+ * arrays it points to are device memory read by the enqueued kernels.
+ */
+typedef struct {
+  float softcap;        /* 0: none; otherwise finite and > 0 */
+  int causal;           /* 0 or 1 */
+  const float* slopes;  /* [H] fp32, finite values, or NULL: no bias */
+  const int* q_pos;     /* [B,Tq] int32, or NULL: row i is at position i */
+  const int* key_begin; /* [B,Tq] int32, or NULL: 0 */
+  const int* key_end;   /* [B,Tq] int32, or NULL: Tk */
+} attn_score_t;
+
+/*
+ * Forward pass of the scored attention: O and LSE.
+ * Layout: Q [B,H,Tq,d], K [B,Hkv,Tk,d], V [B,Hkv,Tk,dv], O [B,H,Tq,dv], LSE
+ * [B,H,Tq] fp32; H a multiple of Hkv >= 1, heads of a group adjacent (query
+ * head h reads key head h / (H / Hkv)). score = NULL: plain scores, no mask.
+ * ATTN_F32: 1 <= d, dv <= 128; ATTN_BF16: d and dv multiples of 8 up to 128;
+ * else ATTN_ERR_UNSUPPORTED. Tq, Tk <= 2^30, and H / Hkv * Tq too.
+ * K and V rows that lie before every range or behind every range of their
+ * batch entry (unused capacity of a cache) may hold anything, NaN included.
+ * `workspace`: as in attn_fwd_splitkv (256-byte aligned, at least
+ * attn_fwd_scored_workspace_size bytes, not overlapping any argument), else
+ * ATTN_ERR_WORKSPACE; it is scratch, overwritten by each call, so calls that
+ * may overlap on the GPU need one each. Other errors as attn_fwd;
+ * asynchronous on `stream`; equal calls give bitwise equal results.
+ */
+ATTN_API attn_status_t attn_fwd_scored(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int H,
+                                       int Hkv, int Tq, int Tk, int d, int dv, float scale, const attn_score_t* score,
+                                       attn_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace attn_fwd_scored needs (0 is possible; 0 for invalid
+ * arguments as well). A rule of the shapes only.
+ */
+ATTN_API size_t attn_fwd_scored_workspace_size(int B, int H, int Hkv, int Tq, int Tk, int d, int dv,
+                                               attn_dtype_t dtype);
+
+/*
+ * Backward pass of the scored attention: dQ [B,H,Tq,d], dK [B,Hkv,Tk,d] and
+ * dV [B,Hkv,Tk,dv], the last two summed over the query heads that share the
+ * key head. With T_ij = 1 - (t_ij / softcap)^2 (1 without a cap):
+ *   P = exp(S - LSE),  D = rowsum(dO o O),  dV = P^T dO,
+ *   dS = P o (dO V^T - D) o T,  dQ = scale * dS K,  dK = scale * dS^T Q
+ * (the bias and the ranges have no gradient). `O` and `LSE` must be the
+ * outputs of attn_fwd_scored on the same inputs, scale and score. Shapes as
+ * attn_fwd_scored; every input must be finite (the LSE of empty rows
+ * excepted). Sums run in a fixed order: equal calls give bitwise equal
+ * results. Workspace and errors as attn_fwd_scored, with
+ * attn_bwd_scored_workspace_size.
+ */
+ATTN_API attn_status_t attn_bwd_scored(const void* Q, const void* K, const void* V, const void* O, const float* LSE,
+                                       const void* dO, void* dQ, void* dK, void* dV, int B, int H, int Hkv, int Tq,
+                                       int Tk, int d, int dv, float scale, const attn_score_t* score,
+                                       attn_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+ATTN_API size_t attn_bwd_scored_workspace_size(int B, int H, int Hkv, int Tq, int Tk, int d, int dv,
+                                               attn_dtype_t dtype);
+
+/*
+ * Rotary positions. Pair i (of rot / 2) of a head's first rot elements, (u,
+ * v) = (x[2i], x[2i + 1]) with interleaved = 1 and (x[i], x[i + rot / 2])
+ * with interleaved = 0, is turned by the angle a = pos * f_i:
+ *   u' = m (u cos a - v sin a),  v' = m (v cos a + u sin a)
+ * and the elements from rot on are copied. The plan holds each f_i as a
+ * 64-bit fraction of a turn, so pos * f_i modulo one turn is one integer
+ * product, off by less than |pos| * 2^-65 turns at any int32 position.
+ */
+#define ATTN_ROPE_MAX_PAIRS 128
+typedef struct {
+  int rot;                                        /* rotated elements of a head, even, 2..256 */
+  int interleaved;                                /* 0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1) */
+  float mscale;                                   /* m above */
+  int reserved;
+  unsigned long long turns[ATTN_ROPE_MAX_PAIRS];  /* f_i / (2 pi) * 2^64 */
+} attn_rope_t;
+
+/*
+ * Fills a plan (host only). Base frequencies f_i = theta^(-2i / rot). A
+ * context stretched by `factor` >= 1: with original_length == 0 every f_i is
+ * divided by it (positions interpolated); otherwise, with r = original_length
+ * * f_i / (2 pi) the turns a pair makes over the original context, pairs with
+ * r >= high_turns keep f_i, pairs with r <= low_turns take f_i / factor, and
+ * the ones between a mixture linear in r. Errors: ATTN_ERR_INVALID_ARG (rot
+ * odd, < 2 or > 256; theta <= 1; factor < 1; original_length < 0; unless 0 <=
+ * low_turns < high_turns with original_length > 0; mscale <= 0; anything not
+ * finite; plan NULL).
+ */
+ATTN_API attn_status_t attn_rope_init(attn_rope_t* plan, int rot, int interleaved, double theta, double factor,
+                                      double original_length, double low_turns, double high_turns, double mscale);
+
+/*
+ * Rotates the queries and keys of B * T tokens: Q [B,H,T,d] -> Qout and K
+ * [B,Hkv,T,d] -> Kout, any H, Hkv >= 0 (0: none, pointers ignored). inverse
+ * = 1 turns by -a: the transpose, which is the gradient (dQ from dQout).
+ * strides: 12 element strides, those of batch, head and token for Q, Qout, K
+ * and Kout in this order; rows of d elements are contiguous. Strides are >=
+ * 0; Qout and Kout must place no two elements at one address. In place (Qout
+ * == Q with equal strides) is allowed; any other overlap between an output
+ * and an input or the other output is refused. pos: int32 [B,T] device
+ * positions of any sign, or NULL: token t is at position t. rot <= d <= 256.
+ * Pointers aligned to the element size. cos, sin and the products are fp32,
+ * rounded once to the type. Errors: ATTN_ERR_INVALID_ARG,
+ * ATTN_ERR_UNSUPPORTED (d > 256), ATTN_ERR_MISALIGNED, ATTN_ERR_CUDA.
+ * Asynchronous on `stream`; the plan and the strides are read during the call.
+ */
+ATTN_API attn_status_t attn_rope(const attn_rope_t* plan, const void* Q, void* Qout, const void* K, void* Kout,
+                                 const long long* strides, const int* pos, int B, int H, int Hkv, int T, int d,
+                                 int inverse, attn_dtype_t dtype, void* stream);
+
+/*
  * One step of the online softmax, on the device: for each of the n query
  * rows, fold one block of bs keys into the running state ("Tiled attention
  * with an online softmax", section "Task": the online_softmax_step of the

@@ -14,12 +14,15 @@ attention
 tiled
     The tiled restatement with an online softmax (one key block at a time),
     used only to check the block-size invariance the pages promise.
+scored
+    Capped and biased scores with a range of keys per query row and shared
+    key heads, their gradients, and rotary positions.
 
 Every function is pinned by a CPU test against something other than itself:
 the worked examples printed on "Tiled attention with an online softmax"
 (section "Examples"), closed forms, brute-force scalar loops on tiny inputs,
 central finite differences, and CPU float64 ``torch.autograd``.
 """
-from . import attention, tiled  # noqa: F401
+from . import attention, scored, tiled  # noqa: F401
 
-__all__ = ["attention", "tiled"]
+__all__ = ["attention", "scored", "tiled"]

@@ -1,0 +1,423 @@
+"""Scored attention (capped scores, distance bias, key ranges, shared key
+heads): host checks on the CPU, parity with the float64 oracle on the GPU.
+
+Tolerances: fp32 as every fp32 test (1e-5 of the largest value for O and LSE,
+1e-4 for gradients). bf16: O per row as every bf16 test; LSE 1e-4 absolute
+(products of bf16 values summed in fp32 over d <= 128 terms: 128 * 2^-24 of
+sum |q k| ~ 10, then a few fp32 steps of values up to 50); gradients 5e-3 in
+the Frobenius norm (P, dS, O in D and the result are each rounded to bf16,
+uniformly within half a step of 2^-8: four times 2^-9 / sqrt(3) = 1.1e-3,
+added in squares 2.3e-3).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import exact_tiled_softmax_attn_gb300 as B
+from oracle import scored as ref
+
+from parity import check_o, frob_rel, max_rel, np64
+
+
+# ------------------------------------------------------------------ CPU
+
+def test_oracle_gradients_are_differences():
+    """The oracle's gradients against central differences of its own loss."""
+    g = np.random.default_rng(0)
+    q, k, v, do = (g.standard_normal(s) for s in ((1, 4, 5, 3), (1, 2, 7, 3), (1, 2, 7, 2), (1, 4, 5, 2)))
+    how = dict(scale=0.7, softcap=1.5, slopes=g.standard_normal(4), q_pos=[[2, 3, 4, 5, 6]],
+               key_begin=[[0, 1, 0, 9, 2]], key_end=[[3, 4, 7, 7, 7]], causal=True)
+    r = ref.scored(q, k, v, do, **how)
+    assert np.isneginf(r["LSE"][0, :, 3]).all() and not r["dQ"][0, :, 3].any()
+    for x, name in ((q, "dQ"), (k, "dK"), (v, "dV")):
+        for at in np.ndindex(*x.shape):
+            h = 1e-6
+            old = x[at]
+            loss = []
+            for s in (1, -1):
+                x[at] = old + s * h
+                loss.append((ref.scored(q, k, v, **how)["O"] * do).sum())
+            x[at] = old
+            assert abs((loss[0] - loss[1]) / (2 * h) - r[name][at]) < 1e-7
+
+
+def _fwd(score=None, **kw):
+    a = dict(Q=0x100000, K=0x200000, V=0x300000, O=0x400000, LSE=0x500000, B=1, H=4, Hkv=2, Tq=8, Tk=8, d=64, dv=64,
+             scale=0.125, score=score, dtype=B.ATTN_BF16, workspace=0x9000000, workspace_bytes=1 << 20, stream=0,
+             check=False)
+    a.update(kw)
+    return B.attn_fwd_scored(**a)
+
+
+BAD = [
+    (dict(B=-1), B.ATTN_ERR_INVALID_ARG),
+    (dict(Hkv=0), B.ATTN_ERR_INVALID_ARG),
+    (dict(Hkv=3), B.ATTN_ERR_INVALID_ARG),
+    (dict(scale=0.0), B.ATTN_ERR_INVALID_ARG),
+    (dict(scale=float("nan")), B.ATTN_ERR_INVALID_ARG),
+    (dict(dtype=5), B.ATTN_ERR_INVALID_ARG),
+    (dict(d=136), B.ATTN_ERR_UNSUPPORTED),
+    (dict(dv=60), B.ATTN_ERR_UNSUPPORTED),
+    (dict(dtype=B.ATTN_F32, dv=129), B.ATTN_ERR_UNSUPPORTED),
+    (dict(Tk=(1 << 30) + 1), B.ATTN_ERR_INVALID_ARG),
+    (dict(Tq=1 << 30), B.ATTN_ERR_INVALID_ARG),               # 2 heads a group: more than 2^30 packed rows
+    (dict(B=1 << 20, Hkv=1 << 11, H=1 << 11), B.ATTN_ERR_INVALID_ARG),
+    (dict(Q=None), B.ATTN_ERR_INVALID_ARG),
+    (dict(K=0x200008), B.ATTN_ERR_MISALIGNED),
+    (dict(workspace=None), B.ATTN_ERR_WORKSPACE),
+    (dict(workspace_bytes=64), B.ATTN_ERR_WORKSPACE),
+    (dict(workspace=0x9000010), B.ATTN_ERR_WORKSPACE),
+    (dict(score=B.AttnScore(-1.0, 0, 0, 0, 0, 0)), B.ATTN_ERR_INVALID_ARG),
+    (dict(score=B.AttnScore(float("inf"), 0, 0, 0, 0, 0)), B.ATTN_ERR_INVALID_ARG),
+    (dict(score=B.AttnScore(float("nan"), 0, 0, 0, 0, 0)), B.ATTN_ERR_INVALID_ARG),
+    (dict(score=B.AttnScore(0.0, 2, 0, 0, 0, 0)), B.ATTN_ERR_INVALID_ARG),
+    (dict(score=B.AttnScore(0.0, 0, 0x600002, 0, 0, 0)), B.ATTN_ERR_MISALIGNED),
+    (dict(score=B.AttnScore(0.0, 0, 0, 0, 0, 0x600001)), B.ATTN_ERR_MISALIGNED),
+]
+
+
+@pytest.mark.parametrize("kw,status", BAD + [
+    (dict(O=0x200000), B.ATTN_ERR_INVALID_ARG),                 # output over K
+    (dict(LSE=0x400000), B.ATTN_ERR_INVALID_ARG),
+    (dict(workspace=0x100000), B.ATTN_ERR_WORKSPACE),
+    (dict(score=B.AttnScore(0.0, 0, 0, 0x400000, 0, 0)), B.ATTN_ERR_INVALID_ARG),   # output over q_pos
+    (dict(score=B.AttnScore(0.0, 0, 0x9000000, 0, 0, 0)), B.ATTN_ERR_WORKSPACE),    # workspace over slopes
+])
+def test_forward_refusals(kw, status):
+    assert _fwd(**kw) == status
+
+
+def _bwd(score=None, **kw):
+    a = dict(Q=0x100000, K=0x200000, V=0x300000, O=0x400000, LSE=0x500000, dO=0x600000, dQ=0x700000, dK=0x800000,
+             dV=0x900000, B=1, H=4, Hkv=2, Tq=8, Tk=8, d=64, dv=64, scale=0.125, score=score, dtype=B.ATTN_BF16,
+             workspace=0x9000000, workspace_bytes=1 << 20, stream=0, check=False)
+    a.update(kw)
+    return B.attn_bwd_scored(**a)
+
+
+@pytest.mark.parametrize("kw,status", BAD + [
+    (dict(dQ=0x600000), B.ATTN_ERR_INVALID_ARG),
+    (dict(dK=0x900000), B.ATTN_ERR_INVALID_ARG),
+    (dict(dO=None), B.ATTN_ERR_INVALID_ARG),
+    (dict(workspace=0x800000), B.ATTN_ERR_WORKSPACE),
+    (dict(score=B.AttnScore(0.0, 0, 0, 0, 0x700000, 0)), B.ATTN_ERR_INVALID_ARG),
+])
+def test_backward_refusals(kw, status):
+    # (an output over another output is refused with the workspace's own check first where it is the workspace)
+    assert _bwd(**kw) in ((status, B.ATTN_ERR_WORKSPACE) if "workspace" in kw else (status,))
+
+
+def test_nothing_to_do_needs_no_device():
+    assert _fwd(B=0) == B.ATTN_OK
+    assert _fwd(Tq=0, workspace=None) == B.ATTN_OK
+    assert _fwd(H=0) == B.ATTN_OK
+    assert _bwd(B=0, workspace=None) == B.ATTN_OK
+    for f in (B.attn_fwd_scored_workspace_size, B.attn_bwd_scored_workspace_size):
+        assert f(1, 4, 2, 0, 8, 64, 64, B.ATTN_BF16) == 0
+        assert f(1, 4, 2, 8, 0, 64, 64, B.ATTN_BF16) == 0
+        assert f(1, 4, 3, 8, 8, 64, 64, B.ATTN_BF16) == 0
+        assert f(1, 4, 2, 8, 8, 64, 64, B.ATTN_BF16) > 0
+
+
+def test_wrapper_refusals():
+    q, k = torch.zeros(1, 4, 8, 64), torch.zeros(1, 2, 8, 64)
+    with pytest.raises(ValueError):
+        B.forward_scored(q, k, k)                                # not on a GPU
+    for bad in (dict(q_pos=torch.zeros(1, 8)), dict(key_end=torch.zeros(1, 7, dtype=torch.int32)),
+                dict(slopes=torch.zeros(3)), dict(slopes=torch.zeros(4, dtype=torch.float64)),
+                dict(key_begin=torch.zeros(8, 2, dtype=torch.int32).t()[:1])):
+        with pytest.raises(ValueError):
+            B.forward_scored(q, k, k, **bad)
+    with pytest.raises(ValueError):
+        B.forward_scored(q, torch.zeros(1, 3, 8, 64), torch.zeros(1, 3, 8, 64))
+    with pytest.raises(ValueError):
+        B.forward_scored(q.transpose(2, 3), k, k)
+    with pytest.raises(ValueError):
+        B.forward_scored(q, k, k.bfloat16())
+
+
+# ------------------------------------------------------------------ GPU
+
+def arrays(mask, Bn, Tq, Tk, seed=0):
+    """key_begin, key_end, q_pos as numpy int32 [B, Tq], or None."""
+    g = np.random.default_rng(seed)
+    i = np.arange(Tq)[None] + np.zeros((Bn, 1), np.int64)
+    pos = i + Tk - Tq
+    begin = end = None
+    if mask == "docs":
+        cut = np.sort(g.integers(0, Tk + 1, (Bn, 4)), axis=1)
+        doc = (np.clip(pos, 0, Tk - 1)[:, :, None] >= cut[:, None, :]).sum(-1)
+        edge = np.concatenate([np.zeros((Bn, 1), np.int64), cut, np.full((Bn, 1), Tk)], axis=1)
+        begin = np.take_along_axis(edge, doc, 1)
+        end = np.minimum(np.take_along_axis(edge, doc + 1, 1), pos + 1)
+    elif mask == "prefix":
+        end = np.maximum(pos + 1, Tk // 3)
+    elif mask == "window":
+        begin, end = pos - 70, pos + 1
+    elif mask == "causal":
+        end = pos + 1
+    elif mask == "wild":        # any ranges in any order, empty ones and ones outside [0, Tk) among them
+        begin, end = g.integers(-9, Tk + 9, (Bn, Tq)), g.integers(-9, Tk + 40, (Bn, Tq))
+        pos = g.integers(-300, Tk + 300, (Bn, Tq))
+    elif mask == "empty":
+        begin, end = np.full((Bn, Tq), 3), np.full((Bn, Tq), 3)
+    elif mask == "some":        # whole tiles of padding rows, then one row
+        begin, end = np.zeros((Bn, Tq), np.int64), np.where(i % 300 > 140, 0, Tk)
+    as32 = lambda x: None if x is None else x.astype(np.int32)  # noqa: E731
+    return as32(begin), as32(end), as32(pos)
+
+
+def make(Bn, H, Hkv, Tq, Tk, d, dv, dtype, seed, grad=True):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x = [2.0 * r(Bn, H, Tq, d), r(Bn, Hkv, Tk, d), r(Bn, Hkv, Tk, dv)] + ([r(Bn, H, Tq, dv)] if grad else [])
+    return [t.to(dtype).cuda() for t in x]
+
+
+def check_lse(lse, want, dtype):
+    lse = np64(lse)
+    inf = np.isneginf(want)
+    assert np.array_equal(np.isneginf(lse), inf)
+    if (~inf).any():
+        err = np.abs(lse[~inf] - want[~inf]).max()
+        assert err <= (1e-5 * max(1.0, np.abs(want[~inf]).max()) if dtype == torch.float32 else 1e-4), err
+
+
+def check_grad(g, want, dtype, name):
+    assert np.isfinite(np64(g)).all(), name
+    err = max_rel(g, want) if dtype == torch.float32 else frob_rel(g, want)
+    assert err <= (1e-4 if dtype == torch.float32 else 5e-3), (name, err)
+
+
+def how_of(mask, cap, bias, Bn, H, Tq, Tk, seed=1):
+    begin, end, pos = arrays(mask, Bn, Tq, Tk, seed)
+    gpu = lambda x: None if x is None else torch.from_numpy(x).cuda()  # noqa: E731
+    slopes = torch.exp2(-8.0 * torch.arange(1, H + 1) / H).cuda() if bias else None
+    return dict(softcap=cap, slopes=slopes, q_pos=gpu(pos), key_begin=gpu(begin), key_end=gpu(end))
+
+
+def run_case(shape, mask, cap, bias, dtype, grad, causal=False, scale=None):
+    Bn, H, Hkv, Tq, Tk, d, dv = shape
+    x = make(*shape, dtype, seed=Tq + 3 * Tk + d, grad=grad)
+    how = how_of(mask, cap, bias, Bn, H, Tq, Tk)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    o, lse = B.forward_scored(*x[:3], causal=causal, scale=scale, **how)
+    g = B.backward_scored(*x[:3], o, lse, x[3], causal=causal, scale=scale, **how) if grad else ()
+    torch.cuda.synchronize()
+    assert B.attn_device_status() == B.ATTN_OK
+    r = ref.scored(*x, scale=scale, causal=causal, **how)
+    check_o(o, r["O"], dtype)
+    check_lse(lse, r["LSE"], dtype)
+    for t, name in zip(g, ("dQ", "dK", "dV")):
+        check_grad(t, r[name], dtype, name)
+
+
+TYPES = [torch.float32, torch.bfloat16]
+SHAPES = [  # B, H, Hkv, Tq, Tk, d, dv
+    (1, 1, 1, 1, 1, 64, 64),
+    (2, 4, 2, 130, 130, 64, 64),
+    (1, 6, 2, 200, 333, 128, 128),
+    (2, 3, 1, 129, 257, 40, 128),
+    (1, 4, 4, 300, 300, 96, 64),
+    (1, 8, 1, 37, 500, 128, 128),
+    (1, 2, 1, 513, 100, 80, 80),
+    (1, 2, 2, 640, 640, 128, 128),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("mask,cap,bias", [("none", 0.0, False), ("causal", 5.0, False), ("docs", 0.0, True),
+                                           ("prefix", 3.0, True), ("window", 0.0, False), ("wild", 2.0, True),
+                                           ("some", 0.0, False)])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_forward_and_backward(shape, mask, cap, bias, dtype):
+    run_case(shape, mask, cap, bias, dtype, grad=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 4, 2, 70, 90, 64, 64), (1, 2, 2, 300, 129, 128, 128)])
+def test_causal_flag_is_top_left(shape, dtype):
+    """causal = 1 without positions blocks j > i, as attn_fwd does; rows past Tk see every key."""
+    Bn, H, Hkv, Tq, Tk, d, dv = shape
+    x = make(*shape, dtype, 3)
+    o, lse = B.forward_scored(*x[:3], causal=True)
+    r = ref.scored(*x, scale=1.0 / math.sqrt(d), causal=True)
+    check_o(o, r["O"], dtype)
+    check_lse(lse, r["LSE"], dtype)
+    for t, name in zip(B.backward_scored(*x[:3], o, lse, x[3], causal=True), ("dQ", "dK", "dV")):
+        check_grad(t, r[name], dtype, name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "bf16"])
+def test_rows_that_see_nothing(dtype):
+    x = make(1, 2, 1, 150, 200, 64, 64, dtype, 5)
+    how = how_of("empty", 4.0, True, 1, 2, 150, 200)
+    o, lse = B.forward_scored(*x[:3], **how)
+    g = B.backward_scored(*x[:3], o, lse, x[3], **how)
+    assert not o.any() and torch.isneginf(lse).all()
+    assert not any(t.any() for t in g)
+    # no keys at all, and no queries
+    o, lse = B.forward_scored(x[0], x[1][:, :, :0], x[2][:, :, :0])
+    assert not o.any() and torch.isneginf(lse).all()
+    e = x[0][:, :, :0]
+    dq, dk, dv = B.backward_scored(e, x[1], x[2], e, lse[:, :, :0], e)
+    assert dq.numel() == 0 and not dk.any() and not dv.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("Tq,Tk", [(1, 5000), (3, 700), (200, 700)])
+def test_unused_cache_rows_may_hold_anything(Tq, Tk, dtype):
+    """NaN and infinities before and behind a batch entry's ranges change nothing."""
+    lens = [Tk // 3 + 1, Tk - 5]
+    x = make(2, 8, 2, Tq, Tk, 64, 128, dtype, 7, grad=False)
+    begin = torch.full((2, Tq), 11, dtype=torch.int32, device="cuda")
+    end = torch.tensor(lens, dtype=torch.int32, device="cuda")[:, None].expand(2, Tq).contiguous()
+    o, lse = B.forward_scored(*x, key_begin=begin, key_end=end)
+    for b in range(2):
+        for t, junk in ((x[1], float("inf")), (x[2], float("nan"))):
+            t[b, :, :11] = junk
+            t[b, :, lens[b]:] = junk
+    o2, lse2 = B.forward_scored(*x, key_begin=begin, key_end=end)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape,mask,cap,bias", [
+    ((1, 8, 8, 1, 3000, 128, 128), "causal", 5.0, False),
+    ((3, 8, 2, 1, 1111, 64, 64), "window", 0.0, True),
+    ((2, 16, 2, 3, 2500, 128, 64), "causal", 0.0, False),
+    ((1, 14, 2, 5, 777, 96, 96), "wild", 3.0, True),
+    ((40, 4, 1, 2, 300, 40, 40), "causal", 0.0, True),
+    ((1, 64, 1, 5, 2000, 128, 128), "causal", 0.0, False),
+    ((2, 2, 2, 1, 15, 64, 128), "none", 0.0, False),
+])
+def test_tokens_against_a_cache(shape, mask, cap, bias, dtype):
+    run_case(shape, mask, cap, bias, dtype, grad=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("cap", [0.5, 5.0, 50.0])
+def test_scores_far_beyond_the_cap(cap, dtype):
+    """Scores up to several hundred: the cap flattens them, and its derivative vanishes."""
+    run_case((1, 2, 1, 140, 300, 64, 64), "causal", cap, False, dtype, grad=True, scale=4.0)
+
+
+@pytest.mark.gpu
+def test_bias_at_far_positions():
+    """The bias depends on the distance alone: equal at positions near 0 and near 2^20."""
+    x = make(1, 4, 2, 5, 400, 64, 64, torch.bfloat16, 9, grad=False)
+    r = None
+    for Tk, at in ((400, 0),):
+        how = how_of("causal", 0.0, True, 1, 4, 5, Tk)
+        r = B.forward_scored(*x, **how)
+    k, v = (torch.zeros(1, 2, (1 << 20) + 400, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k[:, :, 1 << 20:], v[:, :, 1 << 20:] = x[1], x[2]
+    far = dict(how, q_pos=how["q_pos"] + (1 << 20), key_end=how["key_end"] + (1 << 20),
+               key_begin=torch.full((1, 5), 1 << 20, dtype=torch.int32, device="cuda"))
+    o, lse = B.forward_scored(x[0], k, v, **far)
+    assert (lse - r[1]).abs().max() <= 1e-4
+    assert (o.float() - r[0].float()).abs().max() <= 2.0 ** -7 * r[0].float().abs().max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "bf16"])
+def test_repeats_are_bitwise_equal_and_replay_from_a_graph(dtype):
+    """Two eager calls and replays of a captured forward and backward give equal bits; the graph follows new inputs."""
+    shape = (2, 6, 2, 260, 260, 64, 64)
+    x = make(*shape, dtype, 11)
+    how = how_of("docs", 5.0, True, 2, 6, 260, 260)
+
+    def both():
+        o, lse = B.forward_scored(*x[:3], **how)
+        return [o, lse, *B.backward_scored(*x[:3], o, lse, x[3], **how)]
+
+    a, b = both(), both()
+    torch.cuda.synchronize()
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        c = both()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(s, t) for s, t in zip(a, c))
+    x[0].copy_(make(*shape, dtype, 12)[0])
+    d = both()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(s, t) for s, t in zip(d, c)) and not torch.equal(a[0], d[0])
+
+
+@pytest.mark.gpu
+def test_on_another_stream():
+    x = make(1, 4, 2, 300, 300, 64, 64, torch.bfloat16, 13)
+    want = B.forward_scored(*x[:3], causal=True)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        o, lse = B.forward_scored(*x[:3], causal=True, stream=stream)
+        g = B.backward_scored(*x[:3], o, lse, x[3], causal=True, stream=stream)
+        s.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and all(t.isfinite().all() for t in g)
+
+
+@pytest.mark.gpu
+def test_guard_rows_stay_as_they_were():
+    """Nothing is written behind the outputs or the stated workspace."""
+    Bn, H, Hkv, Tq, Tk, d, dv = 1, 4, 2, 131, 140, 72, 40
+    for dt, code in ((torch.bfloat16, B.ATTN_BF16), (torch.float32, B.ATTN_F32)):
+        x = make(Bn, H, Hkv, Tq, Tk, d, dv, dt, 17)
+
+        def guarded(n, dtype):
+            return torch.full((n + 4096,), 7.0, dtype=dtype, device="cuda")
+        o, lse = guarded(Bn * H * Tq * dv, dt), guarded(Bn * H * Tq, torch.float32)
+        dq, dk, dv_ = (guarded(t.numel(), dt) for t in x[:3])
+        nf, nb = (f(Bn, H, Hkv, Tq, Tk, d, dv, code) for f in (B.attn_fwd_scored_workspace_size,
+                                                              B.attn_bwd_scored_workspace_size))
+        ws = torch.full((max(nf, nb) + 4096,), 7, dtype=torch.uint8, device="cuda")
+        sc = B.AttnScore(0.0, 1, 0, 0, 0, 0)
+        B.attn_fwd_scored(*x[:3], o, lse, Bn, H, Hkv, Tq, Tk, d, dv, 0.1, sc, code, ws, nf)
+        torch.cuda.synchronize()
+        assert (ws[nf:] == 7).all()
+        B.attn_bwd_scored(*x[:3], o, lse, x[3], dq, dk, dv_, Bn, H, Hkv, Tq, Tk, d, dv, 0.1, sc, code, ws, nb)
+        torch.cuda.synchronize()
+        assert (ws[nb:] == 7).all()
+        for t, n in ((o, Bn * H * Tq * dv), (lse, Bn * H * Tq), (dq, x[0].numel()), (dk, x[1].numel()),
+                     (dv_, x[2].numel())):
+            assert (t[n:] == 7.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "bf16"])
+def test_rope_then_attention_then_both_gradients(dtype):
+    """A layer's use: rotary positions, capped attention over documents, and the gradients back to the unrotated
+    queries and keys, against the same chain in float64."""
+    Bn, H, Hkv, T, d = 2, 6, 2, 270, 64
+    q, k, v, do = make(Bn, H, Hkv, T, T, d, d, dtype, 19)
+    how = how_of("docs", 6.0, False, Bn, H, T, T)
+    plan = B.rope_plan(48, theta=500.0)
+    pos = how["q_pos"]
+    qr, kr = B.rope(q, k, plan, pos=pos)
+    o, lse = B.forward_scored(qr, kr, v, **how)
+    dqr, dkr, dv = B.backward_scored(qr, kr, v, o, lse, do, **how)
+    dq, dk = B.rope(dqr, dkr, plan, pos=pos, inverse=True)
+    f = ref.rope_frequencies(48, theta=500.0)
+    p = pos.cpu().numpy()
+    # the chain in float64 from what the attention was given: the rotated values as they were rounded
+    r = ref.scored(qr, kr, v, do, scale=1.0 / math.sqrt(d), **how)
+    check_o(o, r["O"], dtype)
+    check_grad(dq, ref.rope(r["dQ"], p, f, inverse=True), dtype, "dQ")
+    check_grad(dk, ref.rope(r["dK"], p, f, inverse=True), dtype, "dK")
+    check_grad(dv, r["dV"], dtype, "dV")
+    # a half step of the type for each of the two products' sums
+    bound = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -21
+    assert np.abs(np64(qr) - ref.rope(q, p, f)).max() <= bound * np64(q).__abs__().max() * 1.5
