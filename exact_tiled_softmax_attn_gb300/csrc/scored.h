@@ -63,6 +63,7 @@ struct ScoredFwd {
   const CUtensorMap* tmV;
   uint32_t* status;
   int num_sms;
+  size_t l2_bytes;
   cudaStream_t stream;
 };
 
@@ -88,6 +89,9 @@ struct ScoredBwd {
 // CUDA cores (fp32 problems)
 cudaError_t launch_scored_fwd_simt(const ScoredFwd& a, bool bf16);
 cudaError_t launch_scored_bwd_simt(const ScoredBwd& a, bool bf16);
+
+// bf16 on the tensor cores; tmQ, tmK, tmV with 128-row boxes
+cudaError_t launch_scored_fwd_bf16(const ScoredFwd& a);
 
 // O and LSE from the partial results of the key ranges, in range order
 cudaError_t launch_scored_merge(const ScoredFwd& a, bool bf16);

@@ -34,7 +34,7 @@ attn_status_t check_scored(int B, int H, int Hkv, int Tq, int Tk, int d, int dv,
 
 attn_status_t check_score(const attn_score_t& sc, int B, int H, int Tq, float scale) {
   if (!(scale > 0.f) || !isfinite(scale)) return ATTN_ERR_INVALID_ARG;
-  if (!(sc.softcap >= 0.f) || !isfinite(sc.softcap)) return ATTN_ERR_INVALID_ARG;
+  if (sc.softcap != 0.f && !(sc.softcap >= 1e-4f && sc.softcap <= 1e6f)) return ATTN_ERR_INVALID_ARG;
   if (sc.causal != 0 && sc.causal != 1) return ATTN_ERR_INVALID_ARG;
   for (const void* x : {static_cast<const void*>(sc.slopes), static_cast<const void*>(sc.q_pos),
                         static_cast<const void*>(sc.key_begin), static_cast<const void*>(sc.key_end)})
@@ -59,7 +59,9 @@ ScoredProblem problem(int B, int H, int Hkv, int Tq, int Tk, int d, int dv) {
 
 // Key ranges of the forward: the CUDA-core kernel runs two 64-row tiles per
 // SM at a time.
+bool fwd_tensor(const ScoredProblem& p, attn_dtype_t dt) { return dt == ATTN_BF16 && p.R > 64; }
 void fwd_splits(const ScoredProblem& p, attn_dtype_t dt, int* S, int* keys) {
+  if (fwd_tensor(p, dt)) return;
   const long long units = static_cast<long long>(p.B) * p.Hkv * ((p.R + 63) / 64);
   const int want = wave_splits(units, p.n_kt, 2 * kSms);
   const int tiles = want > 1 ? (p.n_kt + want - 1) / want : p.n_kt;
@@ -203,9 +205,22 @@ attn_status_t attn_fwd_scored(const void* Q, const void* K, const void* V, void*
   a.LSEpart = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.lsepart);
   a.status = di->status;
   a.num_sms = di->num_sms;
+  a.l2_bytes = static_cast<size_t>(di->l2_bytes);
   a.stream = st;
   e = launch_scored_plan(a.p, a.mask, a.plan, st);
-  if (e == cudaSuccess) e = launch_scored_fwd_simt(a, bf16);
+  if (e == cudaSuccess && fwd_tensor(a.p, dtype)) {
+    CUtensorMap mq, mk, mv;
+    const int heads = B * Hkv;
+    if ((s = make_map(&mq, Q, d, a.p.R, heads)) != ATTN_OK) return s;
+    if ((s = make_map(&mk, K, d, Tk, heads)) != ATTN_OK) return s;
+    if ((s = make_map(&mv, V, dv, Tk, heads)) != ATTN_OK) return s;
+    a.tmQ = &mq;
+    a.tmK = &mk;
+    a.tmV = &mv;
+    e = launch_scored_fwd_bf16(a);
+  } else if (e == cudaSuccess) {
+    e = launch_scored_fwd_simt(a, bf16);
+  }
   if (e == cudaSuccess && a.n_splits > 1) e = launch_scored_merge(a, bf16);
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }

@@ -1,0 +1,584 @@
+// bf16 scored-attention forward on tcgen05 tensor cores (d, dv <= 128).
+//
+// The pipeline is that of the plain forward (fwd_bf16.cu): one persistent CTA
+// per SM, a unit of two 128-row query tiles that share every K/V tile, a
+// producer warp (TMA, one K/V ring), an MMA warp, and two softmax warpgroups
+// with a thread per query row, which keep a row's 128 scores in registers and
+// write P (bf16) over them in tensor memory. What differs:
+//   - rows are the packed rows of a key head (scored.h), so grouped query
+//     heads share key tiles with no copy;
+//   - each row tile of a unit runs over its own key tiles, those its ranges'
+//     hull meets, and only tiles with a key that some row does not see are
+//     masked, by each row's range;
+//   - scores are capped and biased in the softmax threads (scored_math.cuh);
+//   - units are claimed at run time (documents make their lengths unequal),
+//     longest first under a causal mask;
+//   - rows of V outside the unit's hull are zeroed in shared memory (P is 0
+//     there, but 0 times what an unused cache row holds need not be).
+// TMEM: row tile t keeps S_t (and P_t over it) at columns [256 t, 256 t +
+// 128) and O_t at [256 t + 128, 256 t + 128 + dv).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "bwd_common.cuh"
+#include "common.cuh"
+#include "ptx.cuh"
+#include "scored.h"
+#include "scored_math.cuh"
+
+namespace attn {
+namespace scored_fwd {
+
+using bwd::UnitQueue;
+using bwd::uq_push;
+using bwd::uq_read;
+using scored::Cap;
+using scored::dup;
+
+constexpr int BM = 128, BN = 128;
+constexpr int BOX_BYTES = 128 * 64 * 2;
+constexpr float TAU = 8.0f;        // the running reference moves when the maximum grows by more (log2 units)
+constexpr int NUM_THREADS = 384;
+constexpr int REG_CTRL = 96;
+constexpr int REG_SOFTMAX = 200;
+
+// One tile width for Q, K, V and O rows: 64 where d and dv fit, else 128.
+template <int HD>
+struct Cfg {
+  static constexpr int KB = HD / 64;
+  static constexpr int TILE = BM * HD * 2;
+  static constexpr int NSLOT_FIT = (227 * 1024 - 2 * TILE - 1024) / TILE;
+  static constexpr int NSLOT = NSLOT_FIT < 10 ? NSLOT_FIT : 10;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_KV = OFF_Q + 2 * TILE;
+  static constexpr int OFF_BAR = OFF_KV + NSLOT * TILE;
+  // q_full, q_empty, full[NSLOT], empty[NSLOT], s_full[2], p_full[2], o_full[2], drain, unit queue
+  static constexpr int NBAR = 2 + 2 * NSLOT + 7 + 2 * UnitQueue::N;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_MISC + 16 + 4 * UnitQueue::N;
+  static constexpr int UQ_READERS = 1 + 256;
+  static constexpr uint32_t IDESC_S = ptx::idesc_bf16(BM, BN, false, false);
+  static constexpr uint32_t IDESC_PV = ptx::idesc_bf16(BM, HD, false, true);
+};
+
+struct Params {
+  ScoredProblem p;
+  ScoredPlan plan;
+  __nv_bfloat16* O;
+  float* LSE;
+  uint32_t* status;
+  int n_pairs, total, group;
+  float sc2;   // scale * log2(e)
+  Cap cap;
+};
+
+// A unit: the row tiles 2 qb and 2 qb + 1 of key head bh, the key tiles
+// [s[t], e[t]) of each, [s0, e0) of both, and the hull [lo, hi) of their keys.
+struct Unit {
+  int bh, b, qb, s[2], e[2], s0, e0, lo, hi;
+  int4 tile[2];
+};
+
+__device__ __forceinline__ Unit load_unit(const Params& P, int x) {
+  Unit u;
+  bwd::grouped_unit(x, P.n_pairs, P.p.B * P.p.Hkv, P.group, true, &u.bh, &u.qb);
+  u.b = u.bh / P.p.Hkv;
+  u.lo = 0x7fffffff;
+  u.hi = 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int rt = 2 * u.qb + t;
+    u.tile[t] = rt < P.p.n_rt ? __ldg(P.plan.tiles + static_cast<long long>(u.b) * P.p.n_rt + rt)
+                              : make_int4(0, 0, 0x7fffffff, 0);
+    const bool live = u.tile[t].y > 0;
+    u.s[t] = live ? u.tile[t].x / BN : 0;
+    u.e[t] = live ? (u.tile[t].y + BN - 1) / BN : 0;
+    if (live) {
+      u.lo = min(u.lo, u.tile[t].x);
+      u.hi = max(u.hi, u.tile[t].y);
+    }
+  }
+  u.s0 = u.hi > 0 ? u.lo / BN : 0;
+  u.e0 = (u.hi + BN - 1) / BN;
+  return u;
+}
+
+template <int HD, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    scored_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params P) {
+  using C = Cfg<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if ((ptx::smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(P.status, ATTN_DEV_BAD_SMEM);
+    return;
+  }
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sKV = smem + C::OFF_KV;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_full = bars + 0;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* kv_full = bars + 2;
+  uint64_t* kv_empty = kv_full + C::NSLOT;
+  uint64_t* s_full = kv_empty + C::NSLOT;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* drain = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 4);
+  const UnitQueue uq{reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16), drain + 1, drain + 1 + UnitQueue::N};
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(q_full, 1);
+    ptx::mbar_init(q_empty, 1);
+    for (int s = 0; s < C::NSLOT; ++s) {
+      ptx::mbar_init(kv_full + s, 1);
+      ptx::mbar_init(kv_empty + s, 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(s_full + t, 1);
+      ptx::mbar_init(p_full + t, 128);
+      ptx::mbar_init(o_full + t, 1);
+    }
+    ptx::mbar_init(drain, 1);
+    for (int s = 0; s < UnitQueue::N; ++s) {
+      ptx::mbar_init(uq.full + s, 1);
+      ptx::mbar_init(uq.empty + s, C::UQ_READERS);
+    }
+    *abort_flag = 0u;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(tmem_slot, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Item i of the K/V stream (K and V of the units' key tiles in order) sits
+  // in ring slot i % NSLOT; the counters run across units.
+  auto slot = [](uint32_t i) { return static_cast<int>(i % C::NSLOT); };
+  auto par = [](uint32_t i) { return (i / C::NSLOT) & 1u; };
+
+  const int wg = warp >> 2;
+  if (wg == 0) {
+    ptx::reg_release<REG_CTRL>();
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ producer
+      ptx::WaitCtx w{abort_flag, P.status, 1u};
+      ptx::tma_prefetch_desc(&tmQ);
+      ptx::tma_prefetch_desc(&tmK);
+      ptx::tma_prefetch_desc(&tmV);
+      uint32_t item = 0, u_it = 0, pu = 0;
+      bool ok = true;
+      // a unit is claimed and published before the one before it is loaded
+      int x = min(static_cast<int>(atomicAdd(P.plan.counters, 1u)), P.total);
+      ok = uq_push(uq, pu++, x, w);
+      while (ok && x < P.total) {
+        const Unit u = load_unit(P, x);
+        x = min(static_cast<int>(atomicAdd(P.plan.counters, 1u)), P.total);
+        if (!(ok = uq_push(uq, pu++, x, w))) break;
+        if (u.hi == 0) continue;
+        if (!(ok = ptx::mbar_wait(q_empty, (u_it & 1u) ^ 1u, w))) break;
+        ptx::mbar_arrive_expect_tx(q_full, 2 * C::TILE);
+        for (int t = 0; t < 2; ++t)
+          for (int c = 0; c < C::KB; ++c)
+            ptx::tma_load_3d(sQ + t * C::TILE + c * BOX_BYTES, &tmQ, q_full, c * 64, (2 * u.qb + t) * BM, u.bh);
+        ++u_it;
+        for (int j = u.s0; ok && j < u.e0; ++j)
+          for (int kv = 0; kv < 2; ++kv, ++item) {
+            const int sl = slot(item);
+            if (!(ok = ptx::mbar_wait(kv_empty + sl, par(item) ^ 1u, w))) break;
+            ptx::mbar_arrive_expect_tx(kv_full + sl, C::TILE);
+            for (int c = 0; c < C::KB; ++c)
+              ptx::tma_load_3d(sKV + sl * C::TILE + c * BOX_BYTES, kv ? &tmV : &tmK, kv_full + sl, c * 64, j * BN,
+                               u.bh);
+          }
+      }
+      if (!ok) {
+        // let the copies in flight land before the CTA exits
+        for (uint32_t n = (item > (uint32_t)C::NSLOT ? item - C::NSLOT : 0u); n < item; ++n)
+          ptx::mbar_wait_drain(kv_full + slot(n), par(n));
+        if (u_it > 0) ptx::mbar_wait_drain(q_full, (u_it - 1) & 1u);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      // The whole warp follows the schedule; the lane elect.sync picks (lane
+      // 0) issues the MMAs and commits (see fwd_bf16.cu).
+      ptx::WaitCtx w{abort_flag, P.status, 3u};
+      const uint32_t sQa = ptx::smem_u32(sQ), sKVa = ptx::smem_u32(sKV);
+      auto mma_S = [&](int t, int sl) {
+        const uint32_t d = tmem + t * 256;
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * BOX_BYTES + (kk & 3) * 32;
+          const uint64_t a = ptx::sdesc_advance(ptx::sdesc_sw128(sQa + t * C::TILE, 16, 1024), off);
+          const uint64_t b = ptx::sdesc_advance(ptx::sdesc_sw128(sKVa + sl * C::TILE, 16, 1024), off);
+          ptx::mma_ss(d, a, b, C::IDESC_S, kk > 0 ? 1u : 0u);
+        }
+        ptx::mma_commit(s_full + t);
+      };
+      auto mma_PV = [&](int t, int sl, bool acc) {
+        const uint32_t d = tmem + t * 256 + 128, a = tmem + t * 256;
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk) {
+          const uint64_t b = ptx::sdesc_advance(ptx::sdesc_sw128(sKVa + sl * C::TILE, BOX_BYTES, 1024), kk * 2048);
+          ptx::mma_ts(d, a + kk * 8, b, C::IDESC_PV, (acc || kk > 0) ? 1u : 0u);
+        }
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, w));
+      };
+      uint32_t item = 0, u_it = 0, ru = 0, pp[2] = {0u, 0u};
+      bool ok = true, moved = false;
+      while (ok) {
+        int x;
+        if (!(ok = uq_read(uq, ru, &x, w))) break;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+        ++ru;
+        if (x >= P.total) break;
+        const Unit u = load_unit(P, x);
+        if (u.hi == 0) continue;
+        const int n = u.e0 - u.s0;
+        if (!(ok = wait(q_full, u_it & 1u))) break;
+        if (!(ok = wait(kv_full + slot(item), par(item)))) break;
+        ptx::tc_fence_after();
+        // (selects by constant index keep pp, s and e in registers)
+        if (ptx::elect_one()) {
+          moved |= lane != 0;
+          if (u.s[0] == u.s0 && u.e[0] > u.s[0]) mma_S(0, slot(item));
+          if (u.s[1] == u.s0 && u.e[1] > u.s[1]) mma_S(1, slot(item));
+          ptx::mma_commit(kv_empty + slot(item));
+          if (n == 1) ptx::mma_commit(q_empty);   // no later MMA reads Q: the next unit's may load
+        }
+        __syncwarp();
+        // each step waits for the next step's tiles while its own MMAs run
+        if (!(ok = wait(kv_full + slot(item + 1), par(item + 1)))) break;
+        if (n > 1 && !(ok = wait(kv_full + slot(item + 2), par(item + 2)))) break;
+        for (int j = u.s0; j < u.e0; ++j, item += 2) {
+          const uint32_t iv = item + 1, ikn = item + 2;   // V_j, K_{j+1}: resident
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const bool act = j >= u.s[t] && j < u.e[t];
+            const bool next = j + 1 >= u.s[t] && j + 1 < u.e[t];
+            if (act) {
+              if (!(ok = wait(p_full + t, pp[t] & 1u))) break;
+              ++pp[t];
+              ptx::tc_fence_after();
+            }
+            if (ptx::elect_one()) {
+              moved |= lane != 0;
+              if (act) mma_PV(t, slot(iv), j > u.s[t]);
+              if (next) mma_S(t, slot(ikn));
+              if (act && !next) ptx::mma_commit(o_full + t);
+              if (t == 1) {
+                ptx::mma_commit(kv_empty + slot(iv));
+                if (j + 1 < u.e0) ptx::mma_commit(kv_empty + slot(ikn));
+                if (j + 2 == u.e0) ptx::mma_commit(q_empty);   // the unit's last S products are out
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (j + 1 < u.e0 && !(ok = wait(kv_full + slot(iv + 2), par(iv + 2)))) break;
+          if (j + 2 < u.e0 && !(ok = wait(kv_full + slot(ikn + 2), par(ikn + 2)))) break;
+        }
+        if (!ok) break;
+        ++u_it;
+      }
+      if (!ok) {
+        if (ptx::elect_one()) ptx::mma_commit(drain);
+        __syncwarp();
+        ptx::mbar_wait_drain(drain, 0u);
+      }
+      if (__any_sync(0xffffffffu, moved) && lane == 0) atomicOr(P.status, ATTN_DEV_ISSUER);
+    }
+  } else {
+    ptx::reg_acquire<REG_SOFTMAX>();
+    // ------------------------------------------------------------ softmax
+    const int t = wg - 1;
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t tS = tmem + (static_cast<uint32_t>(quad * 32) << 16) + t * 256;
+    const uint32_t tO = tS + 128;
+    ptx::WaitCtx w{abort_flag, P.status, 4u + t};
+    const float sc2 = P.sc2;
+    const int R = P.p.R, dv = P.p.dv;
+    uint32_t sp = 0, op = 0, ru = 0, item = 0;
+    bool ok = true;
+    while (ok) {
+      int x;
+      if (!(ok = uq_read(uq, ru, &x, w))) break;
+      ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+      ++ru;
+      if (x >= P.total) break;
+      const Unit u = load_unit(P, x);
+      const int rt = 2 * u.qb + t;
+      if (rt >= P.p.n_rt) {
+        item += 2 * (u.e0 - u.s0);
+        continue;
+      }
+      const int row = rt * BM + r;
+      const bool row_ok = row < R;
+      const int4 ri = __ldg(P.plan.rows + static_cast<long long>(u.b) * P.p.rpad() + row);
+      const int4 th = t ? u.tile[1] : u.tile[0];
+      const int s_t = t ? u.s[1] : u.s[0], e_t = t ? u.e[1] : u.e[0];
+      float slope2 = 0.f;
+      if (BIAS && row_ok) slope2 = __ldg(P.p.slopes + (u.bh - u.b * P.p.Hkv) * P.p.G + row / P.p.Tq) * scored::kLog2e;
+      float m_used = -CUDART_INF_F, l = 0.f;
+      for (int j = s_t; j < e_t; ++j) {
+        const int kv0 = j * BN;
+        // every lane must agree before the warp-wide tcgen05 loads
+        if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full + t, sp & 1u, w)))) break;
+        ++sp;
+        ptx::tc_fence_after();
+        uint32_t raw[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + c * 32, raw[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld_wait(raw[c]);
+        float* s = reinterpret_cast<float*>(&raw[0][0]);
+        // a key of the tile that some row does not see
+        const bool partial = kv0 < th.z || kv0 + BN > th.w;
+        const int lo = ri.x - kv0, hi = ri.y - kv0;   // this row sees columns [lo, hi)
+        if (partial && (kv0 < u.lo || kv0 + BN > u.hi)) {
+          // the unit's first or last key tile: zero the rows of V that no row sees
+          const uint32_t iv = item + 2 * (j - u.s0) + 1;
+          if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(kv_full + slot(iv), par(iv), w)))) break;
+          if (kv0 + r < u.lo || kv0 + r >= u.hi) {
+            uint4* vr = reinterpret_cast<uint4*>(sKV + slot(iv) * C::TILE + r * 128);
+#pragma unroll
+            for (int c = 0; c < C::KB; ++c)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) vr[c * (BOX_BYTES / 16) + e] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          ptx::fence_proxy_async_smem();
+        }
+        if constexpr (BIAS) {
+          // the changed scores in log2 units, in place
+          bool poly = true;
+          if constexpr (CAP) {
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 128; i += 2) amax = ptx::fmax3(amax, fabsf(s[i]), fabsf(s[i + 1]));
+            poly = __all_sync(0xffffffffu, amax <= P.cap.limit);
+          }
+          // the distance changes sign inside the tile for some row of the warp
+          const int dist = kv0 - ri.z;
+          const bool cross = __any_sync(0xffffffffu, dist < 0 && dist > -(BN - 1));
+          const float delta = static_cast<float>(dist);
+          const float c1 = dist < 0 ? slope2 : -slope2;   // -slope2 * |key - pos| = c1 * (key - pos)
+          const float2 c1v = dup(c1), base = dup(c1 * delta);
+#pragma unroll
+          for (int i = 0; i < 128; i += 2) {
+            float2 v = make_float2(s[i], s[i + 1]);
+            float2 b = ptx::ffma2(make_float2(static_cast<float>(i), static_cast<float>(i + 1)), c1v, base);
+            if (cross)
+              b = make_float2(-slope2 * fabsf(delta + static_cast<float>(i)),
+                              -slope2 * fabsf(delta + static_cast<float>(i + 1)));
+            if constexpr (CAP) {
+              if (poly)
+                v = ptx::ffma2(v, scored::cap_poly(v, P.cap), b);
+              else
+                v = make_float2(scored::cap_any(v.x, P.cap) + b.x, scored::cap_any(v.y, P.cap) + b.y);
+            } else {
+              v = ptx::ffma2(v, dup(sc2), b);
+            }
+            s[i] = v.x;
+            s[i + 1] = v.y;
+          }
+        }
+        if (partial) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i < lo || i >= hi) s[i] = -CUDART_INF_F;
+        }
+        float m4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(s[k], s[k + 4]);
+#pragma unroll
+        for (int i = 8; i < 128; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = ptx::fmax3(m4[k], s[i + k], s[i + 4 + k]);
+        float mx = ptx::fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+        bool poly = true;
+        if constexpr (!BIAS) {
+          if constexpr (CAP) {
+            if (partial) {   // out of the cap's arithmetic; P is set to 0 below
+#pragma unroll
+              for (int i = 0; i < 128; ++i)
+                if (i < lo || i >= hi) s[i] = 0.f;
+            }
+            float a4[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) a4[k] = fmaxf(fabsf(s[k]), fabsf(s[k + 4]));
+#pragma unroll
+            for (int i = 8; i < 128; i += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) a4[k] = ptx::fmax3(a4[k], fabsf(s[i + k]), fabsf(s[i + 4 + k]));
+            poly = __all_sync(0xffffffffu, ptx::fmax3(a4[0], a4[1], fmaxf(a4[2], a4[3])) <= P.cap.limit);
+            mx = mx == -CUDART_INF_F ? mx : scored::cap_any(mx, P.cap);   // the cap is monotone
+          } else {
+            mx *= sc2;
+          }
+        }
+        const float m_new = fmaxf(m_used, mx);
+        bool need = false;
+        float corr = 1.0f;
+        if (j == s_t) {
+          m_used = m_new;
+        } else if (m_new > m_used + TAU) {
+          need = true;
+          corr = ptx::ex2(m_used - m_new);   // 0 when m_used = -inf
+          l *= corr;
+          m_used = m_new;
+        }
+        const float ref = (m_used == -CUDART_INF_F) ? 0.f : m_used;   // no key seen yet
+        float2 ls[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
+        // p = 2^(changed score - ref); EXPR gives the exponents of a pair
+        auto exps = [&](auto expr) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int a = 64 * h + 2 * i;
+              const float2 e = expr(make_float2(s[a], s[a + 1]));
+              float2 p = make_float2(ptx::ex2(e.x), ptx::ex2(e.y));
+              if (CAP && !BIAS && partial) {
+                if (a < lo || a >= hi) p.x = 0.f;
+                if (a + 1 < lo || a + 1 >= hi) p.y = 0.f;
+              }
+              ls[i & 3] = ptx::fadd2(ls[i & 3], p);
+              pk[i] = ptx::pack_bf16(p.x, p.y);
+            }
+            ptx::tmem_st32(tS + 32 * h, pk);
+          }
+        };
+        const float2 nref = dup(-ref);
+        if constexpr (BIAS) {
+          exps([&](float2 v) { return ptx::fadd2(v, nref); });
+        } else if constexpr (CAP) {
+          if (poly)
+            exps([&](float2 v) { return ptx::ffma2(v, scored::cap_poly(v, P.cap), nref); });
+          else
+            exps([&](float2 v) {
+              return make_float2(scored::cap_any(v.x, P.cap) - ref, scored::cap_any(v.y, P.cap) - ref);
+            });
+        } else {
+          exps([&](float2 v) { return ptx::ffma2(v, dup(sc2), nref); });
+        }
+        l += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
+        if (__any_sync(0xffffffffu, need)) {
+          // O_t *= corr before the next PV product adds to it; the previous
+          // one is complete (issued before the S product just consumed)
+#pragma unroll 1
+          for (int c = 0; c < HD / 32; ++c) {
+            uint32_t o[32];
+            ptx::tmem_ld32(tO + c * 32, o);
+            ptx::tmem_ld_wait(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+            ptx::tmem_st32(tO + c * 32, o);
+          }
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(p_full + t);
+      }
+      if (!ok) break;
+      item += 2 * (u.e0 - u.s0);
+      // ---------------------------------------------------------- epilogue
+      if (e_t > s_t) {
+        if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(o_full + t, op & 1u, w)))) break;
+        ++op;
+        ptx::tc_fence_after();
+      }
+      const float inv_l = (l > 0.f) ? 1.0f / l : 0.f;
+      const float lse = (l > 0.f) ? (m_used + log2f(l)) * 0.69314718055994530942f : -CUDART_INF_F;
+      const long long at = static_cast<long long>(u.bh) * R + (row_ok ? row : 0);
+      __nv_bfloat16* orow = P.O + at * dv;
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t o[32];
+        ptx::tmem_ld32(tO + c * 32, o);
+        ptx::tmem_ld_wait(o);
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          pk[i] = l > 0.f ? ptx::pack_bf16(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l)
+                          : 0u;
+        if (row_ok) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (c * 32 + 8 * v < dv) dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+        }
+      }
+      if (row_ok) P.LSE[at] = lse;
+      ptx::tc_fence_before();
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD, bool CAP, bool BIAS>
+cudaError_t launch(const ScoredFwd& a) {
+  using C = Cfg<HD>;
+  static_assert(C::SMEM <= 227 * 1024, "shared memory");
+  Params P;
+  P.p = a.p;
+  P.plan = a.plan;
+  P.O = static_cast<__nv_bfloat16*>(a.O);
+  P.LSE = a.LSE;
+  P.status = a.status;
+  P.sc2 = a.p.scale * scored::kLog2e;
+  P.cap = scored::make_cap(a.p.scale, a.p.softcap);
+  const int heads = a.p.B * a.p.Hkv;
+  P.n_pairs = (a.p.n_rt + 1) / 2;
+  P.total = P.n_pairs * heads;
+  // heads in groups whose keys and values fill about half of L2
+  const size_t per_head = static_cast<size_t>(a.p.Tk) * (a.p.d + a.p.dv) * 2;
+  size_t g = per_head * heads <= 2 * a.l2_bytes ? heads : a.l2_bytes / 2 / per_head;
+  P.group = static_cast<int>(g < 1 ? 1 : g > static_cast<size_t>(heads) ? heads : g);
+  const int grid = P.total < a.num_sms ? P.total : a.num_sms;
+  auto kern = scored_fwd_kernel<HD, CAP, BIAS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  // the register split must fit the launch allocation (see ptx::reg_acquire)
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+  if (fa.numRegs < REG_CTRL || fa.numRegs > REG_SOFTMAX || 3 * fa.numRegs < REG_CTRL + 2 * REG_SOFTMAX)
+    return cudaErrorInvalidConfiguration;
+  kern<<<grid, NUM_THREADS, C::SMEM, a.stream>>>(*a.tmQ, *a.tmK, *a.tmV, P);
+  return cudaGetLastError();
+}
+
+template <int HD>
+cudaError_t modes(const ScoredFwd& a) {
+  const bool cap = a.p.softcap > 0.f, bias = a.p.slopes != nullptr;
+  if (cap) return bias ? launch<HD, true, true>(a) : launch<HD, true, false>(a);
+  return bias ? launch<HD, false, true>(a) : launch<HD, false, false>(a);
+}
+
+}  // namespace scored_fwd
+
+cudaError_t launch_scored_fwd_bf16(const ScoredFwd& a) {
+  return a.p.d <= 64 && a.p.dv <= 64 ? scored_fwd::modes<64>(a) : scored_fwd::modes<128>(a);
+}
+
+}  // namespace attn

@@ -1,0 +1,74 @@
+// Arithmetic of the scored attention shared by its tensor-core kernels: the
+// tanh cap and the launch-wide constants of the changed scores, all in log2
+// units (scores times log2(e)), as the exponentials take them.
+#pragma once
+
+#include <stdint.h>
+
+#include "ptx.cuh"
+#include "scored.h"
+
+namespace attn {
+namespace scored {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// y = cap2 * tanh(k s), s the raw product q.k, k = scale / softcap, cap2 =
+// softcap * log2(e). For |k s| <= kPolyMax: s times a polynomial in s^2 with
+// k and cap2 in its coefficients. tanh(x) / x is fitted by a degree-4
+// polynomial in x^2 on |x| <= 0.6 (least squares with Lawson's reweighting);
+// |x * poly - tanh(x)| <= 2.0e-8, 8e-8 as evaluated in fp32, the size of
+// fp32's own rounding there. It costs 6 two-lane FMA-pipe instructions per
+// pair of scores, against 2 special-function instructions a score for the
+// formula 1 - 2 / (1 + e^(2x)) that every other |x| takes. Scores of a
+// trained layer lie well inside the cap, so nearly all tiles take the first.
+struct Cap {
+  float k2;        // 2 k log2(e): e^(2 k s) = 2^(k2 s)
+  float cap2;      // softcap * log2(e)
+  float ninv2;     // -1 / cap2^2
+  float limit;     // kPolyMax / k, or -1 where k^8 leaves fp32's range
+  float c[5];      // polynomial in s^2
+};
+
+constexpr float kPolyMax = 0.6f;
+
+inline Cap make_cap(float scale, float softcap) {
+  Cap r{};
+  if (!(softcap > 0.f)) return r;
+  const double c[5] = {0.9999996274092242, -0.333312085910721, 0.13299210221337304, -0.05169674295522158,
+                       0.014976960081731636};
+  const double k = static_cast<double>(scale) / softcap, cap2 = softcap * 1.4426950408889634;
+  const double k2 = 2.0 * k * 1.4426950408889634;
+  r.k2 = k2 < 1e30 ? static_cast<float>(k2) : 1e30f;   // (any score but 0 is at the cap there)
+  r.cap2 = static_cast<float>(cap2);
+  r.ninv2 = static_cast<float>(-1.0 / (cap2 * cap2));
+  const double k8 = k * k * k * k * k * k * k * k;
+  r.limit = k8 > 1e-30 && k8 < 1e30 ? static_cast<float>(kPolyMax / k) : -1.f;
+  double kk = k * cap2;
+  for (int i = 0; i < 5; ++i, kk *= k * k) r.c[i] = static_cast<float>(c[i] * kk);
+  return r;
+}
+
+__device__ __forceinline__ float2 dup(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ float2 cap_poly(float2 s, const Cap& c) {   // the factor of s
+  const float2 u = ptx::fmul2(s, s);
+  float2 g = ptx::ffma2(dup(c.c[4]), u, dup(c.c[3]));
+  g = ptx::ffma2(g, u, dup(c.c[2]));
+  g = ptx::ffma2(g, u, dup(c.c[1]));
+  return ptx::ffma2(g, u, dup(c.c[0]));
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// cap2 * tanh(k s) for any s: -cap2 and cap2 at the infinities.
+__device__ __forceinline__ float cap_any(float s, const Cap& c) {
+  return fmaf(-2.f * c.cap2, rcp_approx(1.f + ptx::ex2(s * c.k2)), c.cap2);
+}
+
+}  // namespace scored
+}  // namespace attn

@@ -306,7 +306,7 @@ ATTN_API attn_status_t attn_bwd_noalloc(const void* Q, const void* K, const void
  * arrays it points to are device memory read by the enqueued kernels.
  */
 typedef struct {
-  float softcap;        /* 0: none; otherwise finite and > 0 */
+  float softcap;        /* 0: none; otherwise from 1e-4 to 1e6 */
   int causal;           /* 0 or 1 */
   const float* slopes;  /* [H] fp32, finite values, or NULL: no bias */
   const int* q_pos;     /* [B,Tq] int32, or NULL: row i is at position i */

@@ -71,6 +71,8 @@ BAD = [
     (dict(workspace=0x9000010), B.ATTN_ERR_WORKSPACE),
     (dict(score=B.AttnScore(-1.0, 0, 0, 0, 0, 0)), B.ATTN_ERR_INVALID_ARG),
     (dict(score=B.AttnScore(float("inf"), 0, 0, 0, 0, 0)), B.ATTN_ERR_INVALID_ARG),
+    (dict(score=B.AttnScore(1e-5, 0, 0, 0, 0, 0)), B.ATTN_ERR_INVALID_ARG),
+    (dict(score=B.AttnScore(2e6, 0, 0, 0, 0, 0)), B.ATTN_ERR_INVALID_ARG),
     (dict(score=B.AttnScore(float("nan"), 0, 0, 0, 0, 0)), B.ATTN_ERR_INVALID_ARG),
     (dict(score=B.AttnScore(0.0, 2, 0, 0, 0, 0)), B.ATTN_ERR_INVALID_ARG),
     (dict(score=B.AttnScore(0.0, 0, 0x600002, 0, 0, 0)), B.ATTN_ERR_MISALIGNED),
