@@ -24,6 +24,7 @@ struct ScoredProblem {
   float scale;
   float softcap;          // 0: none
   const float* slopes;    // [H] or null
+  __host__ __device__ int n_words() const { return (n_rt + 31) / 32; }   // of a bit list of row tiles
   __host__ __device__ int rpad() const { return n_rt * kScoredTile; }
 };
 
@@ -31,10 +32,15 @@ struct ScoredProblem {
 struct ScoredPlan {
   int4* rows;      // [B][rpad]: {key begin, key end, position, 0}; begin = INT_MAX, end = 0 for rows that see nothing
   int4* tiles;     // [B][n_rt]: {min begin, max end over the rows that see keys, max begin, min end over all rows}
-  int2* ktiles;    // [B][n_kt]: {first row tile, row tiles} whose hull meets the key tile (backward only), or null
+  int* kcount;     // [B][n_kt]: row tiles whose hull meets the key tile (backward only), or null
+  uint32_t* kbits; // [B][n_kt][n_words]: which they are, one bit each
+  int* even;       // [B][n_rt]: the position of a row tile's first row where its rows are of one head and at
+                   // consecutive positions, else kScoredUneven (backward with a bias only), or null
   float* slope2;   // [Hkv][rpad]: slope * log2(e) of each packed row (backward with a bias only), or null
   uint32_t* counters;   // two unit counters, zeroed
 };
+
+constexpr int kScoredUneven = -0x7fffffff;
 
 struct ScoredMask {   // the caller's arrays
   const int* q_pos;
@@ -81,8 +87,14 @@ struct ScoredBwd {
   void* dV;
   float* D;         // [B * Hkv][rpad]: rowsum(dO o O), 0 behind row R
   float* NL;        // [B * Hkv][rpad]: -LSE * log2(e), -inf for rows that see nothing and behind row R
+  const CUtensorMap* tmQ;   // bf16 only
+  const CUtensorMap* tmK;
+  const CUtensorMap* tmV;
+  const CUtensorMap* tmdO;
+  const CUtensorMap* tmO;
   uint32_t* status;
   int num_sms;
+  size_t l2_bytes;
   cudaStream_t stream;
 };
 
@@ -92,6 +104,7 @@ cudaError_t launch_scored_bwd_simt(const ScoredBwd& a, bool bf16);
 
 // bf16 on the tensor cores; tmQ, tmK, tmV with 128-row boxes
 cudaError_t launch_scored_fwd_bf16(const ScoredFwd& a);
+cudaError_t launch_scored_bwd_bf16(const ScoredBwd& a);
 
 // O and LSE from the partial results of the key ranges, in range order
 cudaError_t launch_scored_merge(const ScoredFwd& a, bool bf16);

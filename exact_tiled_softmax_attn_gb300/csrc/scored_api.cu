@@ -70,12 +70,12 @@ void fwd_splits(const ScoredProblem& p, attn_dtype_t dt, int* S, int* keys) {
 }
 
 struct Layout {
-  size_t rows, tiles, counters, ktiles, slope2, D, NL, opart, lsepart, total;
+  size_t rows, tiles, counters, kcount, kbits, even, slope2, D, NL, opart, lsepart, total;
   int n_splits, split_keys;
 };
 
 // Forward: rows | tiles | counters | Opart | LSEpart. Backward: rows | tiles |
-// counters | ktiles | slope2 | D | NL. Each part starts on 256 bytes.
+// counters | kcount | kbits | even | slope2 | D | NL. Each part starts on 256 bytes.
 Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
   Layout L{};
   L.n_splits = 1;
@@ -92,7 +92,9 @@ Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
   L.tiles = take(B * p.n_rt * sizeof(int4));
   L.counters = take(256);
   if (bwd) {
-    L.ktiles = take(B * p.n_kt * sizeof(int2));
+    L.kcount = take(B * p.n_kt * sizeof(int));
+    L.kbits = take(B * p.n_kt * p.n_words() * sizeof(uint32_t));
+    L.even = take(B * p.n_rt * sizeof(int));
     L.slope2 = take(p.Hkv * rpad * sizeof(float));
     L.D = take(heads * rpad * sizeof(float));
     L.NL = take(heads * rpad * sizeof(float));
@@ -113,8 +115,14 @@ ScoredPlan plan_at(const Layout& L, void* ws, bool bwd, bool bias) {
   s.rows = reinterpret_cast<int4*>(w + L.rows);
   s.tiles = reinterpret_cast<int4*>(w + L.tiles);
   s.counters = reinterpret_cast<uint32_t*>(w + L.counters);
-  if (bwd) s.ktiles = reinterpret_cast<int2*>(w + L.ktiles);
-  if (bwd && bias) s.slope2 = reinterpret_cast<float*>(w + L.slope2);
+  if (bwd) {
+    s.kcount = reinterpret_cast<int*>(w + L.kcount);
+    s.kbits = reinterpret_cast<uint32_t*>(w + L.kbits);
+    if (bias) {
+      s.even = reinterpret_cast<int*>(w + L.even);
+      s.slope2 = reinterpret_cast<float*>(w + L.slope2);
+    }
+  }
   return s;
 }
 
@@ -287,9 +295,24 @@ attn_status_t attn_bwd_scored(const void* Q, const void* K, const void* V, const
   a.NL = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.NL);
   a.status = di->status;
   a.num_sms = di->num_sms;
+  a.l2_bytes = static_cast<size_t>(di->l2_bytes);
   a.stream = st;
+  CUtensorMap mq, mk, mv, mdo, mo;
+  if (bf16) {
+    const int heads = B * Hkv;
+    if ((s = make_map(&mq, Q, d, a.p.R, heads)) != ATTN_OK) return s;
+    if ((s = make_map(&mk, K, d, Tk, heads)) != ATTN_OK) return s;
+    if ((s = make_map(&mv, V, dv, Tk, heads)) != ATTN_OK) return s;
+    if ((s = make_map(&mdo, dO, dv, a.p.R, heads)) != ATTN_OK) return s;
+    if ((s = make_map(&mo, O, dv, a.p.R, heads)) != ATTN_OK) return s;
+    a.tmQ = &mq;
+    a.tmK = &mk;
+    a.tmV = &mv;
+    a.tmdO = &mdo;
+    a.tmO = &mo;
+  }
   e = launch_scored_plan(a.p, ScoredMask{sc.q_pos, sc.key_begin, sc.key_end, sc.causal}, a.plan, st);
-  if (e == cudaSuccess) e = launch_scored_bwd_simt(a, bf16);
+  if (e == cudaSuccess) e = bf16 ? launch_scored_bwd_bf16(a) : launch_scored_bwd_simt(a, false);
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 

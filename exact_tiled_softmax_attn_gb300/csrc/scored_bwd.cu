@@ -1,0 +1,1226 @@
+// bf16 scored-attention backward on tcgen05 tensor cores (d, dv <= 128).
+//
+//   D  = rowsum(dO o O),  P = 2^(S2 - LSE2)  (scores in log2 units)
+//   dV = P^T dO,  dS = P o T o (dO V^T - D),  dQ = scale dS K,  dK = scale dS^T Q
+// with T = 1 - (capped score / cap)^2, or 1 without a cap. Two kernels, with
+// the pipelines of the plain backward (bwd_bf16.cu):
+//   - dq_kernel: a unit is one 128-row tile of packed rows; Q and dO stay in
+//     tensor memory as A operands, dQ accumulates there over the key tiles
+//     the rows see, and D and -LSE log2(e) go to the workspace;
+//   - dkdv_kernel: a unit is one 128-key tile; K and V stay in shared memory,
+//     and dK and dV accumulate in tensor memory over the row tiles that see
+//     a key of it (a bit list from the plan), which with packed rows sums
+//     them over the query heads that share the key head.
+// Both sum in a fixed order. Differences from the plain kernels: the units'
+// tile lists come from the plan and are claimed at run time; the factor P T,
+// which dS needs, takes the place of P in the registers between the two
+// passes over a tile, so the cap costs arithmetic but no storage; ranges and
+// bias are applied per row (dq) and per column (dkdv).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "bwd_common.cuh"
+#include "common.cuh"
+#include "ptx.cuh"
+#include "scored.h"
+#include "scored_math.cuh"
+
+namespace attn {
+namespace scored_bwd {
+
+using bwd::BOX_BYTES;
+using bwd::BT;
+using bwd::packed_col;
+using bwd::sw128_offset;
+using bwd::UnitQueue;
+using bwd::uq_push;
+using bwd::uq_read;
+using scored::Cap;
+using scored::dup;
+
+struct Params {
+  ScoredProblem p;
+  ScoredPlan plan;
+  const float* LSE;
+  float* NL;
+  float* D;
+  __nv_bfloat16* dQ;
+  __nv_bfloat16* dK;
+  __nv_bfloat16* dV;
+  uint32_t* status;
+  uint32_t* counter;   // this launch's unit counter
+  int n_blocks, total, group;
+  float sc2;           // scale * log2(e)
+  Cap cap;
+};
+
+__device__ __forceinline__ int claim(const Params& P) {
+  return min(static_cast<int>(atomicAdd(P.counter, 1u)), P.total);
+}
+
+// ---------------------------------------------------------------- dQ
+
+template <int HD>
+struct CfgQ {
+  static constexpr int KB = HD / 64;
+  static constexpr int TILE = BT * HD * 2;
+  static constexpr int DPART_BYTES = 2 * 2 * BT * 4;   // [unit parity][row group][128] fp32 partial D
+  static constexpr int NSLOT_FIT = (227 * 1024 - DPART_BYTES - 256) / TILE;
+  static constexpr int NSLOT = NSLOT_FIT < 16 ? NSLOT_FIT : 16;
+  static constexpr int OFF_RING = 0;
+  static constexpr int OFF_DPART = OFF_RING + NSLOT * TILE;
+  static constexpr int OFF_BAR = OFF_DPART + DPART_BYTES;
+  // full[NSLOT], empty[NSLOT], qd_ready, s_full, s_free, dp_full, ds_full, dq_full, drain, dpart_full, unit queue
+  static constexpr int NBAR = 2 * NSLOT + 8 + 2 * UnitQueue::N;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_MISC + 16 + 4 * UnitQueue::N;
+  static constexpr int UQ_READERS = 1 + 256;
+  static constexpr uint32_t IDESC_S = ptx::idesc_bf16(BT, BT, false, false);
+  static constexpr uint32_t IDESC_DQ = ptx::idesc_bf16(BT, HD, false, true);
+  // Q and dO as packed bf16, the S and dP tiles, the dQ accumulator
+  static constexpr uint32_t T_Q = 0, T_DO = 64, T_S = 128, T_DP = 256, T_DQ = 384;
+};
+constexpr int DQ_THREADS = 320;
+
+struct UnitQ {
+  int bh, b, rt, j0, nk;   // row tile rt of key head bh; key tiles [j0, j0 + nk)
+  int4 tile;
+};
+
+__device__ __forceinline__ UnitQ load_unit_q(const Params& P, int x) {
+  UnitQ u;
+  bwd::grouped_unit(x, P.n_blocks, P.p.B * P.p.Hkv, P.group, true, &u.bh, &u.rt);
+  u.b = u.bh / P.p.Hkv;
+  u.tile = __ldg(P.plan.tiles + static_cast<long long>(u.b) * P.p.n_rt + u.rt);
+  u.j0 = u.tile.y > 0 ? u.tile.x / BT : 0;
+  u.nk = u.tile.y > 0 ? (u.tile.y + BT - 1) / BT - u.j0 : 0;
+  return u;
+}
+
+// Warps: 0 producer, 1 MMA, 2-5 and 6-9 two row groups of a thread per query
+// row; group g works on key columns [64 g, 64 g + 64) of every row.
+template <int HD, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(DQ_THREADS, 1)
+    dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+              const __grid_constant__ CUtensorMap tmO, const __grid_constant__ Params P) {
+  using C = CfgQ<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if ((ptx::smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(P.status, ATTN_DEV_BAD_SMEM);
+    return;
+  }
+  uint8_t* ring = smem + C::OFF_RING;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* full = bars;
+  uint64_t* empty = full + C::NSLOT;
+  uint64_t* qd_ready = empty + C::NSLOT;   // the row threads staged a unit's Q and dO (and read its O)
+  uint64_t* s_full = qd_ready + 1;
+  uint64_t* s_free = qd_ready + 2;
+  uint64_t* dp_full = qd_ready + 3;
+  uint64_t* ds_full = qd_ready + 4;
+  uint64_t* dq_full = qd_ready + 5;
+  uint64_t* drain = qd_ready + 6;
+  uint64_t* dpart_full = qd_ready + 7;
+  float* dpart = reinterpret_cast<float*>(smem + C::OFF_DPART);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 4);
+  const UnitQueue uq{reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16), qd_ready + 8,
+                     qd_ready + 8 + UnitQueue::N};
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NSLOT; ++s) {
+      ptx::mbar_init(full + s, 1);
+      ptx::mbar_init(empty + s, 1);
+    }
+    for (int s = 0; s < UnitQueue::N; ++s) {
+      ptx::mbar_init(uq.full + s, 1);
+      ptx::mbar_init(uq.empty + s, C::UQ_READERS);
+    }
+    ptx::mbar_init(qd_ready, 256);
+    ptx::mbar_init(s_full, 1);
+    ptx::mbar_init(s_free, 256);
+    ptx::mbar_init(dp_full, 1);
+    ptx::mbar_init(ds_full, 256);
+    ptx::mbar_init(dq_full, 1);
+    ptx::mbar_init(drain, 1);
+    ptx::mbar_init(dpart_full, 256);
+    *abort_flag = 0u;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(tmem_slot, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Ring item i sits in slot i % NSLOT. A unit whose first item is i0 has Q,
+  // dO, O at i0 .. i0 + 2 and K_j, V_j at i0 + 3 + 2 j and i0 + 4 + 2 j.
+  auto slot = [](uint32_t i) { return static_cast<int>(i % C::NSLOT); };
+  auto par = [](uint32_t i) { return (i / C::NSLOT) & 1u; };
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ producer
+    ptx::WaitCtx w{abort_flag, P.status, 5u};
+    ptx::tma_prefetch_desc(&tmQ);
+    ptx::tma_prefetch_desc(&tmK);
+    ptx::tma_prefetch_desc(&tmV);
+    ptx::tma_prefetch_desc(&tmdO);
+    ptx::tma_prefetch_desc(&tmO);
+    uint32_t item = 0, pu = 0;
+    auto load = [&](const CUtensorMap* map, int row, int bh) {
+      const int s = slot(item);
+      if (!ptx::mbar_wait(empty + s, par(item) ^ 1u, w)) return false;
+      ptx::mbar_arrive_expect_tx(full + s, C::TILE);
+      for (int c = 0; c < C::KB; ++c)
+        ptx::tma_load_3d(ring + s * C::TILE + c * BOX_BYTES, map, full + s, c * 64, row, bh);
+      ++item;
+      return true;
+    };
+    int x = claim(P);
+    bool ok = uq_push(uq, pu++, x, w);
+    while (ok && x < P.total) {
+      const UnitQ u = load_unit_q(P, x);
+      x = claim(P);
+      if (!(ok = uq_push(uq, pu++, x, w))) break;
+      if (u.nk == 0) continue;
+      ok = load(&tmQ, u.rt * BT, u.bh) && load(&tmdO, u.rt * BT, u.bh) && load(&tmO, u.rt * BT, u.bh);
+      for (int j = 0; ok && j < u.nk; ++j)
+        ok = load(&tmK, (u.j0 + j) * BT, u.bh) && load(&tmV, (u.j0 + j) * BT, u.bh);
+    }
+    if (!ok) {
+      for (uint32_t n = (item > static_cast<uint32_t>(C::NSLOT) ? item - C::NSLOT : 0u); n < item; ++n)
+        ptx::mbar_wait_drain(full + slot(n), par(n));
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    ptx::WaitCtx w{abort_flag, P.status, 6u};
+    const uint32_t aR = ptx::smem_u32(ring);
+    auto kmaj = [](uint32_t base, int kk) {
+      return ptx::sdesc_advance(ptx::sdesc_sw128(base, 16, 1024), (kk >> 2) * BOX_BYTES + (kk & 3) * 32);
+    };
+    auto mnmaj = [](uint32_t base, int kk) {
+      return ptx::sdesc_advance(ptx::sdesc_sw128(base, BOX_BYTES, 1024), kk * 2048);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, w));
+    };
+    auto mma_s = [&](uint32_t ik) {
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk)
+        ptx::mma_ts(tmem + C::T_S, tmem + C::T_Q + 8 * kk, kmaj(aR + slot(ik) * C::TILE, kk), C::IDESC_S, kk > 0);
+      ptx::mma_commit(s_full);
+    };
+    auto mma_dp = [&](uint32_t iv) {
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk)
+        ptx::mma_ts(tmem + C::T_DP, tmem + C::T_DO + 8 * kk, kmaj(aR + slot(iv) * C::TILE, kk), C::IDESC_S, kk > 0);
+      ptx::mma_commit(dp_full);
+      ptx::mma_commit(empty + slot(iv));
+    };
+    uint32_t item = 0, u_it = 0, sp = 0, ru = 0;
+    bool ok = true, moved = false;
+    while (ok) {
+      int x;
+      if (!(ok = uq_read(uq, ru, &x, w))) break;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+      ++ru;
+      if (x >= P.total) break;
+      const int nk = load_unit_q(P, x).nk;
+      if (nk == 0) continue;
+      const uint32_t i0 = item;
+      // Q and dO are in TMEM: the three staging slots go back to the ring
+      if (!(ok = wait(qd_ready, u_it & 1u))) break;
+      if (lane == 0)
+        for (int k = 0; k < 3; ++k) ptx::mbar_arrive(empty + slot(i0 + k));
+      __syncwarp();
+      if (!(ok = wait(full + slot(i0 + 3), par(i0 + 3)))) break;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+        moved |= lane != 0;
+        mma_s(i0 + 3);
+      }
+      __syncwarp();
+      if (!(ok = wait(full + slot(i0 + 4), par(i0 + 4)))) break;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+        moved |= lane != 0;
+        mma_dp(i0 + 4);
+      }
+      __syncwarp();
+      if (nk > 1 && !(ok = wait(full + slot(i0 + 5), par(i0 + 5)))) break;
+      for (int j = 0; j < nk; ++j, ++sp) {
+        const uint32_t ik = i0 + 3 + 2 * j;   // K_j; V_{j+1} = ik + 3, K_{j+1} = ik + 2, K_{j+2} = ik + 4
+        if (j + 1 < nk) {
+          if (!(ok = wait(s_free, sp & 1u))) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            moved |= lane != 0;
+            mma_s(ik + 2);
+          }
+          __syncwarp();
+        }
+        if (!(ok = wait(ds_full, sp & 1u))) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          moved |= lane != 0;
+#pragma unroll
+          for (int kk = 0; kk < BT / 16; ++kk)
+            ptx::mma_ts(tmem + C::T_DQ, tmem + C::T_DP + packed_col(kk), mnmaj(aR + slot(ik) * C::TILE, kk),
+                        C::IDESC_DQ, (j > 0 || kk > 0) ? 1u : 0u);
+          ptx::mma_commit(empty + slot(ik));
+        }
+        __syncwarp();
+        if (j + 1 < nk) {
+          if (!(ok = wait(full + slot(ik + 3), par(ik + 3)))) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            moved |= lane != 0;
+            mma_dp(ik + 3);
+          }
+          __syncwarp();
+        }
+        if (j + 2 < nk && !(ok = wait(full + slot(ik + 4), par(ik + 4)))) break;
+      }
+      if (!ok) break;
+      if (ptx::elect_one()) {
+        moved |= lane != 0;
+        ptx::mma_commit(dq_full);
+      }
+      __syncwarp();
+      item = i0 + 3 + 2 * nk;
+      ++u_it;
+    }
+    if (!ok) {
+      if (ptx::elect_one()) ptx::mma_commit(drain);
+      __syncwarp();
+      ptx::mbar_wait_drain(drain, 0u);
+    }
+    if (__any_sync(0xffffffffu, moved) && lane == 0) atomicOr(P.status, ATTN_DEV_ISSUER);
+  } else if (warp >= 2) {
+    // ------------------------------------------------------------ row groups
+    const int g = (warp - 2) >> 2;
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::T_S + 64 * g, tDP = tmem + lane_off + C::T_DP + 64 * g;
+    const uint32_t tDQ = tmem + lane_off + C::T_DQ + (HD / 2) * g;
+    const uint32_t tQ = tmem + lane_off + C::T_Q + (HD / 4) * g, tDO = tmem + lane_off + C::T_DO + (HD / 4) * g;
+    ptx::WaitCtx w{abort_flag, P.status, 7u + g};
+    const float sc2 = P.sc2, scale = P.p.scale;
+    const int R = P.p.R, d = P.p.d, rpad = P.p.rpad();
+    // Stage a unit: this group's half of row r of Q and dO into TMEM, its
+    // half of D_r into dpart. Rows past R load as zeros.
+    auto stage = [&](uint32_t i0, uint32_t u) {
+      for (int k = 0; k < 3; ++k)
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait(full + slot(i0 + k), par(i0 + k), w))) return false;
+      const uint8_t* sq = ring + slot(i0) * C::TILE;
+      const uint8_t* sdo = ring + slot(i0 + 1) * C::TILE;
+      const uint8_t* so = ring + slot(i0 + 2) * C::TILE;
+      {
+        uint32_t v[HD / 4];
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sq + sw128_offset(r, (HD / 2) * g + 8 * k));
+          v[4 * k] = x.x;
+          v[4 * k + 1] = x.y;
+          v[4 * k + 2] = x.z;
+          v[4 * k + 3] = x.w;
+        }
+        if constexpr (HD == 128) ptx::tmem_st32(tQ, v); else ptx::tmem_st16(tQ, v);
+      }
+      float part = 0.f;
+      {
+        uint32_t v[HD / 4];
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t off = sw128_offset(r, (HD / 2) * g + 8 * k);
+          const uint4 x = *reinterpret_cast<const uint4*>(sdo + off);
+          const uint4 o = *reinterpret_cast<const uint4*>(so + off);
+          v[4 * k] = x.x;
+          v[4 * k + 1] = x.y;
+          v[4 * k + 2] = x.z;
+          v[4 * k + 3] = x.w;
+          const __nv_bfloat162* dov = reinterpret_cast<const __nv_bfloat162*>(&x);
+          const __nv_bfloat162* ov = reinterpret_cast<const __nv_bfloat162*>(&o);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = __bfloat1622float2(ov[e]), b = __bfloat1622float2(dov[e]);
+            part = fmaf(a.x, b.x, part);
+            part = fmaf(a.y, b.y, part);
+          }
+        }
+        if constexpr (HD == 128) ptx::tmem_st32(tDO, v); else ptx::tmem_st16(tDO, v);
+      }
+      dpart[((u & 1u) * 2 + g) * BT + r] = part;
+      ptx::mbar_arrive(dpart_full);
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(qd_ready);
+      return true;
+    };
+    // the CTA's next unit with a key tile: 1, 0 at the end, -1 on a timeout;
+    // rows of a unit without one get their results here
+    uint32_t ru = 0;
+    auto next_unit = [&](UnitQ* u) {
+      for (;;) {
+        int x;
+        if (!uq_read(uq, ru, &x, w)) return -1;
+        ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+        ++ru;
+        if (x >= P.total) return 0;
+        *u = load_unit_q(P, x);
+        if (u->nk > 0) return 1;
+        const int row = u->rt * BT + r;
+        if (g == 0) {
+          P.D[static_cast<long long>(u->bh) * rpad + row] = 0.f;
+          P.NL[static_cast<long long>(u->bh) * rpad + row] = -CUDART_INF_F;
+        }
+        if (row < R) {
+          uint4* q = reinterpret_cast<uint4*>(P.dQ + (static_cast<long long>(u->bh) * R + row) * d);
+          for (int c = g; c < d / 8; c += 2) q[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    };
+    uint32_t item = 0, u_it = 0, sp = 0;
+    UnitQ u, un;
+    const int first = next_unit(&u);
+    bool have = first == 1;
+    bool ok = first >= 0 && (!have || stage(0u, 0u));
+    while (ok && have) {
+      const int row = u.rt * BT + r;
+      const bool row_ok = row < R;
+      const int4 ri = __ldg(P.plan.rows + static_cast<long long>(u.b) * rpad + row);
+      const float lse = row_ok ? P.LSE[static_cast<long long>(u.bh) * R + row] : -CUDART_INF_F;
+      const float nlse2 = (lse == -CUDART_INF_F) ? -CUDART_INF_F : -lse * scored::kLog2e;
+      float slope2 = 0.f;
+      if (BIAS) slope2 = __ldg(P.plan.slope2 + static_cast<long long>(u.bh - u.b * P.p.Hkv) * rpad + row);
+      if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dpart_full, u_it & 1u, w)))) break;
+      const float* dpu = dpart + (u_it & 1u) * 2 * BT;
+      const float dd = dpu[r] + dpu[BT + r];
+      if (g == 0) {   // for every row of the padded tile: the dK/dV kernel reads whole 128-row slices
+        P.D[static_cast<long long>(u.bh) * rpad + row] = dd;
+        P.NL[static_cast<long long>(u.bh) * rpad + row] = nlse2;
+      }
+      for (int j = 0; j < u.nk; ++j, ++sp) {
+        if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full, sp & 1u, w)))) break;
+        ptx::tc_fence_after();
+        float f[64];   // P T
+        const int kv0 = (u.j0 + j) * BT + 64 * g;   // key of this thread's first column
+        {
+          uint32_t v[2][32];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) ptx::tmem_ld32(tS + c * 32, v[c]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) ptx::tmem_ld_wait(v[c]);
+          // S is in registers: the next S product may overwrite it
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(s_free);
+          const float* s = reinterpret_cast<const float*>(&v[0][0]);
+          bool poly = true;
+          if constexpr (CAP) {
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) amax = ptx::fmax3(amax, fabsf(s[i]), fabsf(s[i + 1]));
+            poly = __all_sync(0xffffffffu, amax <= P.cap.limit);
+          }
+          const int dist = kv0 - ri.z;
+          const float delta = static_cast<float>(dist);
+          const float c1 = dist < 0 ? slope2 : -slope2;
+          const float2 c1v = dup(c1), base = dup(fmaf(c1, delta, nlse2));
+          bool cross = false;
+          if constexpr (BIAS) cross = __any_sync(0xffffffffu, dist < 0 && dist > -63);
+          auto tile = [&](auto capped) {   // capped: 0 plain, 1 polynomial, 2 formula
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              const float2 t = make_float2(s[i], s[i + 1]);
+              float2 add = dup(nlse2);
+              if constexpr (BIAS) {
+                add = ptx::ffma2(make_float2(static_cast<float>(i), static_cast<float>(i + 1)), c1v, base);
+                if (cross)
+                  add = make_float2(fmaf(-slope2, fabsf(delta + static_cast<float>(i)), nlse2),
+                                    fmaf(-slope2, fabsf(delta + static_cast<float>(i + 1)), nlse2));
+              }
+              if constexpr (decltype(capped)::value == 0) {
+                const float2 e = ptx::ffma2(t, dup(sc2), add);
+                f[i] = ptx::ex2(e.x);
+                f[i + 1] = ptx::ex2(e.y);
+              } else {
+                float2 y;
+                if constexpr (decltype(capped)::value == 1)
+                  y = ptx::fmul2(t, scored::cap_poly(t, P.cap));
+                else
+                  y = make_float2(scored::cap_any(t.x, P.cap), scored::cap_any(t.y, P.cap));
+                const float2 e = ptx::fadd2(y, add);
+                const float2 grad = ptx::ffma2(ptx::fmul2(y, y), dup(P.cap.ninv2), dup(1.f));
+                const float2 pg = ptx::fmul2(make_float2(ptx::ex2(e.x), ptx::ex2(e.y)), grad);
+                f[i] = pg.x;
+                f[i + 1] = pg.y;
+              }
+            }
+          };
+          if constexpr (!CAP) {
+            tile(std::integral_constant<int, 0>{});
+          } else {
+            if (poly)
+              tile(std::integral_constant<int, 1>{});
+            else
+              tile(std::integral_constant<int, 2>{});
+          }
+        }
+        if (kv0 < u.tile.z || kv0 + 64 > u.tile.w) {
+          const int lo = ri.x - kv0, hi = ri.y - kv0;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i < lo || i >= hi) f[i] = 0.f;
+        }
+        if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dp_full, sp & 1u, w)))) break;
+        ptx::tc_fence_after();
+        uint32_t v[2][32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) ptx::tmem_ld32(tDP + c * 32, v[c]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) ptx::tmem_ld_wait(v[c]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = ptx::fadd2(make_float2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])),
+                                        dup(-dd));
+            const float2 rr = ptx::fmul2(make_float2(f[c * 32 + 2 * i], f[c * 32 + 2 * i + 1]), e);
+            pk[i] = ptx::pack_bf16(rr.x, rr.y);
+          }
+          ptx::tmem_st16(tDP + c * 16, pk);   // over this group's own first columns (already read)
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ds_full);
+      }
+      if (!ok) break;
+      // the next unit's Q and dO go into TMEM now: the products that read
+      // this unit's have completed (their results were consumed above)
+      const uint32_t i_next = item + 3 + 2 * u.nk;
+      const int nx = next_unit(&un);
+      ok = nx >= 0;
+      if (!ok) break;
+      const bool have_next = nx == 1;
+      if (have_next && !(ok = stage(i_next, u_it + 1))) break;
+      if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dq_full, u_it & 1u, w)))) break;
+      ptx::tc_fence_after();
+      __nv_bfloat16* out = P.dQ + (static_cast<long long>(u.bh) * R + (row_ok ? row : 0)) * d;
+#pragma unroll
+      for (int c = 0; c < HD / 64; ++c) {
+        uint32_t v[32];
+        ptx::tmem_ld32(tDQ + c * 32, v);
+        ptx::tmem_ld_wait(v);
+        if (row_ok) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int col = (HD / 2) * g + c * 32 + 8 * e;
+            uint4 a;
+            a.x = ptx::pack_bf16(__uint_as_float(v[8 * e + 0]) * scale, __uint_as_float(v[8 * e + 1]) * scale);
+            a.y = ptx::pack_bf16(__uint_as_float(v[8 * e + 2]) * scale, __uint_as_float(v[8 * e + 3]) * scale);
+            a.z = ptx::pack_bf16(__uint_as_float(v[8 * e + 4]) * scale, __uint_as_float(v[8 * e + 5]) * scale);
+            a.w = ptx::pack_bf16(__uint_as_float(v[8 * e + 6]) * scale, __uint_as_float(v[8 * e + 7]) * scale);
+            if (col < d) *reinterpret_cast<uint4*>(out + col) = a;
+          }
+        }
+      }
+      // (the next unit's first dQ product, which overwrites the accumulator,
+      // waits for this group's first dS of that unit, issued after this)
+      ptx::tc_fence_before();
+      item = i_next;
+      ++u_it;
+      have = have_next;
+      u = un;
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- dK, dV
+
+constexpr int KV_THREADS = 512;
+constexpr int KV_REG_CTRL = 96, KV_REG_PDS = 168, KV_REG_EPI = 80, KV_REG_LAUNCH = 128;
+
+template <int HD>
+struct CfgKV {
+  static constexpr int KB = HD / 64;
+  static constexpr int TILE = BT * HD * 2;
+  static constexpr int NQ = 3, NO = 2, NL = 2;   // rings: Q tiles, dO tiles, slices of NL and D
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = OFF_K + TILE;
+  static constexpr int OFF_Q = OFF_V + TILE;
+  static constexpr int OFF_DO = OFF_Q + NQ * TILE;
+  static constexpr int OFF_LSE = OFF_DO + NO * TILE;
+  static constexpr int OFF_D = OFF_LSE + NL * BT * 4;
+  static constexpr int OFF_BAR = OFF_D + NL * BT * 4;
+  // kv_full, kv_empty, q_full[NQ], q_empty[NQ], o_full[NO], o_empty[NO], l_full[NL], l_empty[NL], s_full,
+  // dp_full, p_full, ds_full, acc_full, dv_free, dk_free, drain, unit queue
+  static constexpr int NBAR = 2 + 2 * NQ + 2 * NO + 2 * NL + 8 + 2 * UnitQueue::N;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_MISC + 16 + 4 * UnitQueue::N;
+  static constexpr int UQ_READERS = 1 + 256 + 128;
+  static constexpr uint32_t IDESC_S = ptx::idesc_bf16(BT, BT, false, false);
+  static constexpr uint32_t IDESC_ACC = ptx::idesc_bf16(BT, HD, false, true);
+};
+
+struct UnitKV {
+  int bh, b, kb, nq;       // key tile kb of key head bh, nq row tiles
+  const uint32_t* bits;    // the row tiles as bits
+};
+
+__device__ __forceinline__ UnitKV load_unit_kv(const Params& P, int x) {
+  UnitKV u;
+  bwd::grouped_unit(x, P.n_blocks, P.p.B * P.p.Hkv, P.group, false, &u.bh, &u.kb);
+  u.b = u.bh / P.p.Hkv;
+  const long long at = static_cast<long long>(u.b) * P.p.n_kt + u.kb;
+  u.nq = __ldg(P.plan.kcount + at);
+  u.bits = P.plan.kbits + at * P.p.n_words();
+  return u;
+}
+
+// Walks the set bits of a unit's list; the caller takes u.nq of them.
+struct TileList {
+  const uint32_t* words;
+  int base;
+  uint32_t bits;
+  __device__ __forceinline__ explicit TileList(const uint32_t* w) : words(w), base(-32), bits(0u) {}
+  __device__ __forceinline__ int next() {
+    while (bits == 0u) {
+      base += 32;
+      bits = __ldg(words++);
+    }
+    const int i = __ffs(bits) - 1;
+    bits &= bits - 1u;
+    return base + i;
+  }
+};
+
+// 32 x 32 bits, row i in lane i; returns column `lane` (bit i from lane i).
+__device__ __forceinline__ uint32_t transpose32(uint32_t x, int lane) {
+  uint32_t m = 0x0000ffffu;
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+    x = (lane & j) ? ((x & ~m) | ((y & ~m) >> j)) : ((x & m) | ((y & m) << j));
+    m ^= m << (j >> 1);
+  }
+  return x;
+}
+
+// The lanes [lo - first, hi - first) of a warp whose lane i stands for key first + i.
+__device__ __forceinline__ uint32_t lane_range(int lo, int hi, int first) {
+  const int a = max(lo - first, 0), b = min(hi - first, 32);
+  if (b <= a) return 0u;
+  return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
+}
+
+// Warps: 0 producer, 1 MMA, 4-7 and 8-11 P / dS (a thread per key; group h
+// works on query columns [64 h, 64 h + 64)), 12-15 epilogue.
+// TMEM: dV [0, 128), dK [128, 256), S^T [256, 384), dP^T [384, 512).
+template <int HD, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(KV_THREADS, 1)
+    dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                const __grid_constant__ Params P) {
+  using C = CfgKV<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if ((ptx::smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(P.status, ATTN_DEV_BAD_SMEM);
+    return;
+  }
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sdO = smem + C::OFF_DO;
+  float* sLSE = reinterpret_cast<float*>(smem + C::OFF_LSE);
+  float* sD = reinterpret_cast<float*>(smem + C::OFF_D);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* kv_full = bars + 0;
+  uint64_t* kv_empty = bars + 1;
+  uint64_t* q_full = bars + 2;
+  uint64_t* q_empty = q_full + C::NQ;
+  uint64_t* o_full = q_empty + C::NQ;
+  uint64_t* o_empty = o_full + C::NO;
+  uint64_t* l_full = o_empty + C::NO;
+  uint64_t* l_empty = l_full + C::NL;
+  uint64_t* s_full = l_empty + C::NL;
+  uint64_t* dp_full = s_full + 1;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* ds_full = s_full + 3;
+  uint64_t* acc_full = s_full + 4;
+  uint64_t* dv_free = s_full + 5;
+  uint64_t* dk_free = s_full + 6;
+  uint64_t* drain = s_full + 7;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 4);
+  const UnitQueue uq{reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16), s_full + 8,
+                     s_full + 8 + UnitQueue::N};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < UnitQueue::N; ++s) {
+      ptx::mbar_init(uq.full + s, 1);
+      ptx::mbar_init(uq.empty + s, C::UQ_READERS);
+    }
+    ptx::mbar_init(kv_full, 1);
+    ptx::mbar_init(kv_empty, 1);
+    for (int s = 0; s < C::NQ; ++s) {
+      ptx::mbar_init(q_full + s, 1);
+      ptx::mbar_init(q_empty + s, 1);
+    }
+    for (int s = 0; s < C::NO; ++s) {
+      ptx::mbar_init(o_full + s, 1);
+      ptx::mbar_init(o_empty + s, 1);
+    }
+    for (int s = 0; s < C::NL; ++s) {
+      ptx::mbar_init(l_full + s, 1);
+      ptx::mbar_init(l_empty + s, 256);
+    }
+    ptx::mbar_init(s_full, 1);
+    ptx::mbar_init(dp_full, 1);
+    ptx::mbar_init(p_full, 256);
+    ptx::mbar_init(ds_full, 256);
+    ptx::mbar_init(acc_full, 1);
+    ptx::mbar_init(dv_free, 128);
+    ptx::mbar_init(dk_free, 128);
+    ptx::mbar_init(drain, 1);
+    *abort_flag = 0u;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(tmem_slot, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t T_DV = 0, T_DK = 128, T_ST = 256, T_DP = 384;
+  // Row tile number n (counted across units) uses slot n % NQ, n % NO, n % NL.
+  auto qslot = [](uint32_t n) { return static_cast<int>(n % C::NQ); };
+  auto qpar = [](uint32_t n) { return (n / C::NQ) & 1u; };
+  auto oslot = [](uint32_t n) { return static_cast<int>(n % C::NO); };
+  auto opar = [](uint32_t n) { return (n / C::NO) & 1u; };
+  auto lslot = [](uint32_t n) { return static_cast<int>(n % C::NL); };
+  auto lpar = [](uint32_t n) { return (n / C::NL) & 1u; };
+  const int rpad = P.p.rpad();
+
+  const int wg = warp >> 2;
+  if (wg == 0) {
+    ptx::reg_release<KV_REG_CTRL>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer
+      ptx::WaitCtx w{abort_flag, P.status, 1u};
+      ptx::tma_prefetch_desc(&tmQ);
+      ptx::tma_prefetch_desc(&tmK);
+      ptx::tma_prefetch_desc(&tmV);
+      ptx::tma_prefetch_desc(&tmdO);
+      uint32_t u_it = 0, q_it = 0, q_issued = 0, o_issued = 0, l_issued = 0, pu = 0;
+      int x = claim(P);
+      bool ok = uq_push(uq, pu++, x, w);
+      while (ok && x < P.total) {
+        const UnitKV u = load_unit_kv(P, x);
+        x = claim(P);
+        if (!(ok = uq_push(uq, pu++, x, w))) break;
+        if (u.nq == 0) continue;
+        if (!(ok = ptx::mbar_wait(kv_empty, (u_it & 1u) ^ 1u, w))) break;
+        ptx::mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+        for (int c = 0; c < C::KB; ++c) {
+          ptx::tma_load_3d(sK + c * BOX_BYTES, &tmK, kv_full, c * 64, u.kb * BT, u.bh);
+          ptx::tma_load_3d(sV + c * BOX_BYTES, &tmV, kv_full, c * 64, u.kb * BT, u.bh);
+        }
+        ++u_it;
+        TileList list(u.bits);
+        for (int ii = 0; ii < u.nq; ++ii, ++q_it) {
+          const int rt = list.next();
+          const int qs = qslot(q_it), os = oslot(q_it), ls = lslot(q_it);
+          const long long row0 = static_cast<long long>(u.bh) * rpad + static_cast<long long>(rt) * BT;
+          if (!(ok = ptx::mbar_wait(q_empty + qs, qpar(q_it) ^ 1u, w))) break;
+          ptx::mbar_arrive_expect_tx(q_full + qs, C::TILE);
+          for (int c = 0; c < C::KB; ++c)
+            ptx::tma_load_3d(sQ + qs * C::TILE + c * BOX_BYTES, &tmQ, q_full + qs, c * 64, rt * BT, u.bh);
+          q_issued = q_it + 1;
+          if (!(ok = ptx::mbar_wait(l_empty + ls, lpar(q_it) ^ 1u, w))) break;
+          ptx::mbar_arrive_expect_tx(l_full + ls, 2 * BT * 4);
+          ptx::bulk_load(sLSE + ls * BT, P.NL + row0, BT * 4, l_full + ls);
+          ptx::bulk_load(sD + ls * BT, P.D + row0, BT * 4, l_full + ls);
+          l_issued = q_it + 1;
+          if (!(ok = ptx::mbar_wait(o_empty + os, opar(q_it) ^ 1u, w))) break;
+          ptx::mbar_arrive_expect_tx(o_full + os, C::TILE);
+          for (int c = 0; c < C::KB; ++c)
+            ptx::tma_load_3d(sdO + os * C::TILE + c * BOX_BYTES, &tmdO, o_full + os, c * 64, rt * BT, u.bh);
+          o_issued = q_it + 1;
+        }
+      }
+      if (!ok) {
+        // let the copies in flight land before the CTA exits
+        if (u_it > 0) ptx::mbar_wait_drain(kv_full, (u_it - 1) & 1u);
+        for (uint32_t n = (q_issued > (uint32_t)C::NQ ? q_issued - C::NQ : 0u); n < q_issued; ++n)
+          ptx::mbar_wait_drain(q_full + qslot(n), qpar(n));
+        for (uint32_t n = (o_issued > (uint32_t)C::NO ? o_issued - C::NO : 0u); n < o_issued; ++n)
+          ptx::mbar_wait_drain(o_full + oslot(n), opar(n));
+        for (uint32_t n = (l_issued > (uint32_t)C::NL ? l_issued - C::NL : 0u); n < l_issued; ++n)
+          ptx::mbar_wait_drain(l_full + lslot(n), lpar(n));
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      ptx::WaitCtx w{abort_flag, P.status, 2u};
+      const uint32_t aK = ptx::smem_u32(sK), aV = ptx::smem_u32(sV), aQ = ptx::smem_u32(sQ), adO = ptx::smem_u32(sdO);
+      auto kmaj = [](uint32_t base, int kk) {
+        return ptx::sdesc_advance(ptx::sdesc_sw128(base, 16, 1024), (kk >> 2) * BOX_BYTES + (kk & 3) * 32);
+      };
+      auto mnmaj = [](uint32_t base, int kk) {
+        return ptx::sdesc_advance(ptx::sdesc_sw128(base, BOX_BYTES, 1024), kk * 2048);
+      };
+      auto mma_st = [&](uint32_t n) {   // S^T = K Q^T
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          ptx::mma_ss(tmem + T_ST, kmaj(aK, kk), kmaj(aQ + qslot(n) * C::TILE, kk), C::IDESC_S, kk > 0);
+        ptx::mma_commit(s_full);
+      };
+      auto mma_dpt = [&](uint32_t n) {   // dP^T = V dO^T
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          ptx::mma_ss(tmem + T_DP, kmaj(aV, kk), kmaj(adO + oslot(n) * C::TILE, kk), C::IDESC_S, kk > 0);
+        ptx::mma_commit(dp_full);
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, w));
+      };
+      uint32_t u_it = 0, q_it = 0, pp = 0, ru = 0;
+      bool ok = true, moved = false;
+      while (ok) {
+        int x;
+        if (!(ok = uq_read(uq, ru, &x, w))) break;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+        ++ru;
+        if (x >= P.total) break;
+        const int nq = load_unit_kv(P, x).nq;
+        if (nq == 0) continue;
+        if (!(ok = wait(kv_full, u_it & 1u))) break;
+        if (!(ok = wait(q_full + qslot(q_it), qpar(q_it)))) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          moved |= lane != 0;
+          mma_st(q_it);
+        }
+        __syncwarp();
+        if (!(ok = wait(o_full + oslot(q_it), opar(q_it)))) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          moved |= lane != 0;
+          mma_dpt(q_it);
+          // K and V are read by no later MMA of a one-tile unit
+          if (nq == 1) ptx::mma_commit(kv_empty);
+        }
+        __syncwarp();
+        if (nq > 1 && !(ok = wait(q_full + qslot(q_it + 1), qpar(q_it + 1)))) break;
+        for (int ii = 0; ii < nq; ++ii) {
+          const uint32_t it = q_it + ii;
+          const bool more = ii + 1 < nq;
+          // dV += P^T dO, then the next S^T (which overwrites P^T). A unit's
+          // first dV (dK) overwrites the accumulator: the epilogue must have
+          // read the previous unit's.
+          if (ii == 0 && !(ok = wait(dv_free, (u_it & 1u) ^ 1u))) break;
+          if (!(ok = wait(p_full, pp & 1u))) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            moved |= lane != 0;
+#pragma unroll
+            for (int kk = 0; kk < BT / 16; ++kk)
+              ptx::mma_ts(tmem + T_DV, tmem + T_ST + packed_col(kk), mnmaj(adO + oslot(it) * C::TILE, kk),
+                          C::IDESC_ACC, (ii > 0 || kk > 0) ? 1u : 0u);
+            ptx::mma_commit(o_empty + oslot(it));
+            if (more) mma_st(it + 1);
+          }
+          __syncwarp();
+          if (ii == 0 && !(ok = wait(dk_free, (u_it & 1u) ^ 1u))) break;
+          if (!(ok = wait(ds_full, pp & 1u))) break;
+          ++pp;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            moved |= lane != 0;
+#pragma unroll
+            for (int kk = 0; kk < BT / 16; ++kk)
+              ptx::mma_ts(tmem + T_DK, tmem + T_DP + packed_col(kk), mnmaj(aQ + qslot(it) * C::TILE, kk),
+                          C::IDESC_ACC, (ii > 0 || kk > 0) ? 1u : 0u);
+            ptx::mma_commit(q_empty + qslot(it));
+          }
+          __syncwarp();
+          if (more) {
+            if (!(ok = wait(o_full + oslot(it + 1), opar(it + 1)))) break;
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+              moved |= lane != 0;
+              mma_dpt(it + 1);
+              if (ii + 2 == nq) ptx::mma_commit(kv_empty);   // the unit's last product of K or V
+            }
+            __syncwarp();
+          }
+          if (ii + 2 < nq && !(ok = wait(q_full + qslot(it + 2), qpar(it + 2)))) break;
+        }
+        if (!ok) break;
+        if (ptx::elect_one()) {
+          moved |= lane != 0;
+          ptx::mma_commit(acc_full);
+        }
+        __syncwarp();
+        q_it += nq;
+        ++u_it;
+      }
+      if (!ok) {
+        if (ptx::elect_one()) ptx::mma_commit(drain);
+        __syncwarp();
+        ptx::mbar_wait_drain(drain, 0u);
+      }
+      if (__any_sync(0xffffffffu, moved) && lane == 0) atomicOr(P.status, ATTN_DEV_ISSUER);
+    }
+  } else if (wg <= 2) {
+    ptx::reg_acquire<KV_REG_PDS>();
+    // ------------------------------------------------------------ P / dS (thread = key row)
+    const int h = wg - 1;
+    const int quad = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tST = tmem + lane_off + T_ST + 64 * h, tDP = tmem + lane_off + T_DP + 64 * h;
+    ptx::WaitCtx w{abort_flag, P.status, 3u};
+    const float sc2 = P.sc2;
+    const float2 neg1 = dup(-1.f);
+    uint32_t q_it = 0, ru = 0;
+    bool ok = true;
+    while (ok) {
+      int x;
+      if (!(ok = uq_read(uq, ru, &x, w))) break;
+      ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+      ++ru;
+      if (x >= P.total) break;
+      const UnitKV u = load_unit_kv(P, x);
+      const int key0 = u.kb * BT + quad * 32;   // key of lane 0
+      const int key = key0 + lane;
+      TileList list(u.bits);
+      for (int ii = 0; ii < u.nq; ++ii, ++q_it) {
+        const int rt = list.next();
+        const int ls = lslot(q_it);
+        const float* nlse2 = sLSE + ls * BT + 64 * h;
+        const float* dd = sD + ls * BT + 64 * h;
+        // Which of this warp's keys each of the 64 columns' rows sees, unless
+        // all rows see all keys of the tile: bit c of seen[c / 32] for this
+        // thread's key.
+        const int4 th = __ldg(P.plan.tiles + static_cast<long long>(u.b) * P.p.n_rt + rt);
+        const bool partial = u.kb * BT < th.z || u.kb * BT + BT > th.w;
+        uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+        const int4* rows = P.plan.rows + static_cast<long long>(u.b) * rpad + rt * BT + 64 * h;
+        if (partial) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int4 ri = __ldg(rows + 32 * c + lane);
+            seen[c] = transpose32(lane_range(ri.x, ri.y, key0), lane);
+          }
+        }
+        // bias: one slope and consecutive positions for the tile's rows (the
+        // plan says), else each column's own, from lanes c and c + 32
+        float pos0 = 0.f, slope2 = 0.f, cpos[2], cslope[2];
+        bool even = true;
+        if constexpr (BIAS) {
+          const float* sl = P.plan.slope2 + static_cast<long long>(u.bh - u.b * P.p.Hkv) * rpad + rt * BT + 64 * h;
+          const int first = __ldg(P.plan.even + static_cast<long long>(u.b) * P.p.n_rt + rt);
+          even = first != kScoredUneven;
+          if (even) {
+            pos0 = static_cast<float>(key - first - 64 * h);   // key - position of column 0
+            slope2 = __ldg(P.plan.slope2 + static_cast<long long>(u.bh - u.b * P.p.Hkv) * rpad + rt * BT);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              cpos[c] = __int_as_float(__ldg(rows + 32 * c + lane).z);
+              cslope[c] = __ldg(sl + 32 * c + lane);
+            }
+          }
+        }
+        // the staged slices of this tile are visible once l_full completed
+        if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(l_full + ls, lpar(q_it), w)))) break;
+        if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full, q_it & 1u, w)))) break;
+        ptx::tc_fence_after();
+        // pass 1: P^T, packed bf16 over the first half of this group's S^T
+        // columns; P^T T stays in registers for pass 2
+        uint32_t keep[2][16];
+        {
+          uint32_t rs[2][32];
+          ptx::tmem_ld32(tST, rs[0]);
+          ptx::tmem_ld32(tST + 32, rs[1]);
+          ptx::tmem_ld_wait(rs[0]);
+          ptx::tmem_ld_wait(rs[1]);
+          bool poly = true;
+          if constexpr (CAP) {
+            float amax = 0.f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                amax = ptx::fmax3(amax, fabsf(__uint_as_float(rs[c][i])), fabsf(__uint_as_float(rs[c][i + 1])));
+            poly = __all_sync(0xffffffffu, amax <= P.cap.limit);
+          }
+          // the distance pos0 - column changes sign inside the tile for some key of the warp
+          const bool cross = BIAS && __any_sync(0xffffffffu, pos0 > 0.f && pos0 < 63.f);
+          const float c1 = pos0 > 0.f ? -slope2 : slope2;   // -slope2 |pos0 - column| = c1 (pos0 - column)
+          const float2 nc1 = dup(-c1), base = dup(c1 * pos0);
+          auto tile = [&](auto capped, auto masked) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const float4 l4 = ptx::lds128(nlse2 + c * 32 + 2 * i);
+                float2 p2[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  const int a = 2 * (i + q);   // column within the 32
+                  const float2 t = make_float2(__uint_as_float(rs[c][a]), __uint_as_float(rs[c][a + 1]));
+                  float2 add = q ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
+                  if constexpr (BIAS) {
+                    const float n0 = static_cast<float>(c * 32 + a), n1 = static_cast<float>(c * 32 + a + 1);
+                    if (even && !cross) {
+                      add = ptx::fadd2(add, ptx::ffma2(make_float2(n0, n1), nc1, base));
+                    } else if (even) {
+                      add = make_float2(fmaf(-slope2, fabsf(pos0 - n0), add.x), fmaf(-slope2, fabsf(pos0 - n1), add.y));
+                    } else {
+                      const int q0 = __shfl_sync(0xffffffffu, __float_as_int(cpos[c]), a),
+                                q1 = __shfl_sync(0xffffffffu, __float_as_int(cpos[c]), a + 1);
+                      const float s0 = __shfl_sync(0xffffffffu, cslope[c], a),
+                                  s1 = __shfl_sync(0xffffffffu, cslope[c], a + 1);
+                      add = make_float2(fmaf(-s0, fabsf(static_cast<float>(key - q0)), add.x),
+                                        fmaf(-s1, fabsf(static_cast<float>(key - q1)), add.y));
+                    }
+                  }
+                  float2 p, k2;
+                  if constexpr (decltype(capped)::value == 0) {
+                    const float2 e = ptx::ffma2(t, dup(sc2), add);
+                    p = make_float2(ptx::ex2(e.x), ptx::ex2(e.y));
+                  } else {
+                    float2 y;
+                    if constexpr (decltype(capped)::value == 1)
+                      y = ptx::fmul2(t, scored::cap_poly(t, P.cap));
+                    else
+                      y = make_float2(scored::cap_any(t.x, P.cap), scored::cap_any(t.y, P.cap));
+                    const float2 e = ptx::fadd2(y, add);
+                    p = make_float2(ptx::ex2(e.x), ptx::ex2(e.y));
+                    k2 = ptx::ffma2(ptx::fmul2(y, y), dup(P.cap.ninv2), dup(1.f));
+                  }
+                  if constexpr (decltype(masked)::value) {
+                    if (!(seen[c] & (1u << a))) p.x = 0.f;
+                    if (!(seen[c] & (2u << a))) p.y = 0.f;
+                  }
+                  p2[q] = p;
+                  pk[i + q] = ptx::pack_bf16(p.x, p.y);
+                  if constexpr (decltype(capped)::value != 0) {
+                    k2 = ptx::fmul2(p, k2);
+                    keep[c][i + q] = ptx::pack_bf16(k2.x, k2.y);
+                  } else {
+                    keep[c][i + q] = pk[i + q];
+                  }
+                }
+              }
+              ptx::tmem_st16(tST + c * 16, pk);
+            }
+          };
+          auto either = [&](auto capped) {
+            if (partial)
+              tile(capped, std::true_type{});
+            else
+              tile(capped, std::false_type{});
+          };
+          if constexpr (!CAP) {
+            either(std::integral_constant<int, 0>{});
+          } else {
+            if (poly)
+              either(std::integral_constant<int, 1>{});
+            else
+              either(std::integral_constant<int, 2>{});
+          }
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(p_full);
+        // pass 2: dS^T = P^T T (dP^T - D), bf16 over dP^T
+        if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dp_full, q_it & 1u, w)))) break;
+        ptx::tc_fence_after();
+        {
+          uint32_t rd[2][32];
+          ptx::tmem_ld32(tDP, rd[0]);
+          ptx::tmem_ld32(tDP + 32, rd[1]);
+          ptx::tmem_ld_wait(rd[0]);
+          ptx::tmem_ld_wait(rd[1]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float4 d4 = ptx::lds128(dd + c * 32 + 2 * i);
+              const float2 pf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&keep[c][i]));
+              const float2 pg = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&keep[c][i + 1]));
+              const float2 e01 = ptx::ffma2(make_float2(d4.x, d4.y), neg1,
+                                            make_float2(__uint_as_float(rd[c][2 * i]), __uint_as_float(rd[c][2 * i + 1])));
+              const float2 e23 = ptx::ffma2(make_float2(d4.z, d4.w), neg1,
+                                            make_float2(__uint_as_float(rd[c][2 * i + 2]),
+                                                        __uint_as_float(rd[c][2 * i + 3])));
+              const float2 s01 = ptx::fmul2(pf, e01), s23 = ptx::fmul2(pg, e23);
+              pk[i] = ptx::pack_bf16(s01.x, s01.y);
+              pk[i + 1] = ptx::pack_bf16(s23.x, s23.y);
+            }
+            ptx::tmem_st16(tDP + c * 16, pk);
+          }
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ds_full);
+        ptx::mbar_arrive(l_empty + ls);
+      }
+    }
+  } else {
+    ptx::reg_release<KV_REG_EPI>();
+    // ------------------------------------------------------------ dK / dV epilogue
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    ptx::WaitCtx w{abort_flag, P.status, 4u};
+    const float scale = P.p.scale;
+    const int Tk = P.p.Tk;
+    uint32_t u_it = 0, ru = 0;
+    bool ok = true;
+    while (ok) {
+      int x;
+      if (!(ok = uq_read(uq, ru, &x, w))) break;
+      ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+      ++ru;
+      if (x >= P.total) break;
+      const UnitKV u = load_unit_kv(P, x);
+      const int key = u.kb * BT + r;
+      const bool key_ok = key < Tk;
+      const long long at = static_cast<long long>(u.bh) * Tk + (key_ok ? key : 0);
+      if (u.nq == 0) {   // no row sees a key of the tile
+        if (key_ok) {
+          for (int c = 0; c < P.p.d / 8; ++c) reinterpret_cast<uint4*>(P.dK + at * P.p.d)[c] = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < P.p.dv / 8; ++c) reinterpret_cast<uint4*>(P.dV + at * P.p.dv)[c] = make_uint4(0, 0, 0, 0);
+        }
+        continue;
+      }
+      if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(acc_full, u_it & 1u, w)))) break;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int acc = 0; acc < 2; ++acc) {   // dV first, released as soon as it is read, then scale * dK
+        const uint32_t tcol = tmem + lane_off + (acc ? T_DK : T_DV);
+        const int width = acc ? P.p.d : P.p.dv;
+        __nv_bfloat16* orow = acc ? P.dK + at * width : P.dV + at * width;
+        const float mul = acc ? scale : 1.0f;
+#pragma unroll
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t v[32];
+          ptx::tmem_ld32(tcol + c * 32, v);
+          ptx::tmem_ld_wait(v);
+          if (key_ok) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint4 a;
+              a.x = ptx::pack_bf16(__uint_as_float(v[8 * e + 0]) * mul, __uint_as_float(v[8 * e + 1]) * mul);
+              a.y = ptx::pack_bf16(__uint_as_float(v[8 * e + 2]) * mul, __uint_as_float(v[8 * e + 3]) * mul);
+              a.z = ptx::pack_bf16(__uint_as_float(v[8 * e + 4]) * mul, __uint_as_float(v[8 * e + 5]) * mul);
+              a.w = ptx::pack_bf16(__uint_as_float(v[8 * e + 6]) * mul, __uint_as_float(v[8 * e + 7]) * mul);
+              if (c * 32 + 8 * e < width) reinterpret_cast<uint4*>(orow + c * 32)[e] = a;
+            }
+          }
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(acc ? dk_free : dv_free);
+      }
+      ++u_it;
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD, bool CAP, bool BIAS>
+cudaError_t launch(const ScoredBwd& a) {
+  static_assert(CfgQ<HD>::SMEM <= 227 * 1024 && CfgKV<HD>::SMEM <= 227 * 1024, "shared memory");
+  static_assert(KV_REG_CTRL + 2 * KV_REG_PDS + KV_REG_EPI <= 4 * KV_REG_LAUNCH, "register split");
+  const ScoredProblem& p = a.p;
+  Params P;
+  P.p = p;
+  P.plan = a.plan;
+  P.LSE = a.LSE;
+  P.NL = a.NL;
+  P.D = a.D;
+  P.dQ = static_cast<__nv_bfloat16*>(a.dQ);
+  P.dK = static_cast<__nv_bfloat16*>(a.dK);
+  P.dV = static_cast<__nv_bfloat16*>(a.dV);
+  P.status = a.status;
+  P.sc2 = p.scale * scored::kLog2e;
+  P.cap = scored::make_cap(p.scale, p.softcap);
+  const int heads = p.B * p.Hkv;
+  // heads in groups whose streamed tiles fill about half of L2
+  auto group = [&](size_t per_head) {
+    size_t g = per_head * heads <= 2 * a.l2_bytes ? heads : a.l2_bytes / 2 / per_head;
+    return static_cast<int>(g < 1 ? 1 : g > static_cast<size_t>(heads) ? heads : g);
+  };
+  auto kq = dq_kernel<HD, CAP, BIAS>;
+  auto kk = dkdv_kernel<HD, CAP, BIAS>;
+  cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgQ<HD>::SMEM);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgKV<HD>::SMEM);
+  if (e != cudaSuccess) return e;
+  // the register split must fit the launch allocation (see ptx::reg_acquire)
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, kk)) != cudaSuccess) return e;
+  if (fa.numRegs != KV_REG_LAUNCH) return cudaErrorInvalidConfiguration;
+  P.n_blocks = p.n_rt;
+  P.total = p.n_rt * heads;
+  P.group = group(static_cast<size_t>(p.Tk) * (p.d + p.dv) * 2);
+  P.counter = a.plan.counters;
+  kq<<<P.total < a.num_sms ? P.total : a.num_sms, DQ_THREADS, CfgQ<HD>::SMEM, a.stream>>>(*a.tmQ, *a.tmK, *a.tmV,
+                                                                                          *a.tmdO, *a.tmO, P);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  P.n_blocks = p.n_kt;
+  P.total = p.n_kt * heads;
+  P.group = group(static_cast<size_t>(p.R) * ((p.d + p.dv) * 2 + 8));
+  P.counter = a.plan.counters + 1;
+  kk<<<P.total < a.num_sms ? P.total : a.num_sms, KV_THREADS, CfgKV<HD>::SMEM, a.stream>>>(*a.tmQ, *a.tmK, *a.tmV,
+                                                                                           *a.tmdO, P);
+  return cudaGetLastError();
+}
+
+template <int HD>
+cudaError_t modes(const ScoredBwd& a) {
+  const bool cap = a.p.softcap > 0.f, bias = a.p.slopes != nullptr;
+  if (cap) return bias ? launch<HD, true, true>(a) : launch<HD, true, false>(a);
+  return bias ? launch<HD, false, true>(a) : launch<HD, false, false>(a);
+}
+
+}  // namespace scored_bwd
+
+cudaError_t launch_scored_bwd_bf16(const ScoredBwd& a) {
+  return a.p.d <= 64 && a.p.dv <= 64 ? scored_bwd::modes<64>(a) : scored_bwd::modes<128>(a);
+}
+
+}  // namespace attn

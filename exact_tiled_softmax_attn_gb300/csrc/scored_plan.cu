@@ -37,6 +37,15 @@ __global__ void __launch_bounds__(kScoredTile) plan_rows_kernel(const ScoredProb
   if (out.slope2 && b == 0)
     for (int k = 0; k < p.Hkv; ++k)
       out.slope2[static_cast<long long>(k) * p.rpad() + row] = valid ? p.slopes[k * p.G + row / p.Tq] * LOG2E : 0.f;
+  if (out.even) {
+    __shared__ int first;
+    if (threadIdx.x == 0) first = pos;
+    __syncthreads();
+    const int head0 = tile * kScoredTile / p.Tq;
+    const bool same = !valid || (pos == first + static_cast<int>(threadIdx.x) && row / p.Tq == head0);
+    const bool all = __syncthreads_and(same);
+    if (threadIdx.x == 0) out.even[b * static_cast<long long>(p.n_rt) + tile] = all ? first : kScoredUneven;
+  }
   // hull over the rows that see keys; the keys that every row sees
   int v[4] = {lo, -hi, valid ? -lo : -INT_MAX, valid ? hi : INT_MAX};   // minima of all four
   if (!valid) v[2] = INT_MAX;
@@ -64,20 +73,19 @@ __global__ void __launch_bounds__(128) plan_keys_kernel(const ScoredProblem p, c
   if (w >= static_cast<long long>(p.B) * p.n_kt) return;
   const int b = static_cast<int>(w / p.n_kt), kt = static_cast<int>(w % p.n_kt);
   const int k0 = kt * kScoredTile, k1 = k0 + kScoredTile;
-  int first = INT_MAX, nlast = INT_MAX;   // nlast: minus the last tile
-  for (int t = lane; t < p.n_rt; t += 32) {
-    const int4 h = out.tiles[static_cast<long long>(b) * p.n_rt + t];
-    if (h.x < k1 && h.y > k0) {
-      first = min(first, t);
-      nlast = min(nlast, -t);
+  int count = 0;
+  for (int t0 = 0; t0 < p.n_rt; t0 += 32) {
+    const int t = t0 + lane;
+    bool meets = false;
+    if (t < p.n_rt) {
+      const int4 h = out.tiles[static_cast<long long>(b) * p.n_rt + t];
+      meets = h.x < k1 && h.y > k0;
     }
+    const unsigned word = __ballot_sync(0xffffffffu, meets);
+    count += __popc(word);
+    if (lane == 0) out.kbits[w * p.n_words() + t0 / 32] = word;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
-    nlast = min(nlast, __shfl_xor_sync(0xffffffffu, nlast, o));
-  }
-  if (lane == 0) out.ktiles[w] = first == INT_MAX ? make_int2(0, 0) : make_int2(first, -nlast - first + 1);
+  if (lane == 0) out.kcount[w] = count;
 }
 
 // One warp per row; every lane holds the row's weights' sum.
@@ -120,7 +128,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ Op
 cudaError_t launch_scored_plan(const ScoredProblem& p, const ScoredMask& m, const ScoredPlan& plan, cudaStream_t s) {
   scored::plan_rows_kernel<<<p.n_rt * p.B, kScoredTile, 0, s>>>(p, m, plan);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || plan.ktiles == nullptr) return e;
+  if (e != cudaSuccess || plan.kcount == nullptr) return e;
   const long long warps = static_cast<long long>(p.B) * p.n_kt;
   scored::plan_keys_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, s>>>(p, plan);
   return cudaGetLastError();

@@ -356,9 +356,11 @@ __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const S
 #pragma unroll
     for (int e = 0; e < 4 * NCV; ++e) av[i][e] = 0.f;
   }
-  const int2 list = plan.ktiles[static_cast<long long>(b) * p.n_kt + k0 / kScoredTile];
-  for (int r0 = list.x * kScoredTile; r0 < min(p.R, (list.x + list.y) * kScoredTile); r0 += BM) {
-    const int4 hull = plan.tiles[static_cast<long long>(b) * p.n_rt + r0 / kScoredTile];
+  const uint32_t* list = plan.kbits + (static_cast<long long>(b) * p.n_kt + k0 / kScoredTile) * p.n_words();
+  for (int r0 = 0; r0 < p.R; r0 += BM) {
+    const int rt = r0 / kScoredTile;
+    if (!(list[rt / 32] >> (rt % 32) & 1u)) continue;
+    const int4 hull = plan.tiles[static_cast<long long>(b) * p.n_rt + rt];
     if (hull.x >= k0 + BN || hull.y <= k0) continue;
     __syncthreads();
     load_tile<T, NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
