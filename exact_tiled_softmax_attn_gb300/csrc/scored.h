@@ -60,6 +60,7 @@ struct ScoredFwd {
   const void* V;
   void* O;
   float* LSE;
+  int* start;         // few-row kernel: [B + 1], and n_splits is its grid
   int n_splits;       // key ranges of split_keys keys (a multiple of 128) each, as units of their own
   int split_keys;
   float* Opart;       // [n_splits][B * Hkv * R][dv] fp32, n_splits > 1
@@ -99,14 +100,17 @@ struct ScoredBwd {
 };
 
 // CUDA cores (fp32 problems)
-cudaError_t launch_scored_fwd_simt(const ScoredFwd& a, bool bf16);
-cudaError_t launch_scored_bwd_simt(const ScoredBwd& a, bool bf16);
+cudaError_t launch_scored_fwd_simt(const ScoredFwd& a);
+cudaError_t launch_scored_bwd_simt(const ScoredBwd& a);
 
 // bf16 on the tensor cores; tmQ, tmK, tmV with 128-row boxes
 cudaError_t launch_scored_fwd_bf16(const ScoredFwd& a);
+// bf16, at most 64 packed rows a key head; tmK, tmV with 64-row boxes
+constexpr int kScoredTokenRows = 64;
+cudaError_t launch_scored_tokens_bf16(const ScoredFwd& a);
 cudaError_t launch_scored_bwd_bf16(const ScoredBwd& a);
 
-// O and LSE from the partial results of the key ranges, in range order
-cudaError_t launch_scored_merge(const ScoredFwd& a, bool bf16);
+// fp32 O and LSE from the partial results of the key ranges, in range order
+cudaError_t launch_scored_merge(const ScoredFwd& a);
 
 }  // namespace attn

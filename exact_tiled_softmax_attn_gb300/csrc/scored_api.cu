@@ -59,9 +59,7 @@ ScoredProblem problem(int B, int H, int Hkv, int Tq, int Tk, int d, int dv) {
 
 // Key ranges of the forward: the CUDA-core kernel runs two 64-row tiles per
 // SM at a time.
-bool fwd_tensor(const ScoredProblem& p, attn_dtype_t dt) { return dt == ATTN_BF16 && p.R > 64; }
-void fwd_splits(const ScoredProblem& p, attn_dtype_t dt, int* S, int* keys) {
-  if (fwd_tensor(p, dt)) return;
+void fwd_splits(const ScoredProblem& p, int* S, int* keys) {
   const long long units = static_cast<long long>(p.B) * p.Hkv * ((p.R + 63) / 64);
   const int want = wave_splits(units, p.n_kt, 2 * kSms);
   const int tiles = want > 1 ? (p.n_kt + want - 1) / want : p.n_kt;
@@ -69,12 +67,17 @@ void fwd_splits(const ScoredProblem& p, attn_dtype_t dt, int* S, int* keys) {
   *keys = tiles * kScoredTile;
 }
 
+// bf16 with at most 64 packed rows per key head: the few-row kernel, which
+// streams the keys with every SM; more rows fill tcgen05 tiles.
+bool fwd_tokens(const ScoredProblem& p, attn_dtype_t dt) { return dt == ATTN_BF16 && p.R <= kScoredTokenRows; }
+
 struct Layout {
-  size_t rows, tiles, counters, kcount, kbits, even, slope2, D, NL, opart, lsepart, total;
+  size_t start, rows, tiles, counters, kcount, kbits, even, slope2, D, NL, opart, lsepart, total;
   int n_splits, split_keys;
 };
 
-// Forward: rows | tiles | counters | Opart | LSEpart. Backward: rows | tiles |
+// Forward: rows | tiles | counters | Opart | LSEpart, with few rows in bf16
+// start | Opart | LSEpart. Backward: rows | tiles |
 // counters | kcount | kbits | even | slope2 | D | NL. Each part starts on 256 bytes.
 Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
   Layout L{};
@@ -88,6 +91,16 @@ Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
     return at;
   };
   const size_t B = p.B, rpad = p.rpad(), heads = B * p.Hkv;
+  if (!bwd && fwd_tokens(p, dt)) {
+    // one CTA per SM, two where 16 rows are enough, and at least a 64-key stage each
+    const long long stages = static_cast<long long>(heads) * ((p.Tk + 63) / 64), want = p.R <= 16 ? 2 * kSms : kSms;
+    L.n_splits = static_cast<int>(stages < want ? stages : want);
+    L.start = take((B + 1) * sizeof(int));
+    L.opart = take(static_cast<size_t>(L.n_splits) * 2 * p.R * p.dv * sizeof(float));
+    L.lsepart = take(static_cast<size_t>(L.n_splits) * 2 * p.R * sizeof(float));
+    L.total = off;
+    return L;
+  }
   L.rows = take(B * rpad * sizeof(int4));
   L.tiles = take(B * p.n_rt * sizeof(int4));
   L.counters = take(256);
@@ -99,7 +112,7 @@ Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
     L.D = take(heads * rpad * sizeof(float));
     L.NL = take(heads * rpad * sizeof(float));
   } else {
-    fwd_splits(p, dt, &L.n_splits, &L.split_keys);
+    if (dt == ATTN_F32) fwd_splits(p, &L.n_splits, &L.split_keys);
     if (L.n_splits > 1) {
       L.opart = take(L.n_splits * heads * p.R * p.dv * sizeof(float));
       L.lsepart = take(L.n_splits * heads * p.R * sizeof(float));
@@ -215,21 +228,25 @@ attn_status_t attn_fwd_scored(const void* Q, const void* K, const void* V, void*
   a.num_sms = di->num_sms;
   a.l2_bytes = static_cast<size_t>(di->l2_bytes);
   a.stream = st;
-  e = launch_scored_plan(a.p, a.mask, a.plan, st);
-  if (e == cudaSuccess && fwd_tensor(a.p, dtype)) {
-    CUtensorMap mq, mk, mv;
+  a.start = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + L.start);
+  const bool tokens = fwd_tokens(a.p, dtype);
+  CUtensorMap mq, mk, mv;
+  if (bf16) {
     const int heads = B * Hkv;
+    const unsigned key_rows = tokens ? 64u : 128u;
     if ((s = make_map(&mq, Q, d, a.p.R, heads)) != ATTN_OK) return s;
-    if ((s = make_map(&mk, K, d, Tk, heads)) != ATTN_OK) return s;
-    if ((s = make_map(&mv, V, dv, Tk, heads)) != ATTN_OK) return s;
+    if ((s = make_map(&mk, K, d, Tk, heads, false, key_rows)) != ATTN_OK) return s;
+    if ((s = make_map(&mv, V, dv, Tk, heads, false, key_rows)) != ATTN_OK) return s;
     a.tmQ = &mq;
     a.tmK = &mk;
     a.tmV = &mv;
-    e = launch_scored_fwd_bf16(a);
-  } else if (e == cudaSuccess) {
-    e = launch_scored_fwd_simt(a, bf16);
   }
-  if (e == cudaSuccess && a.n_splits > 1) e = launch_scored_merge(a, bf16);
+  if (tokens) {
+    e = launch_scored_tokens_bf16(a);
+  } else if ((e = launch_scored_plan(a.p, a.mask, a.plan, st)) == cudaSuccess) {
+    e = bf16 ? launch_scored_fwd_bf16(a) : launch_scored_fwd_simt(a);
+    if (e == cudaSuccess && a.n_splits > 1) e = launch_scored_merge(a);
+  }
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
@@ -312,7 +329,7 @@ attn_status_t attn_bwd_scored(const void* Q, const void* K, const void* V, const
     a.tmO = &mo;
   }
   e = launch_scored_plan(a.p, ScoredMask{sc.q_pos, sc.key_begin, sc.key_end, sc.causal}, a.plan, st);
-  if (e == cudaSuccess) e = bf16 ? launch_scored_bwd_bf16(a) : launch_scored_bwd_simt(a, false);
+  if (e == cudaSuccess) e = bf16 ? launch_scored_bwd_bf16(a) : launch_scored_bwd_simt(a);
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 

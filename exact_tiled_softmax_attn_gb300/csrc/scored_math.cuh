@@ -49,6 +49,18 @@ inline Cap make_cap(float scale, float softcap) {
   return r;
 }
 
+constexpr int kPosLimit = 1 << 30;
+
+// The keys [lo, hi) token t of batch entry b sees (lo >= hi: none) and its position.
+__device__ __forceinline__ void row_range(const ScoredProblem& p, const ScoredMask& m, int b, int t, int* lo, int* hi,
+                                          int* pos) {
+  const long long at = static_cast<long long>(b) * p.Tq + t;
+  *pos = m.q_pos ? min(max(__ldg(m.q_pos + at), -kPosLimit), kPosLimit) : t;
+  *lo = m.key_begin ? max(__ldg(m.key_begin + at), 0) : 0;
+  *hi = m.key_end ? min(__ldg(m.key_end + at), p.Tk) : p.Tk;
+  if (m.causal) *hi = min(*hi, *pos + 1);
+}
+
 __device__ __forceinline__ float2 dup(float x) { return make_float2(x, x); }
 
 __device__ __forceinline__ float2 cap_poly(float2 s, const Cap& c) {   // the factor of s

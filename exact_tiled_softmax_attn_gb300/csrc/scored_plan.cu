@@ -1,17 +1,14 @@
 // Plan of a scored-attention call: the key range of every packed query row,
 // the hull of the ranges of each 128-row tile, and the row tiles that each
 // 128-key tile meets. Also the merge of partial results over key ranges.
-#include <cuda_bf16.h>
 #include <limits.h>
 #include <math_constants.h>
 
 #include "scored.h"
+#include "scored_math.cuh"
 
 namespace attn {
 namespace scored {
-
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr int kPosLimit = 1 << 30;
 
 // One block per (row tile, batch entry), one thread per row.
 __global__ void __launch_bounds__(kScoredTile) plan_rows_kernel(const ScoredProblem p, const ScoredMask m,
@@ -21,12 +18,7 @@ __global__ void __launch_bounds__(kScoredTile) plan_rows_kernel(const ScoredProb
   const bool valid = row < p.R;
   int lo = INT_MAX, hi = 0, pos = 0;
   if (valid) {
-    const int t = row % p.Tq;
-    const long long at = static_cast<long long>(b) * p.Tq + t;
-    pos = m.q_pos ? min(max(m.q_pos[at], -kPosLimit), kPosLimit) : t;
-    lo = m.key_begin ? max(m.key_begin[at], 0) : 0;
-    hi = m.key_end ? min(m.key_end[at], p.Tk) : p.Tk;
-    if (m.causal) hi = min(hi, pos + 1);
+    row_range(p, m, b, row % p.Tq, &lo, &hi, &pos);
     if (lo >= hi) {
       lo = INT_MAX;
       hi = 0;
@@ -36,7 +28,7 @@ __global__ void __launch_bounds__(kScoredTile) plan_rows_kernel(const ScoredProb
   out.rows[n] = make_int4(lo, hi, pos, 0);
   if (out.slope2 && b == 0)
     for (int k = 0; k < p.Hkv; ++k)
-      out.slope2[static_cast<long long>(k) * p.rpad() + row] = valid ? p.slopes[k * p.G + row / p.Tq] * LOG2E : 0.f;
+      out.slope2[static_cast<long long>(k) * p.rpad() + row] = valid ? p.slopes[k * p.G + row / p.Tq] * kLog2e : 0.f;
   if (out.even) {
     __shared__ int first;
     if (threadIdx.x == 0) first = pos;
@@ -89,9 +81,8 @@ __global__ void __launch_bounds__(128) plan_keys_kernel(const ScoredProblem p, c
 }
 
 // One warp per row; every lane holds the row's weights' sum.
-template <typename T>
 __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ Opart,
-                                                    const float* __restrict__ LSEpart, T* __restrict__ O,
+                                                    const float* __restrict__ LSEpart, float* __restrict__ O,
                                                     float* __restrict__ LSE, long long rows, int dv, int n_splits) {
   const int lane = threadIdx.x & 31;
   const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 5;
@@ -119,7 +110,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ Op
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c)
-    if (lane + 32 * c < dv) O[r * dv + lane + 32 * c] = static_cast<T>(acc[c]);
+    if (lane + 32 * c < dv) O[r * dv + lane + 32 * c] = acc[c];
   if (lane == 0) LSE[r] = lse;
 }
 
@@ -134,15 +125,10 @@ cudaError_t launch_scored_plan(const ScoredProblem& p, const ScoredMask& m, cons
   return cudaGetLastError();
 }
 
-cudaError_t launch_scored_merge(const ScoredFwd& a, bool bf16) {
+cudaError_t launch_scored_merge(const ScoredFwd& a) {
   const long long rows = static_cast<long long>(a.p.B) * a.p.Hkv * a.p.R;
-  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
-  if (bf16)
-    scored::merge_kernel<<<grid, 256, 0, a.stream>>>(a.Opart, a.LSEpart, static_cast<__nv_bfloat16*>(a.O), a.LSE, rows,
-                                                     a.p.dv, a.n_splits);
-  else
-    scored::merge_kernel<<<grid, 256, 0, a.stream>>>(a.Opart, a.LSEpart, static_cast<float*>(a.O), a.LSE, rows,
-                                                     a.p.dv, a.n_splits);
+  scored::merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, a.stream>>>(
+      a.Opart, a.LSEpart, static_cast<float*>(a.O), a.LSE, rows, a.p.dv, a.n_splits);
   return cudaGetLastError();
 }
 

@@ -1,4 +1,4 @@
-// Scored attention on CUDA cores, forward and backward, in fp32 arithmetic.
+// fp32 scored attention on CUDA cores, forward and backward.
 //
 // 64-row by 64-key tiles, 256 threads as 16 x 16, each with a 4 x 4 piece of
 // a score tile and 4 rows by 4 columns per 64 of the accumulators. Per 16
@@ -7,7 +7,6 @@
 // warp reads at one column fall into different banks). Bound by the FMA rate
 // and those reads. Row tiles visit only the key tiles their ranges' hull
 // meets, and key tiles only the row tiles whose hull meets them.
-#include <cuda_bf16.h>
 #include <math_constants.h>
 #include <stdint.h>
 
@@ -24,22 +23,19 @@ struct Pitch {
   static constexpr int v = 64 * NC + 4;
 };
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-
 // 64 rows of `d` elements from row r0 into a tile of pitch 64 * NC + 4, zeros
 // past column d and outside rows [lo, hi).
-template <typename T, int NC>
-__device__ __forceinline__ void load_tile(float* s, const T* g, int r0, int lo, int hi, int d) {
+template <int NC>
+__device__ __forceinline__ void load_tile(float* s, const float* g, int r0, int lo, int hi, int d) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int r = warp; r < 64; r += NT / 32) {
     const int row = r0 + r;
     const bool in = row >= lo && row < hi;
-    const T* src = g + static_cast<long long>(in ? row : 0) * d;
+    const float* src = g + static_cast<long long>(in ? row : 0) * d;
 #pragma unroll
     for (int c = 0; c < 2 * NC; ++c) {
       const int k = lane + 32 * c;
-      s[r * Pitch<NC>::v + k] = (in && k < d) ? to_f(src[k]) : 0.f;
+      s[r * Pitch<NC>::v + k] = (in && k < d) ? src[k] : 0.f;
     }
   }
 }
@@ -125,14 +121,14 @@ __device__ __forceinline__ void acc_cols(float (&acc)[4][4 * NC], const float* w
   }
 }
 
-template <typename T, int NC>
-__device__ __forceinline__ void store_row(T* row, const float (&acc)[4 * NC], float mul, int d) {
+template <int NC>
+__device__ __forceinline__ void store_row(float* row, const float (&acc)[4 * NC], float mul, int d) {
   const int tx = threadIdx.x & 15;
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (4 * tx + 64 * c + e < d) row[4 * tx + 64 * c + e] = static_cast<T>(acc[4 * c + e] * mul);
+      if (4 * tx + 64 * c + e < d) row[4 * tx + 64 * c + e] = acc[4 * c + e] * mul;
 }
 
 // The changed score of raw product x, and its derivative by scale * x.
@@ -177,10 +173,10 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-template <typename T, int NCK, int NCV>
-__global__ void __launch_bounds__(NT) fwd_kernel(const ScoredProblem p, const ScoredPlan plan, const T* __restrict__ Q,
-                                                  const T* __restrict__ K, const T* __restrict__ V,
-                                                  T* __restrict__ O, float* __restrict__ LSE, int n_splits,
+template <int NCK, int NCV>
+__global__ void __launch_bounds__(NT) fwd_kernel(const ScoredProblem p, const ScoredPlan plan, const float* __restrict__ Q,
+                                                  const float* __restrict__ K, const float* __restrict__ V,
+                                                  float* __restrict__ O, float* __restrict__ LSE, int n_splits,
                                                   int split_keys, float* __restrict__ Opart,
                                                   float* __restrict__ LSEpart) {
   extern __shared__ __align__(16) float smem[];
@@ -196,9 +192,9 @@ __global__ void __launch_bounds__(NT) fwd_kernel(const ScoredProblem p, const Sc
   const RowInfo ri = row_info(p, plan, bh, r0);
   const int4 hull = plan.tiles[static_cast<long long>(b) * p.n_rt + r0 / kScoredTile];
   const int k_lo = max(hull.x, split * split_keys), k_hi = min(hull.y, (split + 1) * split_keys);
-  load_tile<T, NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
-  const T* Kh = K + static_cast<long long>(bh) * p.Tk * p.d;
-  const T* Vh = V + static_cast<long long>(bh) * p.Tk * p.dv;
+  load_tile<NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
+  const float* Kh = K + static_cast<long long>(bh) * p.Tk * p.d;
+  const float* Vh = V + static_cast<long long>(bh) * p.Tk * p.dv;
   float acc[4][4 * NCV], m[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -209,8 +205,8 @@ __global__ void __launch_bounds__(NT) fwd_kernel(const ScoredProblem p, const Sc
   }
   for (int k0 = k_lo / BN * BN; k0 < k_hi; k0 += BN) {
     __syncthreads();
-    load_tile<T, NCK>(sK, Kh, k0, k_lo, k_hi, p.d);
-    load_tile<T, NCV>(sV, Vh, k0, k_lo, k_hi, p.dv);
+    load_tile<NCK>(sK, Kh, k0, k_lo, k_hi, p.d);
+    load_tile<NCV>(sV, Vh, k0, k_lo, k_hi, p.dv);
     __syncthreads();
     float x[4][4];
     dot_tile<NCK>(x, sQ, sK, p.d);
@@ -251,21 +247,21 @@ __global__ void __launch_bounds__(NT) fwd_kernel(const ScoredProblem p, const Sc
     const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
     const float lse = l[i] > 0.f ? m[i] + logf(l[i]) : -CUDART_INF_F;
     if (n_splits > 1) {
-      store_row<float, NCV>(Opart + (split * rows + row) * p.dv, acc[i], inv, p.dv);
+      store_row<NCV>(Opart + (split * rows + row) * p.dv, acc[i], inv, p.dv);
       if (tx == 0) LSEpart[split * rows + row] = lse;
     } else {
-      store_row<T, NCV>(O + row * p.dv, acc[i], inv, p.dv);
+      store_row<NCV>(O + row * p.dv, acc[i], inv, p.dv);
       if (tx == 0) LSE[row] = lse;
     }
   }
 }
 
 // dQ of a 64-row tile, and D = rowsum(dO o O) of its rows for the dK/dV kernel.
-template <typename T, int NCK, int NCV>
-__global__ void __launch_bounds__(NT) dq_kernel(const ScoredProblem p, const ScoredPlan plan, const T* __restrict__ Q,
-                                                 const T* __restrict__ K, const T* __restrict__ V,
-                                                 const T* __restrict__ O, const float* __restrict__ LSE,
-                                                 const T* __restrict__ dO, T* __restrict__ dQ,
+template <int NCK, int NCV>
+__global__ void __launch_bounds__(NT) dq_kernel(const ScoredProblem p, const ScoredPlan plan, const float* __restrict__ Q,
+                                                 const float* __restrict__ K, const float* __restrict__ V,
+                                                 const float* __restrict__ O, const float* __restrict__ LSE,
+                                                 const float* __restrict__ dO, float* __restrict__ dQ,
                                                  float* __restrict__ D) {
   extern __shared__ __align__(16) float smem[];
   float* sQ = smem;
@@ -280,9 +276,9 @@ __global__ void __launch_bounds__(NT) dq_kernel(const ScoredProblem p, const Sco
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const RowInfo ri = row_info(p, plan, bh, r0);
   const int4 hull = plan.tiles[static_cast<long long>(b) * p.n_rt + r0 / kScoredTile];
-  load_tile<T, NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
-  load_tile<T, NCV>(sdO, dO + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);
-  load_tile<T, NCV>(sV, O + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);   // O, until the loop
+  load_tile<NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
+  load_tile<NCV>(sdO, dO + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);
+  load_tile<NCV>(sV, O + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);   // O, until the loop
   __syncthreads();
   float lse[4], dd[4], acc[4][4 * NCK];
 #pragma unroll
@@ -298,12 +294,12 @@ __global__ void __launch_bounds__(NT) dq_kernel(const ScoredProblem p, const Sco
 #pragma unroll
     for (int e = 0; e < 4 * NCK; ++e) acc[i][e] = 0.f;
   }
-  const T* Kh = K + static_cast<long long>(bh) * p.Tk * p.d;
-  const T* Vh = V + static_cast<long long>(bh) * p.Tk * p.dv;
+  const float* Kh = K + static_cast<long long>(bh) * p.Tk * p.d;
+  const float* Vh = V + static_cast<long long>(bh) * p.Tk * p.dv;
   for (int k0 = hull.x / BN * BN; k0 < hull.y; k0 += BN) {
     __syncthreads();
-    load_tile<T, NCK>(sK, Kh, k0, hull.x, hull.y, p.d);
-    load_tile<T, NCV>(sV, Vh, k0, hull.x, hull.y, p.dv);
+    load_tile<NCK>(sK, Kh, k0, hull.x, hull.y, p.d);
+    load_tile<NCV>(sV, Vh, k0, hull.x, hull.y, p.dv);
     __syncthreads();
     float x[4][4], y[4][4];
     dot_tile<NCK>(x, sQ, sK, p.d);
@@ -325,16 +321,16 @@ __global__ void __launch_bounds__(NT) dq_kernel(const ScoredProblem p, const Sco
   for (int i = 0; i < 4; ++i) {
     const int r = r0 + 4 * ty + i;
     if (r < p.R)
-      store_row<T, NCK>(dQ + (static_cast<long long>(bh) * p.R + r) * p.d, acc[i], p.scale, p.d);
+      store_row<NCK>(dQ + (static_cast<long long>(bh) * p.R + r) * p.d, acc[i], p.scale, p.d);
   }
 }
 
-template <typename T, int NCK, int NCV>
+template <int NCK, int NCV>
 __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const ScoredPlan plan,
-                                                   const T* __restrict__ Q, const T* __restrict__ K,
-                                                   const T* __restrict__ V, const float* __restrict__ LSE,
-                                                   const T* __restrict__ dO, const float* __restrict__ D,
-                                                   T* __restrict__ dK, T* __restrict__ dV) {
+                                                   const float* __restrict__ Q, const float* __restrict__ K,
+                                                   const float* __restrict__ V, const float* __restrict__ LSE,
+                                                   const float* __restrict__ dO, const float* __restrict__ D,
+                                                   float* __restrict__ dK, float* __restrict__ dV) {
   extern __shared__ __align__(16) float smem[];
   float* sQ = smem;
   float* sK = sQ + BM * Pitch<NCK>::v;
@@ -346,8 +342,8 @@ __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const S
   const int bh = blockIdx.x / nt, k0 = (blockIdx.x - bh * nt) * BN;
   const int b = bh / p.Hkv;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  load_tile<T, NCK>(sK, K + static_cast<long long>(bh) * p.Tk * p.d, k0, 0, p.Tk, p.d);
-  load_tile<T, NCV>(sV, V + static_cast<long long>(bh) * p.Tk * p.dv, k0, 0, p.Tk, p.dv);
+  load_tile<NCK>(sK, K + static_cast<long long>(bh) * p.Tk * p.d, k0, 0, p.Tk, p.d);
+  load_tile<NCV>(sV, V + static_cast<long long>(bh) * p.Tk * p.dv, k0, 0, p.Tk, p.dv);
   float ak[4][4 * NCK], av[4][4 * NCV];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -363,8 +359,8 @@ __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const S
     const int4 hull = plan.tiles[static_cast<long long>(b) * p.n_rt + rt];
     if (hull.x >= k0 + BN || hull.y <= k0) continue;
     __syncthreads();
-    load_tile<T, NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
-    load_tile<T, NCV>(sdO, dO + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);
+    load_tile<NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
+    load_tile<NCV>(sdO, dO + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);
     const RowInfo ri = row_info(p, plan, bh, r0);
     __syncthreads();
     float x[4][4], y[4][4];
@@ -394,65 +390,59 @@ __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const S
   for (int i = 0; i < 4; ++i) {
     const int key = k0 + 4 * ty + i;
     if (key < p.Tk) {
-      store_row<T, NCK>(dK + (static_cast<long long>(bh) * p.Tk + key) * p.d, ak[i], p.scale, p.d);
-      store_row<T, NCV>(dV + (static_cast<long long>(bh) * p.Tk + key) * p.dv, av[i], 1.f, p.dv);
+      store_row<NCK>(dK + (static_cast<long long>(bh) * p.Tk + key) * p.d, ak[i], p.scale, p.d);
+      store_row<NCV>(dV + (static_cast<long long>(bh) * p.Tk + key) * p.dv, av[i], 1.f, p.dv);
     }
   }
 }
 
-template <typename T, int NCK, int NCV>
+template <int NCK, int NCV>
 cudaError_t fwd(const ScoredFwd& a) {
   const ScoredProblem& p = a.p;
   const int smem = (BM * Pitch<NCK>::v + BN * Pitch<NCK>::v + BN * Pitch<NCV>::v + BM * LDP) * 4;
-  auto kern = fwd_kernel<T, NCK, NCV>;
+  auto kern = fwd_kernel<NCK, NCV>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((p.R + BM - 1) / BM * p.B * p.Hkv, a.n_splits);
-  kern<<<grid, NT, smem, a.stream>>>(p, a.plan, static_cast<const T*>(a.Q), static_cast<const T*>(a.K),
-                                     static_cast<const T*>(a.V), static_cast<T*>(a.O), a.LSE, a.n_splits,
+  kern<<<grid, NT, smem, a.stream>>>(p, a.plan, static_cast<const float*>(a.Q), static_cast<const float*>(a.K),
+                                     static_cast<const float*>(a.V), static_cast<float*>(a.O), a.LSE, a.n_splits,
                                      a.split_keys, a.Opart, a.LSEpart);
   return cudaGetLastError();
 }
 
-template <typename T, int NCK, int NCV>
+template <int NCK, int NCV>
 cudaError_t bwd(const ScoredBwd& a) {
   const ScoredProblem& p = a.p;
   const int tiles = 2 * BM * (Pitch<NCK>::v + Pitch<NCV>::v);
   const int smem_q = (tiles + BM * LDP) * 4, smem_kv = (tiles + 2 * BM * LDP) * 4;
-  auto kq = dq_kernel<T, NCK, NCV>;
-  auto kk = dkdv_kernel<T, NCK, NCV>;
+  auto kq = dq_kernel<NCK, NCV>;
+  auto kk = dkdv_kernel<NCK, NCV>;
   cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
   if (e != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv)) != cudaSuccess) return e;
-  const T *Q = static_cast<const T*>(a.Q), *K = static_cast<const T*>(a.K), *V = static_cast<const T*>(a.V),
-          *dO = static_cast<const T*>(a.dO);
-  kq<<<(p.R + BM - 1) / BM * p.B * p.Hkv, NT, smem_q, a.stream>>>(p, a.plan, Q, K, V, static_cast<const T*>(a.O),
-                                                                        a.LSE, dO, static_cast<T*>(a.dQ), a.D);
+  const float *Q = static_cast<const float*>(a.Q), *K = static_cast<const float*>(a.K), *V = static_cast<const float*>(a.V),
+          *dO = static_cast<const float*>(a.dO);
+  kq<<<(p.R + BM - 1) / BM * p.B * p.Hkv, NT, smem_q, a.stream>>>(p, a.plan, Q, K, V, static_cast<const float*>(a.O),
+                                                                        a.LSE, dO, static_cast<float*>(a.dQ), a.D);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   kk<<<(p.Tk + BN - 1) / BN * p.B * p.Hkv, NT, smem_kv, a.stream>>>(p, a.plan, Q, K, V, a.LSE, dO, a.D,
-                                                                          static_cast<T*>(a.dK),
-                                                                          static_cast<T*>(a.dV));
+                                                                          static_cast<float*>(a.dK),
+                                                                          static_cast<float*>(a.dV));
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t fwd_t(const ScoredFwd& a) {
-  if (a.p.d <= 64) return a.p.dv <= 64 ? fwd<T, 1, 1>(a) : fwd<T, 1, 2>(a);
-  return a.p.dv <= 64 ? fwd<T, 2, 1>(a) : fwd<T, 2, 2>(a);
+cudaError_t fwd_any(const ScoredFwd& a) {
+  if (a.p.d <= 64) return a.p.dv <= 64 ? fwd<1, 1>(a) : fwd<1, 2>(a);
+  return a.p.dv <= 64 ? fwd<2, 1>(a) : fwd<2, 2>(a);
 }
-template <typename T>
-cudaError_t bwd_t(const ScoredBwd& a) {
-  if (a.p.d <= 64) return a.p.dv <= 64 ? bwd<T, 1, 1>(a) : bwd<T, 1, 2>(a);
-  return a.p.dv <= 64 ? bwd<T, 2, 1>(a) : bwd<T, 2, 2>(a);
+cudaError_t bwd_any(const ScoredBwd& a) {
+  if (a.p.d <= 64) return a.p.dv <= 64 ? bwd<1, 1>(a) : bwd<1, 2>(a);
+  return a.p.dv <= 64 ? bwd<2, 1>(a) : bwd<2, 2>(a);
 }
 
 }  // namespace scored_simt
 
-cudaError_t launch_scored_fwd_simt(const ScoredFwd& a, bool bf16) {
-  return bf16 ? scored_simt::fwd_t<__nv_bfloat16>(a) : scored_simt::fwd_t<float>(a);
-}
-cudaError_t launch_scored_bwd_simt(const ScoredBwd& a, bool bf16) {
-  return bf16 ? scored_simt::bwd_t<__nv_bfloat16>(a) : scored_simt::bwd_t<float>(a);
-}
+cudaError_t launch_scored_fwd_simt(const ScoredFwd& a) { return scored_simt::fwd_any(a); }
+cudaError_t launch_scored_bwd_simt(const ScoredBwd& a) { return scored_simt::bwd_any(a); }
 
 }  // namespace attn
