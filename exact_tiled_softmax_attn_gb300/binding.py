@@ -12,6 +12,7 @@ is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -346,66 +347,70 @@ def backward(q, k, v, o, lse, do, causal: bool = False, scale: Optional[float] =
     return dq, dk, dvv
 
 
-def _device_of(t):
-    """The CUDA device index of tensor t."""
-    if not t.is_cuda:
+# The current stream's handle without building a torch.cuda.Stream for it (3 us of a small call's 15).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _call_on(index, stream, call):
+    """call(stream handle) with CUDA device `index`, and a stream given for the call, made current, so that what the
+    call allocates belongs to the stream its kernels run on."""
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    return t.device.index
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return call(_raw_stream(index))
+        with torch.cuda.device(index):
+            return call(_raw_stream(index))
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=index)
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
-class _on:
-    """Makes a tensor's device, and a stream given for the call, current, so that what the call allocates belongs to
-    the stream its kernels run on. Costs nothing where both are current already."""
+_workspace_size = functools.lru_cache(maxsize=4096)(
+    lambda fn, *shape: getattr(load_library(), fn)(*shape))   # a rule of the shapes
 
-    def __init__(self, index, stream):
-        self.guards = []
-        if index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(index))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=index)
-            self.guards.append(torch.cuda.stream(stream))
 
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+def _row_array(name, t, rows, dev):
+    """The address of an optional int32 [B, Tq] array of row values."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.shape != rows or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous int32 {list(rows)} tensor on Q's device")
+    return t.data_ptr()
 
 
 def _scored_args(q, k, v, causal, scale, softcap, slopes, q_pos, key_begin, key_end):
-    """Checks shapes, types and devices; (B, H, Hkv, Tq, Tk, d, dv, dtype, scale, AttnScore)."""
-    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+    """Checks shapes, types and devices; (shape arguments, scale, AttnScore, device index)."""
+    qs, ks, vs = q.shape, k.shape, v.shape
+    if len(qs) != 4 or len(ks) != 4 or len(vs) != 4:
         raise ValueError("expected [B, H, T, d] tensors")
-    B, H, Tq, d = q.shape
-    Hkv, Tk, dv = k.shape[1], k.shape[2], v.shape[3]
-    if k.shape != (B, Hkv, Tk, d) or v.shape != (B, Hkv, Tk, dv):
+    B, H, Tq, d = qs
+    _, Hkv, Tk, dv = vs
+    if ks[0] != B or vs[0] != B or ks[1] != Hkv or ks[2] != Tk or ks[3] != d:
         raise ValueError("Q, K, V shapes disagree")
     if Hkv == 0 or H % Hkv:
         raise ValueError("the number of query heads must be a multiple of the number of key heads")
-    dev = q.get_device()
-    for t in (q, k, v):
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-        if t.dtype != q.dtype or t.get_device() != dev:
-            raise ValueError("Q, K and V must have one dtype and device")
-    for name, t in (("q_pos", q_pos), ("key_begin", key_begin), ("key_end", key_end)):
-        if t is not None and (t.dtype != torch.int32 or t.shape != (B, Tq) or not t.is_contiguous() or
-                              t.get_device() != dev):
-            raise ValueError(f"{name} must be a contiguous int32 [B, Tq] tensor on Q's device")
-    if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (H,) or not slopes.is_contiguous() or
-                               slopes.get_device() != dev):
-        raise ValueError("slopes must be a contiguous fp32 [H] tensor on Q's device")
-    score = AttnScore(softcap, int(causal), _ptr(slopes), _ptr(q_pos), _ptr(key_begin), _ptr(key_end))
-    return B, H, Hkv, Tq, Tk, d, dv, _dtype_code(q), 1.0 / math.sqrt(d) if scale is None else float(scale), score
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("tensors must be contiguous")
+    dev, dtype = q.get_device(), q.dtype
+    if k.dtype != dtype or v.dtype != dtype or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("Q, K and V must have one dtype and device")
+    rows = (B, Tq)
+    if slopes is not None:
+        if slopes.dtype != torch.float32 or slopes.shape != (H,) or not slopes.is_contiguous() or \
+                slopes.get_device() != dev:
+            raise ValueError("slopes must be a contiguous fp32 [H] tensor on Q's device")
+        slopes = slopes.data_ptr()
+    score = AttnScore(softcap, 1 if causal else 0, slopes, _row_array("q_pos", q_pos, rows, dev),
+                      _row_array("key_begin", key_begin, rows, dev), _row_array("key_end", key_end, rows, dev))
+    shape = (B, H, Hkv, Tq, Tk, d, dv)
+    return shape, 1.0 / math.sqrt(d) if scale is None else scale, score, _dtype_code(q), dev
 
 
-def _workspace(given, nbytes, like):
-    if given is not None:
-        return given
-    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device)
+def _workspace(given, nbytes, device):
+    return torch.empty(nbytes or 1, dtype=torch.uint8, device=device) if given is None else given
 
 
 def forward_scored(q, k, v, causal: bool = False, scale: Optional[float] = None, softcap: float = 0.0, slopes=None,
@@ -416,31 +421,39 @@ def forward_scored(q, k, v, causal: bool = False, scale: Optional[float] = None,
     |q_pos - key| where slopes ([H] fp32) is given, and limited to keys [key_begin, key_end) of each query row
     (int32 [B, Tq], shared by the heads) and, with causal, to keys at or before q_pos (default: the row index).
     Allocates O, LSE and, unless given, the workspace (uint8, attn_fwd_scored_workspace_size bytes)."""
-    B, H, Hkv, Tq, Tk, d, dv, dt, scale, score = _scored_args(q, k, v, causal, scale, softcap, slopes, q_pos,
-                                                              key_begin, key_end)
-    with _on(_device_of(q), stream):
-        o = torch.empty((B, H, Tq, dv), dtype=q.dtype, device=q.device)
-        lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
-        ws = _workspace(workspace, attn_fwd_scored_workspace_size(B, H, Hkv, Tq, Tk, d, dv, dt), q)
-        attn_fwd_scored(q, k, v, o, lse, B, H, Hkv, Tq, Tk, d, dv, scale, score, dt, ws, ws.numel(), stream)
-    return o, lse
+    shape, scale, score, dt, dev = _scored_args(q, k, v, causal, scale, softcap, slopes, q_pos, key_begin, key_end)
+    B, H, _, Tq, _, _, dv = shape
+
+    def call(handle):
+        device = q.device
+        o = torch.empty((B, H, Tq, dv), dtype=q.dtype, device=device)
+        lse = torch.empty((B, H, Tq), dtype=torch.float32, device=device)
+        ws = _workspace(workspace, _workspace_size("attn_fwd_scored_workspace_size", *shape, dt), device)
+        _check(load_library().attn_fwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                              *shape, scale, score, dt, ws.data_ptr(), ws.numel(), handle),
+               "attn_fwd_scored")
+        return o, lse
+    return _call_on(dev, stream, call)
 
 
 def backward_scored(q, k, v, o, lse, do, causal: bool = False, scale: Optional[float] = None, softcap: float = 0.0,
                     slopes=None, q_pos=None, key_begin=None, key_end=None, stream=None, workspace=None):
     """dQ, dK, dV of forward_scored's O (same arguments; dK and dV summed over the heads that share them)."""
-    B, H, Hkv, Tq, Tk, d, dv, dt, scale, score = _scored_args(q, k, v, causal, scale, softcap, slopes, q_pos,
-                                                              key_begin, key_end)
-    for name, t, shape, dtype in (("O", o, (B, H, Tq, dv), q.dtype), ("dO", do, (B, H, Tq, dv), q.dtype),
-                                  ("LSE", lse, (B, H, Tq), torch.float32)):
-        if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != q.get_device():
-            raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on Q's device")
-    with _on(_device_of(q), stream):
+    shape, scale, score, dt, dev = _scored_args(q, k, v, causal, scale, softcap, slopes, q_pos, key_begin, key_end)
+    B, H, _, Tq, _, _, dv = shape
+    for name, t, want, dtype in (("O", o, (B, H, Tq, dv), q.dtype), ("dO", do, (B, H, Tq, dv), q.dtype),
+                                 ("LSE", lse, (B, H, Tq), torch.float32)):
+        if t.shape != want or t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{name} must be a contiguous {dtype} {list(want)} tensor on Q's device")
+
+    def call(handle):
         dq, dk, dvv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        ws = _workspace(workspace, attn_bwd_scored_workspace_size(B, H, Hkv, Tq, Tk, d, dv, dt), q)
-        attn_bwd_scored(q, k, v, o, lse, do, dq, dk, dvv, B, H, Hkv, Tq, Tk, d, dv, scale, score, dt, ws, ws.numel(),
-                        stream)
-    return dq, dk, dvv
+        ws = _workspace(workspace, _workspace_size("attn_bwd_scored_workspace_size", *shape, dt), q.device)
+        _check(load_library().attn_bwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                              do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dvv.data_ptr(), *shape,
+                                              scale, score, dt, ws.data_ptr(), ws.numel(), handle), "attn_bwd_scored")
+        return dq, dk, dvv
+    return _call_on(dev, stream, call)
 
 
 def rope_plan(rot: int, interleaved: bool = False, theta: float = 10000.0, factor: float = 1.0,
@@ -460,26 +473,32 @@ def rope(q, k, plan: AttnRope, pos=None, inverse: bool = False, out=None, stream
 
     pos: int32 [B, T] positions (default: the token index); inverse turns back, which is the gradient. Returns
     new contiguous tensors, or writes `out` = (q_out, k_out), which may be (q, k) themselves."""
-    if q.dim() != 4 or k.dim() != 4 or q.dtype != k.dtype or q.get_device() != k.get_device():
+    qs, ks = q.shape, k.shape
+    dev, dtype = q.get_device(), q.dtype
+    if len(qs) != 4 or len(ks) != 4 or k.dtype != dtype or k.get_device() != dev:
         raise ValueError("expected two [B, H, T, d] tensors of one dtype and device")
-    B, H, T, d = q.shape
-    Hkv = k.shape[1]
-    if k.shape != (B, Hkv, T, d):
+    B, H, T, d = qs
+    Hkv = ks[1]
+    if ks[0] != B or ks[2] != T or ks[3] != d:
         raise ValueError("Q and K shapes disagree")
-    if pos is not None and (pos.dtype != torch.int32 or pos.shape != (B, T) or not pos.is_contiguous() or
-                            pos.get_device() != q.get_device()):
-        raise ValueError("pos must be a contiguous int32 [B, T] tensor on Q's device")
-    with _on(_device_of(q), stream):
-        if out is None:
-            out = (torch.empty((B, H, T, d), dtype=q.dtype, device=q.device),
-                   torch.empty((B, Hkv, T, d), dtype=q.dtype, device=q.device))
-        strides = []
-        for t, shape in ((q, q.shape), (out[0], q.shape), (k, k.shape), (out[1], k.shape)):
-            if t.shape != shape or t.dtype != q.dtype or t.get_device() != q.get_device():
-                raise ValueError("outputs must have the shapes, dtype and device of Q and K")
-            st = t.stride()
-            if st[3] != 1 and d > 1:
-                raise ValueError("the last dimension must be contiguous")
-            strides += st[:3]
-        attn_rope(plan, q, out[0], k, out[1], strides, pos, B, H, Hkv, T, d, int(inverse), _dtype_code(q), stream)
-    return out
+    where = _row_array("pos", pos, (B, T), dev)
+    q0, q1, q2, q3 = q.stride()
+    k0, k1, k2, k3 = k.stride()
+    if (q3 != 1 or k3 != 1) and d > 1:
+        raise ValueError("the last dimension must be contiguous")
+    if out is None:
+        c = T * d
+        strides = _STRIDES(q0, q1, q2, H * c, c, d, k0, k1, k2, Hkv * c, c, d)
+    else:
+        a, b = out
+        if a.shape != qs or b.shape != ks or a.dtype != dtype or b.dtype != dtype or a.get_device() != dev or \
+                b.get_device() != dev or (d > 1 and (a.stride(3) != 1 or b.stride(3) != 1)):
+            raise ValueError("outputs must have the shapes, dtype and device of Q and K and contiguous rows")
+        strides = _STRIDES(q0, q1, q2, *a.stride()[:3], k0, k1, k2, *b.stride()[:3])
+
+    def call(handle):
+        a, b = out or (torch.empty(qs, dtype=dtype, device=q.device), torch.empty(ks, dtype=dtype, device=q.device))
+        _check(load_library().attn_rope(plan, q.data_ptr(), a.data_ptr(), k.data_ptr(), b.data_ptr(), strides, where,
+                                        B, H, Hkv, T, d, 1 if inverse else 0, _dtype_code(q), handle), "attn_rope")
+        return a, b
+    return _call_on(dev, stream, call)

@@ -439,6 +439,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Two fp32 lanes per instruction (sm_100 and later), each lane rounded as
 // the scalar operation would be: a * b + c and a + b.
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {

@@ -26,7 +26,8 @@ attn_status_t check_scored(int B, int H, int Hkv, int Tq, int Tk, int d, int dv,
   // work units (64-row or 64-key tiles of every head) are counted in int
   const double heads = static_cast<double>(B) * Hkv;
   const double rows = static_cast<double>(H / Hkv) * Tq;
-  if (heads * ((rows > Tk ? rows : Tk) / 64.0 + 2.0) > 2147483647.0) return ATTN_ERR_INVALID_ARG;
+  if (heads * ((rows > Tk ? rows : Tk) / 64.0 + 2.0) > 2147483647.0 || heads * rows > 2147483647.0)
+    return ATTN_ERR_INVALID_ARG;
   if (d > 128 || dv > 128) return ATTN_ERR_UNSUPPORTED;
   if (dt == ATTN_BF16 && (d % 8 || dv % 8)) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
@@ -234,7 +235,7 @@ attn_status_t attn_fwd_scored(const void* Q, const void* K, const void* V, void*
   if (bf16) {
     const int heads = B * Hkv;
     const unsigned key_rows = tokens ? 64u : 128u;
-    if ((s = make_map(&mq, Q, d, a.p.R, heads)) != ATTN_OK) return s;
+    if (!tokens && (s = make_map(&mq, Q, d, a.p.R, heads)) != ATTN_OK) return s;
     if ((s = make_map(&mk, K, d, Tk, heads, false, key_rows)) != ATTN_OK) return s;
     if ((s = make_map(&mv, V, dv, Tk, heads, false, key_rows)) != ATTN_OK) return s;
     a.tmQ = &mq;

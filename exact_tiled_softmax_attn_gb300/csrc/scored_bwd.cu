@@ -40,7 +40,12 @@ using bwd::UnitQueue;
 using bwd::uq_push;
 using bwd::uq_read;
 using scored::Cap;
+using scored::add2;
 using scored::dup;
+using scored::f2;
+using scored::F2;
+using scored::fma2;
+using scored::mul2;
 
 struct Params {
   ScoredProblem p;
@@ -316,6 +321,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     const uint32_t tQ = tmem + lane_off + C::T_Q + (HD / 4) * g, tDO = tmem + lane_off + C::T_DO + (HD / 4) * g;
     ptx::WaitCtx w{abort_flag, P.status, 7u + g};
     const float sc2 = P.sc2, scale = P.p.scale;
+    const scored::CapPoly cap_poly(P.cap);
+    const F2 sc2v = dup(sc2), ninv2 = dup(P.cap.ninv2), one = dup(1.f);
     const int R = P.p.R, d = P.p.d, rpad = P.p.rpad();
     // Stage a unit: this group's half of row r of Q and dO into TMEM, its
     // half of D_r into dpart. Rows past R load as zeros.
@@ -401,11 +408,13 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       const int4 ri = __ldg(P.plan.rows + static_cast<long long>(u.b) * rpad + row);
       const float lse = row_ok ? P.LSE[static_cast<long long>(u.bh) * R + row] : -CUDART_INF_F;
       const float nlse2 = (lse == -CUDART_INF_F) ? -CUDART_INF_F : -lse * scored::kLog2e;
+      const F2 nlv = dup(nlse2);
       float slope2 = 0.f;
       if (BIAS) slope2 = __ldg(P.plan.slope2 + static_cast<long long>(u.bh - u.b * P.p.Hkv) * rpad + row);
       if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dpart_full, u_it & 1u, w)))) break;
       const float* dpu = dpart + (u_it & 1u) * 2 * BT;
       const float dd = dpu[r] + dpu[BT + r];
+      const F2 ndd = dup(-dd);
       if (g == 0) {   // for every row of the padded tile: the dK/dV kernel reads whole 128-row slices
         P.D[static_cast<long long>(u.bh) * rpad + row] = dd;
         P.NL[static_cast<long long>(u.bh) * rpad + row] = nlse2;
@@ -427,44 +436,43 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
           const float* s = reinterpret_cast<const float*>(&v[0][0]);
           bool poly = true;
           if constexpr (CAP) {
-            float amax = 0.f;
+            float hi = s[0], lo = s[0];
 #pragma unroll
-            for (int i = 0; i < 64; i += 2) amax = ptx::fmax3(amax, fabsf(s[i]), fabsf(s[i + 1]));
-            poly = __all_sync(0xffffffffu, amax <= P.cap.limit);
+            for (int i = 0; i < 64; i += 2) {
+              hi = ptx::fmax3(hi, s[i], s[i + 1]);
+              lo = ptx::fmin3(lo, s[i], s[i + 1]);
+            }
+            poly = __all_sync(0xffffffffu, hi <= P.cap.limit && lo >= -P.cap.limit);
           }
           const int dist = kv0 - ri.z;
           const float delta = static_cast<float>(dist);
           const float c1 = dist < 0 ? slope2 : -slope2;
-          const float2 c1v = dup(c1), base = dup(fmaf(c1, delta, nlse2));
+          const F2 c1v = dup(c1), base = dup(fmaf(c1, delta, nlse2));
           bool cross = false;
           if constexpr (BIAS) cross = __any_sync(0xffffffffu, dist < 0 && dist > -63);
           auto tile = [&](auto capped) {   // capped: 0 plain, 1 polynomial, 2 formula
 #pragma unroll
             for (int i = 0; i < 64; i += 2) {
-              const float2 t = make_float2(s[i], s[i + 1]);
-              float2 add = dup(nlse2);
+              const F2 t = f2(s[i], s[i + 1]);
+              F2 add = nlv, p;
               if constexpr (BIAS) {
-                add = ptx::ffma2(make_float2(static_cast<float>(i), static_cast<float>(i + 1)), c1v, base);
+                add = fma2(f2(static_cast<float>(i), static_cast<float>(i + 1)), c1v, base);
                 if (cross)
-                  add = make_float2(fmaf(-slope2, fabsf(delta + static_cast<float>(i)), nlse2),
-                                    fmaf(-slope2, fabsf(delta + static_cast<float>(i + 1)), nlse2));
+                  add = f2(fmaf(-slope2, fabsf(delta + static_cast<float>(i)), nlse2),
+                           fmaf(-slope2, fabsf(delta + static_cast<float>(i + 1)), nlse2));
               }
               if constexpr (decltype(capped)::value == 0) {
-                const float2 e = ptx::ffma2(t, dup(sc2), add);
-                f[i] = ptx::ex2(e.x);
-                f[i + 1] = ptx::ex2(e.y);
+                p = scored::ex2(fma2(t, sc2v, add));
               } else {
-                float2 y;
+                F2 y;
                 if constexpr (decltype(capped)::value == 1)
-                  y = ptx::fmul2(t, scored::cap_poly(t, P.cap));
+                  y = mul2(t, cap_poly(t));
                 else
-                  y = make_float2(scored::cap_any(t.x, P.cap), scored::cap_any(t.y, P.cap));
-                const float2 e = ptx::fadd2(y, add);
-                const float2 grad = ptx::ffma2(ptx::fmul2(y, y), dup(P.cap.ninv2), dup(1.f));
-                const float2 pg = ptx::fmul2(make_float2(ptx::ex2(e.x), ptx::ex2(e.y)), grad);
-                f[i] = pg.x;
-                f[i + 1] = pg.y;
+                  y = scored::cap_any(t, P.cap);
+                p = mul2(scored::ex2(add2(y, add)), fma2(mul2(y, y), ninv2, one));
               }
+              f[i] = p.x;
+              f[i + 1] = p.y;
             }
           };
           if constexpr (!CAP) {
@@ -494,10 +502,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 e = ptx::fadd2(make_float2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])),
-                                        dup(-dd));
-            const float2 rr = ptx::fmul2(make_float2(f[c * 32 + 2 * i], f[c * 32 + 2 * i + 1]), e);
-            pk[i] = ptx::pack_bf16(rr.x, rr.y);
+            const F2 e = add2(f2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])), ndd);
+            pk[i] = scored::pack_bf16(mul2(f2(f[c * 32 + 2 * i], f[c * 32 + 2 * i + 1]), e));
           }
           ptx::tmem_st16(tDP + c * 16, pk);   // over this group's own first columns (already read)
         }
@@ -622,13 +628,6 @@ __device__ __forceinline__ uint32_t transpose32(uint32_t x, int lane) {
     m ^= m << (j >> 1);
   }
   return x;
-}
-
-// The lanes [lo - first, hi - first) of a warp whose lane i stands for key first + i.
-__device__ __forceinline__ uint32_t lane_range(int lo, int hi, int first) {
-  const int a = max(lo - first, 0), b = min(hi - first, 32);
-  if (b <= a) return 0u;
-  return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
 // Warps: 0 producer, 1 MMA, 4-7 and 8-11 P / dS (a thread per key; group h
@@ -903,7 +902,8 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
     const uint32_t tST = tmem + lane_off + T_ST + 64 * h, tDP = tmem + lane_off + T_DP + 64 * h;
     ptx::WaitCtx w{abort_flag, P.status, 3u};
     const float sc2 = P.sc2;
-    const float2 neg1 = dup(-1.f);
+    const F2 sc2v = dup(sc2), ninv2 = dup(P.cap.ninv2), one = dup(1.f), neg1 = dup(-1.f);
+    const scored::CapPoly cap_poly(P.cap);
     uint32_t q_it = 0, ru = 0;
     bool ok = true;
     while (ok) {
@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int4 ri = __ldg(rows + 32 * c + lane);
-            seen[c] = transpose32(lane_range(ri.x, ri.y, key0), lane);
+            seen[c] = transpose32(scored::bit_range(ri.x - key0, ri.y - key0), lane);
           }
         }
         // bias: one slope and consecutive positions for the tile's rows (the
@@ -969,90 +969,92 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
           ptx::tmem_ld_wait(rs[1]);
           bool poly = true;
           if constexpr (CAP) {
-            float amax = 0.f;
+            float hi = __uint_as_float(rs[0][0]), lo = hi;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                amax = ptx::fmax3(amax, fabsf(__uint_as_float(rs[c][i])), fabsf(__uint_as_float(rs[c][i + 1])));
-            poly = __all_sync(0xffffffffu, amax <= P.cap.limit);
+              for (int i = 0; i < 32; i += 2) {
+                hi = ptx::fmax3(hi, __uint_as_float(rs[c][i]), __uint_as_float(rs[c][i + 1]));
+                lo = ptx::fmin3(lo, __uint_as_float(rs[c][i]), __uint_as_float(rs[c][i + 1]));
+              }
+            poly = __all_sync(0xffffffffu, hi <= P.cap.limit && lo >= -P.cap.limit);
           }
           // the distance pos0 - column changes sign inside the tile for some key of the warp
           const bool cross = BIAS && __any_sync(0xffffffffu, pos0 > 0.f && pos0 < 63.f);
           const float c1 = pos0 > 0.f ? -slope2 : slope2;   // -slope2 |pos0 - column| = c1 (pos0 - column)
-          const float2 nc1 = dup(-c1), base = dup(c1 * pos0);
-          auto tile = [&](auto capped, auto masked) {
+          const F2 nc1 = dup(-c1), base = dup(c1 * pos0);
+          auto tile = [&](auto capped, auto distance, auto masked) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               uint32_t pk[16];
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
                 const float4 l4 = ptx::lds128(nlse2 + c * 32 + 2 * i);
-                float2 p2[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                   const int a = 2 * (i + q);   // column within the 32
-                  const float2 t = make_float2(__uint_as_float(rs[c][a]), __uint_as_float(rs[c][a + 1]));
-                  float2 add = q ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
+                  const F2 t = f2(__uint_as_float(rs[c][a]), __uint_as_float(rs[c][a + 1]));
+                  F2 add = q ? f2(l4.z, l4.w) : f2(l4.x, l4.y);
                   if constexpr (BIAS) {
                     const float n0 = static_cast<float>(c * 32 + a), n1 = static_cast<float>(c * 32 + a + 1);
-                    if (even && !cross) {
-                      add = ptx::fadd2(add, ptx::ffma2(make_float2(n0, n1), nc1, base));
-                    } else if (even) {
-                      add = make_float2(fmaf(-slope2, fabsf(pos0 - n0), add.x), fmaf(-slope2, fabsf(pos0 - n1), add.y));
+                    if constexpr (decltype(distance)::value == 0) {
+                      add = add2(add, fma2(f2(n0, n1), nc1, base));
+                    } else if constexpr (decltype(distance)::value == 1) {
+                      add = f2(fmaf(-slope2, fabsf(pos0 - n0), add.x), fmaf(-slope2, fabsf(pos0 - n1), add.y));
                     } else {
                       const int q0 = __shfl_sync(0xffffffffu, __float_as_int(cpos[c]), a),
                                 q1 = __shfl_sync(0xffffffffu, __float_as_int(cpos[c]), a + 1);
                       const float s0 = __shfl_sync(0xffffffffu, cslope[c], a),
                                   s1 = __shfl_sync(0xffffffffu, cslope[c], a + 1);
-                      add = make_float2(fmaf(-s0, fabsf(static_cast<float>(key - q0)), add.x),
-                                        fmaf(-s1, fabsf(static_cast<float>(key - q1)), add.y));
+                      add = f2(fmaf(-s0, fabsf(static_cast<float>(key - q0)), add.x),
+                               fmaf(-s1, fabsf(static_cast<float>(key - q1)), add.y));
                     }
                   }
-                  float2 p, k2;
+                  F2 p, grad;
                   if constexpr (decltype(capped)::value == 0) {
-                    const float2 e = ptx::ffma2(t, dup(sc2), add);
-                    p = make_float2(ptx::ex2(e.x), ptx::ex2(e.y));
+                    p = scored::ex2(fma2(t, sc2v, add));
                   } else {
-                    float2 y;
+                    F2 y;
                     if constexpr (decltype(capped)::value == 1)
-                      y = ptx::fmul2(t, scored::cap_poly(t, P.cap));
+                      y = mul2(t, cap_poly(t));
                     else
-                      y = make_float2(scored::cap_any(t.x, P.cap), scored::cap_any(t.y, P.cap));
-                    const float2 e = ptx::fadd2(y, add);
-                    p = make_float2(ptx::ex2(e.x), ptx::ex2(e.y));
-                    k2 = ptx::ffma2(ptx::fmul2(y, y), dup(P.cap.ninv2), dup(1.f));
+                      y = scored::cap_any(t, P.cap);
+                    p = scored::ex2(add2(y, add));
+                    grad = fma2(mul2(y, y), ninv2, one);
                   }
-                  if constexpr (decltype(masked)::value) {
-                    if (!(seen[c] & (1u << a))) p.x = 0.f;
-                    if (!(seen[c] & (2u << a))) p.y = 0.f;
-                  }
-                  p2[q] = p;
-                  pk[i + q] = ptx::pack_bf16(p.x, p.y);
-                  if constexpr (decltype(capped)::value != 0) {
-                    k2 = ptx::fmul2(p, k2);
-                    keep[c][i + q] = ptx::pack_bf16(k2.x, k2.y);
-                  } else {
+                  if constexpr (decltype(masked)::value)
+                    p = f2(seen[c] & (1u << a) ? p.x : 0.f, seen[c] & (2u << a) ? p.y : 0.f);
+                  pk[i + q] = scored::pack_bf16(p);
+                  if constexpr (decltype(capped)::value != 0)
+                    keep[c][i + q] = scored::pack_bf16(mul2(p, grad));
+                  else
                     keep[c][i + q] = pk[i + q];
-                  }
                 }
               }
               ptx::tmem_st16(tST + c * 16, pk);
             }
           };
+          // (variants of their own where they are frequent; the others mask always)
           auto either = [&](auto capped) {
-            if (partial)
-              tile(capped, std::true_type{});
+            using zero = std::integral_constant<int, 0>;
+            if (BIAS && !even)
+              tile(capped, std::integral_constant<int, BIAS ? 2 : 0>{}, std::true_type{});
+            else if (cross)
+              tile(capped, std::integral_constant<int, BIAS ? 1 : 0>{}, std::true_type{});
+            else if (partial)
+              tile(capped, zero{}, std::true_type{});
             else
-              tile(capped, std::false_type{});
+              tile(capped, zero{}, std::false_type{});
           };
           if constexpr (!CAP) {
             either(std::integral_constant<int, 0>{});
           } else {
             if (poly)
               either(std::integral_constant<int, 1>{});
+            else if (BIAS && !even)
+              tile(std::integral_constant<int, 2>{}, std::integral_constant<int, BIAS ? 2 : 0>{}, std::true_type{});
             else
-              either(std::integral_constant<int, 2>{});
+              tile(std::integral_constant<int, 2>{}, std::integral_constant<int, BIAS ? 1 : 0>{}, std::true_type{});
           }
         }
         ptx::tmem_st_wait();
@@ -1073,16 +1075,14 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               const float4 d4 = ptx::lds128(dd + c * 32 + 2 * i);
-              const float2 pf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&keep[c][i]));
-              const float2 pg = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&keep[c][i + 1]));
-              const float2 e01 = ptx::ffma2(make_float2(d4.x, d4.y), neg1,
-                                            make_float2(__uint_as_float(rd[c][2 * i]), __uint_as_float(rd[c][2 * i + 1])));
-              const float2 e23 = ptx::ffma2(make_float2(d4.z, d4.w), neg1,
-                                            make_float2(__uint_as_float(rd[c][2 * i + 2]),
-                                                        __uint_as_float(rd[c][2 * i + 3])));
-              const float2 s01 = ptx::fmul2(pf, e01), s23 = ptx::fmul2(pg, e23);
-              pk[i] = ptx::pack_bf16(s01.x, s01.y);
-              pk[i + 1] = ptx::pack_bf16(s23.x, s23.y);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                // P T as two floats: a bf16 is the upper half of a float
+                const F2 pt = f2(__uint_as_float(keep[c][i + q] << 16), __uint_as_float(keep[c][i + q] & 0xffff0000u));
+                const F2 e = fma2(q ? f2(d4.z, d4.w) : f2(d4.x, d4.y), neg1,
+                                  f2(__uint_as_float(rd[c][2 * (i + q)]), __uint_as_float(rd[c][2 * (i + q) + 1])));
+                pk[i + q] = scored::pack_bf16(mul2(pt, e));
+              }
             }
             ptx::tmem_st16(tDP + c * 16, pk);
           }

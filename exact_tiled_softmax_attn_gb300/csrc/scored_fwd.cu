@@ -22,6 +22,8 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "bwd_common.cuh"
 #include "common.cuh"
 #include "ptx.cuh"
@@ -35,7 +37,12 @@ using bwd::UnitQueue;
 using bwd::uq_push;
 using bwd::uq_read;
 using scored::Cap;
+using scored::add2;
 using scored::dup;
+using scored::f2;
+using scored::F2;
+using scored::fma2;
+using scored::mul2;
 
 constexpr int BM = 128, BN = 128;
 constexpr int BOX_BYTES = 128 * 64 * 2;
@@ -235,16 +242,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, w));
       };
       uint32_t item = 0, u_it = 0, ru = 0, pp[2] = {0u, 0u};
-      bool ok = true, moved = false;
-      while (ok) {
-        int x;
-        if (!(ok = uq_read(uq, ru, &x, w))) break;
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
-        ++ru;
-        if (x >= P.total) break;
-        const Unit u = load_unit(P, x);
-        if (u.hi == 0) continue;
+      bool moved = false;
+      // the next unit with keys; false at the end (x = P.total) or on a timeout
+      auto next_unit = [&](Unit* u, int* x) {
+        do {
+          if (!uq_read(uq, ru, x, w)) return false;
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+          ++ru;
+          if (*x >= P.total) return true;
+          *u = load_unit(P, *x);
+        } while (u->hi == 0);
+        return true;
+      };
+      int x;
+      Unit u, un;
+      bool ok = next_unit(&u, &x);
+      while (ok && x < P.total) {
         const int n = u.e0 - u.s0;
         if (!(ok = wait(q_full, u_it & 1u))) break;
         if (!(ok = wait(kv_full + slot(item), par(item)))) break;
@@ -261,6 +275,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // each step waits for the next step's tiles while its own MMAs run
         if (!(ok = wait(kv_full + slot(item + 1), par(item + 1)))) break;
         if (n > 1 && !(ok = wait(kv_full + slot(item + 2), par(item + 2)))) break;
+        if (!(ok = next_unit(&un, &x))) break;   // (published before this unit's keys were loaded)
         for (int j = u.s0; j < u.e0; ++j, item += 2) {
           const uint32_t iv = item + 1, ikn = item + 2;   // V_j, K_{j+1}: resident
 #pragma unroll
@@ -291,6 +306,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         if (!ok) break;
         ++u_it;
+        u = un;
       }
       if (!ok) {
         if (ptx::elect_one()) ptx::mma_commit(drain);
@@ -309,28 +325,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t tO = tS + 128;
     ptx::WaitCtx w{abort_flag, P.status, 4u + t};
     const float sc2 = P.sc2;
+    const F2 sc2v = dup(sc2);
+    const scored::CapPoly cap_poly(P.cap);
     const int R = P.p.R, dv = P.p.dv;
     uint32_t sp = 0, op = 0, ru = 0, item = 0;
-    bool ok = true;
-    while (ok) {
+    // A unit as this thread sees it: its row's range and slope with it. The
+    // next one is read before this one's epilogue, which covers the loads.
+    struct Mine {
       int x;
-      if (!(ok = uq_read(uq, ru, &x, w))) break;
+      Unit u;
+      int4 row;
+      float slope2;
+    };
+    auto next_unit = [&](Mine* m) {
+      if (!uq_read(uq, ru, &m->x, w)) return false;
       ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
       ++ru;
-      if (x >= P.total) break;
-      const Unit u = load_unit(P, x);
-      const int rt = 2 * u.qb + t;
-      if (rt >= P.p.n_rt) {
-        item += 2 * (u.e0 - u.s0);
-        continue;
+      if (m->x >= P.total) return true;
+      m->u = load_unit(P, m->x);
+      const int row = (2 * m->u.qb + t) * BM + r;   // (rows up to rpad have entries)
+      if (2 * m->u.qb + t < P.p.n_rt) {
+        m->row = __ldg(P.plan.rows + static_cast<long long>(m->u.b) * P.p.rpad() + row);
+        if (BIAS && row < R)
+          m->slope2 = __ldg(P.p.slopes + (m->u.bh - m->u.b * P.p.Hkv) * P.p.G + row / P.p.Tq) * scored::kLog2e;
       }
+      return true;
+    };
+    Mine me{}, nx{};
+    bool ok = next_unit(&me);
+    while (ok && me.x < P.total) {
+      const Unit& u = me.u;
+      const int rt = 2 * u.qb + t;
+      const bool have = rt < P.p.n_rt;
       const int row = rt * BM + r;
       const bool row_ok = row < R;
-      const int4 ri = __ldg(P.plan.rows + static_cast<long long>(u.b) * P.p.rpad() + row);
+      const int4 ri = me.row;
       const int4 th = t ? u.tile[1] : u.tile[0];
       const int s_t = t ? u.s[1] : u.s[0], e_t = t ? u.e[1] : u.e[0];
-      float slope2 = 0.f;
-      if (BIAS && row_ok) slope2 = __ldg(P.p.slopes + (u.bh - u.b * P.p.Hkv) * P.p.G + row / P.p.Tq) * scored::kLog2e;
+      const float slope2 = me.slope2;
       float m_used = -CUDART_INF_F, l = 0.f;
       for (int j = s_t; j < e_t; ++j) {
         const int kv0 = j * BN;
@@ -338,15 +370,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full + t, sp & 1u, w)))) break;
         ++sp;
         ptx::tc_fence_after();
-        uint32_t raw[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + c * 32, raw[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld_wait(raw[c]);
-        float* s = reinterpret_cast<float*>(&raw[0][0]);
-        // a key of the tile that some row does not see
+        // a key of the tile that some row does not see; bit i of seen[c]:
+        // this row sees key 32 c + i
         const bool partial = kv0 < th.z || kv0 + BN > th.w;
-        const int lo = ri.x - kv0, hi = ri.y - kv0;   // this row sees columns [lo, hi)
+        uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (partial) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) seen[c] = scored::bit_range(ri.x - kv0 - 32 * c, ri.y - kv0 - 32 * c);
+        }
         if (partial && (kv0 < u.lo || kv0 + BN > u.hi)) {
           // the unit's first or last key tile: zero the rows of V that no row sees
           const uint32_t iv = item + 2 * (j - u.s0) + 1;
@@ -360,73 +391,116 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           ptx::fence_proxy_async_smem();
         }
+        float mx;
+        bool poly = true;   // the tile's scores lie inside the cap polynomial's range (those of the whole warp)
+        uint32_t raw[BIAS ? 2 : 4][32];
+        float* s = reinterpret_cast<float*>(&raw[0][0]);
         if constexpr (BIAS) {
-          // the changed scores in log2 units, in place
-          bool poly = true;
-          if constexpr (CAP) {
-            float amax = 0.f;
-#pragma unroll
-            for (int i = 0; i < 128; i += 2) amax = ptx::fmax3(amax, fabsf(s[i]), fabsf(s[i + 1]));
-            poly = __all_sync(0xffffffffu, amax <= P.cap.limit);
-          }
-          // the distance changes sign inside the tile for some row of the warp
+          // The changed scores in log2 units, written back over the raw ones,
+          // 32 at a time. The distance changes sign inside the tile for some
+          // row of the warp (cross), or is linear in the key for all.
           const int dist = kv0 - ri.z;
           const bool cross = __any_sync(0xffffffffu, dist < 0 && dist > -(BN - 1));
           const float delta = static_cast<float>(dist);
           const float c1 = dist < 0 ? slope2 : -slope2;   // -slope2 * |key - pos| = c1 * (key - pos)
-          const float2 c1v = dup(c1), base = dup(c1 * delta);
+          const F2 c1v = dup(c1), base = dup(c1 * delta);
+          float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+          ptx::tmem_ld32(tS, raw[0]);
 #pragma unroll
-          for (int i = 0; i < 128; i += 2) {
-            float2 v = make_float2(s[i], s[i + 1]);
-            float2 b = ptx::ffma2(make_float2(static_cast<float>(i), static_cast<float>(i + 1)), c1v, base);
-            if (cross)
-              b = make_float2(-slope2 * fabsf(delta + static_cast<float>(i)),
-                              -slope2 * fabsf(delta + static_cast<float>(i + 1)));
-            if constexpr (CAP) {
-              if (poly)
-                v = ptx::ffma2(v, scored::cap_poly(v, P.cap), b);
+          for (int c = 0; c < 4; ++c) {
+            ptx::tmem_ld_wait(raw[c & 1]);
+            if (c < 3) ptx::tmem_ld32(tS + 32 * (c + 1), raw[(c + 1) & 1]);
+            float* x = s + 32 * (c & 1);
+            auto biased = [&](auto capped, auto crossing) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float n0 = static_cast<float>(32 * c + i), n1 = static_cast<float>(32 * c + i + 1);
+                F2 v = f2(x[i], x[i + 1]), b;
+                if constexpr (decltype(crossing)::value)
+                  b = f2(-slope2 * fabsf(delta + n0), -slope2 * fabsf(delta + n1));
+                else
+                  b = fma2(f2(n0, n1), c1v, base);
+                if constexpr (decltype(capped)::value == 0)
+                  v = fma2(v, sc2v, b);
+                else if constexpr (decltype(capped)::value == 1)
+                  v = fma2(v, cap_poly(v), b);
+                else
+                  v = add2(scored::cap_any(v, P.cap), b);
+                x[i] = v.x;
+                x[i + 1] = v.y;
+              }
+            };
+            auto either = [&](auto capped) {
+              if (cross)
+                biased(capped, std::true_type{});
               else
-                v = make_float2(scored::cap_any(v.x, P.cap) + b.x, scored::cap_any(v.y, P.cap) + b.y);
+                biased(capped, std::false_type{});
+            };
+            if constexpr (!CAP) {
+              either(std::integral_constant<int, 0>{});
             } else {
-              v = ptx::ffma2(v, dup(sc2), b);
+              float hi = x[0], lo = x[0];   // (min and max in one instruction each; an absolute value takes its own)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                hi = ptx::fmax3(hi, x[i], x[i + 1]);
+                lo = ptx::fmin3(lo, x[i], x[i + 1]);
+              }
+              if (__all_sync(0xffffffffu, hi <= P.cap.limit && lo >= -P.cap.limit))
+                either(std::integral_constant<int, 1>{});
+              else
+                either(std::integral_constant<int, 2>{});
             }
-            s[i] = v.x;
-            s[i + 1] = v.y;
+            if (partial) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(seen[c] & (1u << i))) x[i] = -CUDART_INF_F;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) m4[k] = ptx::fmax3(m4[k], x[i + k], x[i + 4 + k]);
+            ptx::tmem_st32(tS + 32 * c, raw[c & 1]);
           }
-        }
-        if (partial) {
+          mx = ptx::fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+          ptx::tmem_st_wait();
+        } else {
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i < lo || i >= hi) s[i] = -CUDART_INF_F;
-        }
-        float m4[4];
+          for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + c * 32, raw[c]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(s[k], s[k + 4]);
+          for (int c = 0; c < 4; ++c) ptx::tmem_ld_wait(raw[c]);
+          auto max_of = [&] {
+            float m4[4];
 #pragma unroll
-        for (int i = 8; i < 128; i += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m4[k] = ptx::fmax3(m4[k], s[i + k], s[i + 4 + k]);
-        float mx = ptx::fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-        bool poly = true;
-        if constexpr (!BIAS) {
-          if constexpr (CAP) {
-            if (partial) {   // out of the cap's arithmetic; P is set to 0 below
-#pragma unroll
-              for (int i = 0; i < 128; ++i)
-                if (i < lo || i >= hi) s[i] = 0.f;
-            }
-            float a4[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) a4[k] = fmaxf(fabsf(s[k]), fabsf(s[k + 4]));
+            for (int k = 0; k < 4; ++k) m4[k] = fmaxf(s[k], s[k + 4]);
 #pragma unroll
             for (int i = 8; i < 128; i += 8)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) a4[k] = ptx::fmax3(a4[k], fabsf(s[i + k]), fabsf(s[i + 4 + k]));
-            poly = __all_sync(0xffffffffu, ptx::fmax3(a4[0], a4[1], fmaxf(a4[2], a4[3])) <= P.cap.limit);
-            mx = mx == -CUDART_INF_F ? mx : scored::cap_any(mx, P.cap);   // the cap is monotone
-          } else {
-            mx *= sc2;
+              for (int k = 0; k < 4; ++k) m4[k] = ptx::fmax3(m4[k], s[i + k], s[i + 4 + k]);
+            return ptx::fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+          };
+          mx = max_of();
+          if constexpr (CAP) {
+            // (minima and maxima in one instruction each; absolute values would take one of their own)
+            float n4[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) n4[k] = fminf(s[k], s[k + 4]);
+#pragma unroll
+            for (int i = 8; i < 128; i += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) n4[k] = ptx::fmin3(n4[k], s[i + k], s[i + 4 + k]);
+            const float mn = ptx::fmin3(n4[0], n4[1], fminf(n4[2], n4[3]));
+            poly = __all_sync(0xffffffffu, mx <= P.cap.limit && mn >= -P.cap.limit);
           }
+          if (partial) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (!(seen[i / 32] & (1u << (i % 32)))) s[i] = -CUDART_INF_F;
+            mx = max_of();
+          }
+          if constexpr (CAP)
+            mx = mx == -CUDART_INF_F ? mx : scored::cap_any(mx, P.cap);   // the cap is monotone
+          else
+            mx *= sc2;
         }
         const float m_new = fmaxf(m_used, mx);
         bool need = false;
@@ -440,43 +514,58 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           m_used = m_new;
         }
         const float ref = (m_used == -CUDART_INF_F) ? 0.f : m_used;   // no key seen yet
-        float2 ls[4];
+        F2 ls[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
-        // p = 2^(changed score - ref); EXPR gives the exponents of a pair
-        auto exps = [&](auto expr) {
+        for (int k = 0; k < 4; ++k) ls[k] = dup(0.f);
+        const F2 nref = dup(-ref);
+        // p = 2^(changed score - ref) of a chunk's 32 scores; expr gives a pair's exponents
+        auto exps = [&](const float* x, int c, uint32_t bits, auto masked, auto expr) {
+          uint32_t pk[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int a = 64 * h + 2 * i;
-              const float2 e = expr(make_float2(s[a], s[a + 1]));
-              float2 p = make_float2(ptx::ex2(e.x), ptx::ex2(e.y));
-              if (CAP && !BIAS && partial) {
-                if (a < lo || a >= hi) p.x = 0.f;
-                if (a + 1 < lo || a + 1 >= hi) p.y = 0.f;
-              }
-              ls[i & 3] = ptx::fadd2(ls[i & 3], p);
-              pk[i] = ptx::pack_bf16(p.x, p.y);
-            }
-            ptx::tmem_st32(tS + 32 * h, pk);
+          for (int i = 0; i < 16; ++i) {
+            F2 p = scored::ex2(expr(f2(x[2 * i], x[2 * i + 1])));
+            if constexpr (decltype(masked)::value)
+              p = f2(bits & (1u << (2 * i)) ? p.x : 0.f, bits & (2u << (2 * i)) ? p.y : 0.f);
+            ls[i & 3] = add2(ls[i & 3], p);
+            pk[i] = scored::pack_bf16(p);
           }
+          ptx::tmem_st16(tS + 16 * c, pk);
         };
-        const float2 nref = dup(-ref);
-        if constexpr (BIAS) {
-          exps([&](float2 v) { return ptx::fadd2(v, nref); });
-        } else if constexpr (CAP) {
-          if (poly)
-            exps([&](float2 v) { return ptx::ffma2(v, scored::cap_poly(v, P.cap), nref); });
-          else
-            exps([&](float2 v) {
-              return make_float2(scored::cap_any(v.x, P.cap) - ref, scored::cap_any(v.y, P.cap) - ref);
-            });
+        if constexpr (CAP || BIAS) {
+          // What the changes need and a whole row of scores do not fit the
+          // registers together: the scores come from tensor memory once more,
+          // 32 at a time (P overwrites only what has been read).
+          auto again = [&](auto masked, auto expr) {
+            uint32_t x[2][32];
+            ptx::tmem_ld32(tS, x[0]);
+#pragma unroll 1   // (the whole row unrolled misses the instruction cache)
+            for (int c = 0; c < 4; c += 2) {
+              ptx::tmem_ld_wait(x[0]);
+              ptx::tmem_ld32(tS + 32 * (c + 1), x[1]);
+              exps(reinterpret_cast<const float*>(x[0]), c, c ? seen[2] : seen[0], masked, expr);
+              ptx::tmem_ld_wait(x[1]);
+              if (c == 0) ptx::tmem_ld32(tS + 64, x[0]);
+              exps(reinterpret_cast<const float*>(x[1]), c + 1, c ? seen[3] : seen[1], masked, expr);
+            }
+          };
+          // (a variant of its own without masks: a condition per element would
+          // be turned into selects that every tile pays for)
+          if constexpr (BIAS) {
+            again(std::false_type{}, [&](F2 v) { return add2(v, nref); });   // masked as -inf already
+          } else if (poly && !partial) {
+            again(std::false_type{}, [&](F2 v) { return fma2(v, cap_poly(v), nref); });
+          } else if (poly) {
+            again(std::true_type{}, [&](F2 v) { return fma2(v, cap_poly(v), nref); });
+          } else {
+            again(std::true_type{}, [&](F2 v) { return add2(scored::cap_any(v, P.cap), nref); });
+          }
         } else {
-          exps([&](float2 v) { return ptx::ffma2(v, dup(sc2), nref); });
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            exps(s + 32 * c, c, 0u, std::false_type{}, [&](F2 v) { return fma2(v, sc2v, nref); });
         }
-        l += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
+        const F2 lsum = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+        l += lsum.x + lsum.y;
         if (__any_sync(0xffffffffu, need)) {
           // O_t *= corr before the next PV product adds to it; the previous
           // one is complete (issued before the S product just consumed)
@@ -496,7 +585,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
       item += 2 * (u.e0 - u.s0);
+      if (!(ok = next_unit(&nx))) break;
       // ---------------------------------------------------------- epilogue
+      if (!have) {   // an odd number of row tiles
+        me = nx;
+        continue;
+      }
       if (e_t > s_t) {
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(o_full + t, op & 1u, w)))) break;
         ++op;
@@ -525,6 +619,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (row_ok) P.LSE[at] = lse;
       ptx::tc_fence_before();
+      me = nx;
     }
   }
 

@@ -61,14 +61,47 @@ __device__ __forceinline__ void row_range(const ScoredProblem& p, const ScoredMa
   if (m.causal) *hi = min(*hi, *pos + 1);
 }
 
-__device__ __forceinline__ float2 dup(float x) { return make_float2(x, x); }
+// Two fp32 lanes (ptx::ffma2 and its kin).
+using F2 = float2;
+__device__ __forceinline__ F2 f2(float x, float y) { return make_float2(x, y); }
+__device__ __forceinline__ F2 dup(float x) { return make_float2(x, x); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return ptx::ffma2(a, b, c); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) { return ptx::fmul2(a, b); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) { return ptx::fadd2(a, b); }
+__device__ __forceinline__ F2 ex2(F2 a) {
+  return f2(ptx::ex2(a.x), ptx::ex2(a.y));
+}
+__device__ __forceinline__ uint32_t pack_bf16(F2 a) {
+  return ptx::pack_bf16(a.x, a.y);
+}
 
-__device__ __forceinline__ float2 cap_poly(float2 s, const Cap& c) {   // the factor of s
-  const float2 u = ptx::fmul2(s, s);
-  float2 g = ptx::ffma2(dup(c.c[4]), u, dup(c.c[3]));
-  g = ptx::ffma2(g, u, dup(c.c[2]));
-  g = ptx::ffma2(g, u, dup(c.c[1]));
-  return ptx::ffma2(g, u, dup(c.c[0]));
+// The polynomial's value at a pair of scores, the factor of s. Its
+// coefficients are held as register pairs: read as constants they cost two
+// moves per use, more than the arithmetic (1629 instructions per 128 x 32
+// scores, 600 of them moves, before).
+struct CapPoly {
+  F2 c0, c1, c2, c3, c4;
+  __device__ __forceinline__ explicit CapPoly(const Cap& c)
+      : c0(pin(c.c[0])), c1(pin(c.c[1])), c2(pin(c.c[2])), c3(pin(c.c[3])), c4(pin(c.c[4])) {}
+  static __device__ __forceinline__ F2 pin(float x) {
+    F2 r;
+    asm volatile("mov.b32 %0, %2;\n\tmov.b32 %1, %2;" : "=f"(r.x), "=f"(r.y) : "f"(x));
+    return r;
+  }
+  __device__ __forceinline__ F2 operator()(F2 s) const {
+    const F2 u = mul2(s, s);
+    F2 g = fma2(c4, u, c3);
+    g = fma2(g, u, c2);
+    g = fma2(g, u, c1);
+    return fma2(g, u, c0);
+  }
+};
+
+// Bits [lo, hi) of a word, both any integers.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  const int a = max(lo, 0), b = min(hi, 32);
+  if (b <= a) return 0u;
+  return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -80,6 +113,9 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // cap2 * tanh(k s) for any s: -cap2 and cap2 at the infinities.
 __device__ __forceinline__ float cap_any(float s, const Cap& c) {
   return fmaf(-2.f * c.cap2, rcp_approx(1.f + ptx::ex2(s * c.k2)), c.cap2);
+}
+__device__ __forceinline__ F2 cap_any(F2 s, const Cap& c) {
+  return f2(cap_any(s.x, c), cap_any(s.y, c));
 }
 
 }  // namespace scored

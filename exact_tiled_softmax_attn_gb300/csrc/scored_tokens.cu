@@ -473,57 +473,94 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::THREADS, Cfg<HD, RT>::CTAS)
 }
 
 // Rows whose pair is spread over several CTAs: their partial results joined
-// in CTA order. Rows of pairs without a key: zeros. One warp per row.
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params P, int grid) {
-  const int lane = threadIdx.x & 31;
-  const long long n = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+// in a fixed order. Rows of pairs without a key: zeros. One block per row;
+// warp w adds parts w, w + 8, ... (a float4 of the row per lane), so that a
+// row of many parts costs a few loads in a row and not all of them: with one
+// warp per row the join of 38 parts took 29 us, three times the main kernel.
+constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
+constexpr int MAX_GRID = 304;   // CTAs of the main kernel
+
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ Params P, int grid) {
+  __shared__ float weight[MAX_GRID];
+  __shared__ float red[JOIN_WARPS];
+  __shared__ float4 part[JOIN_WARPS][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int R = P.p.R, dv = P.p.dv;
-  if (n >= static_cast<long long>(P.p.B) * P.p.Hkv * R) return;
-  const int bh = static_cast<int>(n / R), r = static_cast<int>(n - static_cast<long long>(bh) * R);
+  const int bh = blockIdx.x / R, r = blockIdx.x - bh * R;
   const int b = bh / P.p.Hkv, h = bh - b * P.p.Hkv;
-  const int total = P.start[P.p.B], s0 = P.start[b], stages = (P.start[b + 1] - s0) / P.p.Hkv;
+  const int total = __ldg(P.start + P.p.B), s0 = __ldg(P.start + b), s1 = __ldg(P.start + b + 1);
+  const long long n = blockIdx.x;
+  const int stages = (s1 - s0) / P.p.Hkv;
   __nv_bfloat16* out = P.O + n * dv;
   if (stages == 0) {
-    for (int c = lane; c < dv; c += 32) out[c] = __float2bfloat16_rn(0.f);
-    if (lane == 0) P.LSE[n] = -CUDART_INF_F;
+    if (tid < dv) out[tid] = __float2bfloat16_rn(0.f);
+    if (tid == 0) P.LSE[n] = -CUDART_INF_F;
     return;
   }
   // CTA c has the stages [c total / grid, (c + 1) total / grid)
   const int x0 = s0 + h * stages, x1 = x0 + stages;
-  const long long g = grid;
-  auto cta_of = [&](int x) {   // the largest c with c total / grid <= x
-    int c = static_cast<int>(static_cast<long long>(x) * g / total);
-    while (c + 1 < grid && (c + 1) * static_cast<long long>(total) / g <= x) ++c;
-    while (c > 0 && c * static_cast<long long>(total) / g > x) --c;
+  const long long g = grid, tot = total;
+  auto begin = [&](int c) { return static_cast<int>(c * tot / g); };
+  auto cta_of = [&](int x) {   // the largest c with begin(c) <= x
+    int c = static_cast<int>(x * g / tot);
+    while (c + 1 < grid && begin(c + 1) <= x) ++c;
     return c;
   };
   const int c0 = cta_of(x0), c1 = cta_of(x1 - 1);
   if (c0 == c1) return;   // written by that CTA
+  const int parts = c1 - c0 + 1;
+  // the pair starts in c0 (its last part) and goes on in the others (their first part)
+  auto at = [&](int i) { return ((c0 + i) * 2LL + (i == 0 ? 1 : 0)) * R + r; };
   float mx = -CUDART_INF_F;
-  for (int c = c0 + lane; c <= c1; c += 32) {
-    const long long begin = c * static_cast<long long>(total) / g, end = (c + 1) * static_cast<long long>(total) / g;
-    if (begin < end) mx = fmaxf(mx, P.LSEpart[(c * 2LL + (x0 < begin ? 0 : 1)) * R + r]);
+  for (int i = tid; i < parts; i += JOIN_THREADS) {
+    const bool some = begin(c0 + i) < begin(c0 + i + 1);   // a CTA without stages wrote nothing
+    const float v = some ? P.LSEpart[at(i)] : -CUDART_INF_F;
+    weight[i] = v;
+    mx = fmaxf(mx, v);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-  if (mx != -CUDART_INF_F) {
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const long long begin = c * static_cast<long long>(total) / g, end = (c + 1) * static_cast<long long>(total) / g;
-      if (begin == end) continue;
-      const long long at = (c * 2LL + (x0 < begin ? 0 : 1)) * R + r;
-      const float w = expf(P.LSEpart[at] - mx);
-      sum += w;
+  if (lane == 0) red[warp] = mx;
+  __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < dv) acc[i] = fmaf(w, P.Opart[at * dv + lane + 32 * i], acc[i]);
+  for (int i = 0; i < JOIN_WARPS; ++i) mx = fmaxf(mx, red[i]);
+  const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  const int col = 4 * lane;
+#pragma unroll 4
+  for (int i = warp; i < parts; i += JOIN_WARPS) {
+    const float w = expf(weight[i] - ref);
+    if (w > 0.f) {
+      sum += w;
+      if (col < dv) {
+        const float4 v = *reinterpret_cast<const float4*>(P.Opart + at(i) * dv + col);
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+      }
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  part[warp][lane] = acc;
+  __syncthreads();   // (red has been read)
+  if (lane == 0) red[warp] = sum;
+  __syncthreads();
+  if (warp > 0) return;
+  sum = red[0];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < dv) out[lane + 32 * i] = __float2bfloat16_rn(acc[i] * inv);
+  for (int i = 1; i < JOIN_WARPS; ++i) {
+    const float4 v = part[i][lane];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+    sum += red[i];
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  if (col < dv)
+    *reinterpret_cast<uint2*>(out + col) =
+        make_uint2(ptx::pack_bf16(acc.x * inv, acc.y * inv), ptx::pack_bf16(acc.z * inv, acc.w * inv));
   if (lane == 0) P.LSE[n] = sum > 0.f ? mx + logf(sum) : -CUDART_INF_F;
 }
 
@@ -531,6 +568,7 @@ template <int HD, int RT>
 cudaError_t launch(const ScoredFwd& a) {
   using C = Cfg<HD, RT>;
   static_assert(C::NST >= 2 && C::SMEM <= 227 * 1024, "shared memory");
+  if (a.n_splits > MAX_GRID) return cudaErrorInvalidValue;
   Params P;
   P.p = a.p;
   P.mask = a.mask;
@@ -549,7 +587,7 @@ cudaError_t launch(const ScoredFwd& a) {
   kern<<<a.n_splits, C::THREADS, C::SMEM, a.stream>>>(*a.tmK, *a.tmV, P);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long rows = static_cast<long long>(a.p.B) * a.p.Hkv * a.p.R;
-  join_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, a.stream>>>(P, a.n_splits);
+  join_kernel<<<static_cast<unsigned>(rows), JOIN_THREADS, 0, a.stream>>>(P, a.n_splits);
   return cudaGetLastError();
 }
 

@@ -126,7 +126,7 @@ def test_nothing_to_do_needs_no_device():
 def test_wrapper_refusals():
     q, k = torch.zeros(1, 4, 8, 64), torch.zeros(1, 2, 8, 64)
     with pytest.raises(ValueError):
-        B.forward_scored(q, k, k)                                # not on a GPU
+        B.forward_scored(q, k, k)   # not on a GPU
     for bad in (dict(q_pos=torch.zeros(1, 8)), dict(key_end=torch.zeros(1, 7, dtype=torch.int32)),
                 dict(slopes=torch.zeros(3)), dict(slopes=torch.zeros(4, dtype=torch.float64)),
                 dict(key_begin=torch.zeros(8, 2, dtype=torch.int32).t()[:1])):
