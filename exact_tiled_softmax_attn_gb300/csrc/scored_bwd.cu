@@ -231,16 +231,23 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       ptx::mma_commit(empty + slot(iv));
     };
     uint32_t item = 0, u_it = 0, sp = 0, ru = 0;
-    bool ok = true, moved = false;
-    while (ok) {
-      int x;
-      if (!(ok = uq_read(uq, ru, &x, w))) break;
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
-      ++ru;
-      if (x >= P.total) break;
-      const int nk = load_unit_q(P, x).nk;
-      if (nk == 0) continue;
+    bool moved = false;
+    // key tiles of the next unit that has any, 0 at the end, -1 on a timeout
+    auto next_unit = [&]() {
+      for (;;) {
+        int x;
+        if (!uq_read(uq, ru, &x, w)) return -1;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+        ++ru;
+        if (x >= P.total) return 0;
+        const int nk = load_unit_q(P, x).nk;
+        if (nk > 0) return nk;
+      }
+    };
+    int nk = next_unit(), nk_next = 0;
+    bool ok = nk >= 0;
+    while (ok && nk > 0) {
       const uint32_t i0 = item;
       // Q and dO are in TMEM: the three staging slots go back to the ring
       if (!(ok = wait(qd_ready, u_it & 1u))) break;
@@ -262,6 +269,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       }
       __syncwarp();
       if (nk > 1 && !(ok = wait(full + slot(i0 + 5), par(i0 + 5)))) break;
+      // (published before this unit's tiles were loaded)
+      nk_next = next_unit();
+      ok = nk_next >= 0;
+      if (!ok) break;
       for (int j = 0; j < nk; ++j, ++sp) {
         const uint32_t ik = i0 + 3 + 2 * j;   // K_j; V_{j+1} = ik + 3, K_{j+1} = ik + 2, K_{j+2} = ik + 4
         if (j + 1 < nk) {
@@ -303,6 +314,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       __syncwarp();
       item = i0 + 3 + 2 * nk;
       ++u_it;
+      nk = nk_next;
     }
     if (!ok) {
       if (ptx::elect_one()) ptx::mma_commit(drain);
@@ -321,7 +333,6 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     const uint32_t tQ = tmem + lane_off + C::T_Q + (HD / 4) * g, tDO = tmem + lane_off + C::T_DO + (HD / 4) * g;
     ptx::WaitCtx w{abort_flag, P.status, 7u + g};
     const float sc2 = P.sc2, scale = P.p.scale;
-    const scored::CapPoly cap_poly(P.cap);
     const F2 sc2v = dup(sc2), ninv2 = dup(P.cap.ninv2), one = dup(1.f);
     const int R = P.p.R, d = P.p.d, rpad = P.p.rpad();
     // Stage a unit: this group's half of row r of Q and dO into TMEM, its
@@ -377,16 +388,29 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     // the CTA's next unit with a key tile: 1, 0 at the end, -1 on a timeout;
     // rows of a unit without one get their results here
     uint32_t ru = 0;
-    auto next_unit = [&](UnitQ* u) {
+    // (with what this thread's row needs: read one unit ahead, so that the
+    // loads' latency does not fall between units)
+    struct Mine {
+      UnitQ u;
+      int4 row;
+      float lse, slope2;
+    };
+    auto next_unit = [&](Mine* m) {
       for (;;) {
         int x;
         if (!uq_read(uq, ru, &x, w)) return -1;
         ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
         ++ru;
         if (x >= P.total) return 0;
+        UnitQ* u = &m->u;
         *u = load_unit_q(P, x);
-        if (u->nk > 0) return 1;
         const int row = u->rt * BT + r;
+        if (u->nk > 0) {
+          m->row = __ldg(P.plan.rows + static_cast<long long>(u->b) * rpad + row);
+          m->lse = row < R ? __ldg(P.LSE + static_cast<long long>(u->bh) * R + row) : -CUDART_INF_F;
+          if (BIAS) m->slope2 = __ldg(P.plan.slope2 + static_cast<long long>(u->bh - u->b * P.p.Hkv) * rpad + row);
+          return 1;
+        }
         if (g == 0) {
           P.D[static_cast<long long>(u->bh) * rpad + row] = 0.f;
           P.NL[static_cast<long long>(u->bh) * rpad + row] = -CUDART_INF_F;
@@ -398,19 +422,22 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       }
     };
     uint32_t item = 0, u_it = 0, sp = 0;
-    UnitQ u, un;
-    const int first = next_unit(&u);
+    Mine me{}, nx{};
+    const int first = next_unit(&me);
     bool have = first == 1;
     bool ok = first >= 0 && (!have || stage(0u, 0u));
     while (ok && have) {
+      const UnitQ& u = me.u;
       const int row = u.rt * BT + r;
       const bool row_ok = row < R;
-      const int4 ri = __ldg(P.plan.rows + static_cast<long long>(u.b) * rpad + row);
-      const float lse = row_ok ? P.LSE[static_cast<long long>(u.bh) * R + row] : -CUDART_INF_F;
+      const int4 ri = me.row;
+      const float lse = me.lse, slope2 = me.slope2;
+      const int more = next_unit(&nx);
+      ok = more >= 0;
+      if (!ok) break;
+      const bool have_next = more == 1;
       const float nlse2 = (lse == -CUDART_INF_F) ? -CUDART_INF_F : -lse * scored::kLog2e;
       const F2 nlv = dup(nlse2);
-      float slope2 = 0.f;
-      if (BIAS) slope2 = __ldg(P.plan.slope2 + static_cast<long long>(u.bh - u.b * P.p.Hkv) * rpad + row);
       if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dpart_full, u_it & 1u, w)))) break;
       const float* dpu = dpart + (u_it & 1u) * 2 * BT;
       const float dd = dpu[r] + dpu[BT + r];
@@ -434,7 +461,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
           ptx::tc_fence_before();
           ptx::mbar_arrive(s_free);
           const float* s = reinterpret_cast<const float*>(&v[0][0]);
-          bool poly = true;
+          int form = 0;   // of the cap
           if constexpr (CAP) {
             float hi = s[0], lo = s[0];
 #pragma unroll
@@ -442,7 +469,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
               hi = ptx::fmax3(hi, s[i], s[i + 1]);
               lo = ptx::fmin3(lo, s[i], s[i + 1]);
             }
-            poly = __all_sync(0xffffffffu, hi <= P.cap.limit && lo >= -P.cap.limit);
+            form = scored::cap_form(P.cap, lo, hi);
           }
           const int dist = kv0 - ri.z;
           const float delta = static_cast<float>(dist);
@@ -450,7 +477,9 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
           const F2 c1v = dup(c1), base = dup(fmaf(c1, delta, nlse2));
           bool cross = false;
           if constexpr (BIAS) cross = __any_sync(0xffffffffu, dist < 0 && dist > -63);
-          auto tile = [&](auto capped) {   // capped: 0 plain, 1 polynomial, 2 formula
+          auto tile = [&](auto capped) {
+            constexpr int kForm = decltype(capped)::value;
+            const scored::CapPoly<kForm == scored::kCapPoly2 ? kForm : scored::kCapPoly4> cap_poly(P.cap);
 #pragma unroll
             for (int i = 0; i < 64; i += 2) {
               const F2 t = f2(s[i], s[i + 1]);
@@ -461,11 +490,11 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                   add = f2(fmaf(-slope2, fabsf(delta + static_cast<float>(i)), nlse2),
                            fmaf(-slope2, fabsf(delta + static_cast<float>(i + 1)), nlse2));
               }
-              if constexpr (decltype(capped)::value == 0) {
+              if constexpr (kForm == 0) {
                 p = scored::ex2(fma2(t, sc2v, add));
               } else {
                 F2 y;
-                if constexpr (decltype(capped)::value == 1)
+                if constexpr (kForm != scored::kCapFormula)
                   y = mul2(t, cap_poly(t));
                 else
                   y = scored::cap_any(t, P.cap);
@@ -478,10 +507,11 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
           if constexpr (!CAP) {
             tile(std::integral_constant<int, 0>{});
           } else {
-            if (poly)
-              tile(std::integral_constant<int, 1>{});
-            else
-              tile(std::integral_constant<int, 2>{});
+            switch (form) {
+              case scored::kCapPoly2: tile(std::integral_constant<int, scored::kCapPoly2>{}); break;
+              case scored::kCapPoly4: tile(std::integral_constant<int, scored::kCapPoly4>{}); break;
+              default: tile(std::integral_constant<int, scored::kCapFormula>{});
+            }
           }
         }
         if (kv0 < u.tile.z || kv0 + 64 > u.tile.w) {
@@ -515,10 +545,6 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       // the next unit's Q and dO go into TMEM now: the products that read
       // this unit's have completed (their results were consumed above)
       const uint32_t i_next = item + 3 + 2 * u.nk;
-      const int nx = next_unit(&un);
-      ok = nx >= 0;
-      if (!ok) break;
-      const bool have_next = nx == 1;
       if (have_next && !(ok = stage(i_next, u_it + 1))) break;
       if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dq_full, u_it & 1u, w)))) break;
       ptx::tc_fence_after();
@@ -547,7 +573,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       item = i_next;
       ++u_it;
       have = have_next;
-      u = un;
+      me = nx;
     }
   }
 
@@ -805,16 +831,23 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, w));
       };
       uint32_t u_it = 0, q_it = 0, pp = 0, ru = 0;
-      bool ok = true, moved = false;
-      while (ok) {
-        int x;
-        if (!(ok = uq_read(uq, ru, &x, w))) break;
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
-        ++ru;
-        if (x >= P.total) break;
-        const int nq = load_unit_kv(P, x).nq;
-        if (nq == 0) continue;
+      bool moved = false;
+      // row tiles of the next unit that has any, 0 at the end, -1 on a timeout
+      auto next_unit = [&]() {
+        for (;;) {
+          int x;
+          if (!uq_read(uq, ru, &x, w)) return -1;
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+          ++ru;
+          if (x >= P.total) return 0;
+          const int n = load_unit_kv(P, x).nq;
+          if (n > 0) return n;
+        }
+      };
+      int nq = next_unit(), nq_next = 0;
+      bool ok = nq >= 0;
+      while (ok && nq > 0) {
         if (!(ok = wait(kv_full, u_it & 1u))) break;
         if (!(ok = wait(q_full + qslot(q_it), qpar(q_it)))) break;
         ptx::tc_fence_after();
@@ -833,6 +866,10 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         }
         __syncwarp();
         if (nq > 1 && !(ok = wait(q_full + qslot(q_it + 1), qpar(q_it + 1)))) break;
+        // (published before this unit's tiles were loaded)
+        nq_next = next_unit();
+        ok = nq_next >= 0;
+        if (!ok) break;
         for (int ii = 0; ii < nq; ++ii) {
           const uint32_t it = q_it + ii;
           const bool more = ii + 1 < nq;
@@ -885,6 +922,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         __syncwarp();
         q_it += nq;
         ++u_it;
+        nq = nq_next;
       }
       if (!ok) {
         if (ptx::elect_one()) ptx::mma_commit(drain);
@@ -903,57 +941,113 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
     ptx::WaitCtx w{abort_flag, P.status, 3u};
     const float sc2 = P.sc2;
     const F2 sc2v = dup(sc2), ninv2 = dup(P.cap.ninv2), one = dup(1.f), neg1 = dup(-1.f);
-    const scored::CapPoly cap_poly(P.cap);
     uint32_t q_it = 0, ru = 0;
-    bool ok = true;
-    while (ok) {
-      int x;
-      if (!(ok = uq_read(uq, ru, &x, w))) break;
-      ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
-      ++ru;
-      if (x >= P.total) break;
-      const UnitKV u = load_unit_kv(P, x);
-      const int key0 = u.kb * BT + quad * 32;   // key of lane 0
-      const int key = key0 + lane;
-      TileList list(u.bits);
-      for (int ii = 0; ii < u.nq; ++ii, ++q_it) {
-        const int rt = list.next();
+    // A walk over the units and their row tiles two tiles ahead of the
+    // arithmetic: what a tile needs from memory (its row tile's hull, and for
+    // a partial tile its rows' ranges) is loaded while earlier ones are worked
+    // on. `Tile` is one step of it; kb < 0: the end.
+    struct Tile {
+      int kb, b, kvh, rt;
+      int4 hull;
+      int even;
+    };
+    UnitKV wu{};
+    TileList wl(nullptr);
+    int wn = 0;
+    auto advance = [&](Tile* t) {   // false on a timeout
+      while (wn == 0) {
+        int x;
+        if (!uq_read(uq, ru, &x, w)) return false;
+        ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+        ++ru;
+        if (x >= P.total) {
+          t->kb = -1;
+          wn = -1;
+          return true;
+        }
+        wu = load_unit_kv(P, x);
+        wl = TileList(wu.bits);
+        wn = wu.nq;
+      }
+      if (wn < 0) {
+        t->kb = -1;
+        return true;
+      }
+      --wn;
+      t->kb = wu.kb;
+      t->b = wu.b;
+      t->kvh = wu.bh - wu.b * P.p.Hkv;
+      t->rt = wl.next();
+      const long long at = static_cast<long long>(wu.b) * P.p.n_rt + t->rt;
+      t->hull = __ldg(P.plan.tiles + at);
+      if constexpr (BIAS) t->even = __ldg(P.plan.even + at);
+      return true;
+    };
+    auto is_partial = [&](const Tile& t) { return t.kb * BT < t.hull.z || t.kb * BT + BT > t.hull.w; };
+    // columns c and 32 + c of this group, for lane c
+    struct Rows {
+      int4 r[2];
+      float slope2[2];
+    };
+    auto load_rows = [&](const Tile& t, Rows* o) {
+      const bool uneven = BIAS && t.even == kScoredUneven;
+      if (!is_partial(t) && !uneven) return;
+      const int4* rows = P.plan.rows + static_cast<long long>(t.b) * rpad + t.rt * BT + 64 * h + lane;
+      o->r[0] = __ldg(rows);
+      o->r[1] = __ldg(rows + 32);
+      if (uneven) {
+        const float* sl = P.plan.slope2 + static_cast<long long>(t.kvh) * rpad + t.rt * BT + 64 * h + lane;
+        o->slope2[0] = __ldg(sl);
+        o->slope2[1] = __ldg(sl + 32);
+      }
+    };
+    Tile cur{}, nxt{};
+    Rows rows{};
+    float slope_cur = 0.f, slope_nxt = 0.f;
+    auto load_slope = [&](const Tile& t) {
+      return t.kb >= 0 ? __ldg(P.plan.slope2 + static_cast<long long>(t.kvh) * rpad + t.rt * BT) : 0.f;
+    };
+    bool ok = advance(&cur);
+    if (ok && cur.kb >= 0) load_rows(cur, &rows);
+    if (BIAS && ok) slope_cur = load_slope(cur);
+    if (ok) ok = advance(&nxt);
+    {
+      while (ok && cur.kb >= 0) {
         const int ls = lslot(q_it);
         const float* nlse2 = sLSE + ls * BT + 64 * h;
         const float* dd = sD + ls * BT + 64 * h;
+        const int key0 = cur.kb * BT + quad * 32;   // key of lane 0
+        const int key = key0 + lane;
         // Which of this warp's keys each of the 64 columns' rows sees, unless
         // all rows see all keys of the tile: bit c of seen[c / 32] for this
         // thread's key.
-        const int4 th = __ldg(P.plan.tiles + static_cast<long long>(u.b) * P.p.n_rt + rt);
-        const bool partial = u.kb * BT < th.z || u.kb * BT + BT > th.w;
+        const bool partial = is_partial(cur);
         uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
-        const int4* rows = P.plan.rows + static_cast<long long>(u.b) * rpad + rt * BT + 64 * h;
         if (partial) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int4 ri = __ldg(rows + 32 * c + lane);
-            seen[c] = transpose32(scored::bit_range(ri.x - key0, ri.y - key0), lane);
-          }
+          for (int c = 0; c < 2; ++c)
+            seen[c] = transpose32(scored::bit_range(rows.r[c].x - key0, rows.r[c].y - key0), lane);
         }
         // bias: one slope and consecutive positions for the tile's rows (the
         // plan says), else each column's own, from lanes c and c + 32
-        float pos0 = 0.f, slope2 = 0.f, cpos[2], cslope[2];
+        float pos0 = 0.f, slope2 = 0.f, cslope[2];
+        int cpos[2];
         bool even = true;
         if constexpr (BIAS) {
-          const float* sl = P.plan.slope2 + static_cast<long long>(u.bh - u.b * P.p.Hkv) * rpad + rt * BT + 64 * h;
-          const int first = __ldg(P.plan.even + static_cast<long long>(u.b) * P.p.n_rt + rt);
-          even = first != kScoredUneven;
-          if (even) {
-            pos0 = static_cast<float>(key - first - 64 * h);   // key - position of column 0
-            slope2 = __ldg(P.plan.slope2 + static_cast<long long>(u.bh - u.b * P.p.Hkv) * rpad + rt * BT);
-          } else {
+          even = cur.even != kScoredUneven;
+          pos0 = even ? static_cast<float>(key - cur.even - 64 * h) : 0.f;   // key - position of column 0
+          slope2 = slope_cur;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              cpos[c] = __int_as_float(__ldg(rows + 32 * c + lane).z);
-              cslope[c] = __ldg(sl + 32 * c + lane);
-            }
+          for (int c = 0; c < 2; ++c) {
+            cpos[c] = rows.r[c].z;
+            cslope[c] = rows.slope2[c];
           }
+          slope_nxt = load_slope(nxt);
         }
+        // the next tile's rows, and the tile after it
+        if (nxt.kb >= 0) load_rows(nxt, &rows);
+        const Tile after = nxt;
+        if (!(ok = advance(&nxt))) break;
         // the staged slices of this tile are visible once l_full completed
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(l_full + ls, lpar(q_it), w)))) break;
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full, q_it & 1u, w)))) break;
@@ -967,7 +1061,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
           ptx::tmem_ld32(tST + 32, rs[1]);
           ptx::tmem_ld_wait(rs[0]);
           ptx::tmem_ld_wait(rs[1]);
-          bool poly = true;
+          int form = 0;   // of the cap
           if constexpr (CAP) {
             float hi = __uint_as_float(rs[0][0]), lo = hi;
 #pragma unroll
@@ -977,13 +1071,15 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
                 hi = ptx::fmax3(hi, __uint_as_float(rs[c][i]), __uint_as_float(rs[c][i + 1]));
                 lo = ptx::fmin3(lo, __uint_as_float(rs[c][i]), __uint_as_float(rs[c][i + 1]));
               }
-            poly = __all_sync(0xffffffffu, hi <= P.cap.limit && lo >= -P.cap.limit);
+            form = scored::cap_form(P.cap, lo, hi);
           }
           // the distance pos0 - column changes sign inside the tile for some key of the warp
           const bool cross = BIAS && __any_sync(0xffffffffu, pos0 > 0.f && pos0 < 63.f);
           const float c1 = pos0 > 0.f ? -slope2 : slope2;   // -slope2 |pos0 - column| = c1 (pos0 - column)
           const F2 nc1 = dup(-c1), base = dup(c1 * pos0);
           auto tile = [&](auto capped, auto distance, auto masked) {
+            constexpr int kForm = decltype(capped)::value;
+            const scored::CapPoly<kForm == scored::kCapPoly2 ? kForm : scored::kCapPoly4> cap_poly(P.cap);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               uint32_t pk[16];
@@ -1002,8 +1098,8 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
                     } else if constexpr (decltype(distance)::value == 1) {
                       add = f2(fmaf(-slope2, fabsf(pos0 - n0), add.x), fmaf(-slope2, fabsf(pos0 - n1), add.y));
                     } else {
-                      const int q0 = __shfl_sync(0xffffffffu, __float_as_int(cpos[c]), a),
-                                q1 = __shfl_sync(0xffffffffu, __float_as_int(cpos[c]), a + 1);
+                      const int q0 = __shfl_sync(0xffffffffu, cpos[c], a),
+                                q1 = __shfl_sync(0xffffffffu, cpos[c], a + 1);
                       const float s0 = __shfl_sync(0xffffffffu, cslope[c], a),
                                   s1 = __shfl_sync(0xffffffffu, cslope[c], a + 1);
                       add = f2(fmaf(-s0, fabsf(static_cast<float>(key - q0)), add.x),
@@ -1011,11 +1107,11 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
                     }
                   }
                   F2 p, grad;
-                  if constexpr (decltype(capped)::value == 0) {
+                  if constexpr (kForm == 0) {
                     p = scored::ex2(fma2(t, sc2v, add));
                   } else {
                     F2 y;
-                    if constexpr (decltype(capped)::value == 1)
+                    if constexpr (kForm != scored::kCapFormula)
                       y = mul2(t, cap_poly(t));
                     else
                       y = scored::cap_any(t, P.cap);
@@ -1025,7 +1121,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
                   if constexpr (decltype(masked)::value)
                     p = f2(seen[c] & (1u << a) ? p.x : 0.f, seen[c] & (2u << a) ? p.y : 0.f);
                   pk[i + q] = scored::pack_bf16(p);
-                  if constexpr (decltype(capped)::value != 0)
+                  if constexpr (kForm != 0)
                     keep[c][i + q] = scored::pack_bf16(mul2(p, grad));
                   else
                     keep[c][i + q] = pk[i + q];
@@ -1049,12 +1145,15 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
           if constexpr (!CAP) {
             either(std::integral_constant<int, 0>{});
           } else {
-            if (poly)
-              either(std::integral_constant<int, 1>{});
+            constexpr int kF = scored::kCapFormula, kUneven = BIAS ? 2 : 0, kAbs = BIAS ? 1 : 0;
+            if (form == scored::kCapPoly2)
+              either(std::integral_constant<int, scored::kCapPoly2>{});
+            else if (form == scored::kCapPoly4)
+              either(std::integral_constant<int, scored::kCapPoly4>{});
             else if (BIAS && !even)
-              tile(std::integral_constant<int, 2>{}, std::integral_constant<int, BIAS ? 2 : 0>{}, std::true_type{});
+              tile(std::integral_constant<int, kF>{}, std::integral_constant<int, kUneven>{}, std::true_type{});
             else
-              tile(std::integral_constant<int, 2>{}, std::integral_constant<int, BIAS ? 1 : 0>{}, std::true_type{});
+              tile(std::integral_constant<int, kF>{}, std::integral_constant<int, kAbs>{}, std::true_type{});
           }
         }
         ptx::tmem_st_wait();
@@ -1091,6 +1190,9 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         ptx::tc_fence_before();
         ptx::mbar_arrive(ds_full);
         ptx::mbar_arrive(l_empty + ls);
+        cur = after;
+        slope_cur = slope_nxt;
+        ++q_it;
       }
     }
   } else {

@@ -326,7 +326,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     ptx::WaitCtx w{abort_flag, P.status, 4u + t};
     const float sc2 = P.sc2;
     const F2 sc2v = dup(sc2);
-    const scored::CapPoly cap_poly(P.cap);
     const int R = P.p.R, dv = P.p.dv;
     uint32_t sp = 0, op = 0, ru = 0, item = 0;
     // A unit as this thread sees it: its row's range and slope with it. The
@@ -392,7 +391,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ptx::fence_proxy_async_smem();
         }
         float mx;
-        bool poly = true;   // the tile's scores lie inside the cap polynomial's range (those of the whole warp)
+        int form = 0;   // of the cap
         uint32_t raw[BIAS ? 2 : 4][32];
         float* s = reinterpret_cast<float*>(&raw[0][0]);
         if constexpr (BIAS) {
@@ -412,6 +411,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (c < 3) ptx::tmem_ld32(tS + 32 * (c + 1), raw[(c + 1) & 1]);
             float* x = s + 32 * (c & 1);
             auto biased = [&](auto capped, auto crossing) {
+              constexpr int form = decltype(capped)::value;
+              const scored::CapPoly<form == scored::kCapPoly2 ? form : scored::kCapPoly4> poly(P.cap);
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
                 const float n0 = static_cast<float>(32 * c + i), n1 = static_cast<float>(32 * c + i + 1);
@@ -420,10 +421,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                   b = f2(-slope2 * fabsf(delta + n0), -slope2 * fabsf(delta + n1));
                 else
                   b = fma2(f2(n0, n1), c1v, base);
-                if constexpr (decltype(capped)::value == 0)
+                if constexpr (form == 0)
                   v = fma2(v, sc2v, b);
-                else if constexpr (decltype(capped)::value == 1)
-                  v = fma2(v, cap_poly(v), b);
+                else if constexpr (form != scored::kCapFormula)
+                  v = fma2(v, poly(v), b);
                 else
                   v = add2(scored::cap_any(v, P.cap), b);
                 x[i] = v.x;
@@ -439,16 +440,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if constexpr (!CAP) {
               either(std::integral_constant<int, 0>{});
             } else {
-              float hi = x[0], lo = x[0];   // (min and max in one instruction each; an absolute value takes its own)
+              float hi = x[0], lo = x[0];   // (minima and maxima in one instruction each)
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
                 hi = ptx::fmax3(hi, x[i], x[i + 1]);
                 lo = ptx::fmin3(lo, x[i], x[i + 1]);
               }
-              if (__all_sync(0xffffffffu, hi <= P.cap.limit && lo >= -P.cap.limit))
-                either(std::integral_constant<int, 1>{});
-              else
-                either(std::integral_constant<int, 2>{});
+              switch (scored::cap_form(P.cap, lo, hi)) {
+                case scored::kCapPoly2: either(std::integral_constant<int, scored::kCapPoly2>{}); break;
+                case scored::kCapPoly4: either(std::integral_constant<int, scored::kCapPoly4>{}); break;
+                default: either(std::integral_constant<int, scored::kCapFormula>{});
+              }
             }
             if (partial) {
 #pragma unroll
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k) n4[k] = ptx::fmin3(n4[k], s[i + k], s[i + 4 + k]);
             const float mn = ptx::fmin3(n4[0], n4[1], fminf(n4[2], n4[3]));
-            poly = __all_sync(0xffffffffu, mx <= P.cap.limit && mn >= -P.cap.limit);
+            form = scored::cap_form(P.cap, mn, mx);
           }
           if (partial) {
 #pragma unroll
@@ -552,10 +554,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           // be turned into selects that every tile pays for)
           if constexpr (BIAS) {
             again(std::false_type{}, [&](F2 v) { return add2(v, nref); });   // masked as -inf already
-          } else if (poly && !partial) {
-            again(std::false_type{}, [&](F2 v) { return fma2(v, cap_poly(v), nref); });
-          } else if (poly) {
-            again(std::true_type{}, [&](F2 v) { return fma2(v, cap_poly(v), nref); });
+          } else if (form == scored::kCapPoly2 && !partial) {
+            const scored::CapPoly<scored::kCapPoly2> poly(P.cap);
+            again(std::false_type{}, [&](F2 v) { return fma2(v, poly(v), nref); });
+          } else if (form != scored::kCapFormula) {
+            const scored::CapPoly<scored::kCapPoly4> poly(P.cap);
+            if (partial)
+              again(std::true_type{}, [&](F2 v) { return fma2(v, poly(v), nref); });
+            else
+              again(std::false_type{}, [&](F2 v) { return fma2(v, poly(v), nref); });
           } else {
             again(std::true_type{}, [&](F2 v) { return add2(scored::cap_any(v, P.cap), nref); });
           }

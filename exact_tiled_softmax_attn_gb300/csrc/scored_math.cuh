@@ -14,39 +14,55 @@ namespace scored {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // y = cap2 * tanh(k s), s the raw product q.k, k = scale / softcap, cap2 =
-// softcap * log2(e). For |k s| <= kPolyMax: s times a polynomial in s^2 with
-// k and cap2 in its coefficients. tanh(x) / x is fitted by a degree-4
-// polynomial in x^2 on |x| <= 0.6 (least squares with Lawson's reweighting);
-// |x * poly - tanh(x)| <= 2.0e-8, 8e-8 as evaluated in fp32, the size of
-// fp32's own rounding there. It costs 6 two-lane FMA-pipe instructions per
-// pair of scores, against 2 special-function instructions a score for the
-// formula 1 - 2 / (1 + e^(2x)) that every other |x| takes. Scores of a
-// trained layer lie well inside the cap, so nearly all tiles take the first.
+// softcap * log2(e). Three forms, chosen per warp and tile by the largest
+// |k s|: s times a polynomial in s^2 that has k and cap2 in its coefficients,
+// of degree 2 up to 0.25 and of degree 4 up to 0.6, and beyond (or where k^8
+// leaves fp32's range) the formula 1 - 2 / (1 + e^(2x)). The polynomials are
+// fits of tanh(x) / x in x^2 (least squares with Lawson's reweighting): |x *
+// poly - tanh(x)| <= 4.9e-8 and 2.0e-8, below 1e-7 as evaluated in fp32, the
+// size of fp32's own rounding. Per pair of scores they cost 4 and 6 two-lane
+// FMA-pipe instructions (2 issue cycles each); the formula costs 2
+// special-function instructions a score more than the uncapped exponential.
+// Scores of a trained layer lie well inside the cap.
 struct Cap {
   float k2;        // 2 k log2(e): e^(2 k s) = 2^(k2 s)
   float cap2;      // softcap * log2(e)
   float ninv2;     // -1 / cap2^2
-  float limit;     // kPolyMax / k, or -1 where k^8 leaves fp32's range
-  float c[5];      // polynomial in s^2
+  float limit2;    // |s| up to which the polynomial of degree 2 holds, or -1
+  float limit4;    // and that of degree 4
+  float c2[3];     // polynomials in s^2
+  float c4[5];
 };
-
-constexpr float kPolyMax = 0.6f;
 
 inline Cap make_cap(float scale, float softcap) {
   Cap r{};
   if (!(softcap > 0.f)) return r;
-  const double c[5] = {0.9999996274092242, -0.333312085910721, 0.13299210221337304, -0.05169674295522158,
-                       0.014976960081731636};
+  const double c2[3] = {0.9999986329868529, -0.3331570156541373, 0.12762232173572735};
+  const double c4[5] = {0.9999996274092242, -0.333312085910721, 0.13299210221337304, -0.05169674295522158,
+                        0.014976960081731636};
   const double k = static_cast<double>(scale) / softcap, cap2 = softcap * 1.4426950408889634;
   const double k2 = 2.0 * k * 1.4426950408889634;
   r.k2 = k2 < 1e30 ? static_cast<float>(k2) : 1e30f;   // (any score but 0 is at the cap there)
   r.cap2 = static_cast<float>(cap2);
   r.ninv2 = static_cast<float>(-1.0 / (cap2 * cap2));
   const double k8 = k * k * k * k * k * k * k * k;
-  r.limit = k8 > 1e-30 && k8 < 1e30 ? static_cast<float>(kPolyMax / k) : -1.f;
+  const bool fits = k8 > 1e-30 && k8 < 1e30;
+  r.limit2 = fits ? static_cast<float>(0.25 / k) : -1.f;
+  r.limit4 = fits ? static_cast<float>(0.6 / k) : -1.f;
   double kk = k * cap2;
-  for (int i = 0; i < 5; ++i, kk *= k * k) r.c[i] = static_cast<float>(c[i] * kk);
+  for (int i = 0; i < 5; ++i, kk *= k * k) {
+    if (i < 3) r.c2[i] = static_cast<float>(c2[i] * kk);
+    r.c4[i] = static_cast<float>(c4[i] * kk);
+  }
   return r;
+}
+
+// Which form a warp takes for scores within [lo, hi] (of this thread).
+enum { kCapPoly2 = 1, kCapPoly4 = 2, kCapFormula = 3 };
+__device__ __forceinline__ int cap_form(const Cap& c, float lo, float hi) {
+  const float a = fmaxf(hi, -lo);
+  if (__all_sync(0xffffffffu, a <= c.limit2)) return kCapPoly2;
+  return __all_sync(0xffffffffu, a <= c.limit4) ? kCapPoly4 : kCapFormula;
 }
 
 constexpr int kPosLimit = 1 << 30;
@@ -75,25 +91,30 @@ __device__ __forceinline__ uint32_t pack_bf16(F2 a) {
   return ptx::pack_bf16(a.x, a.y);
 }
 
-// The polynomial's value at a pair of scores, the factor of s. Its
-// coefficients are held as register pairs: read as constants they cost two
-// moves per use, more than the arithmetic (1629 instructions per 128 x 32
-// scores, 600 of them moves, before).
+// A polynomial's value at a pair of scores, the factor of s. Its coefficients
+// are held as register pairs from the construction on: read as constants they
+// cost two moves per use, more than the arithmetic (1629 instructions per 128
+// x 32 scores, 600 of them moves). Constructed where a tile's form is known,
+// they are live no longer than needed.
+__device__ __forceinline__ F2 pin(float x) {
+  F2 r;
+  asm volatile("mov.b32 %0, %2;\n\tmov.b32 %1, %2;" : "=f"(r.x), "=f"(r.y) : "f"(x));
+  return r;
+}
+template <int FORM>
 struct CapPoly {
-  F2 c0, c1, c2, c3, c4;
-  __device__ __forceinline__ explicit CapPoly(const Cap& c)
-      : c0(pin(c.c[0])), c1(pin(c.c[1])), c2(pin(c.c[2])), c3(pin(c.c[3])), c4(pin(c.c[4])) {}
-  static __device__ __forceinline__ F2 pin(float x) {
-    F2 r;
-    asm volatile("mov.b32 %0, %2;\n\tmov.b32 %1, %2;" : "=f"(r.x), "=f"(r.y) : "f"(x));
-    return r;
+  static constexpr int N = FORM == kCapPoly2 ? 3 : 5;
+  F2 c[N];
+  __device__ __forceinline__ explicit CapPoly(const Cap& cap) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = pin(FORM == kCapPoly2 ? cap.c2[i % 3] : cap.c4[i]);
   }
   __device__ __forceinline__ F2 operator()(F2 s) const {
     const F2 u = mul2(s, s);
-    F2 g = fma2(c4, u, c3);
-    g = fma2(g, u, c2);
-    g = fma2(g, u, c1);
-    return fma2(g, u, c0);
+    F2 g = fma2(c[N - 1], u, c[N - 2]);
+#pragma unroll
+    for (int i = N - 3; i >= 0; --i) g = fma2(g, u, c[i]);
+    return g;
   }
 };
 
