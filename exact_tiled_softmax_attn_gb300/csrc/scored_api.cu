@@ -26,7 +26,8 @@ attn_status_t check_scored(int B, int H, int Hkv, int Tq, int Tk, int d, int dv,
   // work units (64-row or 64-key tiles of every head) are counted in int
   const double heads = static_cast<double>(B) * Hkv;
   const double rows = static_cast<double>(H / Hkv) * Tq;
-  if (heads * ((rows > Tk ? rows : Tk) / 64.0 + 2.0) > 2147483647.0 || heads * rows > 2147483647.0)
+  // (and 128-row tiles with a place for every query head)
+  if (heads * ((rows > Tk ? rows : Tk) / 64.0 + 2.0 + H / Hkv) > 2147483647.0 || heads * rows > 2147483647.0)
     return ATTN_ERR_INVALID_ARG;
   if (d > 128 || dv > 128) return ATTN_ERR_UNSUPPORTED;
   if (dt == ATTN_BF16 && (d % 8 || dv % 8)) return ATTN_ERR_UNSUPPORTED;

@@ -99,8 +99,10 @@ struct UnitQ {
 __device__ __forceinline__ UnitQ load_unit_q(const Params& P, int x) {
   UnitQ u;
   bwd::grouped_unit(x, P.n_blocks, P.p.B * P.p.Hkv, P.group, true, &u.bh, &u.rt);
+  u.rt = scored::packed_block(u.rt, P.n_blocks, P.p.G);
   u.b = u.bh / P.p.Hkv;
-  u.tile = __ldg(P.plan.tiles + static_cast<long long>(u.b) * P.p.n_rt + u.rt);
+  u.tile = u.rt < P.p.n_rt ? __ldg(P.plan.tiles + static_cast<long long>(u.b) * P.p.n_rt + u.rt)
+                           : make_int4(0, 0, 0, 0);
   u.j0 = u.tile.y > 0 ? u.tile.x / BT : 0;
   u.nk = u.tile.y > 0 ? (u.tile.y + BT - 1) / BT - u.j0 : 0;
   return u;
@@ -404,6 +406,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         if (x >= P.total) return 0;
         UnitQ* u = &m->u;
         *u = load_unit_q(P, x);
+        if (u->rt >= P.p.n_rt) continue;
         const int row = u->rt * BT + r;
         if (u->nk > 0) {
           m->row = __ldg(P.plan.rows + static_cast<long long>(u->b) * rpad + row);
@@ -429,7 +432,6 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     while (ok && have) {
       const UnitQ& u = me.u;
       const int row = u.rt * BT + r;
-      const bool row_ok = row < R;
       const int4 ri = me.row;
       const float lse = me.lse, slope2 = me.slope2;
       const int more = next_unit(&nx);
@@ -548,24 +550,26 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       if (have_next && !(ok = stage(i_next, u_it + 1))) break;
       if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dq_full, u_it & 1u, w)))) break;
       ptx::tc_fence_after();
-      __nv_bfloat16* out = P.dQ + (static_cast<long long>(u.bh) * R + (row_ok ? row : 0)) * d;
+      const int row4 = row & ~3;   // (see scored::quad_transpose)
+      __nv_bfloat16* out = P.dQ + (static_cast<long long>(u.bh) * R + row4) * d;
 #pragma unroll
       for (int c = 0; c < HD / 64; ++c) {
         uint32_t v[32];
         ptx::tmem_ld32(tDQ + c * 32, v);
         ptx::tmem_ld_wait(v);
-        if (row_ok) {
+        uint4 pk[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int col = (HD / 2) * g + c * 32 + 8 * e;
-            uint4 a;
-            a.x = ptx::pack_bf16(__uint_as_float(v[8 * e + 0]) * scale, __uint_as_float(v[8 * e + 1]) * scale);
-            a.y = ptx::pack_bf16(__uint_as_float(v[8 * e + 2]) * scale, __uint_as_float(v[8 * e + 3]) * scale);
-            a.z = ptx::pack_bf16(__uint_as_float(v[8 * e + 4]) * scale, __uint_as_float(v[8 * e + 5]) * scale);
-            a.w = ptx::pack_bf16(__uint_as_float(v[8 * e + 6]) * scale, __uint_as_float(v[8 * e + 7]) * scale);
-            if (col < d) *reinterpret_cast<uint4*>(out + col) = a;
-          }
+        for (int e = 0; e < 4; ++e) {
+          pk[e].x = ptx::pack_bf16(__uint_as_float(v[8 * e + 0]) * scale, __uint_as_float(v[8 * e + 1]) * scale);
+          pk[e].y = ptx::pack_bf16(__uint_as_float(v[8 * e + 2]) * scale, __uint_as_float(v[8 * e + 3]) * scale);
+          pk[e].z = ptx::pack_bf16(__uint_as_float(v[8 * e + 4]) * scale, __uint_as_float(v[8 * e + 5]) * scale);
+          pk[e].w = ptx::pack_bf16(__uint_as_float(v[8 * e + 6]) * scale, __uint_as_float(v[8 * e + 7]) * scale);
         }
+        scored::quad_transpose(pk, lane);
+        const int col = (HD / 2) * g + c * 32 + 8 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row4 + i < R && col < d) *reinterpret_cast<uint4*>(out + static_cast<long long>(i) * d + col) = pk[i];
       }
       // (the next unit's first dQ product, which overwrites the accumulator,
       // waits for this group's first dS of that unit, issued after this)
@@ -1229,24 +1233,28 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
       for (int acc = 0; acc < 2; ++acc) {   // dV first, released as soon as it is read, then scale * dK
         const uint32_t tcol = tmem + lane_off + (acc ? T_DK : T_DV);
         const int width = acc ? P.p.d : P.p.dv;
-        __nv_bfloat16* orow = acc ? P.dK + at * width : P.dV + at * width;
+        const int key4 = key & ~3;   // (see scored::quad_transpose)
+        __nv_bfloat16* out = (acc ? P.dK : P.dV) + (static_cast<long long>(u.bh) * Tk + key4) * width;
         const float mul = acc ? scale : 1.0f;
 #pragma unroll
         for (int c = 0; c < HD / 32; ++c) {
           uint32_t v[32];
           ptx::tmem_ld32(tcol + c * 32, v);
           ptx::tmem_ld_wait(v);
-          if (key_ok) {
+          uint4 pk[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint4 a;
-              a.x = ptx::pack_bf16(__uint_as_float(v[8 * e + 0]) * mul, __uint_as_float(v[8 * e + 1]) * mul);
-              a.y = ptx::pack_bf16(__uint_as_float(v[8 * e + 2]) * mul, __uint_as_float(v[8 * e + 3]) * mul);
-              a.z = ptx::pack_bf16(__uint_as_float(v[8 * e + 4]) * mul, __uint_as_float(v[8 * e + 5]) * mul);
-              a.w = ptx::pack_bf16(__uint_as_float(v[8 * e + 6]) * mul, __uint_as_float(v[8 * e + 7]) * mul);
-              if (c * 32 + 8 * e < width) reinterpret_cast<uint4*>(orow + c * 32)[e] = a;
-            }
+          for (int e = 0; e < 4; ++e) {
+            pk[e].x = ptx::pack_bf16(__uint_as_float(v[8 * e + 0]) * mul, __uint_as_float(v[8 * e + 1]) * mul);
+            pk[e].y = ptx::pack_bf16(__uint_as_float(v[8 * e + 2]) * mul, __uint_as_float(v[8 * e + 3]) * mul);
+            pk[e].z = ptx::pack_bf16(__uint_as_float(v[8 * e + 4]) * mul, __uint_as_float(v[8 * e + 5]) * mul);
+            pk[e].w = ptx::pack_bf16(__uint_as_float(v[8 * e + 6]) * mul, __uint_as_float(v[8 * e + 7]) * mul);
           }
+          scored::quad_transpose(pk, lane);
+          const int col = c * 32 + 8 * (lane & 3);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (key4 + i < Tk && col < width)
+              *reinterpret_cast<uint4*>(out + static_cast<long long>(i) * width + col) = pk[i];
         }
         ptx::tc_fence_before();
         ptx::mbar_arrive(acc ? dk_free : dv_free);
@@ -1296,8 +1304,8 @@ cudaError_t launch(const ScoredBwd& a) {
   cudaFuncAttributes fa;
   if ((e = cudaFuncGetAttributes(&fa, kk)) != cudaSuccess) return e;
   if (fa.numRegs != KV_REG_LAUNCH) return cudaErrorInvalidConfiguration;
-  P.n_blocks = p.n_rt;
-  P.total = p.n_rt * heads;
+  P.n_blocks = scored::packed_blocks(p.n_rt, p.G);
+  P.total = P.n_blocks * heads;
   P.group = group(static_cast<size_t>(p.Tk) * (p.d + p.dv) * 2);
   P.counter = a.plan.counters;
   kq<<<P.total < a.num_sms ? P.total : a.num_sms, DQ_THREADS, CfgQ<HD>::SMEM, a.stream>>>(*a.tmQ, *a.tmK, *a.tmV,

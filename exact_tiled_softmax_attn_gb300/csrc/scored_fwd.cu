@@ -91,6 +91,7 @@ struct Unit {
 __device__ __forceinline__ Unit load_unit(const Params& P, int x) {
   Unit u;
   bwd::grouped_unit(x, P.n_pairs, P.p.B * P.p.Hkv, P.group, true, &u.bh, &u.qb);
+  u.qb = scored::packed_block(u.qb, P.n_pairs, P.p.G);
   u.b = u.bh / P.p.Hkv;
   u.lo = 0x7fffffff;
   u.hi = 0;
@@ -328,12 +329,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const F2 sc2v = dup(sc2);
     const int R = P.p.R, dv = P.p.dv;
     uint32_t sp = 0, op = 0, ru = 0, item = 0;
-    // A unit as this thread sees it: its row's range and slope with it. The
-    // next one is read before this one's epilogue, which covers the loads.
+    // A unit as this thread sees it: its row tile's key tiles, its row's range
+    // and slope. The next one is read before this one's epilogue, which
+    // covers the loads.
     struct Mine {
-      int x;
-      Unit u;
-      int4 row;
+      int x, bh, row;              // row: of this thread; n_rt * 128 where the tile does not exist
+      int s0, items;               // the unit's first key tile, its K/V items
+      int s, e;                    // this row tile's key tiles
+      int lo, hi;                  // hull of the unit's keys
+      int all_lo, all_hi;          // keys every row of the tile sees
+      int from, to, pos;           // this row's range and position
       float slope2;
     };
     auto next_unit = [&](Mine* m) {
@@ -341,26 +346,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
       ++ru;
       if (m->x >= P.total) return true;
-      m->u = load_unit(P, m->x);
-      const int row = (2 * m->u.qb + t) * BM + r;   // (rows up to rpad have entries)
-      if (2 * m->u.qb + t < P.p.n_rt) {
-        m->row = __ldg(P.plan.rows + static_cast<long long>(m->u.b) * P.p.rpad() + row);
-        if (BIAS && row < R)
-          m->slope2 = __ldg(P.p.slopes + (m->u.bh - m->u.b * P.p.Hkv) * P.p.G + row / P.p.Tq) * scored::kLog2e;
+      const Unit u = load_unit(P, m->x);
+      m->bh = u.bh;
+      m->s0 = u.s0;
+      m->items = 2 * (u.e0 - u.s0);
+      m->lo = u.lo;
+      m->hi = u.hi;
+      m->s = t ? u.s[1] : u.s[0];
+      m->e = t ? u.e[1] : u.e[0];
+      m->all_lo = t ? u.tile[1].z : u.tile[0].z;
+      m->all_hi = t ? u.tile[1].w : u.tile[0].w;
+      m->row = min(2 * u.qb + t, P.p.n_rt) * BM + r;
+      if (2 * u.qb + t < P.p.n_rt) {
+        const int4 ri = __ldg(P.plan.rows + static_cast<long long>(u.b) * P.p.rpad() + m->row);
+        m->from = ri.x;
+        m->to = ri.y;
+        m->pos = ri.z;
+        if (BIAS && m->row < R)
+          m->slope2 =
+              __ldg(P.p.slopes + (u.bh - u.b * P.p.Hkv) * P.p.G + m->row / P.p.Tq) * scored::kLog2e;
       }
       return true;
     };
     Mine me{}, nx{};
     bool ok = next_unit(&me);
     while (ok && me.x < P.total) {
-      const Unit& u = me.u;
-      const int rt = 2 * u.qb + t;
-      const bool have = rt < P.p.n_rt;
-      const int row = rt * BM + r;
-      const bool row_ok = row < R;
-      const int4 ri = me.row;
-      const int4 th = t ? u.tile[1] : u.tile[0];
-      const int s_t = t ? u.s[1] : u.s[0], e_t = t ? u.e[1] : u.e[0];
+      const int s_t = me.s, e_t = me.e;
       const float slope2 = me.slope2;
       float m_used = -CUDART_INF_F, l = 0.f;
       for (int j = s_t; j < e_t; ++j) {
@@ -369,19 +380,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full + t, sp & 1u, w)))) break;
         ++sp;
         ptx::tc_fence_after();
-        // a key of the tile that some row does not see; bit i of seen[c]:
-        // this row sees key 32 c + i
-        const bool partial = kv0 < th.z || kv0 + BN > th.w;
-        uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-        if (partial) {
+        uint32_t raw[4][32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) seen[c] = scored::bit_range(ri.x - kv0 - 32 * c, ri.y - kv0 - 32 * c);
-        }
-        if (partial && (kv0 < u.lo || kv0 + BN > u.hi)) {
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + c * 32, raw[c]);
+        // a key of the tile that some row does not see
+        const bool partial = kv0 < me.all_lo || kv0 + BN > me.all_hi;
+        if (partial && (kv0 < me.lo || kv0 + BN > me.hi)) {
           // the unit's first or last key tile: zero the rows of V that no row sees
-          const uint32_t iv = item + 2 * (j - u.s0) + 1;
+          const uint32_t iv = item + 2 * (j - me.s0) + 1;
           if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(kv_full + slot(iv), par(iv), w)))) break;
-          if (kv0 + r < u.lo || kv0 + r >= u.hi) {
+          if (kv0 + r < me.lo || kv0 + r >= me.hi) {
             uint4* vr = reinterpret_cast<uint4*>(sKV + slot(iv) * C::TILE + r * 128);
 #pragma unroll
             for (int c = 0; c < C::KB; ++c)
@@ -390,115 +398,94 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           ptx::fence_proxy_async_smem();
         }
-        float mx;
-        int form = 0;   // of the cap
-        uint32_t raw[BIAS ? 2 : 4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld_wait(raw[c]);
         float* s = reinterpret_cast<float*>(&raw[0][0]);
-        if constexpr (BIAS) {
-          // The changed scores in log2 units, written back over the raw ones,
-          // 32 at a time. The distance changes sign inside the tile for some
-          // row of the warp (cross), or is linear in the key for all.
-          const int dist = kv0 - ri.z;
-          const bool cross = __any_sync(0xffffffffu, dist < 0 && dist > -(BN - 1));
-          const float delta = static_cast<float>(dist);
-          const float c1 = dist < 0 ? slope2 : -slope2;   // -slope2 * |key - pos| = c1 * (key - pos)
-          const F2 c1v = dup(c1), base = dup(c1 * delta);
-          float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-          ptx::tmem_ld32(tS, raw[0]);
+        // Maxima of the raw scores, with a bias in groups of 8 keys.
+        constexpr int NG = BIAS ? 16 : 4;
+        float gm[NG];
+        auto maxima = [&] {
+          if constexpr (BIAS) {
+#pragma unroll
+            for (int g = 0; g < 16; ++g)
+              gm[g] = ptx::fmax3(ptx::fmax3(s[8 * g], s[8 * g + 1], s[8 * g + 2]),
+                                 ptx::fmax3(s[8 * g + 3], s[8 * g + 4], s[8 * g + 5]),
+                                 fmaxf(s[8 * g + 6], s[8 * g + 7]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) gm[k] = fmaxf(s[k], s[k + 4]);
+#pragma unroll
+            for (int i = 8; i < 128; i += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) gm[k] = ptx::fmax3(gm[k], s[i + k], s[i + 4 + k]);
+          }
+        };
+        auto all_max = [&] {
+          float m = fmaxf(gm[NG - 2], gm[NG - 1]);
+#pragma unroll
+          for (int g = 0; g < NG - 2; g += 2) m = ptx::fmax3(m, gm[g], gm[g + 1]);
+          return m;
+        };
+        int form = 0;   // of the cap
+        if constexpr (CAP) {
+          // (minima and maxima in one instruction each; absolute values would take one of their own)
+          maxima();
+          float n4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) n4[k] = fminf(s[k], s[k + 4]);
+#pragma unroll
+          for (int i = 8; i < 128; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) n4[k] = ptx::fmin3(n4[k], s[i + k], s[i + 4 + k]);
+          form = scored::cap_form(P.cap, ptx::fmin3(n4[0], n4[1], fminf(n4[2], n4[3])), all_max());
+        }
+        if (partial) {
+          // bit i of a word: this row sees the chunk's key i
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            ptx::tmem_ld_wait(raw[c & 1]);
-            if (c < 3) ptx::tmem_ld32(tS + 32 * (c + 1), raw[(c + 1) & 1]);
-            float* x = s + 32 * (c & 1);
-            auto biased = [&](auto capped, auto crossing) {
-              constexpr int form = decltype(capped)::value;
-              const scored::CapPoly<form == scored::kCapPoly2 ? form : scored::kCapPoly4> poly(P.cap);
+            const uint32_t seen = scored::bit_range(me.from - kv0 - 32 * c, me.to - kv0 - 32 * c);
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float n0 = static_cast<float>(32 * c + i), n1 = static_cast<float>(32 * c + i + 1);
-                F2 v = f2(x[i], x[i + 1]), b;
-                if constexpr (decltype(crossing)::value)
-                  b = f2(-slope2 * fabsf(delta + n0), -slope2 * fabsf(delta + n1));
-                else
-                  b = fma2(f2(n0, n1), c1v, base);
-                if constexpr (form == 0)
-                  v = fma2(v, sc2v, b);
-                else if constexpr (form != scored::kCapFormula)
-                  v = fma2(v, poly(v), b);
-                else
-                  v = add2(scored::cap_any(v, P.cap), b);
-                x[i] = v.x;
-                x[i + 1] = v.y;
-              }
-            };
-            auto either = [&](auto capped) {
-              if (cross)
-                biased(capped, std::true_type{});
-              else
-                biased(capped, std::false_type{});
-            };
-            if constexpr (!CAP) {
-              either(std::integral_constant<int, 0>{});
-            } else {
-              float hi = x[0], lo = x[0];   // (minima and maxima in one instruction each)
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                hi = ptx::fmax3(hi, x[i], x[i + 1]);
-                lo = ptx::fmin3(lo, x[i], x[i + 1]);
-              }
-              switch (scored::cap_form(P.cap, lo, hi)) {
-                case scored::kCapPoly2: either(std::integral_constant<int, scored::kCapPoly2>{}); break;
-                case scored::kCapPoly4: either(std::integral_constant<int, scored::kCapPoly4>{}); break;
-                default: either(std::integral_constant<int, scored::kCapFormula>{});
-              }
-            }
-            if (partial) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(seen[c] & (1u << i))) x[i] = -CUDART_INF_F;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) m4[k] = ptx::fmax3(m4[k], x[i + k], x[i + 4 + k]);
-            ptx::tmem_st32(tS + 32 * c, raw[c & 1]);
+            for (int i = 0; i < 32; ++i)
+              if (!(seen & (1u << i))) s[32 * c + i] = -CUDART_INF_F;
           }
-          mx = ptx::fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-          ptx::tmem_st_wait();
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + c * 32, raw[c]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) ptx::tmem_ld_wait(raw[c]);
-          auto max_of = [&] {
-            float m4[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) m4[k] = fmaxf(s[k], s[k + 4]);
-#pragma unroll
-            for (int i = 8; i < 128; i += 8)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) m4[k] = ptx::fmax3(m4[k], s[i + k], s[i + 4 + k]);
-            return ptx::fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+        }
+        if (!CAP || partial) maxima();
+        // The bias of key i of the tile is c1 * (delta + i) on one side of the
+        // row's position; where it changes sides inside the tile for some row
+        // of the warp (cross) it is -slope2 |delta + i|.
+        const int dist = kv0 - me.pos;
+        const float delta = static_cast<float>(dist);
+        const float c1 = dist < 0 ? slope2 : -slope2;
+        const bool cross = BIAS && __any_sync(0xffffffffu, dist < 0 && dist > -(BN - 1));
+        float mx;
+        if constexpr (BIAS) {
+          // An upper bound of the row's changed scores: per group, its largest
+          // score (the cap is monotone) plus its largest bias. It lies above
+          // the maximum by at most 8 |slope2|, which moves the exponentials
+          // down by so many powers of two and costs no digit; for slopes
+          // above 2.7, where that could reach fp32's range, the maximum
+          // itself is formed.
+          mx = -CUDART_INF_F;
+          auto value = [&](float x) {
+            if constexpr (CAP)
+              return x == -CUDART_INF_F ? x : scored::cap_any(x, P.cap);
+            else
+              return x * sc2;
           };
-          mx = max_of();
-          if constexpr (CAP) {
-            // (minima and maxima in one instruction each; absolute values would take one of their own)
-            float n4[4];
+          if (__all_sync(0xffffffffu, fabsf(slope2) <= 4.f)) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) n4[k] = fminf(s[k], s[k + 4]);
+            for (int g = 0; g < 16; ++g) {
+              // distances of the group's ends; 0 lies between them where their signs differ
+              const float a = delta + static_cast<float>(8 * g), z = a + 7.f;
+              const float near = fmaxf(fmaxf(a, -z), 0.f), far = fmaxf(fabsf(a), fabsf(z));
+              mx = fmaxf(mx, fmaf(-slope2, slope2 > 0.f ? near : far, value(gm[g])));
+            }
+          } else {
 #pragma unroll
-            for (int i = 8; i < 128; i += 8)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) n4[k] = ptx::fmin3(n4[k], s[i + k], s[i + 4 + k]);
-            const float mn = ptx::fmin3(n4[0], n4[1], fminf(n4[2], n4[3]));
-            form = scored::cap_form(P.cap, mn, mx);
+            for (int i = 0; i < 128; ++i) mx = fmaxf(mx, fmaf(-slope2, fabsf(delta + static_cast<float>(i)), value(s[i])));
           }
-          if (partial) {
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (!(seen[i / 32] & (1u << (i % 32)))) s[i] = -CUDART_INF_F;
-            mx = max_of();
-          }
+        } else {
+          mx = all_max();
           if constexpr (CAP)
             mx = mx == -CUDART_INF_F ? mx : scored::cap_any(mx, P.cap);   // the cap is monotone
           else
@@ -520,56 +507,72 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) ls[k] = dup(0.f);
         const F2 nref = dup(-ref);
-        // p = 2^(changed score - ref) of a chunk's 32 scores; expr gives a pair's exponents
-        auto exps = [&](const float* x, int c, uint32_t bits, auto masked, auto expr) {
-          uint32_t pk[16];
+        // p = 2^(changed score - ref), in place of the scores. MASKED: under a
+        // cap the -inf of a masked score does not pass through, so its p is
+        // set; CROSS: the bias by absolute distance.
+        auto exps = [&](auto capped, auto masked, auto crossing) {
+          constexpr int kForm = decltype(capped)::value;
+          constexpr bool kMasked = decltype(masked)::value, kCross = decltype(crossing)::value;
+          const scored::CapPoly<kForm == scored::kCapPoly2 ? kForm : scored::kCapPoly4> poly(P.cap);
+          F2 off[BIAS && !kCross ? 4 : 1];   // c1 * i of a group's pairs
+          if constexpr (BIAS && !kCross) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            F2 p = scored::ex2(expr(f2(x[2 * i], x[2 * i + 1])));
-            if constexpr (decltype(masked)::value)
-              p = f2(bits & (1u << (2 * i)) ? p.x : 0.f, bits & (2u << (2 * i)) ? p.y : 0.f);
-            ls[i & 3] = add2(ls[i & 3], p);
-            pk[i] = scored::pack_bf16(p);
+            for (int k = 0; k < 4; ++k) off[k] = f2(c1 * static_cast<float>(2 * k), c1 * static_cast<float>(2 * k + 1));
           }
-          ptx::tmem_st16(tS + 16 * c, pk);
-        };
-        if constexpr (CAP || BIAS) {
-          // What the changes need and a whole row of scores do not fit the
-          // registers together: the scores come from tensor memory once more,
-          // 32 at a time (P overwrites only what has been read).
-          auto again = [&](auto masked, auto expr) {
-            uint32_t x[2][32];
-            ptx::tmem_ld32(tS, x[0]);
-#pragma unroll 1   // (the whole row unrolled misses the instruction cache)
-            for (int c = 0; c < 4; c += 2) {
-              ptx::tmem_ld_wait(x[0]);
-              ptx::tmem_ld32(tS + 32 * (c + 1), x[1]);
-              exps(reinterpret_cast<const float*>(x[0]), c, c ? seen[2] : seen[0], masked, expr);
-              ptx::tmem_ld_wait(x[1]);
-              if (c == 0) ptx::tmem_ld32(tS + 64, x[0]);
-              exps(reinterpret_cast<const float*>(x[1]), c + 1, c ? seen[3] : seen[1], masked, expr);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+            uint32_t seen = 0xffffffffu;
+            if constexpr (kMasked) seen = scored::bit_range(me.from - kv0 - 32 * c, me.to - kv0 - 32 * c);
+            F2 base = nref;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int n = 32 * c + 2 * i;   // key of the tile
+              if constexpr (BIAS && !kCross) {
+                if (i % 4 == 0) base = dup(fmaf(c1, delta + static_cast<float>(n), -ref));
+              }
+              F2 b = base;
+              if constexpr (BIAS && !kCross) b = add2(off[i % 4], base);
+              if constexpr (BIAS && kCross)
+                b = f2(fmaf(-slope2, fabsf(delta + static_cast<float>(n)), -ref),
+                       fmaf(-slope2, fabsf(delta + static_cast<float>(n + 1)), -ref));
+              const F2 v = f2(s[n], s[n + 1]);
+              F2 x;
+              if constexpr (kForm == 0)
+                x = fma2(v, sc2v, b);
+              else if constexpr (kForm == scored::kCapFormula)
+                x = add2(scored::cap_any(v, P.cap), b);
+              else
+                x = fma2(v, poly(v), b);
+              F2 p = scored::ex2(x);
+              if constexpr (kMasked && CAP)
+                p = f2(seen & (1u << (2 * i)) ? p.x : 0.f, seen & (2u << (2 * i)) ? p.y : 0.f);
+              ls[i & 3] = add2(ls[i & 3], p);
+              pk[i] = scored::pack_bf16(p);
             }
-          };
-          // (a variant of its own without masks: a condition per element would
-          // be turned into selects that every tile pays for)
-          if constexpr (BIAS) {
-            again(std::false_type{}, [&](F2 v) { return add2(v, nref); });   // masked as -inf already
-          } else if (form == scored::kCapPoly2 && !partial) {
-            const scored::CapPoly<scored::kCapPoly2> poly(P.cap);
-            again(std::false_type{}, [&](F2 v) { return fma2(v, poly(v), nref); });
-          } else if (form != scored::kCapFormula) {
-            const scored::CapPoly<scored::kCapPoly4> poly(P.cap);
-            if (partial)
-              again(std::true_type{}, [&](F2 v) { return fma2(v, poly(v), nref); });
-            else
-              again(std::false_type{}, [&](F2 v) { return fma2(v, poly(v), nref); });
-          } else {
-            again(std::true_type{}, [&](F2 v) { return add2(scored::cap_any(v, P.cap), nref); });
+            ptx::tmem_st16(tS + 16 * c, pk);
           }
+        };
+        // (variants of their own where they are frequent: a condition per
+        // element would become selects that every tile pays for)
+        using bias = std::integral_constant<bool, BIAS>;
+        auto either = [&](auto capped) {
+          if (BIAS && cross)
+            exps(capped, std::true_type{}, bias{});
+          else if (CAP && partial)
+            exps(capped, std::true_type{}, std::false_type{});
+          else
+            exps(capped, std::false_type{}, std::false_type{});
+        };
+        if constexpr (!CAP) {
+          either(std::integral_constant<int, 0>{});
         } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            exps(s + 32 * c, c, 0u, std::false_type{}, [&](F2 v) { return fma2(v, sc2v, nref); });
+          if (form == scored::kCapPoly2 && !partial && !(BIAS && cross))
+            exps(std::integral_constant<int, scored::kCapPoly2>{}, std::false_type{}, std::false_type{});
+          else if (form != scored::kCapFormula)
+            either(std::integral_constant<int, scored::kCapPoly4>{});
+          else
+            exps(std::integral_constant<int, scored::kCapFormula>{}, std::true_type{}, bias{});
         }
         const F2 lsum = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
         l += lsum.x + lsum.y;
@@ -591,10 +594,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ptx::mbar_arrive(p_full + t);
       }
       if (!ok) break;
-      item += 2 * (u.e0 - u.s0);
+      item += me.items;
       if (!(ok = next_unit(&nx))) break;
       // ---------------------------------------------------------- epilogue
-      if (!have) {   // an odd number of row tiles
+      if (me.row >= P.p.rpad()) {   // an odd number of row tiles
         me = nx;
         continue;
       }
@@ -605,26 +608,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       const float inv_l = (l > 0.f) ? 1.0f / l : 0.f;
       const float lse = (l > 0.f) ? (m_used + log2f(l)) * 0.69314718055994530942f : -CUDART_INF_F;
-      const long long at = static_cast<long long>(u.bh) * R + (row_ok ? row : 0);
-      __nv_bfloat16* orow = P.O + at * dv;
+      // the four rows of this lane's quad, of which it stores every fourth 16-byte piece
+      const int row4 = me.row & ~3;
+      __nv_bfloat16* out = P.O + (static_cast<long long>(me.bh) * R + row4) * dv;
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
         uint32_t o[32];
         ptx::tmem_ld32(tO + c * 32, o);
         ptx::tmem_ld_wait(o);
-        uint32_t pk[16];
+        uint4 pk[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          pk[i] = l > 0.f ? ptx::pack_bf16(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l)
-                          : 0u;
-        if (row_ok) {
-          uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t v[4];
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (c * 32 + 8 * v < dv) dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+          for (int e = 0; e < 4; ++e)
+            v[e] = l > 0.f ? ptx::pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv_l,
+                                            __uint_as_float(o[8 * i + 2 * e + 1]) * inv_l)
+                           : 0u;
+          pk[i] = make_uint4(v[0], v[1], v[2], v[3]);
         }
+        scored::quad_transpose(pk, lane);
+        const int col = 32 * c + 8 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row4 + i < R && col < dv) *reinterpret_cast<uint4*>(out + static_cast<long long>(i) * dv + col) = pk[i];
       }
-      if (row_ok) P.LSE[at] = lse;
+      if (me.row < R) P.LSE[static_cast<long long>(me.bh) * R + me.row] = lse;
       ptx::tc_fence_before();
       me = nx;
     }
@@ -651,7 +660,7 @@ cudaError_t launch(const ScoredFwd& a) {
   P.sc2 = a.p.scale * scored::kLog2e;
   P.cap = scored::make_cap(a.p.scale, a.p.softcap);
   const int heads = a.p.B * a.p.Hkv;
-  P.n_pairs = (a.p.n_rt + 1) / 2;
+  P.n_pairs = scored::packed_blocks((a.p.n_rt + 1) / 2, a.p.G);
   P.total = P.n_pairs * heads;
   // heads in groups whose keys and values fill about half of L2
   const size_t per_head = static_cast<size_t>(a.p.Tk) * (a.p.d + a.p.dv) * 2;

@@ -65,6 +65,17 @@ __device__ __forceinline__ int cap_form(const Cap& c, float lo, float hi) {
   return __all_sync(0xffffffffu, a <= c.limit4) ? kCapPoly4 : kCapFormula;
 }
 
+// The order of a key head's blocks of packed rows (or pairs of row tiles): a
+// block's length under a causal mask goes by its place within its query head,
+// so the blocks at one place of all G heads follow one another, and a
+// sequence that runs backwards over the numbers gives the longest first. The
+// last head may lack a place: blocks past the last one have nothing to do.
+__host__ __device__ __forceinline__ int packed_blocks(int n, int G) { return (n + G - 1) / G * G; }
+__device__ __forceinline__ int packed_block(int i, int n_padded, int G) {
+  const int per = n_padded / G;
+  return (i % G) * per + i / G;
+}
+
 constexpr int kPosLimit = 1 << 30;
 
 // The keys [lo, hi) token t of batch entry b sees (lo >= hi: none) and its position.
@@ -117,6 +128,28 @@ struct CapPoly {
     return g;
   }
 };
+
+// Piece i of lane q's four 16-byte pieces of its row for piece q of row i of
+// its quad: rows of a warp, one per lane, then go to memory as 64 contiguous
+// bytes per row and instruction. As 16 bytes per row, 32 rows at a time, the
+// stores took a 128-row tile of 256-byte rows about 5000 cycles.
+__device__ __forceinline__ void quad_transpose(uint4 (&v)[4], int lane) {
+#pragma unroll
+  for (int step = 1; step <= 2; step *= 2) {
+    const bool up = lane & step;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & step) continue;
+      uint32_t* a = reinterpret_cast<uint32_t*>(&v[i]);
+      uint32_t* b = reinterpret_cast<uint32_t*>(&v[i + step]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {   // the piece that belongs to the other lane crosses over
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a[e] : b[e], step);
+        if (up) a[e] = got; else b[e] = got;
+      }
+    }
+  }
+}
 
 // Bits [lo, hi) of a word, both any integers.
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
