@@ -9,7 +9,10 @@
 // and so computes each sine and cosine once for all of them; the rest of a
 // head (from rot on) is copied in chunks of its own. Bound by memory: every
 // element is read and written once, in 16-byte accesses where rows, strides
-// and pointers allow.
+// and pointers allow. What a load waits for must not hold the next one back
+// (a store in between may be to the same memory, so the compiler keeps the
+// order): four heads ahead are copied to the thread's own slots in shared
+// memory, which costs no registers.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -56,14 +59,30 @@ __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+constexpr int STAGES = 4;   // heads a thread has in flight
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {   // all but the last N groups of this thread
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // V pairs (or V copied elements) a chunk; INTER: the pairs of a chunk are 2 V
 // adjacent elements, otherwise V elements at i and V at i + rot / 2.
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ Params P) {
   using W = Vec<T, V>;
+  constexpr bool WIDE = sizeof(W) == 16;
+  __shared__ __align__(16) W stage[WIDE ? STAGES : 1][2][WIDE ? NT : 1];
   const int per_token = P.slots * P.chunks;
   const long long tokens = static_cast<long long>(P.B) * P.T;
   const int n = P.tokens_per_block * per_token;
+  const int total = P.heads[0] + P.heads[1];
   for (int i = threadIdx.x; i < n; i += NT) {
     const int tok = i / per_token, rest = i - tok * per_token;
     const int slot = rest / P.chunks, c = rest - slot * P.chunks;
@@ -71,12 +90,35 @@ __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ Params
     if (bt >= tokens) return;
     const int b = static_cast<int>(bt / P.T), t = static_cast<int>(bt - static_cast<long long>(b) * P.T);
     const bool turn = c < P.rot_chunks;
-    int o0, o1;   // the chunk's two places in a row
+    // the chunk's two places in a row
+    const int o0 = !turn ? P.plan.rot + V * (c - P.rot_chunks) : INTER ? 2 * V * c : V * c;
+    const int o1 = !turn ? o0 : INTER ? o0 + V : o0 + P.plan.rot / 2;
+    const long long pos = !turn ? 0 : P.pos ? P.pos[bt] : t;
+    // this token's rows of head 0, less the heads before K's for K
+    const T* x[2];
+    T* y[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      x[k] = static_cast<const T*>(P.x[k]) + b * P.xs[k].b + t * P.xs[k].t - (k ? P.heads[0] * P.xs[k].h : 0);
+      y[k] = static_cast<T*>(P.y[k]) + b * P.ys[k].b + t * P.ys[k].t - (k ? P.heads[0] * P.ys[k].h : 0);
+    }
+    auto row = [&](int h) { return h < P.heads[0] ? x[0] + h * P.xs[0].h : x[1] + h * P.xs[1].h; };
+    auto fetch = [&](int h, int s) {
+      if constexpr (WIDE) {
+        if (h < total) {
+          const T* p = row(h);
+          copy16(&stage[s][0][threadIdx.x], p + o0);
+          if (turn) copy16(&stage[s][1][threadIdx.x], p + o1);
+        }
+        copy_commit();   // (an empty group past the end keeps the count)
+      }
+    };
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int s = 0; s < STAGES - 1; ++s) fetch(slot + s * P.slots, s);
+    }
     float cs[V], sn[V];
     if (turn) {
-      const long long pos = P.pos ? P.pos[bt] : t;
-      o0 = INTER ? 2 * V * c : V * c;
-      o1 = INTER ? o0 + V : o0 + P.plan.rot / 2;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const unsigned long long turns = static_cast<unsigned long long>(pos) * P.plan.turns[V * c + e];
@@ -85,19 +127,22 @@ __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ Params
         sn[e] *= P.sign * P.plan.mscale;
         cs[e] *= P.plan.mscale;
       }
-    } else {
-      o0 = o1 = P.plan.rot + V * (c - P.rot_chunks);
     }
-    const int total = P.heads[0] + P.heads[1];
-#pragma unroll 4
+    int s = 0;
     for (int h = slot; h < total; h += P.slots) {
-      const int k = h >= P.heads[0] ? 1 : 0;
-      const int hh = h - (k ? P.heads[0] : 0);
-      const T* x = static_cast<const T*>(P.x[k]) + b * P.xs[k].b + hh * P.xs[k].h + t * P.xs[k].t;
-      T* y = static_cast<T*>(P.y[k]) + b * P.ys[k].b + hh * P.ys[k].h + t * P.ys[k].t;
-      W u = *reinterpret_cast<const W*>(x + o0);
+      W u, v;
+      if constexpr (WIDE) {
+        fetch(h + (STAGES - 1) * P.slots, s == 0 ? STAGES - 1 : s - 1);   // (the slot read in the last step)
+        copy_wait<STAGES - 1>();
+        u = stage[s][0][threadIdx.x];
+        v = stage[s][1][threadIdx.x];
+        s = s == STAGES - 1 ? 0 : s + 1;
+      } else {
+        u = *reinterpret_cast<const W*>(row(h) + o0);
+        v = *reinterpret_cast<const W*>(row(h) + o1);
+      }
+      T* out = h < P.heads[0] ? y[0] + h * P.ys[0].h : y[1] + h * P.ys[1].h;
       if (turn) {
-        W v = *reinterpret_cast<const W*>(x + o1);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           // pair e of the chunk: (u_e, v_e), or elements 2e, 2e + 1 of the 2 V adjacent ones
@@ -107,10 +152,11 @@ __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ Params
           pu = from_f<T>(a * cs[e] - w * sn[e]);
           pv = from_f<T>(w * cs[e] + a * sn[e]);
         }
-        *reinterpret_cast<W*>(y + o1) = v;
+        *reinterpret_cast<W*>(out + o1) = v;
       }
-      *reinterpret_cast<W*>(y + o0) = u;
+      *reinterpret_cast<W*>(out + o0) = u;
     }
+    if constexpr (WIDE) copy_wait<0>();
   }
 }
 
