@@ -352,20 +352,20 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _call_on(index, stream, call):
-    """call(stream handle) with CUDA device `index`, and a stream given for the call, made current, so that what the
-    call allocates belongs to the stream its kernels run on."""
+def _call_on(index, stream, call, *args):
+    """call(stream handle, *args) with CUDA device `index`, and a stream given for the call, made current, so that
+    what the call allocates belongs to the stream its kernels run on."""
     if index < 0:
         raise ValueError("tensors must be on a CUDA device")
     if stream is None:
         if index == torch.cuda.current_device():
-            return call(_raw_stream(index))
+            return call(_raw_stream(index), *args)
         with torch.cuda.device(index):
-            return call(_raw_stream(index))
+            return call(_raw_stream(index), *args)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=index)
     with torch.cuda.device(index), torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        return call(stream.cuda_stream, *args)
 
 
 _workspace_size = functools.lru_cache(maxsize=4096)(

@@ -70,27 +70,13 @@ struct Cfg {
   static constexpr int OFF_JOIN = NST * STAGE;
   static constexpr int OFF_BAR = OFF_JOIN + JOIN;
   static constexpr int OFF_MISC = OFF_BAR + 2 * NST * 8;
-  static constexpr int SMEM = OFF_MISC + 64 + 4 * THREADS;   // + scan
+  static constexpr int OFF_HULL = OFF_MISC + 64 + 128;   // after the scan: [THREADS] hulls
+  static constexpr int SMEM = OFF_HULL + 8 * THREADS;
 };
 
-// Hull of the ranges of batch entry b's tokens, by a whole warp: [lo, hi),
-// (0, 0) when no token sees a key.
-__device__ __forceinline__ int2 hull_of(const Params& P, int b, int lane) {
-  int lo = 0x7fffffff, hi = 0;
-  for (int t = lane; t < P.p.Tq; t += 32) {
-    int pos, a, z;
-    scored::row_range(P.p, P.mask, b, t, &a, &z, &pos);
-    if (a < z) {
-      lo = min(lo, a);
-      hi = max(hi, z);
-    }
-  }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  return hi > 0 ? make_int2(lo, hi) : make_int2(0, 0);
-}
-
-__device__ __forceinline__ int stages_of(const Params& P, int b) {   // by one thread
+// Hull of the ranges of batch entry b's tokens: [lo, hi), (0, 0) when no
+// token sees a key. By one thread.
+__device__ __forceinline__ int2 hull_of(const Params& P, int b) {
   int lo = 0x7fffffff, hi = 0;
   for (int t = 0; t < P.p.Tq; ++t) {
     int pos, a, z;
@@ -100,35 +86,40 @@ __device__ __forceinline__ int stages_of(const Params& P, int b) {   // by one t
       hi = max(hi, z);
     }
   }
-  return hi > 0 ? (hi - lo + BK - 1) / BK : 0;
+  return hi > 0 ? make_int2(lo, hi) : make_int2(0, 0);
 }
+__device__ __forceinline__ int stages_of(int2 hull) { return (hull.y - hull.x + BK - 1) / BK; }
 
 // The runs of stages a CTA works through, one pair (batch entry, key head)
-// after another. Every warp walks them itself.
+// after another. Every warp walks them itself. `hulls`: those of all batch
+// entries in shared memory, or null where there are more than threads.
 struct Walk {
+  const int2* hulls;
   int b, h, n;        // the pair, and the stages of each pair of b
   int s0, run;        // this run: stages [s0, s0 + run) of the pair
   int2 hull;
   int left;           // stages after this run
 
-  __device__ __forceinline__ void begin(const Params& P, int b0, int off, int count, int lane) {
+  __device__ __forceinline__ int2 hull_at(const Params& P, int e) const { return hulls ? hulls[e] : hull_of(P, e); }
+  __device__ __forceinline__ void begin(const Params& P, const int2* all, int b0, int off, int count) {
+    hulls = all;
     b = b0;
-    hull = hull_of(P, b, lane);
-    n = (hull.y - hull.x + BK - 1) / BK;
+    hull = hull_at(P, b);
+    n = stages_of(hull);
     h = off / n;
     s0 = off - h * n;
     run = min(n - s0, count);
     left = count - run;
   }
-  __device__ __forceinline__ bool next(const Params& P, int lane) {
+  __device__ __forceinline__ bool next(const Params& P) {
     if (left == 0) return false;
     if (++h == P.p.Hkv) {
       h = 0;
       do {   // entries without a key have no stages
         ++b;
-        hull = hull_of(P, b, lane);
+        hull = hull_at(P, b);
       } while (hull.y == 0);
-      n = (hull.y - hull.x + BK - 1) / BK;
+      n = stages_of(hull);
     }
     s0 = 0;
     run = min(n, left);
@@ -189,14 +180,22 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::THREADS, Cfg<HD, RT>::CTAS)
     }
     *abort_flag = 0u;
     ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&tmK);
+    ptx::tma_prefetch_desc(&tmV);
   }
   // This CTA's share of the launch's stages: every thread counts the stages
   // of a run of batch entries.
   const int B = P.p.B;
   const int per = (B + C::THREADS - 1) / C::THREADS;
   const int b_lo = min(B, static_cast<int>(threadIdx.x) * per), b_hi = min(B, b_lo + per);
+  int2* hulls = reinterpret_cast<int2*>(smem + C::OFF_HULL);
+  const bool one = per == 1;   // an entry per thread: its hull is kept
   int mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += stages_of(P, b) * P.p.Hkv;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int2 hull = hull_of(P, b);
+    if (one) hulls[b] = hull;
+    mine += stages_of(hull) * P.p.Hkv;
+  }
   int before = mine;   // inclusive scan over the warp, then over the warps
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -215,8 +214,8 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::THREADS, Cfg<HD, RT>::CTAS)
   const int first = static_cast<int>(cta * total / grid), last = static_cast<int>((cta + 1) * total / grid);
   if (before <= first && first < before + mine) {
     int at = before, b = b_lo;
-    for (;; ++b) {
-      const int n = stages_of(P, b) * P.p.Hkv;
+    for (; !one; ++b) {
+      const int n = stages_of(hull_of(P, b)) * P.p.Hkv;
       if (first < at + n) break;
       at += n;
     }
@@ -227,14 +226,14 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::THREADS, Cfg<HD, RT>::CTAS)
     int at = before;
     for (int b = b_lo; b < b_hi; ++b) {
       P.start[b] = at;
-      at += stages_of(P, b) * P.p.Hkv;
+      if (!one) at += stages_of(hull_of(P, b)) * P.p.Hkv;
     }
     if (threadIdx.x == 0) P.start[B] = total;
   }
   __syncthreads();
   if (last <= first) return;
   Walk wk;
-  wk.begin(P, found[0], found[1], last - first, lane);
+  wk.begin(P, one ? hulls : nullptr, found[0], found[1], last - first);
 
   if (warp == C::WARPS) {
     // ------------------------------------------------------------ producer
@@ -256,7 +255,7 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::THREADS, Cfg<HD, RT>::CTAS)
         }
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-    } while (ok && wk.next(P, lane));
+    } while (ok && wk.next(P));
     if (!ok && lane == 0)   // let the copies in flight land before the CTA exits
       for (uint32_t n = it > static_cast<uint32_t>(C::NST) ? it - C::NST : 0u; n < it; ++n)
         ptx::mbar_wait_drain(full + n % C::NST, (n / C::NST) & 1u);
@@ -469,97 +468,103 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::THREADS, Cfg<HD, RT>::CTAS)
       }
     }
     // (slot 1 is written again after the next run's first barrier)
-  } while (wk.next(P, lane));
+  } while (wk.next(P));
 }
 
 // Rows whose pair is spread over several CTAs: their partial results joined
-// in a fixed order. Rows of pairs without a key: zeros. One block per row;
-// warp w adds parts w, w + 8, ... (a float4 of the row per lane), so that a
-// row of many parts costs a few loads in a row and not all of them: with one
-// warp per row the join of 38 parts took 29 us, three times the main kernel.
+// in a fixed order. Rows of pairs without a key: zeros. WPR warps per row,
+// warp w of them adding parts w, w + WPR, ... (a float4 of the row per lane):
+// eight for rows of many parts, whose loads would otherwise wait for one
+// another (38 parts with one warp: 29 us, three times the main kernel), one
+// for many rows of few parts. The launch overlaps the main kernel's end.
 constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
 constexpr int MAX_GRID = 304;   // CTAs of the main kernel
 
+template <int WPR>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ Params P, int grid) {
-  __shared__ float weight[MAX_GRID];
+  constexpr int ROWS = JOIN_WARPS / WPR;   // of a block
   __shared__ float red[JOIN_WARPS];
-  __shared__ float4 part[JOIN_WARPS][32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ float4 part[WPR > 1 ? JOIN_WARPS : 1][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int own = warp / WPR, w = warp - own * WPR;   // row of the block, and warp of the row
   const int R = P.p.R, dv = P.p.dv;
-  const int bh = blockIdx.x / R, r = blockIdx.x - bh * R;
-  const int b = bh / P.p.Hkv, h = bh - b * P.p.Hkv;
-  const int total = __ldg(P.start + P.p.B), s0 = __ldg(P.start + b), s1 = __ldg(P.start + b + 1);
-  const long long n = blockIdx.x;
-  const int stages = (s1 - s0) / P.p.Hkv;
-  __nv_bfloat16* out = P.O + n * dv;
-  if (stages == 0) {
-    if (tid < dv) out[tid] = __float2bfloat16_rn(0.f);
-    if (tid == 0) P.LSE[n] = -CUDART_INF_F;
-    return;
+  const long long n = static_cast<long long>(blockIdx.x) * ROWS + own;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the main kernel's results
+  int c0 = 0, c1 = -1, r = 0;
+  long long tot = 1;
+  const long long g = grid;
+  auto begin = [&](int c) { return static_cast<int>(c * tot / g); };   // CTA c's first stage
+  if (n < static_cast<long long>(P.p.B) * P.p.Hkv * R) {
+    const int bh = static_cast<int>(n / R);
+    r = static_cast<int>(n - static_cast<long long>(bh) * R);
+    const int b = bh / P.p.Hkv, h = bh - b * P.p.Hkv;
+    tot = P.start[P.p.B];
+    const int s0 = P.start[b], stages = (P.start[b + 1] - s0) / P.p.Hkv;
+    if (stages == 0) {
+      if (w == 0) {
+        for (int c = lane; c < dv; c += 32) P.O[n * dv + c] = __float2bfloat16_rn(0.f);
+        if (lane == 0) P.LSE[n] = -CUDART_INF_F;
+      }
+    } else {
+      auto cta_of = [&](int x) {   // the largest c with begin(c) <= x
+        int c = static_cast<int>(x * g / tot);
+        while (c + 1 < grid && begin(c + 1) <= x) ++c;
+        return c;
+      };
+      c0 = cta_of(s0 + h * stages);
+      c1 = cta_of(s0 + (h + 1) * stages - 1);
+    }
   }
-  // CTA c has the stages [c total / grid, (c + 1) total / grid)
-  const int x0 = s0 + h * stages, x1 = x0 + stages;
-  const long long g = grid, tot = total;
-  auto begin = [&](int c) { return static_cast<int>(c * tot / g); };
-  auto cta_of = [&](int x) {   // the largest c with begin(c) <= x
-    int c = static_cast<int>(x * g / tot);
-    while (c + 1 < grid && begin(c + 1) <= x) ++c;
-    return c;
-  };
-  const int c0 = cta_of(x0), c1 = cta_of(x1 - 1);
-  if (c0 == c1) return;   // written by that CTA
-  const int parts = c1 - c0 + 1;
+  const int parts = c1 > c0 ? c1 - c0 + 1 : 0;   // (one CTA: written by it)
   // the pair starts in c0 (its last part) and goes on in the others (their first part)
   auto at = [&](int i) { return ((c0 + i) * 2LL + (i == 0 ? 1 : 0)) * R + r; };
-  float mx = -CUDART_INF_F;
-  for (int i = tid; i < parts; i += JOIN_THREADS) {
-    const bool some = begin(c0 + i) < begin(c0 + i + 1);   // a CTA without stages wrote nothing
-    const float v = some ? P.LSEpart[at(i)] : -CUDART_INF_F;
-    weight[i] = v;
-    mx = fmaxf(mx, v);
-  }
+  auto lse_of = [&](int i) {   // a CTA without stages wrote nothing
+    return begin(c0 + i) < begin(c0 + i + 1) ? P.LSEpart[at(i)] : -CUDART_INF_F;
+  };
+  float mx = -CUDART_INF_F;   // every warp of a row forms it
+  for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, lse_of(i));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) red[warp] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < JOIN_WARPS; ++i) mx = fmaxf(mx, red[i]);
   const float ref = mx == -CUDART_INF_F ? 0.f : mx;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
   const int col = 4 * lane;
+  for (int i0 = w; i0 < parts; i0 += 32 * WPR) {   // lane k: the weight of part i0 + k WPR
+    const int mine = i0 + lane * WPR;
+    const float weight = mine < parts ? expf(lse_of(mine) - ref) : 0.f;
+    const int count = min(32, (parts - i0 + WPR - 1) / WPR);
 #pragma unroll 4
-  for (int i = warp; i < parts; i += JOIN_WARPS) {
-    const float w = expf(weight[i] - ref);
-    if (w > 0.f) {
-      sum += w;
-      if (col < dv) {
-        const float4 v = *reinterpret_cast<const float4*>(P.Opart + at(i) * dv + col);
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
+    for (int k = 0; k < count; ++k) {
+      const float x = __shfl_sync(0xffffffffu, weight, k);
+      if (x > 0.f && col < dv) {
+        const float4 v = *reinterpret_cast<const float4*>(P.Opart + at(i0 + k * WPR) * dv + col);
+        acc.x = fmaf(x, v.x, acc.x);
+        acc.y = fmaf(x, v.y, acc.y);
+        acc.z = fmaf(x, v.z, acc.z);
+        acc.w = fmaf(x, v.w, acc.w);
       }
+      sum += x;
     }
   }
-  part[warp][lane] = acc;
-  __syncthreads();   // (red has been read)
-  if (lane == 0) red[warp] = sum;
-  __syncthreads();
-  if (warp > 0) return;
-  sum = red[0];
+  if constexpr (WPR > 1) {
+    part[warp][lane] = acc;
+    if (lane == 0) red[warp] = sum;
+    __syncthreads();
+    if (w > 0) return;
 #pragma unroll
-  for (int i = 1; i < JOIN_WARPS; ++i) {
-    const float4 v = part[i][lane];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
-    sum += red[i];
+    for (int i = 1; i < WPR; ++i) {
+      const float4 v = part[warp + i][lane];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+      sum += red[warp + i];
+    }
   }
+  if (parts == 0) return;
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   if (col < dv)
-    *reinterpret_cast<uint2*>(out + col) =
+    *reinterpret_cast<uint2*>(P.O + n * dv + col) =
         make_uint2(ptx::pack_bf16(acc.x * inv, acc.y * inv), ptx::pack_bf16(acc.z * inv, acc.w * inv));
   if (lane == 0) P.LSE[n] = sum > 0.f ? mx + logf(sum) : -CUDART_INF_F;
 }
@@ -586,9 +591,19 @@ cudaError_t launch(const ScoredFwd& a) {
   if (e != cudaSuccess) return e;
   kern<<<a.n_splits, C::THREADS, C::SMEM, a.stream>>>(*a.tmK, *a.tmV, P);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const long long rows = static_cast<long long>(a.p.B) * a.p.Hkv * a.p.R;
-  join_kernel<<<static_cast<unsigned>(rows), JOIN_THREADS, 0, a.stream>>>(P, a.n_splits);
-  return cudaGetLastError();
+  // (rows fit int: the host checks)
+  const int rows = a.p.B * a.p.Hkv * a.p.R;
+  const bool few = a.n_splits <= 8 * a.p.B * a.p.Hkv;   // parts of a row, on average
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = few ? (rows + JOIN_WARPS - 1) / JOIN_WARPS : rows;
+  cfg.blockDim = JOIN_THREADS;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few ? join_kernel<1> : join_kernel<JOIN_WARPS>, P, a.n_splits);
 }
 
 template <int HD>
