@@ -23,11 +23,11 @@ attn_status_t check_scored(int B, int H, int Hkv, int Tq, int Tk, int d, int dv,
   if (Hkv < 1 || H % Hkv) return ATTN_ERR_INVALID_ARG;
   if (dt != ATTN_F32 && dt != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
   if (Tq > kMaxRows || Tk > kMaxRows || static_cast<long long>(H / Hkv) * Tq > kMaxRows) return ATTN_ERR_INVALID_ARG;
-  // work units (64-row or 64-key tiles of every head) are counted in int
+  // work units (32-row or 32-key tiles of every head) are counted in int
   const double heads = static_cast<double>(B) * Hkv;
   const double rows = static_cast<double>(H / Hkv) * Tq;
   // (and 128-row tiles with a place for every query head)
-  if (heads * ((rows > Tk ? rows : Tk) / 64.0 + 2.0 + H / Hkv) > 2147483647.0 || heads * rows > 2147483647.0)
+  if (heads * ((rows > Tk ? rows : Tk) / 32.0 + 2.0 + H / Hkv) > 2147483647.0 || heads * rows > 2147483647.0)
     return ATTN_ERR_INVALID_ARG;
   if (d > 128 || dv > 128) return ATTN_ERR_UNSUPPORTED;
   if (dt == ATTN_BF16 && (d % 8 || dv % 8)) return ATTN_ERR_UNSUPPORTED;
@@ -59,11 +59,11 @@ ScoredProblem problem(int B, int H, int Hkv, int Tq, int Tk, int d, int dv) {
   return p;
 }
 
-// Key ranges of the forward: the CUDA-core kernel runs two 64-row tiles per
-// SM at a time.
+// Key ranges of the forward: the CUDA-core kernel runs about four 32-row tiles
+// per SM at a time.
 void fwd_splits(const ScoredProblem& p, int* S, int* keys) {
-  const long long units = static_cast<long long>(p.B) * p.Hkv * ((p.R + 63) / 64);
-  const int want = wave_splits(units, p.n_kt, 2 * kSms);
+  const long long units = static_cast<long long>(p.B) * p.Hkv * ((p.R + 31) / 32);
+  const int want = wave_splits(units, p.n_kt, 4 * kSms);
   const int tiles = want > 1 ? (p.n_kt + want - 1) / want : p.n_kt;
   *S = want > 1 ? (p.n_kt + tiles - 1) / tiles : 1;
   *keys = tiles * kScoredTile;

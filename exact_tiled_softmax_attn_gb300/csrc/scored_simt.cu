@@ -1,123 +1,145 @@
 // fp32 scored attention on CUDA cores, forward and backward.
 //
-// 64-row by 64-key tiles, 256 threads as 16 x 16, each with a 4 x 4 piece of
-// a score tile and 4 rows by 4 columns per 64 of the accumulators. Per 16
-// products a thread reads 8 floats of shared memory as float4 (rows of a tile
-// lie 64 * NC + 4 floats apart, an odd number of float4, so the 16 rows a
-// warp reads at one column fall into different banks). Bound by the FMA rate
-// and those reads. Row tiles visit only the key tiles their ranges' hull
-// meets, and key tiles only the row tiles whose hull meets them.
+// The forward and the dQ kernel take 32 rows by 64 keys a step, the dK/dV
+// kernel 64 rows by 32 keys: 128 threads, each with a 4 x 4 piece of the
+// scores and 4 rows (keys) by 4 columns per 64 of the accumulators. Small
+// tiles, so that problems of a thousand rows fill the GPU and several CTAs of
+// an SM cover one another's loads and barriers (with 64 x 64 tiles and 256
+// threads a training step of B=2 H=8 T=1000 d=64 took 440 us, one CTA per SM
+// waiting for itself most of the time). Per 16 products a thread reads 8
+// floats of shared memory as float4; rows of a tile lie 64 * NC + 4 floats
+// apart, an odd number of float4, so the rows a warp reads at one column fall
+// into different banks. Scores use two-lane FMAs over even and odd columns.
+// Bound by the FMA rate and those reads. Row tiles visit only the key tiles
+// their ranges' hull meets, and key tiles only the row tiles whose hull meets
+// them.
 #include <math_constants.h>
 #include <stdint.h>
 
+#include "ptx.cuh"
 #include "scored.h"
 
 namespace attn {
 namespace scored_simt {
 
-constexpr int BM = 64, BN = 64, NT = 256;
-constexpr int LDP = BN + 4;
+constexpr int NT = 128;
+constexpr int BM = 32, BN = 64;     // rows and keys of a step: forward, dQ
+constexpr int KM = 64, KN = 32;     // rows and keys of a step: dK/dV
+constexpr int LDP = BN + 4;         // pitch of a tile of weights, 64 keys wide
+constexpr int LDK = KN + 4;         // and 32 keys wide
 
 template <int NC>
 struct Pitch {
   static constexpr int v = 64 * NC + 4;
 };
 
-// 64 rows of `d` elements from row r0 into a tile of pitch 64 * NC + 4, zeros
-// past column d and outside rows [lo, hi).
-template <int NC>
+// ROWS rows of `d` elements from row r0 into a tile of pitch 64 * NC + 4,
+// zeros past column d and outside rows [lo, hi). The copies are asynchronous
+// (loaded() waits for them); 16 bytes each where rows and base allow.
+template <int NC, int ROWS>
 __device__ __forceinline__ void load_tile(float* s, const float* g, int r0, int lo, int hi, int d) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < 64; r += NT / 32) {
-    const int row = r0 + r;
-    const bool in = row >= lo && row < hi;
-    const float* src = g + static_cast<long long>(in ? row : 0) * d;
-#pragma unroll
-    for (int c = 0; c < 2 * NC; ++c) {
-      const int k = lane + 32 * c;
-      s[r * Pitch<NC>::v + k] = (in && k < d) ? src[k] : 0.f;
+  const uint32_t dst = ptx::smem_u32(s);
+  if (d % 4 == 0 && reinterpret_cast<uintptr_t>(g) % 16 == 0) {
+    for (int i = threadIdx.x; i < ROWS * 16 * NC; i += NT) {
+      const int r = i / (16 * NC), k = 4 * (i % (16 * NC)), row = r0 + r;
+      const bool in = row >= lo && row < hi && k < d;
+      const float* src = g + (in ? static_cast<long long>(row) * d + k : 0);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (r * Pitch<NC>::v + k) * 4), "l"(src),
+                   "r"(in ? 16 : 0)
+                   : "memory");
+    }
+  } else {
+    for (int i = threadIdx.x; i < ROWS * 64 * NC; i += NT) {
+      const int r = i / (64 * NC), k = i % (64 * NC), row = r0 + r;
+      const bool in = row >= lo && row < hi && k < d;
+      const float* src = g + (in ? static_cast<long long>(row) * d + k : 0);
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + (r * Pitch<NC>::v + k) * 4), "l"(src),
+                   "r"(in ? 4 : 0)
+                   : "memory");
     }
   }
 }
+__device__ __forceinline__ void loaded() {   // every thread's copies
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+}
 
-// x[i][j] = row (4 ty + i) of a . row (tx + 16 j) of b over d columns
-template <int NC>
+// x[i][j] = row (4 ty + i) of a . row (tx + TX j) of b over d columns, with
+// the threads as rows of TX
+template <int NC, int TX>
 __device__ __forceinline__ void dot_tile(float (&x)[4][4], const float* a, const float* b, int d) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
   constexpr int P = Pitch<NC>::v;
+  float2 y[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) y[i][j] = make_float2(0.f, 0.f);
   const float* ar = a + 4 * ty * P;
   const float* br = b + tx * P;
-  for (int k = 0; k < d; k += 4) {
+#pragma unroll 2
+  for (int k = 0; k < d; k += 4) {   // (columns past d are zeros)
     float4 u[4], v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const float4*>(ar + i * P + k);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float4*>(br + 16 * j * P + k);
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float4*>(br + TX * j * P + k);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        x[i][j] = fmaf(u[i].x, v[j].x, x[i][j]);
-        x[i][j] = fmaf(u[i].y, v[j].y, x[i][j]);
-        x[i][j] = fmaf(u[i].z, v[j].z, x[i][j]);
-        x[i][j] = fmaf(u[i].w, v[j].w, x[i][j]);
+        y[i][j] = ptx::ffma2(make_float2(u[i].x, u[i].y), make_float2(v[j].x, v[j].y), y[i][j]);
+        y[i][j] = ptx::ffma2(make_float2(u[i].z, u[i].w), make_float2(v[j].z, v[j].w), y[i][j]);
       }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[i][j] = y[i][j].x + y[i][j].y;
+}
+
+template <int NC>
+__device__ __forceinline__ void add_products(float (&acc)[4][4 * NC], const float (&u)[4], const float* b) {
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const float4 v = *reinterpret_cast<const float4*>(b + 64 * c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[i][4 * c] = fmaf(u[i], v.x, acc[i][4 * c]);
+      acc[i][4 * c + 1] = fmaf(u[i], v.y, acc[i][4 * c + 1]);
+      acc[i][4 * c + 2] = fmaf(u[i], v.z, acc[i][4 * c + 2]);
+      acc[i][4 * c + 3] = fmaf(u[i], v.w, acc[i][4 * c + 3]);
+    }
   }
 }
 
-// acc[i][4 c + e] += sum_k w[4 ty + i][k] * b[k][4 tx + 64 c + e]   (w row-major, pitch LDP)
+// acc[i][4 c + e] += sum_k w[4 ty + i][k] * b[k][4 tx + 64 c + e] over BN keys
 template <int NC>
 __device__ __forceinline__ void acc_rows(float (&acc)[4][4 * NC], const float* w, const float* b) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   constexpr int P = Pitch<NC>::v;
 #pragma unroll 2
   for (int k = 0; k < BN; k += 4) {
-    float u[4][4];
+    float4 t[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 t = *reinterpret_cast<const float4*>(w + (4 * ty + i) * LDP + k);
-      u[i][0] = t.x, u[i][1] = t.y, u[i][2] = t.z, u[i][3] = t.w;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const float4 v = *reinterpret_cast<const float4*>(b + (k + e) * P + 4 * tx + 64 * c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[i][4 * c] = fmaf(u[i][e], v.x, acc[i][4 * c]);
-          acc[i][4 * c + 1] = fmaf(u[i][e], v.y, acc[i][4 * c + 1]);
-          acc[i][4 * c + 2] = fmaf(u[i][e], v.z, acc[i][4 * c + 2]);
-          acc[i][4 * c + 3] = fmaf(u[i][e], v.w, acc[i][4 * c + 3]);
-        }
-      }
+    for (int i = 0; i < 4; ++i) t[i] = *reinterpret_cast<const float4*>(w + (4 * ty + i) * LDP + k);
+    const float* row = b + k * P + 4 * tx;
+    add_products<NC>(acc, {t[0].x, t[1].x, t[2].x, t[3].x}, row);
+    add_products<NC>(acc, {t[0].y, t[1].y, t[2].y, t[3].y}, row + P);
+    add_products<NC>(acc, {t[0].z, t[1].z, t[2].z, t[3].z}, row + 2 * P);
+    add_products<NC>(acc, {t[0].w, t[1].w, t[2].w, t[3].w}, row + 3 * P);
   }
 }
 
-// acc[i][4 c + e] += sum_r w[r][4 ty + i] * b[r][4 tx + 64 c + e]   (the product with w transposed)
+// acc[i][4 c + e] += sum_r w[r][4 ty + i] * b[r][4 tx + 64 c + e] over KM rows
 template <int NC>
 __device__ __forceinline__ void acc_cols(float (&acc)[4][4 * NC], const float* w, const float* b) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   constexpr int P = Pitch<NC>::v;
 #pragma unroll 4
-  for (int r = 0; r < BM; ++r) {
-    const float4 t = *reinterpret_cast<const float4*>(w + r * LDP + 4 * ty);
-    const float u[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const float4 v = *reinterpret_cast<const float4*>(b + r * P + 4 * tx + 64 * c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i][4 * c] = fmaf(u[i], v.x, acc[i][4 * c]);
-        acc[i][4 * c + 1] = fmaf(u[i], v.y, acc[i][4 * c + 1]);
-        acc[i][4 * c + 2] = fmaf(u[i], v.z, acc[i][4 * c + 2]);
-        acc[i][4 * c + 3] = fmaf(u[i], v.w, acc[i][4 * c + 3]);
-      }
-    }
+  for (int r = 0; r < KM; ++r) {
+    const float4 t = *reinterpret_cast<const float4*>(w + r * LDK + 4 * ty);
+    add_products<NC>(acc, {t.x, t.y, t.z, t.w}, b + r * P + 4 * tx);
   }
 }
 
@@ -149,12 +171,13 @@ struct RowInfo {
   float slope[4];
 };
 
+template <int TX>
 __device__ __forceinline__ RowInfo row_info(const ScoredProblem& p, const ScoredPlan& plan, int bh, int r0) {
   RowInfo ri;
-  const int b = bh / p.Hkv, kvh = bh - b * p.Hkv, ty = threadIdx.x >> 4;
+  const int b = bh / p.Hkv, kvh = bh - b * p.Hkv, ty = threadIdx.x / TX;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = r0 + 4 * ty + i;   // rows up to rpad have entries; BM divides it
+    const int r = r0 + 4 * ty + i;   // (rows up to rpad have entries)
     const int4 w = plan.rows[static_cast<long long>(b) * p.rpad() + r];
     ri.lo[i] = w.x, ri.hi[i] = w.y, ri.pos[i] = w.z;
     ri.slope[i] = p.slopes && r < p.R ? p.slopes[kvh * p.G + r / p.Tq] : 0.f;
@@ -189,10 +212,10 @@ __global__ void __launch_bounds__(NT) fwd_kernel(const ScoredProblem p, const Sc
   const int r0 = (nt - 1 - (blockIdx.x - bh * nt)) * BM;   // causal: the longest rows first
   const int b = bh / p.Hkv;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const RowInfo ri = row_info(p, plan, bh, r0);
+  const RowInfo ri = row_info<16>(p, plan, bh, r0);
   const int4 hull = plan.tiles[static_cast<long long>(b) * p.n_rt + r0 / kScoredTile];
   const int k_lo = max(hull.x, split * split_keys), k_hi = min(hull.y, (split + 1) * split_keys);
-  load_tile<NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
+  load_tile<NCK, BM>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
   const float* Kh = K + static_cast<long long>(bh) * p.Tk * p.d;
   const float* Vh = V + static_cast<long long>(bh) * p.Tk * p.dv;
   float acc[4][4 * NCV], m[4], l[4];
@@ -205,11 +228,11 @@ __global__ void __launch_bounds__(NT) fwd_kernel(const ScoredProblem p, const Sc
   }
   for (int k0 = k_lo / BN * BN; k0 < k_hi; k0 += BN) {
     __syncthreads();
-    load_tile<NCK>(sK, Kh, k0, k_lo, k_hi, p.d);
-    load_tile<NCV>(sV, Vh, k0, k_lo, k_hi, p.dv);
-    __syncthreads();
+    load_tile<NCK, BN>(sK, Kh, k0, k_lo, k_hi, p.d);
+    load_tile<NCV, BN>(sV, Vh, k0, k_lo, k_hi, p.dv);
+    loaded();
     float x[4][4];
-    dot_tile<NCK>(x, sQ, sK, p.d);
+    dot_tile<NCK, 16>(x, sQ, sK, p.d);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float mx = -CUDART_INF_F, g;
@@ -274,12 +297,12 @@ __global__ void __launch_bounds__(NT) dq_kernel(const ScoredProblem p, const Sco
   const int r0 = (nt - 1 - (blockIdx.x - bh * nt)) * BM;
   const int b = bh / p.Hkv;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const RowInfo ri = row_info(p, plan, bh, r0);
+  const RowInfo ri = row_info<16>(p, plan, bh, r0);
   const int4 hull = plan.tiles[static_cast<long long>(b) * p.n_rt + r0 / kScoredTile];
-  load_tile<NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
-  load_tile<NCV>(sdO, dO + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);
-  load_tile<NCV>(sV, O + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);   // O, until the loop
-  __syncthreads();
+  load_tile<NCK, BM>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
+  load_tile<NCV, BM>(sdO, dO + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);
+  load_tile<NCV, BM>(sV, O + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);   // O, until the loop
+  loaded();
   float lse[4], dd[4], acc[4][4 * NCK];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -298,12 +321,12 @@ __global__ void __launch_bounds__(NT) dq_kernel(const ScoredProblem p, const Sco
   const float* Vh = V + static_cast<long long>(bh) * p.Tk * p.dv;
   for (int k0 = hull.x / BN * BN; k0 < hull.y; k0 += BN) {
     __syncthreads();
-    load_tile<NCK>(sK, Kh, k0, hull.x, hull.y, p.d);
-    load_tile<NCV>(sV, Vh, k0, hull.x, hull.y, p.dv);
-    __syncthreads();
+    load_tile<NCK, BN>(sK, Kh, k0, hull.x, hull.y, p.d);
+    load_tile<NCV, BN>(sV, Vh, k0, hull.x, hull.y, p.dv);
+    loaded();
     float x[4][4], y[4][4];
-    dot_tile<NCK>(x, sQ, sK, p.d);
-    dot_tile<NCV>(y, sdO, sV, p.dv);
+    dot_tile<NCK, 16>(x, sQ, sK, p.d);
+    dot_tile<NCV, 16>(y, sdO, sV, p.dv);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -333,17 +356,18 @@ __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const S
                                                    float* __restrict__ dK, float* __restrict__ dV) {
   extern __shared__ __align__(16) float smem[];
   float* sQ = smem;
-  float* sK = sQ + BM * Pitch<NCK>::v;
-  float* sdO = sK + BN * Pitch<NCK>::v;
-  float* sV = sdO + BM * Pitch<NCV>::v;
-  float* sP = sV + BN * Pitch<NCV>::v;
-  float* sW = sP + BM * LDP;
-  const int nt = (p.Tk + BN - 1) / BN;
-  const int bh = blockIdx.x / nt, k0 = (blockIdx.x - bh * nt) * BN;
+  float* sK = sQ + KM * Pitch<NCK>::v;
+  float* sdO = sK + KN * Pitch<NCK>::v;
+  float* sV = sdO + KM * Pitch<NCV>::v;
+  float* sP = sV + KN * Pitch<NCV>::v;
+  float* sW = sP + KM * LDK;
+  const int nt = (p.Tk + KN - 1) / KN;
+  const int bh = blockIdx.x / nt, k0 = (blockIdx.x - bh * nt) * KN;
   const int b = bh / p.Hkv;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  load_tile<NCK>(sK, K + static_cast<long long>(bh) * p.Tk * p.d, k0, 0, p.Tk, p.d);
-  load_tile<NCV>(sV, V + static_cast<long long>(bh) * p.Tk * p.dv, k0, 0, p.Tk, p.dv);
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;     // scores: rows 4 ty + i, keys tx + 8 j
+  const int ky = threadIdx.x >> 4;                            // accumulators: keys 4 ky + i
+  load_tile<NCK, KN>(sK, K + static_cast<long long>(bh) * p.Tk * p.d, k0, 0, p.Tk, p.d);
+  load_tile<NCV, KN>(sV, V + static_cast<long long>(bh) * p.Tk * p.dv, k0, 0, p.Tk, p.dv);
   float ak[4][4 * NCK], av[4][4 * NCV];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -353,42 +377,45 @@ __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const S
     for (int e = 0; e < 4 * NCV; ++e) av[i][e] = 0.f;
   }
   const uint32_t* list = plan.kbits + (static_cast<long long>(b) * p.n_kt + k0 / kScoredTile) * p.n_words();
-  for (int r0 = 0; r0 < p.R; r0 += BM) {
+  for (int r0 = 0; r0 < p.R; r0 += KM) {
     const int rt = r0 / kScoredTile;
     if (!(list[rt / 32] >> (rt % 32) & 1u)) continue;
     const int4 hull = plan.tiles[static_cast<long long>(b) * p.n_rt + rt];
-    if (hull.x >= k0 + BN || hull.y <= k0) continue;
+    if (hull.x >= k0 + KN || hull.y <= k0) continue;
     __syncthreads();
-    load_tile<NCK>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
-    load_tile<NCV>(sdO, dO + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);
-    const RowInfo ri = row_info(p, plan, bh, r0);
-    __syncthreads();
-    float x[4][4], y[4][4];
-    dot_tile<NCK>(x, sQ, sK, p.d);
-    dot_tile<NCV>(y, sdO, sV, p.dv);
+    load_tile<NCK, KM>(sQ, Q + static_cast<long long>(bh) * p.R * p.d, r0, 0, p.R, p.d);
+    load_tile<NCV, KM>(sdO, dO + static_cast<long long>(bh) * p.R * p.dv, r0, 0, p.R, p.dv);
+    const RowInfo ri = row_info<8>(p, plan, bh, r0);
+    float lse[4], dd[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = r0 + 4 * ty + i;
-      const float lse = r < p.R ? LSE[static_cast<long long>(bh) * p.R + r] : 0.f;
-      const float dd = D[static_cast<long long>(bh) * p.rpad() + r];
+      lse[i] = r < p.R ? LSE[static_cast<long long>(bh) * p.R + r] : 0.f;
+      dd[i] = D[static_cast<long long>(bh) * p.rpad() + r];
+    }
+    loaded();
+    float x[4][4], y[4][4];
+    dot_tile<NCK, 8>(x, sQ, sK, p.d);
+    dot_tile<NCV, 8>(y, sdO, sV, p.dv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int key = k0 + tx + 16 * j;
+        const int key = k0 + tx + 8 * j;
         float g;
         const float s = score(x[i][j], p, ri.slope[i], ri.pos[i], key, &g);
         const bool in = key >= ri.lo[i] && key < ri.hi[i];
-        const float e = in ? expf(s - lse) : 0.f;
-        sP[(4 * ty + i) * LDP + tx + 16 * j] = e;
-        sW[(4 * ty + i) * LDP + tx + 16 * j] = in ? e * (y[i][j] - dd) * g : 0.f;
+        const float e = in ? expf(s - lse[i]) : 0.f;
+        sP[(4 * ty + i) * LDK + tx + 8 * j] = e;
+        sW[(4 * ty + i) * LDK + tx + 8 * j] = in ? e * (y[i][j] - dd[i]) * g : 0.f;
       }
-    }
     __syncthreads();
     acc_cols<NCV>(av, sP, sdO);
     acc_cols<NCK>(ak, sW, sQ);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int key = k0 + 4 * ty + i;
+    const int key = k0 + 4 * ky + i;
     if (key < p.Tk) {
       store_row<NCK>(dK + (static_cast<long long>(bh) * p.Tk + key) * p.d, ak[i], p.scale, p.d);
       store_row<NCV>(dV + (static_cast<long long>(bh) * p.Tk + key) * p.dv, av[i], 1.f, p.dv);
@@ -413,8 +440,8 @@ cudaError_t fwd(const ScoredFwd& a) {
 template <int NCK, int NCV>
 cudaError_t bwd(const ScoredBwd& a) {
   const ScoredProblem& p = a.p;
-  const int tiles = 2 * BM * (Pitch<NCK>::v + Pitch<NCV>::v);
-  const int smem_q = (tiles + BM * LDP) * 4, smem_kv = (tiles + 2 * BM * LDP) * 4;
+  const int smem_q = ((BM + BN) * (Pitch<NCK>::v + Pitch<NCV>::v) + BM * LDP) * 4;
+  const int smem_kv = ((KM + KN) * (Pitch<NCK>::v + Pitch<NCV>::v) + 2 * KM * LDK) * 4;
   auto kq = dq_kernel<NCK, NCV>;
   auto kk = dkdv_kernel<NCK, NCV>;
   cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
@@ -425,7 +452,7 @@ cudaError_t bwd(const ScoredBwd& a) {
   kq<<<(p.R + BM - 1) / BM * p.B * p.Hkv, NT, smem_q, a.stream>>>(p, a.plan, Q, K, V, static_cast<const float*>(a.O),
                                                                         a.LSE, dO, static_cast<float*>(a.dQ), a.D);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  kk<<<(p.Tk + BN - 1) / BN * p.B * p.Hkv, NT, smem_kv, a.stream>>>(p, a.plan, Q, K, V, a.LSE, dO, a.D,
+  kk<<<(p.Tk + KN - 1) / KN * p.B * p.Hkv, NT, smem_kv, a.stream>>>(p, a.plan, Q, K, V, a.LSE, dO, a.D,
                                                                           static_cast<float*>(a.dK),
                                                                           static_cast<float*>(a.dV));
   return cudaGetLastError();
