@@ -21,6 +21,8 @@ struct ScoredProblem {
   int R;         // packed query rows of a key head: G * Tq
   int n_rt;      // 128-row tiles of R
   int n_kt;      // 128-key tiles of Tk
+  int kv_splits;   // dK/dV: parts the row tiles of a key tile are cut into, as units of their own
+  int kv_split_tiles;   // row tiles of a part
   float scale;
   float softcap;          // 0: none
   const float* slopes;    // [H] or null
@@ -32,7 +34,7 @@ struct ScoredProblem {
 struct ScoredPlan {
   int4* rows;      // [B][rpad]: {key begin, key end, position, 0}; begin = INT_MAX, end = 0 for rows that see nothing
   int4* tiles;     // [B][n_rt]: {min begin, max end over the rows that see keys, max begin, min end over all rows}
-  int* kcount;     // [B][n_kt]: row tiles whose hull meets the key tile (backward only), or null
+  int* kcount;     // [B][n_kt][kv_splits]: row tiles of the part whose hull meets the key tile (backward only), or null
   uint32_t* kbits; // [B][n_kt][n_words]: which they are, one bit each
   int* even;       // [B][n_rt]: the position of a row tile's first row where its rows are of one head and at
                    // consecutive positions, else kScoredUneven (backward with a bias only), or null
@@ -49,7 +51,21 @@ struct ScoredMask {   // the caller's arrays
   int causal;
 };
 
-cudaError_t launch_scored_plan(const ScoredProblem& p, const ScoredMask& m, const ScoredPlan& plan, cudaStream_t s);
+// Results of what has nothing to do, which the tensor-core kernels leave out
+// (bf16; null pointers: none): rows of row tiles that see no key, and keys of
+// key tiles that no row sees.
+struct ScoredIdle {
+  void* O;
+  float* LSE;
+  void* dQ;
+  float* D;
+  float* NL;
+  void* dK;   // (with one part; the sum of several leaves empty ones out)
+  void* dV;
+};
+
+cudaError_t launch_scored_plan(const ScoredProblem& p, const ScoredMask& m, const ScoredPlan& plan,
+                               const ScoredIdle& idle, cudaStream_t s);
 
 struct ScoredFwd {
   ScoredProblem p;
@@ -87,6 +103,8 @@ struct ScoredBwd {
   void* dK;
   void* dV;
   float* D;         // [B * Hkv][rpad]: rowsum(dO o O), 0 behind row R
+  float* dKpart;    // [kv_splits][B * Hkv * Tk][d] fp32, kv_splits > 1
+  float* dVpart;    // [kv_splits][B * Hkv * Tk][dv]
   float* NL;        // [B * Hkv][rpad]: -LSE * log2(e), -inf for rows that see nothing and behind row R
   const CUtensorMap* tmQ;   // bf16 only
   const CUtensorMap* tmK;
@@ -109,6 +127,9 @@ cudaError_t launch_scored_fwd_bf16(const ScoredFwd& a);
 constexpr int kScoredTokenRows = 64;
 cudaError_t launch_scored_tokens_bf16(const ScoredFwd& a);
 cudaError_t launch_scored_bwd_bf16(const ScoredBwd& a);
+
+// dK and dV from the parts of their row tiles, in order
+cudaError_t launch_scored_kv_sum(const ScoredBwd& a, bool bf16);
 
 // fp32 O and LSE from the partial results of the key ranges, in range order
 cudaError_t launch_scored_merge(const ScoredFwd& a);

@@ -44,7 +44,25 @@ attn_status_t check_score(const attn_score_t& sc, int B, int H, int Tq, float sc
   return ATTN_OK;
 }
 
-ScoredProblem problem(int B, int H, int Hkv, int Tq, int Tk, int d, int dv) {
+// Parts of the row tiles of each key tile in the dK/dV kernel. A key head's
+// query heads are all in one list of row tiles, so few key heads or keys mean
+// few units with long lists: they are cut so that there are about two units
+// per SM (fp32: four, of its 32-key tiles), at least four row tiles each, at
+// most 16 parts. With B=1 Hkv=1 H=8 T=4096 d=128 (32 units, 10 parts) the
+// kernel takes a fifth of the time, the sum of the parts included.
+void kv_split(ScoredProblem* p, attn_dtype_t dt) {
+  const long long heads = static_cast<long long>(p->B) * p->Hkv;
+  const long long units = dt == ATTN_BF16 ? heads * p->n_kt : heads * ((p->Tk + 31) / 32);
+  const long long target = dt == ATTN_BF16 ? 2 * kSms : 4 * kSms;
+  long long S = units > 0 ? (target + units - 1) / units : 1;
+  if (S > p->n_rt / 4) S = p->n_rt / 4;
+  if (S > 16) S = 16;
+  if (S < 1) S = 1;
+  p->kv_split_tiles = p->n_rt > 0 ? (p->n_rt + static_cast<int>(S) - 1) / static_cast<int>(S) : 1;
+  p->kv_splits = p->n_rt > 0 ? (p->n_rt + p->kv_split_tiles - 1) / p->kv_split_tiles : 1;
+}
+
+ScoredProblem problem(int B, int H, int Hkv, int Tq, int Tk, int d, int dv, attn_dtype_t dt) {
   ScoredProblem p{};
   p.B = B;
   p.Hkv = Hkv;
@@ -56,6 +74,7 @@ ScoredProblem problem(int B, int H, int Hkv, int Tq, int Tk, int d, int dv) {
   p.R = p.G * Tq;
   p.n_rt = (p.R + kScoredTile - 1) / kScoredTile;
   p.n_kt = (Tk + kScoredTile - 1) / kScoredTile;
+  kv_split(&p, dt);
   return p;
 }
 
@@ -74,13 +93,13 @@ void fwd_splits(const ScoredProblem& p, int* S, int* keys) {
 bool fwd_tokens(const ScoredProblem& p, attn_dtype_t dt) { return dt == ATTN_BF16 && p.R <= kScoredTokenRows; }
 
 struct Layout {
-  size_t start, rows, tiles, counters, kcount, kbits, even, slope2, D, NL, opart, lsepart, total;
+  size_t start, rows, tiles, counters, kcount, kbits, even, slope2, D, NL, dkpart, dvpart, opart, lsepart, total;
   int n_splits, split_keys;
 };
 
 // Forward: rows | tiles | counters | Opart | LSEpart, with few rows in bf16
 // start | Opart | LSEpart. Backward: rows | tiles |
-// counters | kcount | kbits | even | slope2 | D | NL. Each part starts on 256 bytes.
+// counters | kcount | kbits | even | slope2 | D | NL | dKpart | dVpart. Each part starts on 256 bytes.
 Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
   Layout L{};
   L.n_splits = 1;
@@ -107,12 +126,16 @@ Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
   L.tiles = take(B * p.n_rt * sizeof(int4));
   L.counters = take(256);
   if (bwd) {
-    L.kcount = take(B * p.n_kt * sizeof(int));
+    L.kcount = take(B * p.n_kt * p.kv_splits * sizeof(int));
     L.kbits = take(B * p.n_kt * p.n_words() * sizeof(uint32_t));
     L.even = take(B * p.n_rt * sizeof(int));
     L.slope2 = take(p.Hkv * rpad * sizeof(float));
     L.D = take(heads * rpad * sizeof(float));
     L.NL = take(heads * rpad * sizeof(float));
+    if (p.kv_splits > 1) {
+      L.dkpart = take(p.kv_splits * heads * p.Tk * p.d * sizeof(float));
+      L.dvpart = take(p.kv_splits * heads * p.Tk * p.dv * sizeof(float));
+    }
   } else {
     if (dt == ATTN_F32) fwd_splits(p, &L.n_splits, &L.split_keys);
     if (L.n_splits > 1) {
@@ -165,12 +188,12 @@ extern "C" {
 
 size_t attn_fwd_scored_workspace_size(int B, int H, int Hkv, int Tq, int Tk, int d, int dv, attn_dtype_t dtype) {
   if (check_scored(B, H, Hkv, Tq, Tk, d, dv, dtype) != ATTN_OK) return 0;
-  return layout(problem(B, H, Hkv, Tq, Tk, d, dv), dtype, false).total;
+  return layout(problem(B, H, Hkv, Tq, Tk, d, dv, dtype), dtype, false).total;
 }
 
 size_t attn_bwd_scored_workspace_size(int B, int H, int Hkv, int Tq, int Tk, int d, int dv, attn_dtype_t dtype) {
   if (check_scored(B, H, Hkv, Tq, Tk, d, dv, dtype) != ATTN_OK) return 0;
-  return layout(problem(B, H, Hkv, Tq, Tk, d, dv), dtype, true).total;
+  return layout(problem(B, H, Hkv, Tq, Tk, d, dv, dtype), dtype, true).total;
 }
 
 attn_status_t attn_fwd_scored(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int H, int Hkv,
@@ -190,7 +213,7 @@ attn_status_t attn_fwd_scored(const void* Q, const void* K, const void* V, void*
   if ((s = check_ptr(O, nq * dv * es, align)) != ATTN_OK) return s;
   if ((s = check_ptr(LSE, nq * 4, 4)) != ATTN_OK) return s;
   ScoredFwd a{};
-  a.p = problem(B, H, Hkv, Tq, Tk, d, dv);
+  a.p = problem(B, H, Hkv, Tq, Tk, d, dv, dtype);
   a.p.scale = scale;
   a.p.softcap = sc.softcap;
   a.p.slopes = sc.slopes;
@@ -245,7 +268,8 @@ attn_status_t attn_fwd_scored(const void* Q, const void* K, const void* V, void*
   }
   if (tokens) {
     e = launch_scored_tokens_bf16(a);
-  } else if ((e = launch_scored_plan(a.p, a.mask, a.plan, st)) == cudaSuccess) {
+  } else if ((e = launch_scored_plan(a.p, a.mask, a.plan, bf16 ? ScoredIdle{O, LSE} : ScoredIdle{}, st)) ==
+             cudaSuccess) {
     e = bf16 ? launch_scored_fwd_bf16(a) : launch_scored_fwd_simt(a);
     if (e == cudaSuccess && a.n_splits > 1) e = launch_scored_merge(a);
   }
@@ -272,7 +296,7 @@ attn_status_t attn_bwd_scored(const void* Q, const void* K, const void* V, const
   for (int i = 0; i < 3; ++i)
     if ((s = check_ptr(outs[i], out_bytes[i], align)) != ATTN_OK) return s;
   ScoredBwd a{};
-  a.p = problem(B, H, Hkv, Tq, Tk, d, dv);
+  a.p = problem(B, H, Hkv, Tq, Tk, d, dv, dtype);
   a.p.scale = scale;
   a.p.softcap = sc.softcap;
   a.p.slopes = sc.slopes;
@@ -312,6 +336,8 @@ attn_status_t attn_bwd_scored(const void* Q, const void* K, const void* V, const
   a.dV = dV;
   a.D = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.D);
   a.NL = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.NL);
+  a.dKpart = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.dkpart);
+  a.dVpart = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.dvpart);
   a.status = di->status;
   a.num_sms = di->num_sms;
   a.l2_bytes = static_cast<size_t>(di->l2_bytes);
@@ -330,8 +356,17 @@ attn_status_t attn_bwd_scored(const void* Q, const void* K, const void* V, const
     a.tmdO = &mdo;
     a.tmO = &mo;
   }
-  e = launch_scored_plan(a.p, ScoredMask{sc.q_pos, sc.key_begin, sc.key_end, sc.causal}, a.plan, st);
+  ScoredIdle idle{};
+  if (bf16) {
+    idle = ScoredIdle{nullptr, nullptr, dQ, a.D, a.NL, nullptr, nullptr};
+    if (a.p.kv_splits == 1) {
+      idle.dK = dK;
+      idle.dV = dV;
+    }
+  }
+  e = launch_scored_plan(a.p, ScoredMask{sc.q_pos, sc.key_begin, sc.key_end, sc.causal}, a.plan, idle, st);
   if (e == cudaSuccess) e = bf16 ? launch_scored_bwd_bf16(a) : launch_scored_bwd_simt(a);
+  if (e == cudaSuccess && a.p.kv_splits > 1) e = launch_scored_kv_sum(a, bf16);
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 

@@ -56,6 +56,8 @@ struct Params {
   __nv_bfloat16* dQ;
   __nv_bfloat16* dK;
   __nv_bfloat16* dV;
+  float* dKpart;
+  float* dVpart;
   uint32_t* status;
   uint32_t* counter;   // this launch's unit counter
   int n_blocks, total, group;
@@ -63,9 +65,53 @@ struct Params {
   Cap cap;
 };
 
-__device__ __forceinline__ int claim(const Params& P) {
-  return min(static_cast<int>(atomicAdd(P.counter, 1u)), P.total);
-}
+// The producer's next unit, found while the tiles of the current one are being
+// loaded. Only units that have something to do are handed on (the plan
+// kernels have written the others' results). A unit is claimed three tiles
+// before the end of the one before it, looked up two and published one tile
+// before, so that neither latency holds the loads up: late, because claims
+// further ahead leave the CTAs to end unevenly (two units ahead cost a tenth
+// of the time at 7 units a CTA), and early enough for the other roles to read
+// it while they work on the last tiles. A role that has the last tile of a
+// unit finds the next one published, so no wait for it can hold up the loads
+// that its publication waits for.
+template <typename U>
+struct Next {
+  int x;
+  U u;
+  __device__ __forceinline__ void claim(const Params& P) {
+    x = min(static_cast<int>(atomicAdd(P.counter, 1u)), P.total);
+  }
+  template <typename Load>
+  __device__ __forceinline__ void look_up(const Params& P, Load load) {
+    if (x < P.total) u = load(P, x);
+  }
+  template <typename Load>
+  __device__ __forceinline__ void settle(const Params& P, Load load) {   // past units without work
+    while (x < P.total && u.n == 0) {
+      claim(P);
+      look_up(P, load);
+    }
+  }
+  template <typename Load>
+  __device__ __forceinline__ bool first(const Params& P, Load load, const UnitQueue& q, uint32_t* pu,
+                                        const ptx::WaitCtx& w) {
+    claim(P);
+    look_up(P, load);
+    settle(P, load);
+    return uq_push(q, (*pu)++, x, w);
+  }
+  // the steps that fall before tile i of n
+  template <typename Load>
+  __device__ __forceinline__ bool step(const Params& P, int i, int n, Load load, const UnitQueue& q, uint32_t* pu,
+                                       const ptx::WaitCtx& w) {
+    if (i == max(n - 3, 0)) claim(P);
+    if (i == max(n - 2, 0)) look_up(P, load);
+    if (i != n - 1) return true;
+    settle(P, load);
+    return uq_push(q, (*pu)++, x, w);
+  }
+};
 
 // ---------------------------------------------------------------- dQ
 
@@ -92,7 +138,7 @@ struct CfgQ {
 constexpr int DQ_THREADS = 320;
 
 struct UnitQ {
-  int bh, b, rt, j0, nk;   // row tile rt of key head bh; key tiles [j0, j0 + nk)
+  int bh, b, rt, j0, n;   // row tile rt of key head bh; key tiles [j0, j0 + n)
   int4 tile;
 };
 
@@ -104,7 +150,7 @@ __device__ __forceinline__ UnitQ load_unit_q(const Params& P, int x) {
   u.tile = u.rt < P.p.n_rt ? __ldg(P.plan.tiles + static_cast<long long>(u.b) * P.p.n_rt + u.rt)
                            : make_int4(0, 0, 0, 0);
   u.j0 = u.tile.y > 0 ? u.tile.x / BT : 0;
-  u.nk = u.tile.y > 0 ? (u.tile.y + BT - 1) / BT - u.j0 : 0;
+  u.n = u.tile.y > 0 ? (u.tile.y + BT - 1) / BT - u.j0 : 0;
   return u;
 }
 
@@ -191,16 +237,15 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       ++item;
       return true;
     };
-    int x = claim(P);
-    bool ok = uq_push(uq, pu++, x, w);
-    while (ok && x < P.total) {
-      const UnitQ u = load_unit_q(P, x);
-      x = claim(P);
-      if (!(ok = uq_push(uq, pu++, x, w))) break;
-      if (u.nk == 0) continue;
+    Next<UnitQ> cur, next;
+    bool ok = cur.first(P, load_unit_q, uq, &pu, w);
+    for (; ok && cur.x < P.total; cur = next) {
+      const UnitQ& u = cur.u;
       ok = load(&tmQ, u.rt * BT, u.bh) && load(&tmdO, u.rt * BT, u.bh) && load(&tmO, u.rt * BT, u.bh);
-      for (int j = 0; ok && j < u.nk; ++j)
+      for (int j = 0; ok && j < u.n; ++j) {
+        if (!(ok = next.step(P, j, u.n, load_unit_q, uq, &pu, w))) break;
         ok = load(&tmK, (u.j0 + j) * BT, u.bh) && load(&tmV, (u.j0 + j) * BT, u.bh);
+      }
     }
     if (!ok) {
       for (uint32_t n = (item > static_cast<uint32_t>(C::NSLOT) ? item - C::NSLOT : 0u); n < item; ++n)
@@ -234,18 +279,14 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     };
     uint32_t item = 0, u_it = 0, sp = 0, ru = 0;
     bool moved = false;
-    // key tiles of the next unit that has any, 0 at the end, -1 on a timeout
+    // key tiles of the next unit, 0 at the end, -1 on a timeout
     auto next_unit = [&]() {
-      for (;;) {
-        int x;
-        if (!uq_read(uq, ru, &x, w)) return -1;
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
-        ++ru;
-        if (x >= P.total) return 0;
-        const int nk = load_unit_q(P, x).nk;
-        if (nk > 0) return nk;
-      }
+      int x;
+      if (!uq_read(uq, ru, &x, w)) return -1;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+      ++ru;
+      return x >= P.total ? 0 : load_unit_q(P, x).n;
     };
     int nk = next_unit(), nk_next = 0;
     bool ok = nk >= 0;
@@ -271,11 +312,12 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       }
       __syncwarp();
       if (nk > 1 && !(ok = wait(full + slot(i0 + 5), par(i0 + 5)))) break;
-      // (published before this unit's tiles were loaded)
-      nk_next = next_unit();
-      ok = nk_next >= 0;
-      if (!ok) break;
       for (int j = 0; j < nk; ++j, ++sp) {
+        if (j + 1 == nk) {
+          nk_next = next_unit();
+          ok = nk_next >= 0;
+          if (!ok) break;
+        }
         const uint32_t ik = i0 + 3 + 2 * j;   // K_j; V_{j+1} = ik + 3, K_{j+1} = ik + 2, K_{j+2} = ik + 4
         if (j + 1 < nk) {
           if (!(ok = wait(s_free, sp & 1u))) break;
@@ -387,42 +429,28 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       ptx::mbar_arrive(qd_ready);
       return true;
     };
-    // the CTA's next unit with a key tile: 1, 0 at the end, -1 on a timeout;
-    // rows of a unit without one get their results here
+    // the next unit: 1, 0 at the end, -1 on a timeout (with what this
+    // thread's row needs: read one unit ahead, so that the loads' latency
+    // does not fall between units)
     uint32_t ru = 0;
-    // (with what this thread's row needs: read one unit ahead, so that the
-    // loads' latency does not fall between units)
     struct Mine {
       UnitQ u;
       int4 row;
       float lse, slope2;
     };
     auto next_unit = [&](Mine* m) {
-      for (;;) {
-        int x;
-        if (!uq_read(uq, ru, &x, w)) return -1;
-        ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
-        ++ru;
-        if (x >= P.total) return 0;
-        UnitQ* u = &m->u;
-        *u = load_unit_q(P, x);
-        if (u->rt >= P.p.n_rt) continue;
-        const int row = u->rt * BT + r;
-        if (u->nk > 0) {
-          m->row = __ldg(P.plan.rows + static_cast<long long>(u->b) * rpad + row);
-          m->lse = row < R ? __ldg(P.LSE + static_cast<long long>(u->bh) * R + row) : -CUDART_INF_F;
-          if (BIAS) m->slope2 = __ldg(P.plan.slope2 + static_cast<long long>(u->bh - u->b * P.p.Hkv) * rpad + row);
-          return 1;
-        }
-        if (g == 0) {
-          P.D[static_cast<long long>(u->bh) * rpad + row] = 0.f;
-          P.NL[static_cast<long long>(u->bh) * rpad + row] = -CUDART_INF_F;
-        }
-        if (row < R) {
-          uint4* q = reinterpret_cast<uint4*>(P.dQ + (static_cast<long long>(u->bh) * R + row) * d);
-          for (int c = g; c < d / 8; c += 2) q[c] = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
+      int x;
+      if (!uq_read(uq, ru, &x, w)) return -1;
+      ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+      ++ru;
+      if (x >= P.total) return 0;
+      const UnitQ u = load_unit_q(P, x);
+      const int row = u.rt * BT + r;
+      m->u = u;
+      m->row = __ldg(P.plan.rows + static_cast<long long>(u.b) * rpad + row);
+      m->lse = row < R ? __ldg(P.LSE + static_cast<long long>(u.bh) * R + row) : -CUDART_INF_F;
+      if (BIAS) m->slope2 = __ldg(P.plan.slope2 + static_cast<long long>(u.bh - u.b * P.p.Hkv) * rpad + row);
+      return 1;
     };
     uint32_t item = 0, u_it = 0, sp = 0;
     Mine me{}, nx{};
@@ -434,10 +462,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       const int row = u.rt * BT + r;
       const int4 ri = me.row;
       const float lse = me.lse, slope2 = me.slope2;
-      const int more = next_unit(&nx);
-      ok = more >= 0;
-      if (!ok) break;
-      const bool have_next = more == 1;
+      bool have_next = false;
       const float nlse2 = (lse == -CUDART_INF_F) ? -CUDART_INF_F : -lse * scored::kLog2e;
       const F2 nlv = dup(nlse2);
       if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dpart_full, u_it & 1u, w)))) break;
@@ -448,7 +473,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         P.D[static_cast<long long>(u.bh) * rpad + row] = dd;
         P.NL[static_cast<long long>(u.bh) * rpad + row] = nlse2;
       }
-      for (int j = 0; j < u.nk; ++j, ++sp) {
+      for (int j = 0; j < u.n; ++j, ++sp) {
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full, sp & 1u, w)))) break;
         ptx::tc_fence_after();
         float f[64];   // P T
@@ -522,6 +547,12 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
           for (int i = 0; i < 64; ++i)
             if (i < lo || i >= hi) f[i] = 0.f;
         }
+        if (j + 1 == u.n) {
+          const int more = next_unit(&nx);
+          ok = more >= 0;
+          if (!ok) break;
+          have_next = more == 1;
+        }
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dp_full, sp & 1u, w)))) break;
         ptx::tc_fence_after();
         uint32_t v[2][32];
@@ -546,7 +577,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       if (!ok) break;
       // the next unit's Q and dO go into TMEM now: the products that read
       // this unit's have completed (their results were consumed above)
-      const uint32_t i_next = item + 3 + 2 * u.nk;
+      const uint32_t i_next = item + 3 + 2 * u.n;
       if (have_next && !(ok = stage(i_next, u_it + 1))) break;
       if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dq_full, u_it & 1u, w)))) break;
       ptx::tc_fence_after();
@@ -617,26 +648,31 @@ struct CfgKV {
 };
 
 struct UnitKV {
-  int bh, b, kb, nq;       // key tile kb of key head bh, nq row tiles
-  const uint32_t* bits;    // the row tiles as bits
+  int bh, b, kb, part, n;   // part of the row tiles of key tile kb of key head bh, n row tiles
+  const uint32_t* bits;      // those of the key tile as bits
 };
 
 __device__ __forceinline__ UnitKV load_unit_kv(const Params& P, int x) {
   UnitKV u;
-  bwd::grouped_unit(x, P.n_blocks, P.p.B * P.p.Hkv, P.group, false, &u.bh, &u.kb);
+  int blk;
+  bwd::grouped_unit(x, P.n_blocks, P.p.B * P.p.Hkv, P.group, false, &u.bh, &blk);
+  u.kb = blk / P.p.kv_splits;
+  u.part = blk - u.kb * P.p.kv_splits;
   u.b = u.bh / P.p.Hkv;
   const long long at = static_cast<long long>(u.b) * P.p.n_kt + u.kb;
-  u.nq = __ldg(P.plan.kcount + at);
+  u.n = __ldg(P.plan.kcount + at * P.p.kv_splits + u.part);
   u.bits = P.plan.kbits + at * P.p.n_words();
   return u;
 }
 
-// Walks the set bits of a unit's list; the caller takes u.nq of them.
+// Walks the set bits of a list from bit `first` on; the caller takes a unit's n of them.
 struct TileList {
   const uint32_t* words;
   int base;
   uint32_t bits;
-  __device__ __forceinline__ explicit TileList(const uint32_t* w) : words(w), base(-32), bits(0u) {}
+  __device__ __forceinline__ TileList(const uint32_t* w, int first) : words(w + first / 32), base(first & ~31), bits(0u) {
+    if (w) bits = __ldg(words++) & (0xffffffffu << (first % 32));
+  }
   __device__ __forceinline__ int next() {
     while (bits == 0u) {
       base += 32;
@@ -763,13 +799,10 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
       ptx::tma_prefetch_desc(&tmV);
       ptx::tma_prefetch_desc(&tmdO);
       uint32_t u_it = 0, q_it = 0, q_issued = 0, o_issued = 0, l_issued = 0, pu = 0;
-      int x = claim(P);
-      bool ok = uq_push(uq, pu++, x, w);
-      while (ok && x < P.total) {
-        const UnitKV u = load_unit_kv(P, x);
-        x = claim(P);
-        if (!(ok = uq_push(uq, pu++, x, w))) break;
-        if (u.nq == 0) continue;
+      Next<UnitKV> cur, next;
+      bool ok = cur.first(P, load_unit_kv, uq, &pu, w);
+      for (; ok && cur.x < P.total; cur = next) {
+        const UnitKV& u = cur.u;
         if (!(ok = ptx::mbar_wait(kv_empty, (u_it & 1u) ^ 1u, w))) break;
         ptx::mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
         for (int c = 0; c < C::KB; ++c) {
@@ -777,8 +810,9 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
           ptx::tma_load_3d(sV + c * BOX_BYTES, &tmV, kv_full, c * 64, u.kb * BT, u.bh);
         }
         ++u_it;
-        TileList list(u.bits);
-        for (int ii = 0; ii < u.nq; ++ii, ++q_it) {
+        TileList list(u.bits, u.part * P.p.kv_split_tiles);
+        for (int ii = 0; ii < u.n; ++ii, ++q_it) {
+          if (!(ok = next.step(P, ii, u.n, load_unit_kv, uq, &pu, w))) break;
           const int rt = list.next();
           const int qs = qslot(q_it), os = oslot(q_it), ls = lslot(q_it);
           const long long row0 = static_cast<long long>(u.bh) * rpad + static_cast<long long>(rt) * BT;
@@ -836,18 +870,14 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
       };
       uint32_t u_it = 0, q_it = 0, pp = 0, ru = 0;
       bool moved = false;
-      // row tiles of the next unit that has any, 0 at the end, -1 on a timeout
+      // row tiles of the next unit, 0 at the end, -1 on a timeout
       auto next_unit = [&]() {
-        for (;;) {
-          int x;
-          if (!uq_read(uq, ru, &x, w)) return -1;
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
-          ++ru;
-          if (x >= P.total) return 0;
-          const int n = load_unit_kv(P, x).nq;
-          if (n > 0) return n;
-        }
+        int x;
+        if (!uq_read(uq, ru, &x, w)) return -1;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+        ++ru;
+        return x >= P.total ? 0 : load_unit_kv(P, x).n;
       };
       int nq = next_unit(), nq_next = 0;
       bool ok = nq >= 0;
@@ -870,11 +900,12 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         }
         __syncwarp();
         if (nq > 1 && !(ok = wait(q_full + qslot(q_it + 1), qpar(q_it + 1)))) break;
-        // (published before this unit's tiles were loaded)
-        nq_next = next_unit();
-        ok = nq_next >= 0;
-        if (!ok) break;
         for (int ii = 0; ii < nq; ++ii) {
+          if (ii + 1 == nq) {
+            nq_next = next_unit();
+            ok = nq_next >= 0;
+            if (!ok) break;
+          }
           const uint32_t it = q_it + ii;
           const bool more = ii + 1 < nq;
           // dV += P^T dO, then the next S^T (which overwrites P^T). A unit's
@@ -956,10 +987,10 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
       int even;
     };
     UnitKV wu{};
-    TileList wl(nullptr);
+    TileList wl(nullptr, 0);
     int wn = 0;
     auto advance = [&](Tile* t) {   // false on a timeout
-      while (wn == 0) {
+      if (wn == 0) {
         int x;
         if (!uq_read(uq, ru, &x, w)) return false;
         ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
@@ -970,8 +1001,8 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
           return true;
         }
         wu = load_unit_kv(P, x);
-        wl = TileList(wu.bits);
-        wn = wu.nq;
+        wl = TileList(wu.bits, wu.part * P.p.kv_split_tiles);
+        wn = wu.n;
       }
       if (wn < 0) {
         t->kb = -1;
@@ -1218,15 +1249,9 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
       if (x >= P.total) break;
       const UnitKV u = load_unit_kv(P, x);
       const int key = u.kb * BT + r;
-      const bool key_ok = key < Tk;
-      const long long at = static_cast<long long>(u.bh) * Tk + (key_ok ? key : 0);
-      if (u.nq == 0) {   // no row sees a key of the tile
-        if (key_ok) {
-          for (int c = 0; c < P.p.d / 8; ++c) reinterpret_cast<uint4*>(P.dK + at * P.p.d)[c] = make_uint4(0, 0, 0, 0);
-          for (int c = 0; c < P.p.dv / 8; ++c) reinterpret_cast<uint4*>(P.dV + at * P.p.dv)[c] = make_uint4(0, 0, 0, 0);
-        }
-        continue;
-      }
+      const bool parts = P.p.kv_splits > 1;
+      const long long head = static_cast<long long>(u.bh) * Tk;
+      const long long part_row = (static_cast<long long>(u.part) * P.p.B * P.p.Hkv + u.bh) * Tk;
       if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(acc_full, u_it & 1u, w)))) break;
       ptx::tc_fence_after();
 #pragma unroll
@@ -1234,27 +1259,46 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         const uint32_t tcol = tmem + lane_off + (acc ? T_DK : T_DV);
         const int width = acc ? P.p.d : P.p.dv;
         const int key4 = key & ~3;   // (see scored::quad_transpose)
-        __nv_bfloat16* out = (acc ? P.dK : P.dV) + (static_cast<long long>(u.bh) * Tk + key4) * width;
         const float mul = acc ? scale : 1.0f;
 #pragma unroll
         for (int c = 0; c < HD / 32; ++c) {
           uint32_t v[32];
           ptx::tmem_ld32(tcol + c * 32, v);
           ptx::tmem_ld_wait(v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * mul);
           uint4 pk[4];
+          if (parts) {   // fp32: 16 columns at a time
+            float* out = (acc ? P.dKpart : P.dVpart) + (part_row + key4) * width;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            pk[e].x = ptx::pack_bf16(__uint_as_float(v[8 * e + 0]) * mul, __uint_as_float(v[8 * e + 1]) * mul);
-            pk[e].y = ptx::pack_bf16(__uint_as_float(v[8 * e + 2]) * mul, __uint_as_float(v[8 * e + 3]) * mul);
-            pk[e].z = ptx::pack_bf16(__uint_as_float(v[8 * e + 4]) * mul, __uint_as_float(v[8 * e + 5]) * mul);
-            pk[e].w = ptx::pack_bf16(__uint_as_float(v[8 * e + 6]) * mul, __uint_as_float(v[8 * e + 7]) * mul);
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                pk[e] = make_uint4(v[16 * h + 4 * e], v[16 * h + 4 * e + 1], v[16 * h + 4 * e + 2], v[16 * h + 4 * e + 3]);
+              scored::quad_transpose(pk, lane);
+              const int col = 32 * c + 16 * h + 4 * (lane & 3);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (key4 + i < Tk && col < width)
+                  *reinterpret_cast<uint4*>(out + static_cast<long long>(i) * width + col) = pk[i];
+            }
+          } else {
+            __nv_bfloat16* out = (acc ? P.dK : P.dV) + (head + key4) * width;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t x[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                x[q] = ptx::pack_bf16(__uint_as_float(v[8 * e + 2 * q]), __uint_as_float(v[8 * e + 2 * q + 1]));
+              pk[e] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            scored::quad_transpose(pk, lane);
+            const int col = c * 32 + 8 * (lane & 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (key4 + i < Tk && col < width)
+                *reinterpret_cast<uint4*>(out + static_cast<long long>(i) * width + col) = pk[i];
           }
-          scored::quad_transpose(pk, lane);
-          const int col = c * 32 + 8 * (lane & 3);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (key4 + i < Tk && col < width)
-              *reinterpret_cast<uint4*>(out + static_cast<long long>(i) * width + col) = pk[i];
         }
         ptx::tc_fence_before();
         ptx::mbar_arrive(acc ? dk_free : dv_free);
@@ -1285,6 +1329,8 @@ cudaError_t launch(const ScoredBwd& a) {
   P.dQ = static_cast<__nv_bfloat16*>(a.dQ);
   P.dK = static_cast<__nv_bfloat16*>(a.dK);
   P.dV = static_cast<__nv_bfloat16*>(a.dV);
+  P.dKpart = a.dKpart;
+  P.dVpart = a.dVpart;
   P.status = a.status;
   P.sc2 = p.scale * scored::kLog2e;
   P.cap = scored::make_cap(p.scale, p.softcap);
@@ -1311,8 +1357,8 @@ cudaError_t launch(const ScoredBwd& a) {
   kq<<<P.total < a.num_sms ? P.total : a.num_sms, DQ_THREADS, CfgQ<HD>::SMEM, a.stream>>>(*a.tmQ, *a.tmK, *a.tmV,
                                                                                           *a.tmdO, *a.tmO, P);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  P.n_blocks = p.n_kt;
-  P.total = p.n_kt * heads;
+  P.n_blocks = p.n_kt * p.kv_splits;
+  P.total = P.n_blocks * heads;
   P.group = group(static_cast<size_t>(p.R) * ((p.d + p.dv) * 2 + 8));
   P.counter = a.plan.counters + 1;
   kk<<<P.total < a.num_sms ? P.total : a.num_sms, KV_THREADS, CfgKV<HD>::SMEM, a.stream>>>(*a.tmQ, *a.tmK, *a.tmV,

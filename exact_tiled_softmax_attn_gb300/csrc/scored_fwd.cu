@@ -184,21 +184,39 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ptx::tma_prefetch_desc(&tmV);
       uint32_t item = 0, u_it = 0, pu = 0;
       bool ok = true;
-      // a unit is claimed and published before the one before it is loaded
-      int x = min(static_cast<int>(atomicAdd(P.plan.counters, 1u)), P.total);
-      ok = uq_push(uq, pu++, x, w);
-      while (ok && x < P.total) {
-        const Unit u = load_unit(P, x);
-        x = min(static_cast<int>(atomicAdd(P.plan.counters, 1u)), P.total);
-        if (!(ok = uq_push(uq, pu++, x, w))) break;
-        if (u.hi == 0) continue;
+      // The units with keys alone are handed on (the plan kernel has written
+      // the others' rows). The next unit is claimed three key tiles before
+      // the end of this one, looked up two and published one tile before: see
+      // Next in scored_bwd.cu.
+      Unit u, un;
+      int x, xn = P.total;
+      auto claim = [&] { xn = min(static_cast<int>(atomicAdd(P.plan.counters, 1u)), P.total); };
+      auto look_up = [&] {
+        if (xn < P.total) un = load_unit(P, xn);
+      };
+      auto publish = [&] {   // past units without keys
+        while (xn < P.total && un.hi == 0) {
+          claim();
+          look_up();
+        }
+        return uq_push(uq, pu++, xn, w);
+      };
+      claim();
+      look_up();
+      ok = publish();
+      x = xn;
+      u = un;
+      for (; ok && x < P.total; x = xn, u = un) {
         if (!(ok = ptx::mbar_wait(q_empty, (u_it & 1u) ^ 1u, w))) break;
         ptx::mbar_arrive_expect_tx(q_full, 2 * C::TILE);
         for (int t = 0; t < 2; ++t)
           for (int c = 0; c < C::KB; ++c)
             ptx::tma_load_3d(sQ + t * C::TILE + c * BOX_BYTES, &tmQ, q_full, c * 64, (2 * u.qb + t) * BM, u.bh);
         ++u_it;
-        for (int j = u.s0; ok && j < u.e0; ++j)
+        for (int j = u.s0; ok && j < u.e0; ++j) {
+          if (j == max(u.e0 - 3, u.s0)) claim();
+          if (j == max(u.e0 - 2, u.s0)) look_up();
+          if (j == u.e0 - 1 && !(ok = publish())) break;
           for (int kv = 0; kv < 2; ++kv, ++item) {
             const int sl = slot(item);
             if (!(ok = ptx::mbar_wait(kv_empty + sl, par(item) ^ 1u, w))) break;
@@ -207,6 +225,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               ptx::tma_load_3d(sKV + sl * C::TILE + c * BOX_BYTES, kv ? &tmV : &tmK, kv_full + sl, c * 64, j * BN,
                                u.bh);
           }
+        }
       }
       if (!ok) {
         // let the copies in flight land before the CTA exits
@@ -244,16 +263,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       };
       uint32_t item = 0, u_it = 0, ru = 0, pp[2] = {0u, 0u};
       bool moved = false;
-      // the next unit with keys; false at the end (x = P.total) or on a timeout
+      // the next unit (x = P.total at the end); false on a timeout
       auto next_unit = [&](Unit* u, int* x) {
-        do {
-          if (!uq_read(uq, ru, x, w)) return false;
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
-          ++ru;
-          if (*x >= P.total) return true;
-          *u = load_unit(P, *x);
-        } while (u->hi == 0);
+        if (!uq_read(uq, ru, x, w)) return false;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+        ++ru;
+        if (*x < P.total) *u = load_unit(P, *x);
         return true;
       };
       int x;
@@ -276,8 +292,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // each step waits for the next step's tiles while its own MMAs run
         if (!(ok = wait(kv_full + slot(item + 1), par(item + 1)))) break;
         if (n > 1 && !(ok = wait(kv_full + slot(item + 2), par(item + 2)))) break;
-        if (!(ok = next_unit(&un, &x))) break;   // (published before this unit's keys were loaded)
         for (int j = u.s0; j < u.e0; ++j, item += 2) {
+          if (j + 1 == u.e0 && !(ok = next_unit(&un, &x))) break;
           const uint32_t iv = item + 1, ikn = item + 2;   // V_j, K_{j+1}: resident
 #pragma unroll
           for (int t = 0; t < 2; ++t) {

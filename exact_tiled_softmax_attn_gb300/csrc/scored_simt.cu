@@ -354,6 +354,7 @@ __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const S
                                                    const float* __restrict__ V, const float* __restrict__ LSE,
                                                    const float* __restrict__ dO, const float* __restrict__ D,
                                                    float* __restrict__ dK, float* __restrict__ dV) {
+  // (dK and dV: those of the parts where there are several)
   extern __shared__ __align__(16) float smem[];
   float* sQ = smem;
   float* sK = sQ + KM * Pitch<NCK>::v;
@@ -377,7 +378,8 @@ __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const S
     for (int e = 0; e < 4 * NCV; ++e) av[i][e] = 0.f;
   }
   const uint32_t* list = plan.kbits + (static_cast<long long>(b) * p.n_kt + k0 / kScoredTile) * p.n_words();
-  for (int r0 = 0; r0 < p.R; r0 += KM) {
+  const int rows = p.kv_split_tiles * kScoredTile, part = blockIdx.y;
+  for (int r0 = part * rows; r0 < min(p.R, (part + 1) * rows); r0 += KM) {
     const int rt = r0 / kScoredTile;
     if (!(list[rt / 32] >> (rt % 32) & 1u)) continue;
     const int4 hull = plan.tiles[static_cast<long long>(b) * p.n_rt + rt];
@@ -417,8 +419,9 @@ __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const S
   for (int i = 0; i < 4; ++i) {
     const int key = k0 + 4 * ky + i;
     if (key < p.Tk) {
-      store_row<NCK>(dK + (static_cast<long long>(bh) * p.Tk + key) * p.d, ak[i], p.scale, p.d);
-      store_row<NCV>(dV + (static_cast<long long>(bh) * p.Tk + key) * p.dv, av[i], 1.f, p.dv);
+      const long long at = (static_cast<long long>(part) * p.B * p.Hkv + bh) * p.Tk + key;
+      store_row<NCK>(dK + at * p.d, ak[i], p.scale, p.d);
+      store_row<NCV>(dV + at * p.dv, av[i], 1.f, p.dv);
     }
   }
 }
@@ -452,9 +455,10 @@ cudaError_t bwd(const ScoredBwd& a) {
   kq<<<(p.R + BM - 1) / BM * p.B * p.Hkv, NT, smem_q, a.stream>>>(p, a.plan, Q, K, V, static_cast<const float*>(a.O),
                                                                         a.LSE, dO, static_cast<float*>(a.dQ), a.D);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  kk<<<(p.Tk + KN - 1) / KN * p.B * p.Hkv, NT, smem_kv, a.stream>>>(p, a.plan, Q, K, V, a.LSE, dO, a.D,
-                                                                          static_cast<float*>(a.dK),
-                                                                          static_cast<float*>(a.dV));
+  const bool parts = p.kv_splits > 1;
+  kk<<<dim3((p.Tk + KN - 1) / KN * p.B * p.Hkv, p.kv_splits), NT, smem_kv, a.stream>>>(
+      p, a.plan, Q, K, V, a.LSE, dO, a.D, parts ? a.dKpart : static_cast<float*>(a.dK),
+      parts ? a.dVpart : static_cast<float*>(a.dV));
   return cudaGetLastError();
 }
 

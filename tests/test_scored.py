@@ -226,6 +226,8 @@ SHAPES = [  # B, H, Hkv, Tq, Tk, d, dv
     (1, 8, 1, 37, 500, 128, 128),
     (1, 2, 1, 513, 100, 80, 80),
     (1, 2, 2, 640, 640, 128, 128),
+    (1, 8, 1, 300, 260, 64, 64),      # long lists of row tiles for few key tiles: cut into parts
+    (2, 6, 1, 500, 200, 128, 80),
 ]
 
 
@@ -269,6 +271,49 @@ def test_rows_that_see_nothing(dtype):
     e = x[0][:, :, :0]
     dq, dk, dv = B.backward_scored(e, x[1], x[2], e, lse[:, :, :0], e)
     assert dq.numel() == 0 and not dk.any() and not dv.any()
+
+
+@pytest.mark.gpu
+def test_long_runs_of_idle_row_tiles():
+    """Most row tiles of every head see nothing, in runs longer than any queue between a kernel's warps; the live rows
+    give what they give without the idle ones (bit for bit, except for the order in dK's and dV's sums)."""
+    H, Tq, Tk, d = 64, 5000, 2200, 64
+    q, k, v, do = make(1, H, H, Tq, Tk, d, d, torch.bfloat16, 23)
+    live = (torch.arange(Tq) // 256) % 7 == 0
+    end = torch.where(live, Tk, 0).to(torch.int32)[None].cuda()
+    idx = live.nonzero()[:, 0].cuda()
+    o, lse = B.forward_scored(q, k, v, key_end=end)
+    dq, dk, dv = B.backward_scored(q, k, v, o, lse, do, key_end=end)
+    assert B.attn_device_status() == B.ATTN_OK
+    qc, doc = q[:, :, idx].contiguous(), do[:, :, idx].contiguous()
+    oc, lsec = B.forward_scored(qc, k, v)
+    gc = B.backward_scored(qc, k, v, oc, lsec, doc)
+    assert B.attn_device_status() == B.ATTN_OK
+    assert torch.equal(o[:, :, idx], oc) and torch.equal(lse[:, :, idx], lsec) and torch.equal(dq[:, :, idx], gc[0])
+    rest = (~live).nonzero()[:, 0].cuda()
+    assert not o[:, :, rest].any() and not dq[:, :, rest].any() and torch.isneginf(lse[:, :, rest]).all()
+    for a, b in ((dk, gc[1]), (dv, gc[2])):
+        assert frob_rel(a, b) <= 5e-3
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mask", ["causal", "wild"])
+def test_shared_key_heads_equal_repeated_ones(mask):
+    """16 query heads on 2 key heads, whose row tiles are cut into parts, against 16 key heads with repeated keys."""
+    H, Hkv, T, d = 16, 2, 2048, 64
+    q, k, v, do = make(1, H, Hkv, T, T, d, d, torch.bfloat16, 29)
+    how = how_of(mask, 0.0, True, 1, H, T, T)
+    o, lse = B.forward_scored(q, k, v, **how)
+    dq, dk, dv = B.backward_scored(q, k, v, o, lse, do, **how)
+    assert B.attn_device_status() == B.ATTN_OK
+    kr, vr = (t.repeat_interleave(H // Hkv, 1) for t in (k, v))
+    o2, lse2 = B.forward_scored(q, kr, vr, **how)
+    dq2, dk2, dv2 = B.backward_scored(q, kr, vr, o2, lse2, do, **how)
+    assert B.attn_device_status() == B.ATTN_OK
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(dq, dq2)
+    for a, b in ((dk, dk2), (dv, dv2)):
+        # each of the repeated heads' gradients is rounded once more
+        assert frob_rel(a, b.double().view(1, Hkv, H // Hkv, T, d).sum(2)) <= 5e-3
 
 
 @pytest.mark.gpu
