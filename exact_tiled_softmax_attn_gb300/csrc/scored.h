@@ -36,7 +36,7 @@ struct ScoredPlan {
   int4* tiles;     // [B][n_rt]: {min begin, max end over the rows that see keys, max begin, min end over all rows}
   int* kcount;     // [B][n_kt][kv_splits]: row tiles of the part whose hull meets the key tile (backward only), or null
   uint32_t* kbits; // [B][n_kt][n_words]: which they are, one bit each
-  int* even;       // [B][n_rt]: the position of a row tile's first row where its rows are of one head and at
+  int4* even;      // [B][n_rt]: in .x, the position of a row tile's first row where its rows are of one head and at
                    // consecutive positions, else kScoredUneven (backward with a bias only), or null
   float* slope2;   // [Hkv][rpad]: slope * log2(e) of each packed row (backward with a bias only), or null
   uint32_t* counters;   // two unit counters, zeroed

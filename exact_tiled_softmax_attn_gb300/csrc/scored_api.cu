@@ -128,7 +128,7 @@ Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
   if (bwd) {
     L.kcount = take(B * p.n_kt * p.kv_splits * sizeof(int));
     L.kbits = take(B * p.n_kt * p.n_words() * sizeof(uint32_t));
-    L.even = take(B * p.n_rt * sizeof(int));
+    L.even = take(B * p.n_rt * sizeof(int4));
     L.slope2 = take(p.Hkv * rpad * sizeof(float));
     L.D = take(heads * rpad * sizeof(float));
     L.NL = take(heads * rpad * sizeof(float));
@@ -157,7 +157,7 @@ ScoredPlan plan_at(const Layout& L, void* ws, bool bwd, bool bias) {
     s.kcount = reinterpret_cast<int*>(w + L.kcount);
     s.kbits = reinterpret_cast<uint32_t*>(w + L.kbits);
     if (bias) {
-      s.even = reinterpret_cast<int*>(w + L.even);
+      s.even = reinterpret_cast<int4*>(w + L.even);
       s.slope2 = reinterpret_cast<float*>(w + L.slope2);
     }
   }

@@ -28,6 +28,7 @@
 #include "ptx.cuh"
 #include "scored.h"
 #include "scored_math.cuh"
+#include "scored_queue.cuh"
 
 namespace attn {
 namespace scored_bwd {
@@ -36,9 +37,6 @@ using bwd::BOX_BYTES;
 using bwd::BT;
 using bwd::packed_col;
 using bwd::sw128_offset;
-using bwd::UnitQueue;
-using bwd::uq_push;
-using bwd::uq_read;
 using scored::Cap;
 using scored::add2;
 using scored::dup;
@@ -65,55 +63,13 @@ struct Params {
   Cap cap;
 };
 
-// The producer's next unit, found while the tiles of the current one are being
-// loaded. Only units that have something to do are handed on (the plan
-// kernels have written the others' results). A unit is claimed three tiles
-// before the end of the one before it, looked up two and published one tile
-// before, so that neither latency holds the loads up: late, because claims
-// further ahead leave the CTAs to end unevenly (two units ahead cost a tenth
-// of the time at 7 units a CTA), and early enough for the other roles to read
-// it while they work on the last tiles. A role that has the last tile of a
-// unit finds the next one published, so no wait for it can hold up the loads
-// that its publication waits for.
-template <typename U>
-struct Next {
-  int x;
-  U u;
-  __device__ __forceinline__ void claim(const Params& P) {
-    x = min(static_cast<int>(atomicAdd(P.counter, 1u)), P.total);
-  }
-  template <typename Load>
-  __device__ __forceinline__ void look_up(const Params& P, Load load) {
-    if (x < P.total) u = load(P, x);
-  }
-  template <typename Load>
-  __device__ __forceinline__ void settle(const Params& P, Load load) {   // past units without work
-    while (x < P.total && u.n == 0) {
-      claim(P);
-      look_up(P, load);
-    }
-  }
-  template <typename Load>
-  __device__ __forceinline__ bool first(const Params& P, Load load, const UnitQueue& q, uint32_t* pu,
-                                        const ptx::WaitCtx& w) {
-    claim(P);
-    look_up(P, load);
-    settle(P, load);
-    return uq_push(q, (*pu)++, x, w);
-  }
-  // the steps that fall before tile i of n
-  template <typename Load>
-  __device__ __forceinline__ bool step(const Params& P, int i, int n, Load load, const UnitQueue& q, uint32_t* pu,
-                                       const ptx::WaitCtx& w) {
-    if (i == max(n - 3, 0)) claim(P);
-    if (i == max(n - 2, 0)) look_up(P, load);
-    if (i != n - 1) return true;
-    settle(P, load);
-    return uq_push(q, (*pu)++, x, w);
-  }
-};
-
 // ---------------------------------------------------------------- dQ
+
+struct UnitQ {
+  int bh, b, rt, j0, n;   // row tile rt of key head bh; key tiles [j0, j0 + n)
+  int4 tile;
+};
+using RingQ = scored::UnitRing<UnitQ>;
 
 template <int HD>
 struct CfgQ {
@@ -126,21 +82,16 @@ struct CfgQ {
   static constexpr int OFF_DPART = OFF_RING + NSLOT * TILE;
   static constexpr int OFF_BAR = OFF_DPART + DPART_BYTES;
   // full[NSLOT], empty[NSLOT], qd_ready, s_full, s_free, dp_full, ds_full, dq_full, drain, dpart_full, unit queue
-  static constexpr int NBAR = 2 * NSLOT + 8 + 2 * UnitQueue::N;
+  static constexpr int NBAR = 2 * NSLOT + 8 + 2 * RingQ::N;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM = OFF_MISC + 16 + 4 * UnitQueue::N;
-  static constexpr int UQ_READERS = 1 + 256;
+  static constexpr int SMEM = OFF_MISC + 16 + RingQ::BYTES;
+  static constexpr int READERS = 1 + 256;
   static constexpr uint32_t IDESC_S = ptx::idesc_bf16(BT, BT, false, false);
   static constexpr uint32_t IDESC_DQ = ptx::idesc_bf16(BT, HD, false, true);
   // Q and dO as packed bf16, the S and dP tiles, the dQ accumulator
   static constexpr uint32_t T_Q = 0, T_DO = 64, T_S = 128, T_DP = 256, T_DQ = 384;
 };
 constexpr int DQ_THREADS = 320;
-
-struct UnitQ {
-  int bh, b, rt, j0, n;   // row tile rt of key head bh; key tiles [j0, j0 + n)
-  int4 tile;
-};
 
 __device__ __forceinline__ UnitQ load_unit_q(const Params& P, int x) {
   UnitQ u;
@@ -184,17 +135,13 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
   float* dpart = reinterpret_cast<float*>(smem + C::OFF_DPART);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 4);
-  const UnitQueue uq{reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16), qd_ready + 8,
-                     qd_ready + 8 + UnitQueue::N};
+  const RingQ units{reinterpret_cast<UnitQ*>(smem + C::OFF_MISC + 16), qd_ready + 8, qd_ready + 8 + RingQ::N};
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NSLOT; ++s) {
       ptx::mbar_init(full + s, 1);
       ptx::mbar_init(empty + s, 1);
     }
-    for (int s = 0; s < UnitQueue::N; ++s) {
-      ptx::mbar_init(uq.full + s, 1);
-      ptx::mbar_init(uq.empty + s, C::UQ_READERS);
-    }
+    units.init(C::READERS);
     ptx::mbar_init(qd_ready, 256);
     ptx::mbar_init(s_full, 1);
     ptx::mbar_init(s_free, 256);
@@ -237,13 +184,15 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       ++item;
       return true;
     };
-    Next<UnitQ> cur, next;
-    bool ok = cur.first(P, load_unit_q, uq, &pu, w);
-    for (; ok && cur.x < P.total; cur = next) {
+    auto look = [&](int x) { return load_unit_q(P, x); };
+    auto work = [](const UnitQ& u) { return u.n > 0; };
+    scored::NextUnit<UnitQ> cur{}, next{};
+    bool ok = cur.first(P.counter, P.total, look, work, units, &pu, w);
+    for (; ok && cur.u.bh >= 0; cur = next) {
       const UnitQ& u = cur.u;
       ok = load(&tmQ, u.rt * BT, u.bh) && load(&tmdO, u.rt * BT, u.bh) && load(&tmO, u.rt * BT, u.bh);
       for (int j = 0; ok && j < u.n; ++j) {
-        if (!(ok = next.step(P, j, u.n, load_unit_q, uq, &pu, w))) break;
+        if (!(ok = next.step(j, u.n, P.counter, P.total, look, work, units, &pu, w))) break;
         ok = load(&tmK, (u.j0 + j) * BT, u.bh) && load(&tmV, (u.j0 + j) * BT, u.bh);
       }
     }
@@ -281,12 +230,12 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     bool moved = false;
     // key tiles of the next unit, 0 at the end, -1 on a timeout
     auto next_unit = [&]() {
-      int x;
-      if (!uq_read(uq, ru, &x, w)) return -1;
+      UnitQ u;
+      if (!units.read(ru, &u, w)) return -1;
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+      if (lane == 0) ptx::mbar_arrive(units.empty + ru % RingQ::N);
       ++ru;
-      return x >= P.total ? 0 : load_unit_q(P, x).n;
+      return u.bh < 0 ? 0 : u.n;
     };
     int nk = next_unit(), nk_next = 0;
     bool ok = nk >= 0;
@@ -439,14 +388,12 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       float lse, slope2;
     };
     auto next_unit = [&](Mine* m) {
-      int x;
-      if (!uq_read(uq, ru, &x, w)) return -1;
-      ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+      if (!units.read(ru, &m->u, w)) return -1;
+      ptx::mbar_arrive(units.empty + ru % RingQ::N);
       ++ru;
-      if (x >= P.total) return 0;
-      const UnitQ u = load_unit_q(P, x);
+      const UnitQ& u = m->u;
+      if (u.bh < 0) return 0;
       const int row = u.rt * BT + r;
-      m->u = u;
       m->row = __ldg(P.plan.rows + static_cast<long long>(u.b) * rpad + row);
       m->lse = row < R ? __ldg(P.LSE + static_cast<long long>(u.bh) * R + row) : -CUDART_INF_F;
       if (BIAS) m->slope2 = __ldg(P.plan.slope2 + static_cast<long long>(u.bh - u.b * P.p.Hkv) * rpad + row);
@@ -625,6 +572,21 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
 constexpr int KV_THREADS = 512;
 constexpr int KV_REG_CTRL = 96, KV_REG_PDS = 168, KV_REG_EPI = 80, KV_REG_LAUNCH = 128;
 
+struct UnitKV {
+  int bh, b, kb, part, n;   // part of the row tiles of key tile kb of key head bh, n row tiles
+  const uint32_t* bits;      // those of the key tile as bits
+};
+using RingKV = scored::UnitRing<UnitKV>;
+
+// What the P / dS threads need of a row tile, in its slot of the slices' ring:
+// written by the producer (the first four) and copied from the plan.
+struct alignas(16) TileRec {
+  int kb, b, kvh, rt;   // kb < 0: the end
+  int4 hull;            // the plan's
+  int4 even;            // .x: position of the first row, or kScoredUneven
+  float4 slope2;        // .x: the first row's
+};
+
 template <int HD>
 struct CfgKV {
   static constexpr int KB = HD / 64;
@@ -636,20 +598,16 @@ struct CfgKV {
   static constexpr int OFF_DO = OFF_Q + NQ * TILE;
   static constexpr int OFF_LSE = OFF_DO + NO * TILE;
   static constexpr int OFF_D = OFF_LSE + NL * BT * 4;
-  static constexpr int OFF_BAR = OFF_D + NL * BT * 4;
+  static constexpr int OFF_REC = OFF_D + NL * BT * 4;
+  static constexpr int OFF_BAR = OFF_REC + NL * static_cast<int>(sizeof(TileRec));
   // kv_full, kv_empty, q_full[NQ], q_empty[NQ], o_full[NO], o_empty[NO], l_full[NL], l_empty[NL], s_full,
   // dp_full, p_full, ds_full, acc_full, dv_free, dk_free, drain, unit queue
-  static constexpr int NBAR = 2 + 2 * NQ + 2 * NO + 2 * NL + 8 + 2 * UnitQueue::N;
+  static constexpr int NBAR = 2 + 2 * NQ + 2 * NO + 2 * NL + 8 + 2 * RingKV::N;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM = OFF_MISC + 16 + 4 * UnitQueue::N;
-  static constexpr int UQ_READERS = 1 + 256 + 128;
+  static constexpr int SMEM = OFF_MISC + 16 + RingKV::BYTES;
+  static constexpr int READERS = 1 + 128;   // of the units: the MMA warp (once) and the epilogue threads
   static constexpr uint32_t IDESC_S = ptx::idesc_bf16(BT, BT, false, false);
   static constexpr uint32_t IDESC_ACC = ptx::idesc_bf16(BT, HD, false, true);
-};
-
-struct UnitKV {
-  int bh, b, kb, part, n;   // part of the row tiles of key tile kb of key head bh, n row tiles
-  const uint32_t* bits;      // those of the key tile as bits
 };
 
 __device__ __forceinline__ UnitKV load_unit_kv(const Params& P, int x) {
@@ -737,14 +695,11 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
   uint64_t* drain = s_full + 7;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 4);
-  const UnitQueue uq{reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16), s_full + 8,
-                     s_full + 8 + UnitQueue::N};
+  const RingKV units{reinterpret_cast<UnitKV*>(smem + C::OFF_MISC + 16), s_full + 8, s_full + 8 + RingKV::N};
+  TileRec* recs = reinterpret_cast<TileRec*>(smem + C::OFF_REC);   // [NL]
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < UnitQueue::N; ++s) {
-      ptx::mbar_init(uq.full + s, 1);
-      ptx::mbar_init(uq.empty + s, C::UQ_READERS);
-    }
+    units.init(C::READERS);
     ptx::mbar_init(kv_full, 1);
     ptx::mbar_init(kv_empty, 1);
     for (int s = 0; s < C::NQ; ++s) {
@@ -799,9 +754,11 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
       ptx::tma_prefetch_desc(&tmV);
       ptx::tma_prefetch_desc(&tmdO);
       uint32_t u_it = 0, q_it = 0, q_issued = 0, o_issued = 0, l_issued = 0, pu = 0;
-      Next<UnitKV> cur, next;
-      bool ok = cur.first(P, load_unit_kv, uq, &pu, w);
-      for (; ok && cur.x < P.total; cur = next) {
+      auto look = [&](int x) { return load_unit_kv(P, x); };
+      auto work = [](const UnitKV& u) { return u.n > 0; };
+      scored::NextUnit<UnitKV> cur{}, next{};
+      bool ok = cur.first(P.counter, P.total, look, work, units, &pu, w);
+      for (; ok && cur.u.bh >= 0; cur = next) {
         const UnitKV& u = cur.u;
         if (!(ok = ptx::mbar_wait(kv_empty, (u_it & 1u) ^ 1u, w))) break;
         ptx::mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
@@ -812,7 +769,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         ++u_it;
         TileList list(u.bits, u.part * P.p.kv_split_tiles);
         for (int ii = 0; ii < u.n; ++ii, ++q_it) {
-          if (!(ok = next.step(P, ii, u.n, load_unit_kv, uq, &pu, w))) break;
+          if (!(ok = next.step(ii, u.n, P.counter, P.total, look, work, units, &pu, w))) break;
           const int rt = list.next();
           const int qs = qslot(q_it), os = oslot(q_it), ls = lslot(q_it);
           const long long row0 = static_cast<long long>(u.bh) * rpad + static_cast<long long>(rt) * BT;
@@ -822,7 +779,19 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
             ptx::tma_load_3d(sQ + qs * C::TILE + c * BOX_BYTES, &tmQ, q_full + qs, c * 64, rt * BT, u.bh);
           q_issued = q_it + 1;
           if (!(ok = ptx::mbar_wait(l_empty + ls, lpar(q_it) ^ 1u, w))) break;
-          ptx::mbar_arrive_expect_tx(l_full + ls, 2 * BT * 4);
+          const int kvh = u.bh - u.b * P.p.Hkv;
+          const long long at = static_cast<long long>(u.b) * P.p.n_rt + rt;
+          TileRec* rec = recs + ls;
+          rec->kb = u.kb;
+          rec->b = u.b;
+          rec->kvh = kvh;
+          rec->rt = rt;
+          ptx::mbar_arrive_expect_tx(l_full + ls, 2 * BT * 4 + 16 + (BIAS ? 32 : 0));
+          ptx::bulk_load(&rec->hull, P.plan.tiles + at, 16, l_full + ls);
+          if (BIAS) {
+            ptx::bulk_load(&rec->even, P.plan.even + at, 16, l_full + ls);
+            ptx::bulk_load(&rec->slope2, P.plan.slope2 + static_cast<long long>(kvh) * rpad + rt * BT, 16, l_full + ls);
+          }
           ptx::bulk_load(sLSE + ls * BT, P.NL + row0, BT * 4, l_full + ls);
           ptx::bulk_load(sD + ls * BT, P.D + row0, BT * 4, l_full + ls);
           l_issued = q_it + 1;
@@ -832,6 +801,11 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
             ptx::tma_load_3d(sdO + os * C::TILE + c * BOX_BYTES, &tmdO, o_full + os, c * 64, rt * BT, u.bh);
           o_issued = q_it + 1;
         }
+      }
+      // the end for the P / dS threads: a record without slices
+      if (ok && (ok = ptx::mbar_wait(l_empty + lslot(q_it), lpar(q_it) ^ 1u, w))) {
+        recs[lslot(q_it)].kb = -1;
+        ptx::mbar_arrive(l_full + lslot(q_it));
       }
       if (!ok) {
         // let the copies in flight land before the CTA exits
@@ -872,12 +846,12 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
       bool moved = false;
       // row tiles of the next unit, 0 at the end, -1 on a timeout
       auto next_unit = [&]() {
-        int x;
-        if (!uq_read(uq, ru, &x, w)) return -1;
+        UnitKV u;
+        if (!units.read(ru, &u, w)) return -1;
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+        if (lane == 0) ptx::mbar_arrive(units.empty + ru % RingKV::N);
         ++ru;
-        return x >= P.total ? 0 : load_unit_kv(P, x).n;
+        return u.bh < 0 ? 0 : u.n;
       };
       int nq = next_unit(), nq_next = 0;
       bool ok = nq >= 0;
@@ -976,76 +950,43 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
     ptx::WaitCtx w{abort_flag, P.status, 3u};
     const float sc2 = P.sc2;
     const F2 sc2v = dup(sc2), ninv2 = dup(P.cap.ninv2), one = dup(1.f), neg1 = dup(-1.f);
-    uint32_t q_it = 0, ru = 0;
-    // A walk over the units and their row tiles two tiles ahead of the
-    // arithmetic: what a tile needs from memory (its row tile's hull, and for
-    // a partial tile its rows' ranges) is loaded while earlier ones are worked
-    // on. `Tile` is one step of it; kb < 0: the end.
+    // A row tile as these threads see it, from its record, and (for a partial
+    // tile, or one whose rows' positions are uneven) what its rows need,
+    // loaded as soon as the record is there: columns c and 32 + c of this
+    // group for lane c.
     struct Tile {
-      int kb, b, kvh, rt;
-      int4 hull;
-      int even;
-    };
-    UnitKV wu{};
-    TileList wl(nullptr, 0);
-    int wn = 0;
-    auto advance = [&](Tile* t) {   // false on a timeout
-      if (wn == 0) {
-        int x;
-        if (!uq_read(uq, ru, &x, w)) return false;
-        ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
-        ++ru;
-        if (x >= P.total) {
-          t->kb = -1;
-          wn = -1;
-          return true;
-        }
-        wu = load_unit_kv(P, x);
-        wl = TileList(wu.bits, wu.part * P.p.kv_split_tiles);
-        wn = wu.n;
-      }
-      if (wn < 0) {
-        t->kb = -1;
-        return true;
-      }
-      --wn;
-      t->kb = wu.kb;
-      t->b = wu.b;
-      t->kvh = wu.bh - wu.b * P.p.Hkv;
-      t->rt = wl.next();
-      const long long at = static_cast<long long>(wu.b) * P.p.n_rt + t->rt;
-      t->hull = __ldg(P.plan.tiles + at);
-      if constexpr (BIAS) t->even = __ldg(P.plan.even + at);
-      return true;
-    };
-    auto is_partial = [&](const Tile& t) { return t.kb * BT < t.hull.z || t.kb * BT + BT > t.hull.w; };
-    // columns c and 32 + c of this group, for lane c
-    struct Rows {
+      int kb, all_lo, all_hi, even;
+      float slope2;
       int4 r[2];
-      float slope2[2];
+      float cslope[2];
     };
-    auto load_rows = [&](const Tile& t, Rows* o) {
-      const bool uneven = BIAS && t.even == kScoredUneven;
-      if (!is_partial(t) && !uneven) return;
-      const int4* rows = P.plan.rows + static_cast<long long>(t.b) * rpad + t.rt * BT + 64 * h + lane;
-      o->r[0] = __ldg(rows);
-      o->r[1] = __ldg(rows + 32);
+    auto is_partial = [&](const Tile& t) { return t.kb * BT < t.all_lo || t.kb * BT + BT > t.all_hi; };
+    auto fetch = [&](uint32_t n, Tile* t) {   // once l_full says so
+      const TileRec* rec = recs + lslot(n);
+      t->kb = rec->kb;
+      if (t->kb < 0) return;
+      t->all_lo = rec->hull.z;
+      t->all_hi = rec->hull.w;
+      if constexpr (BIAS) {
+        t->even = rec->even.x;
+        t->slope2 = rec->slope2.x;
+      }
+      const bool uneven = BIAS && t->even == kScoredUneven;
+      if (!is_partial(*t) && !uneven) return;
+      const int row = rec->rt * BT + 64 * h + lane;
+      const int4* rows = P.plan.rows + static_cast<long long>(rec->b) * rpad + row;
+      t->r[0] = __ldg(rows);
+      t->r[1] = __ldg(rows + 32);
       if (uneven) {
-        const float* sl = P.plan.slope2 + static_cast<long long>(t.kvh) * rpad + t.rt * BT + 64 * h + lane;
-        o->slope2[0] = __ldg(sl);
-        o->slope2[1] = __ldg(sl + 32);
+        const float* sl = P.plan.slope2 + static_cast<long long>(rec->kvh) * rpad + row;
+        t->cslope[0] = __ldg(sl);
+        t->cslope[1] = __ldg(sl + 32);
       }
     };
+    uint32_t q_it = 0;
     Tile cur{}, nxt{};
-    Rows rows{};
-    float slope_cur = 0.f, slope_nxt = 0.f;
-    auto load_slope = [&](const Tile& t) {
-      return t.kb >= 0 ? __ldg(P.plan.slope2 + static_cast<long long>(t.kvh) * rpad + t.rt * BT) : 0.f;
-    };
-    bool ok = advance(&cur);
-    if (ok && cur.kb >= 0) load_rows(cur, &rows);
-    if (BIAS && ok) slope_cur = load_slope(cur);
-    if (ok) ok = advance(&nxt);
+    bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(l_full + lslot(0), lpar(0), w));
+    if (ok) fetch(0, &cur);
     {
       while (ok && cur.kb >= 0) {
         const int ls = lslot(q_it);
@@ -1061,30 +1002,13 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         if (partial) {
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            seen[c] = transpose32(scored::bit_range(rows.r[c].x - key0, rows.r[c].y - key0), lane);
+            seen[c] = transpose32(scored::bit_range(cur.r[c].x - key0, cur.r[c].y - key0), lane);
         }
         // bias: one slope and consecutive positions for the tile's rows (the
         // plan says), else each column's own, from lanes c and c + 32
-        float pos0 = 0.f, slope2 = 0.f, cslope[2];
-        int cpos[2];
-        bool even = true;
-        if constexpr (BIAS) {
-          even = cur.even != kScoredUneven;
-          pos0 = even ? static_cast<float>(key - cur.even - 64 * h) : 0.f;   // key - position of column 0
-          slope2 = slope_cur;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            cpos[c] = rows.r[c].z;
-            cslope[c] = rows.slope2[c];
-          }
-          slope_nxt = load_slope(nxt);
-        }
-        // the next tile's rows, and the tile after it
-        if (nxt.kb >= 0) load_rows(nxt, &rows);
-        const Tile after = nxt;
-        if (!(ok = advance(&nxt))) break;
-        // the staged slices of this tile are visible once l_full completed
-        if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(l_full + ls, lpar(q_it), w)))) break;
+        const bool even = !BIAS || cur.even != kScoredUneven;
+        const float pos0 = BIAS && even ? static_cast<float>(key - cur.even - 64 * h) : 0.f;   // key - position of column 0
+        const float slope2 = cur.slope2;
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full, q_it & 1u, w)))) break;
         ptx::tc_fence_after();
         // pass 1: P^T, packed bf16 over the first half of this group's S^T
@@ -1133,10 +1057,10 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
                     } else if constexpr (decltype(distance)::value == 1) {
                       add = f2(fmaf(-slope2, fabsf(pos0 - n0), add.x), fmaf(-slope2, fabsf(pos0 - n1), add.y));
                     } else {
-                      const int q0 = __shfl_sync(0xffffffffu, cpos[c], a),
-                                q1 = __shfl_sync(0xffffffffu, cpos[c], a + 1);
-                      const float s0 = __shfl_sync(0xffffffffu, cslope[c], a),
-                                  s1 = __shfl_sync(0xffffffffu, cslope[c], a + 1);
+                      const int q0 = __shfl_sync(0xffffffffu, cur.r[c].z, a),
+                                q1 = __shfl_sync(0xffffffffu, cur.r[c].z, a + 1);
+                      const float s0 = __shfl_sync(0xffffffffu, cur.cslope[c], a),
+                                  s1 = __shfl_sync(0xffffffffu, cur.cslope[c], a + 1);
                       add = f2(fmaf(-s0, fabsf(static_cast<float>(key - q0)), add.x),
                                fmaf(-s1, fabsf(static_cast<float>(key - q1)), add.y));
                     }
@@ -1194,6 +1118,10 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(p_full);
+        // the next tile's record, where it is there already (behind the last
+        // tile of a unit it waits for that tile's products)
+        const bool early = __all_sync(0xffffffffu, ptx::mbar_test(l_full + lslot(q_it + 1), lpar(q_it + 1)));
+        if (early) fetch(q_it + 1, &nxt);
         // pass 2: dS^T = P^T T (dP^T - D), bf16 over dP^T
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dp_full, q_it & 1u, w)))) break;
         ptx::tc_fence_after();
@@ -1225,9 +1153,12 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         ptx::tc_fence_before();
         ptx::mbar_arrive(ds_full);
         ptx::mbar_arrive(l_empty + ls);
-        cur = after;
-        slope_cur = slope_nxt;
         ++q_it;
+        if (!early) {
+          if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(l_full + lslot(q_it), lpar(q_it), w)))) break;
+          fetch(q_it, &nxt);
+        }
+        cur = nxt;
       }
     }
   } else {
@@ -1242,12 +1173,11 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
     uint32_t u_it = 0, ru = 0;
     bool ok = true;
     while (ok) {
-      int x;
-      if (!(ok = uq_read(uq, ru, &x, w))) break;
-      ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+      UnitKV u;
+      if (!(ok = units.read(ru, &u, w))) break;
+      ptx::mbar_arrive(units.empty + ru % RingKV::N);
       ++ru;
-      if (x >= P.total) break;
-      const UnitKV u = load_unit_kv(P, x);
+      if (u.bh < 0) break;
       const int key = u.kb * BT + r;
       const bool parts = P.p.kv_splits > 1;
       const long long head = static_cast<long long>(u.bh) * Tk;

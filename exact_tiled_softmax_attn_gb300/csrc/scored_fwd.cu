@@ -29,13 +29,11 @@
 #include "ptx.cuh"
 #include "scored.h"
 #include "scored_math.cuh"
+#include "scored_queue.cuh"
 
 namespace attn {
 namespace scored_fwd {
 
-using bwd::UnitQueue;
-using bwd::uq_push;
-using bwd::uq_read;
 using scored::Cap;
 using scored::add2;
 using scored::dup;
@@ -51,6 +49,14 @@ constexpr int NUM_THREADS = 384;
 constexpr int REG_CTRL = 96;
 constexpr int REG_SOFTMAX = 200;
 
+// A unit: the row tiles 2 qb and 2 qb + 1 of key head bh, the key tiles
+// [s[t], e[t]) of each, [s0, e0) of both, and the hull [lo, hi) of their keys.
+struct Unit {
+  int bh, b, qb, s[2], e[2], s0, e0, lo, hi;
+  int all_lo[2], all_hi[2];   // keys that every row of the tile sees
+};
+using Ring = scored::UnitRing<Unit>;
+
 // One tile width for Q, K, V and O rows: 64 where d and dv fit, else 128.
 template <int HD>
 struct Cfg {
@@ -62,10 +68,10 @@ struct Cfg {
   static constexpr int OFF_KV = OFF_Q + 2 * TILE;
   static constexpr int OFF_BAR = OFF_KV + NSLOT * TILE;
   // q_full, q_empty, full[NSLOT], empty[NSLOT], s_full[2], p_full[2], o_full[2], drain, unit queue
-  static constexpr int NBAR = 2 + 2 * NSLOT + 7 + 2 * UnitQueue::N;
+  static constexpr int NBAR = 2 + 2 * NSLOT + 7 + 2 * Ring::N;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM = OFF_MISC + 16 + 4 * UnitQueue::N;
-  static constexpr int UQ_READERS = 1 + 256;
+  static constexpr int SMEM = OFF_MISC + 16 + Ring::BYTES;
+  static constexpr int READERS = 1 + 256;
   static constexpr uint32_t IDESC_S = ptx::idesc_bf16(BM, BN, false, false);
   static constexpr uint32_t IDESC_PV = ptx::idesc_bf16(BM, HD, false, true);
 };
@@ -81,13 +87,6 @@ struct Params {
   Cap cap;
 };
 
-// A unit: the row tiles 2 qb and 2 qb + 1 of key head bh, the key tiles
-// [s[t], e[t]) of each, [s0, e0) of both, and the hull [lo, hi) of their keys.
-struct Unit {
-  int bh, b, qb, s[2], e[2], s0, e0, lo, hi;
-  int4 tile[2];
-};
-
 __device__ __forceinline__ Unit load_unit(const Params& P, int x) {
   Unit u;
   bwd::grouped_unit(x, P.n_pairs, P.p.B * P.p.Hkv, P.group, true, &u.bh, &u.qb);
@@ -98,14 +97,16 @@ __device__ __forceinline__ Unit load_unit(const Params& P, int x) {
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int rt = 2 * u.qb + t;
-    u.tile[t] = rt < P.p.n_rt ? __ldg(P.plan.tiles + static_cast<long long>(u.b) * P.p.n_rt + rt)
-                              : make_int4(0, 0, 0x7fffffff, 0);
-    const bool live = u.tile[t].y > 0;
-    u.s[t] = live ? u.tile[t].x / BN : 0;
-    u.e[t] = live ? (u.tile[t].y + BN - 1) / BN : 0;
+    const int4 tile = rt < P.p.n_rt ? __ldg(P.plan.tiles + static_cast<long long>(u.b) * P.p.n_rt + rt)
+                                    : make_int4(0, 0, 0x7fffffff, 0);
+    const bool live = tile.y > 0;
+    u.s[t] = live ? tile.x / BN : 0;
+    u.e[t] = live ? (tile.y + BN - 1) / BN : 0;
+    u.all_lo[t] = tile.z;
+    u.all_hi[t] = tile.w;
     if (live) {
-      u.lo = min(u.lo, u.tile[t].x);
-      u.hi = max(u.hi, u.tile[t].y);
+      u.lo = min(u.lo, tile.x);
+      u.hi = max(u.hi, tile.y);
     }
   }
   u.s0 = u.hi > 0 ? u.lo / BN : 0;
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint64_t* drain = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 4);
-  const UnitQueue uq{reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16), drain + 1, drain + 1 + UnitQueue::N};
+  const Ring ring{reinterpret_cast<Unit*>(smem + C::OFF_MISC + 16), drain + 1, drain + 1 + Ring::N};
 
   if (threadIdx.x == 0) {
     ptx::mbar_init(q_full, 1);
@@ -153,10 +154,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ptx::mbar_init(o_full + t, 1);
     }
     ptx::mbar_init(drain, 1);
-    for (int s = 0; s < UnitQueue::N; ++s) {
-      ptx::mbar_init(uq.full + s, 1);
-      ptx::mbar_init(uq.empty + s, C::UQ_READERS);
-    }
+    ring.init(C::READERS);
     *abort_flag = 0u;
     ptx::fence_mbar_init();
   }
@@ -184,29 +182,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ptx::tma_prefetch_desc(&tmV);
       uint32_t item = 0, u_it = 0, pu = 0;
       bool ok = true;
-      // The units with keys alone are handed on (the plan kernel has written
-      // the others' rows). The next unit is claimed three key tiles before
-      // the end of this one, looked up two and published one tile before: see
-      // Next in scored_bwd.cu.
-      Unit u, un;
-      int x, xn = P.total;
-      auto claim = [&] { xn = min(static_cast<int>(atomicAdd(P.plan.counters, 1u)), P.total); };
-      auto look_up = [&] {
-        if (xn < P.total) un = load_unit(P, xn);
-      };
-      auto publish = [&] {   // past units without keys
-        while (xn < P.total && un.hi == 0) {
-          claim();
-          look_up();
-        }
-        return uq_push(uq, pu++, xn, w);
-      };
-      claim();
-      look_up();
-      ok = publish();
-      x = xn;
-      u = un;
-      for (; ok && x < P.total; x = xn, u = un) {
+      auto load = [&](int x) { return load_unit(P, x); };
+      auto work = [](const Unit& u) { return u.hi > 0; };
+      scored::NextUnit<Unit> cur{}, next{};
+      ok = cur.first(P.plan.counters, P.total, load, work, ring, &pu, w);
+      for (; ok && cur.u.bh >= 0; cur = next) {
+        const Unit& u = cur.u;
         if (!(ok = ptx::mbar_wait(q_empty, (u_it & 1u) ^ 1u, w))) break;
         ptx::mbar_arrive_expect_tx(q_full, 2 * C::TILE);
         for (int t = 0; t < 2; ++t)
@@ -214,9 +195,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ptx::tma_load_3d(sQ + t * C::TILE + c * BOX_BYTES, &tmQ, q_full, c * 64, (2 * u.qb + t) * BM, u.bh);
         ++u_it;
         for (int j = u.s0; ok && j < u.e0; ++j) {
-          if (j == max(u.e0 - 3, u.s0)) claim();
-          if (j == max(u.e0 - 2, u.s0)) look_up();
-          if (j == u.e0 - 1 && !(ok = publish())) break;
+          if (!(ok = next.step(j - u.s0, u.e0 - u.s0, P.plan.counters, P.total, load, work, ring, &pu, w))) break;
           for (int kv = 0; kv < 2; ++kv, ++item) {
             const int sl = slot(item);
             if (!(ok = ptx::mbar_wait(kv_empty + sl, par(item) ^ 1u, w))) break;
@@ -263,19 +242,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       };
       uint32_t item = 0, u_it = 0, ru = 0, pp[2] = {0u, 0u};
       bool moved = false;
-      // the next unit (x = P.total at the end); false on a timeout
-      auto next_unit = [&](Unit* u, int* x) {
-        if (!uq_read(uq, ru, x, w)) return false;
+      auto next_unit = [&](Unit* u) {
+        if (!ring.read(ru, u, w)) return false;
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+        if (lane == 0) ptx::mbar_arrive(ring.empty + ru % Ring::N);
         ++ru;
-        if (*x < P.total) *u = load_unit(P, *x);
         return true;
       };
-      int x;
       Unit u, un;
-      bool ok = next_unit(&u, &x);
-      while (ok && x < P.total) {
+      bool ok = next_unit(&u);
+      while (ok && u.bh >= 0) {
         const int n = u.e0 - u.s0;
         if (!(ok = wait(q_full, u_it & 1u))) break;
         if (!(ok = wait(kv_full + slot(item), par(item)))) break;
@@ -293,7 +269,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!(ok = wait(kv_full + slot(item + 1), par(item + 1)))) break;
         if (n > 1 && !(ok = wait(kv_full + slot(item + 2), par(item + 2)))) break;
         for (int j = u.s0; j < u.e0; ++j, item += 2) {
-          if (j + 1 == u.e0 && !(ok = next_unit(&un, &x))) break;
+          if (j + 1 == u.e0 && !(ok = next_unit(&un))) break;
           const uint32_t iv = item + 1, ikn = item + 2;   // V_j, K_{j+1}: resident
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -349,7 +325,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // and slope. The next one is read before this one's epilogue, which
     // covers the loads.
     struct Mine {
-      int x, bh, row;              // row: of this thread; n_rt * 128 where the tile does not exist
+      int bh, row;                 // bh < 0: the end; row: of this thread; n_rt * 128 where the tile does not exist
       int s0, items;               // the unit's first key tile, its K/V items
       int s, e;                    // this row tile's key tiles
       int lo, hi;                  // hull of the unit's keys
@@ -358,20 +334,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       float slope2;
     };
     auto next_unit = [&](Mine* m) {
-      if (!uq_read(uq, ru, &m->x, w)) return false;
-      ptx::mbar_arrive(uq.empty + ru % UnitQueue::N);
+      Unit u;
+      if (!ring.read(ru, &u, w)) return false;
+      ptx::mbar_arrive(ring.empty + ru % Ring::N);
       ++ru;
-      if (m->x >= P.total) return true;
-      const Unit u = load_unit(P, m->x);
       m->bh = u.bh;
+      if (u.bh < 0) return true;
       m->s0 = u.s0;
       m->items = 2 * (u.e0 - u.s0);
       m->lo = u.lo;
       m->hi = u.hi;
       m->s = t ? u.s[1] : u.s[0];
       m->e = t ? u.e[1] : u.e[0];
-      m->all_lo = t ? u.tile[1].z : u.tile[0].z;
-      m->all_hi = t ? u.tile[1].w : u.tile[0].w;
+      m->all_lo = t ? u.all_lo[1] : u.all_lo[0];
+      m->all_hi = t ? u.all_hi[1] : u.all_hi[0];
       m->row = min(2 * u.qb + t, P.p.n_rt) * BM + r;
       if (2 * u.qb + t < P.p.n_rt) {
         const int4 ri = __ldg(P.plan.rows + static_cast<long long>(u.b) * P.p.rpad() + m->row);
@@ -386,7 +362,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     };
     Mine me{}, nx{};
     bool ok = next_unit(&me);
-    while (ok && me.x < P.total) {
+    while (ok && me.bh >= 0) {
       const int s_t = me.s, e_t = me.e;
       const float slope2 = me.slope2;
       float m_used = -CUDART_INF_F, l = 0.f;

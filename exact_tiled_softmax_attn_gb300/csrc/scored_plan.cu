@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kScoredTile) plan_rows_kernel(const ScoredProb
     const int head0 = tile * kScoredTile / p.Tq;
     const bool same = !valid || (pos == first + static_cast<int>(threadIdx.x) && row / p.Tq == head0);
     const bool all = __syncthreads_and(same);
-    if (threadIdx.x == 0) out.even[b * static_cast<long long>(p.n_rt) + tile] = all ? first : kScoredUneven;
+    if (threadIdx.x == 0) out.even[b * static_cast<long long>(p.n_rt) + tile] = make_int4(all ? first : kScoredUneven, 0, 0, 0);
   }
   // hull over the rows that see keys; the keys that every row sees
   int v[4] = {lo, -hi, valid ? -lo : -INT_MAX, valid ? hi : INT_MAX};   // minima of all four
