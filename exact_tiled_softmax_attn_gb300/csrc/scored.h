@@ -131,7 +131,7 @@ cudaError_t launch_scored_bwd_bf16(const ScoredBwd& a);
 // dK and dV from the parts of their row tiles, in order
 cudaError_t launch_scored_kv_sum(const ScoredBwd& a, bool bf16);
 
-// fp32 O and LSE from the partial results of the key ranges, in range order
-cudaError_t launch_scored_merge(const ScoredFwd& a);
+// O and LSE from the partial results of the key ranges, in range order
+cudaError_t launch_scored_merge(const ScoredFwd& a, bool bf16);
 
 }  // namespace attn

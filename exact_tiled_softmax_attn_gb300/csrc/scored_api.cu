@@ -78,11 +78,16 @@ ScoredProblem problem(int B, int H, int Hkv, int Tq, int Tk, int d, int dv, attn
   return p;
 }
 
-// Key ranges of the forward: the CUDA-core kernel runs about four 32-row tiles
-// per SM at a time.
-void fwd_splits(const ScoredProblem& p, int* S, int* keys) {
-  const long long units = static_cast<long long>(p.B) * p.Hkv * ((p.R + 31) / 32);
-  const int want = wave_splits(units, p.n_kt, 4 * kSms);
+// Key ranges of the forward, for problems with few units: the fp32 kernel
+// runs about four 32-row tiles per SM at a time, the tensor-core kernel one
+// pair of 128-row tiles, and splits only where the pairs do not fill the SMs.
+void fwd_splits(const ScoredProblem& p, attn_dtype_t dt, int* S, int* keys) {
+  const long long heads = static_cast<long long>(p.B) * p.Hkv;
+  int want = 1;
+  if (dt == ATTN_F32)
+    want = wave_splits(heads * ((p.R + 31) / 32), p.n_kt, 4 * kSms);
+  else if (heads * ((p.R + 255) / 256) < kSms)
+    want = wave_splits(heads * ((p.R + 255) / 256), p.n_kt, kSms);
   const int tiles = want > 1 ? (p.n_kt + want - 1) / want : p.n_kt;
   *S = want > 1 ? (p.n_kt + tiles - 1) / tiles : 1;
   *keys = tiles * kScoredTile;
@@ -137,7 +142,7 @@ Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
       L.dvpart = take(p.kv_splits * heads * p.Tk * p.dv * sizeof(float));
     }
   } else {
-    if (dt == ATTN_F32) fwd_splits(p, &L.n_splits, &L.split_keys);
+    fwd_splits(p, dt, &L.n_splits, &L.split_keys);
     if (L.n_splits > 1) {
       L.opart = take(L.n_splits * heads * p.R * p.dv * sizeof(float));
       L.lsepart = take(L.n_splits * heads * p.R * sizeof(float));
@@ -268,10 +273,10 @@ attn_status_t attn_fwd_scored(const void* Q, const void* K, const void* V, void*
   }
   if (tokens) {
     e = launch_scored_tokens_bf16(a);
-  } else if ((e = launch_scored_plan(a.p, a.mask, a.plan, bf16 ? ScoredIdle{O, LSE} : ScoredIdle{}, st)) ==
+  } else if ((e = launch_scored_plan(a.p, a.mask, a.plan, bf16 && L.n_splits == 1 ? ScoredIdle{O, LSE} : ScoredIdle{}, st)) ==
              cudaSuccess) {
     e = bf16 ? launch_scored_fwd_bf16(a) : launch_scored_fwd_simt(a);
-    if (e == cudaSuccess && a.n_splits > 1) e = launch_scored_merge(a);
+    if (e == cudaSuccess && a.n_splits > 1) e = launch_scored_merge(a, bf16);
   }
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }

@@ -657,7 +657,8 @@ __device__ __forceinline__ uint32_t transpose32(uint32_t x, int lane) {
 // Warps: 0 producer, 1 MMA, 4-7 and 8-11 P / dS (a thread per key; group h
 // works on query columns [64 h, 64 h + 64)), 12-15 epilogue.
 // TMEM: dV [0, 128), dK [128, 256), S^T [256, 384), dP^T [384, 512).
-template <int HD, bool CAP, bool BIAS>
+// PARTS: units are parts of a key tile's row tiles, with partial results.
+template <int HD, bool CAP, bool BIAS, bool PARTS>
 __global__ void __launch_bounds__(KV_THREADS, 1)
     dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -1179,7 +1180,6 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
       ++ru;
       if (u.bh < 0) break;
       const int key = u.kb * BT + r;
-      const bool parts = P.p.kv_splits > 1;
       const long long head = static_cast<long long>(u.bh) * Tk;
       const long long part_row = (static_cast<long long>(u.part) * P.p.B * P.p.Hkv + u.bh) * Tk;
       if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(acc_full, u_it & 1u, w)))) break;
@@ -1198,7 +1198,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * mul);
           uint4 pk[4];
-          if (parts) {   // fp32: 16 columns at a time
+          if constexpr (PARTS) {   // fp32: 16 columns at a time
             float* out = (acc ? P.dKpart : P.dVpart) + (part_row + key4) * width;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -1271,7 +1271,7 @@ cudaError_t launch(const ScoredBwd& a) {
     return static_cast<int>(g < 1 ? 1 : g > static_cast<size_t>(heads) ? heads : g);
   };
   auto kq = dq_kernel<HD, CAP, BIAS>;
-  auto kk = dkdv_kernel<HD, CAP, BIAS>;
+  auto kk = p.kv_splits > 1 ? dkdv_kernel<HD, CAP, BIAS, true> : dkdv_kernel<HD, CAP, BIAS, false>;
   cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgQ<HD>::SMEM);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgKV<HD>::SMEM);

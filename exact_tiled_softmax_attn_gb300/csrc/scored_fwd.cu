@@ -51,8 +51,10 @@ constexpr int REG_SOFTMAX = 200;
 
 // A unit: the row tiles 2 qb and 2 qb + 1 of key head bh, the key tiles
 // [s[t], e[t]) of each, [s0, e0) of both, and the hull [lo, hi) of their keys.
+// With few units the key tiles are cut into ranges (splits), as units of their
+// own: the tiles are then those of the unit's range.
 struct Unit {
-  int bh, b, qb, s[2], e[2], s0, e0, lo, hi;
+  int bh, b, qb, split, s[2], e[2], s0, e0, lo, hi;
   int all_lo[2], all_hi[2];   // keys that every row of the tile sees
 };
 using Ring = scored::UnitRing<Unit>;
@@ -85,12 +87,16 @@ struct Params {
   int n_pairs, total, group;
   float sc2;   // scale * log2(e)
   Cap cap;
+  int n_splits, split_tiles;
+  float* Opart;     // [n_splits][B * Hkv * R][dv]
+  float* LSEpart;   // [n_splits][B * Hkv * R]
 };
 
 __device__ __forceinline__ Unit load_unit(const Params& P, int x) {
   Unit u;
-  bwd::grouped_unit(x, P.n_pairs, P.p.B * P.p.Hkv, P.group, true, &u.bh, &u.qb);
-  u.qb = scored::packed_block(u.qb, P.n_pairs, P.p.G);
+  bwd::grouped_unit(x, P.n_pairs * P.n_splits, P.p.B * P.p.Hkv, P.group, true, &u.bh, &u.qb);
+  u.split = u.qb % P.n_splits;
+  u.qb = scored::packed_block(u.qb / P.n_splits, P.n_pairs, P.p.G);
   u.b = u.bh / P.p.Hkv;
   u.lo = 0x7fffffff;
   u.hi = 0;
@@ -100,8 +106,8 @@ __device__ __forceinline__ Unit load_unit(const Params& P, int x) {
     const int4 tile = rt < P.p.n_rt ? __ldg(P.plan.tiles + static_cast<long long>(u.b) * P.p.n_rt + rt)
                                     : make_int4(0, 0, 0x7fffffff, 0);
     const bool live = tile.y > 0;
-    u.s[t] = live ? tile.x / BN : 0;
-    u.e[t] = live ? (tile.y + BN - 1) / BN : 0;
+    u.s[t] = live ? max(tile.x / BN, u.split * P.split_tiles) : 0;
+    u.e[t] = live ? max(min((tile.y + BN - 1) / BN, (u.split + 1) * P.split_tiles), u.s[t]) : 0;
     u.all_lo[t] = tile.z;
     u.all_hi[t] = tile.w;
     if (live) {
@@ -109,12 +115,13 @@ __device__ __forceinline__ Unit load_unit(const Params& P, int x) {
       u.hi = max(u.hi, tile.y);
     }
   }
-  u.s0 = u.hi > 0 ? u.lo / BN : 0;
-  u.e0 = (u.hi + BN - 1) / BN;
+  u.s0 = u.hi > 0 ? max(u.lo / BN, u.split * P.split_tiles) : 0;
+  u.e0 = max(min((u.hi + BN - 1) / BN, (u.split + 1) * P.split_tiles), u.s0);
   return u;
 }
 
-template <int HD, bool CAP, bool BIAS>
+// SPLIT: key ranges as units of their own, with partial results.
+template <int HD, bool CAP, bool BIAS, bool SPLIT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     scored_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params P) {
@@ -183,7 +190,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t item = 0, u_it = 0, pu = 0;
       bool ok = true;
       auto load = [&](int x) { return load_unit(P, x); };
-      auto work = [](const Unit& u) { return u.hi > 0; };
+      auto work = [](const Unit& u) { return u.e0 > u.s0; };
       scored::NextUnit<Unit> cur{}, next{};
       ok = cur.first(P.plan.counters, P.total, load, work, ring, &pu, w);
       for (; ok && cur.u.bh >= 0; cur = next) {
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // and slope. The next one is read before this one's epilogue, which
     // covers the loads.
     struct Mine {
-      int bh, row;                 // bh < 0: the end; row: of this thread; n_rt * 128 where the tile does not exist
+      int bh, split, row;          // bh < 0: the end; row: of this thread; n_rt * 128 where the tile does not exist
       int s0, items;               // the unit's first key tile, its K/V items
       int s, e;                    // this row tile's key tiles
       int lo, hi;                  // hull of the unit's keys
@@ -340,6 +347,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ++ru;
       m->bh = u.bh;
       if (u.bh < 0) return true;
+      if (SPLIT) m->split = u.split;
       m->s0 = u.s0;
       m->items = 2 * (u.e0 - u.s0);
       m->lo = u.lo;
@@ -602,13 +610,34 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const float lse = (l > 0.f) ? (m_used + log2f(l)) * 0.69314718055994530942f : -CUDART_INF_F;
       // the four rows of this lane's quad, of which it stores every fourth 16-byte piece
       const int row4 = me.row & ~3;
-      __nv_bfloat16* out = P.O + (static_cast<long long>(me.bh) * R + row4) * dv;
+      const long long head = static_cast<long long>(me.bh) * R;
+      const long long part = SPLIT ? static_cast<long long>(me.split) * P.p.B * P.p.Hkv * R + head : 0;
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
         uint32_t o[32];
         ptx::tmem_ld32(tO + c * 32, o);
         ptx::tmem_ld_wait(o);
         uint4 pk[4];
+        if constexpr (SPLIT) {   // partial rows, fp32: 16 columns at a time
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[e] = l > 0.f ? __float_as_uint(__uint_as_float(o[16 * h + 4 * i + e]) * inv_l) : 0u;
+              pk[i] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+            scored::quad_transpose(pk, lane);
+            const int col = 32 * c + 16 * h + 4 * (lane & 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (row4 + i < R && col < dv)
+                *reinterpret_cast<uint4*>(P.Opart + (part + row4 + i) * dv + col) = pk[i];
+          }
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t v[4];
@@ -623,9 +652,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int col = 32 * c + 8 * (lane & 3);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (row4 + i < R && col < dv) *reinterpret_cast<uint4*>(out + static_cast<long long>(i) * dv + col) = pk[i];
+          if (row4 + i < R && col < dv) *reinterpret_cast<uint4*>(P.O + (head + row4 + i) * dv + col) = pk[i];
       }
-      if (me.row < R) P.LSE[static_cast<long long>(me.bh) * R + me.row] = lse;
+      if (me.row < R) (SPLIT ? P.LSEpart + part : P.LSE + head)[me.row] = lse;
       ptx::tc_fence_before();
       me = nx;
     }
@@ -653,13 +682,17 @@ cudaError_t launch(const ScoredFwd& a) {
   P.cap = scored::make_cap(a.p.scale, a.p.softcap);
   const int heads = a.p.B * a.p.Hkv;
   P.n_pairs = scored::packed_blocks((a.p.n_rt + 1) / 2, a.p.G);
-  P.total = P.n_pairs * heads;
+  P.n_splits = a.n_splits;
+  P.split_tiles = a.split_keys / BN;
+  P.Opart = a.Opart;
+  P.LSEpart = a.LSEpart;
+  P.total = P.n_pairs * P.n_splits * heads;
   // heads in groups whose keys and values fill about half of L2
   const size_t per_head = static_cast<size_t>(a.p.Tk) * (a.p.d + a.p.dv) * 2;
   size_t g = per_head * heads <= 2 * a.l2_bytes ? heads : a.l2_bytes / 2 / per_head;
   P.group = static_cast<int>(g < 1 ? 1 : g > static_cast<size_t>(heads) ? heads : g);
   const int grid = P.total < a.num_sms ? P.total : a.num_sms;
-  auto kern = scored_fwd_kernel<HD, CAP, BIAS>;
+  auto kern = a.n_splits > 1 ? scored_fwd_kernel<HD, CAP, BIAS, true> : scored_fwd_kernel<HD, CAP, BIAS, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   // the register split must fit the launch allocation (see ptx::reg_acquire)

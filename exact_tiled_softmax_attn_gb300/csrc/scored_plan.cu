@@ -153,28 +153,46 @@ __global__ void __launch_bounds__(256) kv_sum_kernel(const ScoredProblem p, cons
   }
 }
 
-// One warp per row; every lane holds the row's weights' sum.
-__global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ Opart,
-                                                    const float* __restrict__ LSEpart, float* __restrict__ O,
-                                                    float* __restrict__ LSE, long long rows, int dv, int n_splits) {
+// O and LSE from the key ranges' partial results, in range order; one warp
+// per row. TENSOR: the ranges of the tensor-core kernel, which writes a
+// range's results only where the row's pair of row tiles has keys in it.
+template <typename T, bool TENSOR>
+__global__ void __launch_bounds__(256) merge_kernel(const ScoredProblem p, const int4* __restrict__ tiles,
+                                                    const float* __restrict__ Opart,
+                                                    const float* __restrict__ LSEpart, T* __restrict__ O,
+                                                    float* __restrict__ LSE, int n_splits, int split_keys) {
   const int lane = threadIdx.x & 31;
+  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.R;
   const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 5;
   if (r >= rows) return;
+  int first = 0, last = n_splits - 1;   // ranges with results
+  if constexpr (TENSOR) {
+    const int bh = static_cast<int>(r / p.R), pair = static_cast<int>(r - static_cast<long long>(bh) * p.R) / 256;
+    const int4* t = tiles + static_cast<long long>(bh / p.Hkv) * p.n_rt + 2 * pair;
+    int4 a = t[0];
+    if (2 * pair + 1 < p.n_rt) {
+      const int4 b = t[1];
+      if (a.y == 0 || (b.y > 0 && b.x < a.x)) a.x = b.x;
+      a.y = max(a.y, b.y);
+    }
+    first = a.x / split_keys;
+    last = a.y > 0 ? (a.y - 1) / split_keys : -1;
+  }
   float mx = -CUDART_INF_F;
-  for (int s = lane; s < n_splits; s += 32) mx = fmaxf(mx, LSEpart[s * rows + r]);
+  for (int s = first + lane; s <= last; s += 32) mx = fmaxf(mx, LSEpart[s * rows + r]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   float lse = -CUDART_INF_F, wsum = 0.f;
   if (mx != -CUDART_INF_F) {
 #pragma unroll 4
-    for (int s = 0; s < n_splits; ++s) {
+    for (int s = first; s <= last; ++s) {
       const float w = expf(LSEpart[s * rows + r] - mx);   // 0 for a range without keys
       wsum += w;
-      const float* o = Opart + (s * rows + r) * dv;
+      const float* o = Opart + (s * rows + r) * p.dv;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (lane + 32 * c < dv && w > 0.f) acc[c] = fmaf(w, o[lane + 32 * c], acc[c]);
+        if (lane + 32 * c < p.dv && w > 0.f) acc[c] = fmaf(w, o[lane + 32 * c], acc[c]);
     }
     const float inv = 1.0f / wsum;
 #pragma unroll
@@ -183,7 +201,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ Op
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c)
-    if (lane + 32 * c < dv) O[r * dv + lane + 32 * c] = acc[c];
+    if (lane + 32 * c < p.dv) O[r * p.dv + lane + 32 * c] = static_cast<T>(acc[c]);
   if (lane == 0) LSE[r] = lse;
 }
 
@@ -212,10 +230,16 @@ cudaError_t launch_scored_kv_sum(const ScoredBwd& a, bool bf16) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_scored_merge(const ScoredFwd& a) {
+cudaError_t launch_scored_merge(const ScoredFwd& a, bool bf16) {
   const long long rows = static_cast<long long>(a.p.B) * a.p.Hkv * a.p.R;
-  scored::merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, a.stream>>>(
-      a.Opart, a.LSEpart, static_cast<float*>(a.O), a.LSE, rows, a.p.dv, a.n_splits);
+  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+  if (bf16)
+    scored::merge_kernel<__nv_bfloat16, true><<<grid, 256, 0, a.stream>>>(
+        a.p, a.plan.tiles, a.Opart, a.LSEpart, static_cast<__nv_bfloat16*>(a.O), a.LSE, a.n_splits, a.split_keys);
+  else
+    scored::merge_kernel<float, false><<<grid, 256, 0, a.stream>>>(a.p, a.plan.tiles, a.Opart, a.LSEpart,
+                                                                   static_cast<float*>(a.O), a.LSE, a.n_splits,
+                                                                   a.split_keys);
   return cudaGetLastError();
 }
 

@@ -274,6 +274,17 @@ def test_rows_that_see_nothing(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("mask,cap,bias", [("causal", 4.0, False), ("window", 0.0, True), ("wild", 0.0, False),
+                                           ("some", 3.0, True)])
+@pytest.mark.parametrize("shape", [(1, 2, 1, 150, 3000, 128, 128), (1, 1, 1, 300, 2100, 64, 64),
+                                   (2, 3, 1, 100, 1500, 96, 128)])
+def test_few_rows_against_many_keys(shape, mask, cap, bias, dtype):
+    """More rows than the few-row kernel takes, too few to fill the GPU: the keys are cut into ranges."""
+    run_case(shape, mask, cap, bias, dtype, grad=True)
+
+
+@pytest.mark.gpu
 def test_long_runs_of_idle_row_tiles():
     """Most row tiles of every head see nothing, in runs longer than any queue between a kernel's warps; the live rows
     give what they give without the idle ones (bit for bit, except for the order in dK's and dV's sums)."""
