@@ -636,23 +636,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if (row4 + i < R && col < dv)
                 *reinterpret_cast<uint4*>(P.Opart + (part + row4 + i) * dv + col) = pk[i];
           }
-          continue;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = l > 0.f ? ptx::pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv_l,
+                                              __uint_as_float(o[8 * i + 2 * e + 1]) * inv_l)
+                             : 0u;
+            pk[i] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+          scored::quad_transpose(pk, lane);
+          const int col = 32 * c + 8 * (lane & 3);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (row4 + i < R && col < dv) *reinterpret_cast<uint4*>(P.O + (head + row4 + i) * dv + col) = pk[i];
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = l > 0.f ? ptx::pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv_l,
-                                            __uint_as_float(o[8 * i + 2 * e + 1]) * inv_l)
-                           : 0u;
-          pk[i] = make_uint4(v[0], v[1], v[2], v[3]);
-        }
-        scored::quad_transpose(pk, lane);
-        const int col = 32 * c + 8 * (lane & 3);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (row4 + i < R && col < dv) *reinterpret_cast<uint4*>(P.O + (head + row4 + i) * dv + col) = pk[i];
       }
       if (me.row < R) (SPLIT ? P.LSEpart + part : P.LSE + head)[me.row] = lse;
       ptx::tc_fence_before();
