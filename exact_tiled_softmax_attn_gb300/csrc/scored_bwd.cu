@@ -18,6 +18,7 @@
 // bias are applied per row (dq) and per column (dkdv).
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <limits.h>
 #include <math_constants.h>
 #include <stdint.h>
 
@@ -62,6 +63,22 @@ struct Params {
   float sc2;           // scale * log2(e)
   Cap cap;
 };
+
+// Zeroes the bf16 values of w whose bits of `seen` (value e of word i: bit 2 i + e) are not set.
+__device__ __forceinline__ void mask_pairs(uint32_t (&w)[16], uint32_t seen) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (!(seen & (1u << (2 * i)))) w[i] &= 0xffff0000u;
+    if (!(seen & (2u << (2 * i)))) w[i] &= 0x0000ffffu;
+  }
+}
+
+// Zeroes row r of a box of 64 columns in shared memory (a swizzle moves 16-byte pieces within a row only).
+__device__ __forceinline__ void zero_box_row(uint8_t* box, int r) {
+  uint4* p = reinterpret_cast<uint4*>(box + r * 128);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p[e] = make_uint4(0u, 0u, 0u, 0u);
+}
 
 // ---------------------------------------------------------------- dQ
 
@@ -488,12 +505,6 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             }
           }
         }
-        if (kv0 < u.tile.z || kv0 + 64 > u.tile.w) {
-          const int lo = ri.x - kv0, hi = ri.y - kv0;
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (i < lo || i >= hi) f[i] = 0.f;
-        }
         if (j + 1 == u.n) {
           const int more = next_unit(&nx);
           ok = more >= 0;
@@ -507,16 +518,30 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         for (int c = 0; c < 2; ++c) ptx::tmem_ld32(tDP + c * 32, v[c]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) ptx::tmem_ld_wait(v[c]);
+        uint32_t pk[2][16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const F2 e = add2(f2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])), ndd);
-            pk[i] = scored::pack_bf16(mul2(f2(f[c * 32 + 2 * i], f[c * 32 + 2 * i + 1]), e));
+            pk[c][i] = scored::pack_bf16(mul2(f2(f[c * 32 + 2 * i], f[c * 32 + 2 * i + 1]), e));
           }
-          ptx::tmem_st16(tDP + c * 16, pk);   // over this group's own first columns (already read)
+        // Keys the row does not see, and rows that see none, may hold
+        // anything: the product is masked, not a factor of it.
+        if (kv0 < u.tile.z || kv0 + 64 > u.tile.w) {
+          mask_pairs(pk[0], scored::bit_range(ri.x - kv0, ri.y - kv0));
+          mask_pairs(pk[1], scored::bit_range(ri.x - kv0 - 32, ri.y - kv0 - 32));
         }
+        // and K of the keys that no row of the tile sees is zeroed (each group a box of 64 columns)
+        const int k0 = kv0 - 64 * g;
+        if (k0 < u.tile.x || k0 + BT > u.tile.y) {
+          if (k0 + r < u.tile.x || k0 + r >= u.tile.y)
+            for (int c = g; c < C::KB; c += 2)
+              zero_box_row(ring + slot(item + 3 + 2 * j) * C::TILE + c * BOX_BYTES, r);
+          ptx::fence_proxy_async_smem();
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) ptx::tmem_st16(tDP + c * 16, pk[c]);   // over this group's own first columns (already read)
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(ds_full);
@@ -1117,6 +1142,19 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
           }
         }
         ptx::tmem_st_wait();
+        // Rows that see no key may hold anything, which the weights of 0
+        // would not hold back: their dO and Q become zeros once the products
+        // dP^T and S^T have read them.
+        if (cur.all_lo == INT_MAX) {
+          if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dp_full, q_it & 1u, w)))) break;
+          const int i = quad & 1, c = quad >> 1;   // (the four warps of a group share its 64 rows)
+          if (c < C::KB && cur.r[i].y == 0) {
+            const int row = 64 * h + 32 * i + lane;
+            zero_box_row(sdO + oslot(q_it) * C::TILE + c * BOX_BYTES, row);
+            zero_box_row(sQ + qslot(q_it) * C::TILE + c * BOX_BYTES, row);
+          }
+          ptx::fence_proxy_async_smem();
+        }
         ptx::tc_fence_before();
         ptx::mbar_arrive(p_full);
         // the next tile's record, where it is there already (behind the last
@@ -1132,9 +1170,9 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
           ptx::tmem_ld32(tDP + 32, rd[1]);
           ptx::tmem_ld_wait(rd[0]);
           ptx::tmem_ld_wait(rd[1]);
+          uint32_t pk[2][16];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[16];
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               const float4 d4 = ptx::lds128(dd + c * 32 + 2 * i);
@@ -1144,11 +1182,15 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
                 const F2 pt = f2(__uint_as_float(keep[c][i + q] << 16), __uint_as_float(keep[c][i + q] & 0xffff0000u));
                 const F2 e = fma2(q ? f2(d4.z, d4.w) : f2(d4.x, d4.y), neg1,
                                   f2(__uint_as_float(rd[c][2 * (i + q)]), __uint_as_float(rd[c][2 * (i + q) + 1])));
-                pk[i + q] = scored::pack_bf16(mul2(pt, e));
+                pk[c][i + q] = scored::pack_bf16(mul2(pt, e));
               }
             }
-            ptx::tmem_st16(tDP + c * 16, pk);
+          if (partial) {   // (the product, not a factor of it: see the dQ kernel)
+            mask_pairs(pk[0], seen[0]);
+            mask_pairs(pk[1], seen[1]);
           }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) ptx::tmem_st16(tDP + c * 16, pk[c]);
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();

@@ -606,8 +606,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ++op;
         ptx::tc_fence_after();
       }
-      const float inv_l = (l > 0.f) ? 1.0f / l : 0.f;
-      const float lse = (l > 0.f) ? (m_used + log2f(l)) * 0.69314718055994530942f : -CUDART_INF_F;
+      const bool none = l == 0.f;   // no key seen (a NaN among the row's scores goes through)
+      const float inv_l = none ? 0.f : 1.0f / l;
+      const float lse = none ? -CUDART_INF_F : (m_used + log2f(l)) * 0.69314718055994530942f;
       // the four rows of this lane's quad, of which it stores every fourth 16-byte piece
       const int row4 = me.row & ~3;
       const long long head = static_cast<long long>(me.bh) * R;
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               uint32_t v[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                v[e] = l > 0.f ? __float_as_uint(__uint_as_float(o[16 * h + 4 * i + e]) * inv_l) : 0u;
+                v[e] = none ? 0u : __float_as_uint(__uint_as_float(o[16 * h + 4 * i + e]) * inv_l);
               pk[i] = make_uint4(v[0], v[1], v[2], v[3]);
             }
             scored::quad_transpose(pk, lane);
@@ -642,9 +643,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              v[e] = l > 0.f ? ptx::pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv_l,
-                                              __uint_as_float(o[8 * i + 2 * e + 1]) * inv_l)
-                             : 0u;
+              v[e] = none ? 0u
+                          : ptx::pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv_l,
+                                           __uint_as_float(o[8 * i + 2 * e + 1]) * inv_l);
             pk[i] = make_uint4(v[0], v[1], v[2], v[3]);
           }
           scored::quad_transpose(pk, lane);

@@ -57,12 +57,13 @@ inline Cap make_cap(float scale, float softcap) {
   return r;
 }
 
-// Which form a warp takes for scores within [lo, hi] (of this thread).
+// Which form a warp takes for scores within [lo, hi] (of this thread; NaN, of
+// a thread whose scores are all NaN, goes through any).
 enum { kCapPoly2 = 1, kCapPoly4 = 2, kCapFormula = 3 };
 __device__ __forceinline__ int cap_form(const Cap& c, float lo, float hi) {
   const float a = fmaxf(hi, -lo);
-  if (__all_sync(0xffffffffu, a <= c.limit2)) return kCapPoly2;
-  return __all_sync(0xffffffffu, a <= c.limit4) ? kCapPoly4 : kCapFormula;
+  if (__all_sync(0xffffffffu, !(a > c.limit2))) return kCapPoly2;
+  return __all_sync(0xffffffffu, !(a > c.limit4)) ? kCapPoly4 : kCapFormula;
 }
 
 // The order of a key head's blocks of packed rows (or pairs of row tiles): a

@@ -184,20 +184,21 @@ __global__ void __launch_bounds__(256) merge_kernel(const ScoredProblem p, const
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   float lse = -CUDART_INF_F, wsum = 0.f;
-  if (mx != -CUDART_INF_F) {
+  const float ref = mx == -CUDART_INF_F ? 0.f : mx;
 #pragma unroll 4
-    for (int s = first; s <= last; ++s) {
-      const float w = expf(LSEpart[s * rows + r] - mx);   // 0 for a range without keys
-      wsum += w;
-      const float* o = Opart + (s * rows + r) * p.dv;
+  for (int s = first; s <= last; ++s) {
+    const float w = expf(LSEpart[s * rows + r] - ref);   // 0 for a range without keys
+    wsum += w;
+    const float* o = Opart + (s * rows + r) * p.dv;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (lane + 32 * c < p.dv && w > 0.f) acc[c] = fmaf(w, o[lane + 32 * c], acc[c]);
-    }
+    for (int c = 0; c < 4; ++c)
+      if (lane + 32 * c < p.dv && w != 0.f) acc[c] = fmaf(w, o[lane + 32 * c], acc[c]);
+  }
+  if (wsum != 0.f) {   // (NaN too)
     const float inv = 1.0f / wsum;
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[c] *= inv;
-    lse = mx + logf(wsum);
+    lse = ref + logf(wsum);
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c)

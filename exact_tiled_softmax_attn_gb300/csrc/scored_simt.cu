@@ -13,6 +13,7 @@
 // Bound by the FMA rate and those reads. Row tiles visit only the key tiles
 // their ranges' hull meets, and key tiles only the row tiles whose hull meets
 // them.
+#include <limits.h>
 #include <math_constants.h>
 #include <stdint.h>
 
@@ -267,8 +268,9 @@ __global__ void __launch_bounds__(NT) fwd_kernel(const ScoredProblem p, const Sc
     const int r = r0 + 4 * ty + i;
     if (r >= p.R) continue;
     const long long row = static_cast<long long>(bh) * p.R + r;
-    const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-    const float lse = l[i] > 0.f ? m[i] + logf(l[i]) : -CUDART_INF_F;
+    const bool none = l[i] == 0.f;   // no key seen (a NaN among the row's scores goes through)
+    const float inv = none ? 0.f : 1.f / l[i];
+    const float lse = none ? -CUDART_INF_F : m[i] + logf(l[i]);
     if (n_splits > 1) {
       store_row<NCV>(Opart + (split * rows + row) * p.dv, acc[i], inv, p.dv);
       if (tx == 0) LSEpart[split * rows + row] = lse;
@@ -396,6 +398,15 @@ __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const S
       dd[i] = D[static_cast<long long>(bh) * p.rpad() + r];
     }
     loaded();
+    if (hull.z == INT_MAX) {   // some row sees no key: it may hold anything, and its weights of 0 must stay 0
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (ri.hi[i] > 0) continue;
+        for (int c = tx; c < Pitch<NCK>::v; c += 8) sQ[(4 * ty + i) * Pitch<NCK>::v + c] = 0.f;
+        for (int c = tx; c < Pitch<NCV>::v; c += 8) sdO[(4 * ty + i) * Pitch<NCV>::v + c] = 0.f;
+      }
+      __syncthreads();
+    }
     float x[4][4], y[4][4];
     dot_tile<NCK, 8>(x, sQ, sK, p.d);
     dot_tile<NCV, 8>(y, sdO, sV, p.dv);

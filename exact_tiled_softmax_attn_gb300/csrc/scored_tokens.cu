@@ -441,8 +441,9 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::THREADS, Cfg<HD, RT>::CTAS)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         if (row[r] >= R) continue;
-        const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
-        const float lse = l[r] > 0.f ? (m[r] + log2f(l[r])) * 0.69314718055994530942f : -CUDART_INF_F;
+        const bool none = l[r] == 0.f;   // no key seen (a NaN among the row's scores goes through)
+        const float inv = none ? 0.f : 1.f / l[r];
+        const float lse = none ? -CUDART_INF_F : (m[r] + log2f(l[r])) * 0.69314718055994530942f;
         const long long at = whole ? static_cast<long long>(bh) * R + row[r]
                                    : (static_cast<long long>(blockIdx.x) * 2 + part) * R + row[r];
         if (t == 0) (whole ? P.LSE : P.LSEpart)[at] = lse;
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
 #pragma unroll 4
     for (int k = 0; k < count; ++k) {
       const float x = __shfl_sync(0xffffffffu, weight, k);
-      if (x > 0.f && col < dv) {
+      if (x != 0.f && col < dv) {
         const float4 v = *reinterpret_cast<const float4*>(P.Opart + at(i0 + k * WPR) * dv + col);
         acc.x = fmaf(x, v.x, acc.x);
         acc.y = fmaf(x, v.y, acc.y);
@@ -562,11 +563,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
     }
   }
   if (parts == 0) return;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   if (col < dv)
     *reinterpret_cast<uint2*>(P.O + n * dv + col) =
         make_uint2(ptx::pack_bf16(acc.x * inv, acc.y * inv), ptx::pack_bf16(acc.z * inv, acc.w * inv));
-  if (lane == 0) P.LSE[n] = sum > 0.f ? mx + logf(sum) : -CUDART_INF_F;
+  if (lane == 0) P.LSE[n] = sum == 0.f ? -CUDART_INF_F : ref + logf(sum);
 }
 
 template <int HD, int RT>

@@ -308,7 +308,7 @@ ATTN_API attn_status_t attn_bwd_noalloc(const void* Q, const void* K, const void
 typedef struct {
   float softcap;        /* 0: none; otherwise from 1e-4 to 1e6 */
   int causal;           /* 0 or 1 */
-  const float* slopes;  /* [H] fp32, finite values, or NULL: no bias */
+  const float* slopes;  /* [H] fp32, or NULL: no bias; any sign, slope times distance within fp32's range */
   const int* q_pos;     /* [B,Tq] int32, or NULL: row i is at position i */
   const int* key_begin; /* [B,Tq] int32, or NULL: 0 */
   const int* key_end;   /* [B,Tq] int32, or NULL: Tk */
@@ -321,8 +321,10 @@ typedef struct {
  * head h reads key head h / (H / Hkv)). score = NULL: plain scores, no mask.
  * ATTN_F32: 1 <= d, dv <= 128; ATTN_BF16: d and dv multiples of 8 up to 128;
  * else ATTN_ERR_UNSUPPORTED. Tq, Tk <= 2^30, and H / Hkv * Tq too.
- * K and V rows that lie before every range or behind every range of their
- * batch entry (unused capacity of a cache) may hold anything, NaN included.
+ * What no query reads may hold anything, NaN included: K and V rows that lie
+ * before every range or behind every range of their batch entry (unused
+ * capacity of a cache), and Q rows whose range is empty (padding). A NaN that
+ * a row does see makes its O and LSE NaN.
  * `workspace`: as in attn_fwd_splitkv (256-byte aligned, at least
  * attn_fwd_scored_workspace_size bytes, not overlapping any argument), else
  * ATTN_ERR_WORKSPACE; it is scratch, overwritten by each call, so calls that
@@ -348,10 +350,11 @@ ATTN_API size_t attn_fwd_scored_workspace_size(int B, int H, int Hkv, int Tq, in
  *   dS = P o (dO V^T - D) o T,  dQ = scale * dS K,  dK = scale * dS^T Q
  * (the bias and the ranges have no gradient). `O` and `LSE` must be the
  * outputs of attn_fwd_scored on the same inputs, scale and score. Shapes as
- * attn_fwd_scored; every input must be finite (the LSE of empty rows
- * excepted). Sums run in a fixed order: equal calls give bitwise equal
- * results. Workspace and errors as attn_fwd_scored, with
- * attn_bwd_scored_workspace_size.
+ * attn_fwd_scored. What no query reads may hold anything here too: K and V
+ * rows outside every range of their batch entry, and Q, O and dO rows whose
+ * range is empty; their gradients are 0. Sums run in a fixed order: equal
+ * calls give bitwise equal results. Workspace and errors as attn_fwd_scored,
+ * with attn_bwd_scored_workspace_size.
  */
 ATTN_API attn_status_t attn_bwd_scored(const void* Q, const void* K, const void* V, const void* O, const float* LSE,
                                        const void* dO, void* dQ, void* dK, void* dV, int B, int H, int Hkv, int Tq,
@@ -367,7 +370,8 @@ ATTN_API size_t attn_bwd_scored_workspace_size(int B, int H, int Hkv, int Tq, in
  *   u' = m (u cos a - v sin a),  v' = m (v cos a + u sin a)
  * and the elements from rot on are copied. The plan holds each f_i as a
  * 64-bit fraction of a turn, so pos * f_i modulo one turn is one integer
- * product, off by less than |pos| * 2^-65 turns at any int32 position.
+ * product, off by at most |pos| * 2^-65 turns at any int32 position; its
+ * upper 32 bits go on (2^-32 turns: 1.5e-9 radians).
  */
 #define ATTN_ROPE_MAX_PAIRS 128
 typedef struct {

@@ -479,3 +479,227 @@ def test_rope_then_attention_then_both_gradients(dtype):
     # a half step of the type for each of the two products' sums
     bound = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -21
     assert np.abs(np64(qr) - ref.rope(q, p, f)).max() <= bound * np64(q).__abs__().max() * 1.5
+
+
+# ------------------------------------------------------------------ what no query reads, and what one does
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (4.0, False), (0.0, True), (4.0, True)])
+@pytest.mark.parametrize("shape", [(2, 4, 2, 300, 420, 64, 64), (2, 4, 1, 300, 420, 128, 128), (1, 2, 2, 20, 300, 72, 40),
+                                   (1, 16, 1, 130, 260, 64, 64)])
+def test_padding_may_hold_anything(shape, cap, bias, dtype):
+    """A padded batch: queries that see no key and keys that no query sees are NaN and infinite, and every result is
+    what it is with finite padding (bit for bit, except for the roundings of a cap)."""
+    Bn, H, Hkv, Tq, Tk, d, dv = shape
+    x = make(*shape, dtype, 31)
+    how = how_of("none", cap, bias, Bn, H, Tq, Tk)
+    live = torch.tensor([Tq - 9, Tq // 2 + 3][:Bn])[:, None]
+    i = torch.arange(Tq)[None]
+    begin = torch.full((Bn, Tq), 13).where(i < 40, torch.tensor(21))
+    end = torch.where(i < live, Tk - 30 + torch.arange(Bn)[:, None], 0)
+    how["key_begin"], how["key_end"] = (t.to(torch.int32).cuda() for t in (begin, end))
+
+    def both():
+        o, lse = B.forward_scored(*x[:3], **how)
+        oj = o.clone()
+        for b in range(Bn):
+            oj[b, :, live[b, 0]:] = junk
+        g = B.backward_scored(*x[:3], oj, lse, x[3], **how)
+        assert B.attn_device_status() == B.ATTN_OK
+        return [o, lse, *g]
+    junk = 0.0
+    want = both()
+    assert all(t.isfinite().all() for t in want[2:])
+    for junk in (float("nan"), float("inf")):
+        for b in range(Bn):
+            x[0][b, :, live[b, 0]:] = junk
+            x[3][b, :, live[b, 0]:] = junk
+            for t in x[1:3]:
+                t[b, :, :13] = junk
+                t[b, :, Tk - 30 + b:] = junk
+        got = both()
+        for a, c, name in zip(got, want, ("O", "LSE", "dQ", "dK", "dV")):
+            if dtype == torch.bfloat16 and cap:   # the largest score near by decides how the cap is evaluated
+                check_lse(a, np64(c), dtype) if name == "LSE" else check_grad(a, np64(c), dtype, name)
+            else:
+                assert torch.equal(a, c), (name, junk)
+    for b in range(Bn):
+        assert not got[2][b, :, live[b, 0]:].any()
+        assert not got[3][b, :, :13].any() and not got[4][b, :, Tk - 30 + b:].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+@pytest.mark.parametrize("shape", [(1, 2, 2, 1, 700, 64, 64), (2, 8, 2, 3, 50, 128, 128), (1, 2, 1, 300, 3000, 64, 64),
+                                   (2, 40, 40, 300, 300, 128, 128)])
+def test_a_nan_that_a_row_sees_shows(shape, cap, dtype):
+    Bn, H, Hkv, Tq, Tk, d, dv = shape
+    x = make(*shape, dtype, 37, grad=False)
+    want = B.forward_scored(*x, softcap=cap)
+    x[0][-1, 1, Tq // 2, 3] = float("nan")
+    o, lse = B.forward_scored(*x, softcap=cap)
+    assert o[-1, 1, Tq // 2].isnan().all() and lse[-1, 1, Tq // 2].isnan()
+    o[-1, 1, Tq // 2], lse[-1, 1, Tq // 2] = want[0][-1, 1, Tq // 2], want[1][-1, 1, Tq // 2]
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+# ------------------------------------------------------------------ slopes, positions, row counts
+
+def magnitudes(x, how, scale):
+    """Sums of absolute values behind each result: what a relative error of every term is an error of."""
+    q, k, v, do = (np64(t) for t in x)
+    G = q.shape[1] // k.shape[1]
+    k, v = np.repeat(k, G, 1), np.repeat(v, G, 1)
+    r = ref.scored(*x, scale=scale, **how)
+    j = np.arange(k.shape[2])
+    get = lambda t, default: default if t is None else np64(t)[:, None, :, None]  # noqa: E731
+    pos = get(how["q_pos"], np.arange(q.shape[2])[None, None, :, None])
+    s = scale * q @ k.swapaxes(2, 3)
+    if how["softcap"]:
+        s = how["softcap"] * np.tanh(s / how["softcap"])
+    s = s - np64(how["slopes"])[None, :, None, None] * np.abs(pos - j)
+    seen = (j >= get(how["key_begin"], 0)) & (j < get(how["key_end"], len(j)))
+    p = np.where(seen, np.exp(np.minimum(s - np.where(np.isneginf(r["LSE"]), 0, r["LSE"])[..., None], 0)), 0)
+    a = np.abs
+    ds = p * (a(do) @ a(v).swapaxes(2, 3) + (a(do) * a(r["O"])).sum(-1, keepdims=True))
+    group = lambda t: t.reshape(t.shape[0], -1, G, *t.shape[2:]).sum(2)  # noqa: E731
+    return {"score": scale * (a(q) @ a(k).swapaxes(2, 3)).max(), "O": p @ a(v), "dQ": scale * ds @ a(k),
+            "dK": group(scale * ds.swapaxes(2, 3) @ a(q)), "dV": group(p.swapaxes(2, 3) @ a(do))}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("mask,cap,scale", [("causal", 0.0, None), ("wild", 0.0, None), ("wild", 0.7, 4.0), ("none", 2.0, 0.05)])
+@pytest.mark.parametrize("shape", [(1, 6, 2, 200, 300, 64, 64), (2, 6, 3, 9, 400, 128, 64), (1, 6, 1, 150, 2000, 64, 64)])
+def test_slopes_of_any_size_and_sign(shape, mask, cap, scale, dtype):
+    """Steep slopes leave a row a key or two; negative ones prefer far keys; 0 is none."""
+    Bn, H, Hkv, Tq, Tk, d, dv = shape
+    x = make(*shape, dtype, 41)
+    how = how_of(mask, cap, False, Bn, H, Tq, Tk)
+    how["slopes"] = torch.tensor([4.0, -0.5, 0.0, 9.0, 0.25, -0.01], device="cuda")
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    o, lse = B.forward_scored(*x[:3], scale=scale, **how)
+    g = B.backward_scored(*x[:3], o, lse, x[3], scale=scale, **how)
+    assert B.attn_device_status() == B.ATTN_OK
+    r, size = ref.scored(*x, scale=scale, **how), magnitudes(x, how, scale)
+    # A score is off by the sum of its products (d roundings of sums up to `size`) and by a few half steps of its bias
+    # (up to |slope| times the distance, in log2 units; with ranges of any kind a row's keys may all lie far off).
+    far = (9.0 if mask == "wild" else 0.5) * (Tk + 600) * 1.4427
+    score = d * 2.0 ** -24 * size["score"] + 6 * far * 2.0 ** -24
+    half = 0.0 if dtype == torch.float32 else 2.0 ** -8
+    terms = max(Tk, H // Hkv * Tq, d) * 2.0 ** -24   # roundings of a sum
+    inf = np.isneginf(r["LSE"])
+    assert np.array_equal(np.isneginf(np64(lse)), inf)
+    assert np.abs(np64(lse)[~inf] - r["LSE"][~inf]).max() <= 1e-4 + score
+    # weights off by the score's and the sum's error, rounded once; the result rounded once
+    assert (np.abs(np64(o) - r["O"]) <= (2 * score + terms + 1e-5 + half) * size["O"] + half * np.abs(r["O"]) + 1e-6).all()
+    # P T, dS, the O in D and the result are rounded; T is off by the score's error over the cap
+    rel = 3 * half + 4 * score + terms + 1e-5 + (2 * score / cap if cap else 0.0)
+    for t, name in zip(g, ("dQ", "dK", "dV")):
+        assert (np.abs(np64(t) - r[name]) <= rel * size[name] + half * np.abs(r[name]) + 1e-6).all(), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(2, 12, 1, 5, 900, 64, 128), (1, 4, 1, 16, 500, 128, 40), (1, 2, 2, 64, 130, 64, 64),
+                                   (1, 5, 1, 13, 700, 64, 64), (1, 11, 1, 3, 64, 128, 128), (1, 1, 1, 17, 1, 64, 64)])
+@pytest.mark.parametrize("mask,cap,bias", [("wild", 3.0, True), ("causal", 0.0, False)])
+def test_row_counts_of_the_few_row_kernel(shape, mask, cap, bias):
+    run_case(shape, mask, cap, bias, torch.bfloat16, grad=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Bn,H,Hkv,Tq", [(700, 4, 2, 1), (700, 8, 1, 3), (1200, 1, 1, 40)])
+def test_more_sequences_than_threads(Bn, H, Hkv, Tq):
+    """Sequences of very different lengths, many without a key: every one against a call of its own kind in float64."""
+    Tk, d = 190, 64
+    x = make(Bn, H, Hkv, Tq, Tk, d, d, torch.bfloat16, 43, grad=False)
+    g = torch.Generator().manual_seed(44)
+    n = torch.randint(1, Tk + 1, (Bn, 1), generator=g)
+    n[torch.rand(Bn, 1, generator=g) < 0.4] = 0
+    n[-40:] = 0
+    n[:3] = 0
+    end = n.expand(Bn, Tq).to(torch.int32).contiguous().cuda()
+    o, lse = B.forward_scored(*x, key_end=end)
+    assert B.attn_device_status() == B.ATTN_OK
+    r = ref.scored(*x, scale=1.0 / math.sqrt(d), key_end=end)
+    check_o(o, r["O"], torch.bfloat16)
+    check_lse(lse, r["LSE"], torch.bfloat16)
+
+
+# ------------------------------------------------------------------ graphs, streams, long caches
+
+@pytest.mark.gpu
+def test_a_decoding_step_replays_from_a_graph():
+    """One captured call serves a growing sequence: the lengths are device memory."""
+    q, k, v = make(3, 8, 2, 1, 2000, 128, 128, torch.bfloat16, 47, grad=False)
+    end = torch.tensor([[5], [700], [64]], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    B.forward_scored(q, k, v, key_end=end)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        o, lse = B.forward_scored(q, k, v, key_end=end)
+    for lens in ((5, 700, 64), (2000, 0, 65), (1, 1999, 1000)):
+        end.copy_(torch.tensor(lens, dtype=torch.int32)[:, None])
+        graph.replay()
+        want = B.forward_scored(q, k, v, key_end=end)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert B.attn_device_status() == B.ATTN_OK
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, overlap without a trace in the results."""
+    sets = [make(2, 8, 2, 520, 520, 64, 64, torch.bfloat16, s) for s in (51, 52)]
+    tok = [make(4, 8, 2, 1, 3000, 64, 64, torch.bfloat16, s, grad=False) for s in (53, 54)]
+
+    def work(i):
+        o, lse = B.forward_scored(*sets[i][:3], causal=True, softcap=5.0)
+        return [o, lse, *B.backward_scored(*sets[i][:3], o, lse, sets[i][3], causal=True, softcap=5.0),
+                *B.forward_scored(*tok[i])]
+    want = [work(0), work(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(6):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(work(i))
+    torch.cuda.synchronize()
+    assert B.attn_device_status() == B.ATTN_OK
+    for i in (0, 1):
+        for run in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(run, want[i]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,Tq", [(torch.bfloat16, 1), (torch.bfloat16, 150), (torch.float32, 3)])
+def test_offsets_beyond_32_bits(dtype, Tq):
+    """The last key head of the last sequence lies behind element 2^31 of the cache, its last keys far behind its first."""
+    Bn, H, Hkv, Tk, d = 2, 8, 4, (1 << 22) + 5, 128
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    q = make(Bn, H, Hkv, Tq, 1, d, d, dtype, 57, grad=False)[0]
+    k, v = (torch.empty(Bn, Hkv, Tk, d, dtype=dtype, device="cuda") for _ in range(2))
+    n = 777
+    g = torch.Generator().manual_seed(58)
+    kn, vn = (torch.randn(Bn, Hkv, n, d, generator=g).to(dtype).cuda() for _ in range(2))
+    k[:, :, Tk - n:], v[:, :, Tk - n:] = kn, vn
+    begin = torch.full((Bn, Tq), Tk - n, dtype=torch.int32, device="cuda")
+    o, lse = B.forward_scored(q, k, v, key_begin=begin)
+    assert B.attn_device_status() == B.ATTN_OK
+    r = ref.scored(q, kn, vn, scale=1.0 / math.sqrt(d))
+    check_o(o, r["O"], dtype)
+    check_lse(lse, r["LSE"], dtype)
+    if Tq == 150:
+        do = make(Bn, H, Hkv, Tq, 1, d, d, dtype, 59)[3]
+        dq, dk, dv = B.backward_scored(q, k, v, o, lse, do, key_begin=begin)
+        assert B.attn_device_status() == B.ATTN_OK
+        r = ref.scored(q, kn, vn, do, scale=1.0 / math.sqrt(d))
+        check_grad(dq, r["dQ"], dtype, "dQ")
+        for t, name in ((dk, "dK"), (dv, "dV")):
+            check_grad(t[:, :, Tk - n:], r[name], dtype, name)
+            assert not t[:, :, :Tk - n].any()
