@@ -98,13 +98,13 @@ void fwd_splits(const ScoredProblem& p, attn_dtype_t dt, int* S, int* keys) {
 bool fwd_tokens(const ScoredProblem& p, attn_dtype_t dt) { return dt == ATTN_BF16 && p.R <= kScoredTokenRows; }
 
 struct Layout {
-  size_t start, rows, tiles, counters, kcount, kbits, even, slope2, D, NL, dkpart, dvpart, opart, lsepart, total;
+  size_t start, rows, tiles, counters, kcount, khull, kbits, even, slope2, D, NL, dkpart, dvpart, opart, lsepart, total;
   int n_splits, split_keys;
 };
 
 // Forward: rows | tiles | counters | Opart | LSEpart, with few rows in bf16
 // start | Opart | LSEpart. Backward: rows | tiles |
-// counters | kcount | kbits | even | slope2 | D | NL | dKpart | dVpart. Each part starts on 256 bytes.
+// counters | kcount | khull | kbits | even | slope2 | D | NL | dKpart | dVpart. Each part starts on 256 bytes.
 Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
   Layout L{};
   L.n_splits = 1;
@@ -132,6 +132,7 @@ Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
   L.counters = take(256);
   if (bwd) {
     L.kcount = take(B * p.n_kt * p.kv_splits * sizeof(int));
+    L.khull = take(B * p.n_kt * sizeof(int4));
     L.kbits = take(B * p.n_kt * p.n_words() * sizeof(uint32_t));
     L.even = take(B * p.n_rt * sizeof(int4));
     L.slope2 = take(p.Hkv * rpad * sizeof(float));
@@ -160,6 +161,7 @@ ScoredPlan plan_at(const Layout& L, void* ws, bool bwd, bool bias) {
   s.counters = reinterpret_cast<uint32_t*>(w + L.counters);
   if (bwd) {
     s.kcount = reinterpret_cast<int*>(w + L.kcount);
+    s.khull = reinterpret_cast<int4*>(w + L.khull);
     s.kbits = reinterpret_cast<uint32_t*>(w + L.kbits);
     if (bias) {
       s.even = reinterpret_cast<int4*>(w + L.even);

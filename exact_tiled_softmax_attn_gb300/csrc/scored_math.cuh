@@ -77,6 +77,15 @@ __device__ __forceinline__ int packed_block(int i, int n_padded, int G) {
   return (i % G) * per + i / G;
 }
 
+// Zeroes row r of a swizzled box of 64 bf16 columns in shared memory. The
+// swizzle moves 16-byte pieces within a row only; taken in its order, eight
+// rows' pieces are in different banks.
+__device__ __forceinline__ void zero_box_row(uint8_t* box, int r) {
+  uint4* p = reinterpret_cast<uint4*>(box + r * 128);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p[e ^ (r & 7)] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 constexpr int kPosLimit = 1 << 30;
 
 // The keys [lo, hi) token t of batch entry b sees (lo >= hi: none) and its position.

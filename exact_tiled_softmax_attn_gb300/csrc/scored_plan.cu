@@ -94,12 +94,19 @@ __global__ void __launch_bounds__(128) plan_keys_kernel(const ScoredProblem p, c
   const int k0 = kt * kScoredTile, k1 = k0 + kScoredTile;
   int count = 0;   // lane i: of part i
   bool any = false;
+  int lo = INT_MAX, hi = 0;
+  bool blank = false;
   for (int t0 = 0; t0 < p.n_rt; t0 += 32) {
     const int t = t0 + lane;
     bool meets = false;
     if (t < p.n_rt) {
       const int4 h = out.tiles[static_cast<long long>(b) * p.n_rt + t];
       meets = h.x < k1 && h.y > k0;
+      if (meets) {
+        lo = min(lo, h.x);
+        hi = max(hi, h.y);
+        blank = blank || h.z == INT_MAX;
+      }
     }
     const unsigned word = __ballot_sync(0xffffffffu, meets);
     const int first = lane * p.kv_split_tiles - t0;
@@ -107,6 +114,10 @@ __global__ void __launch_bounds__(128) plan_keys_kernel(const ScoredProblem p, c
     any = any || word != 0u;
     if (lane == 0) out.kbits[w * p.n_words() + t0 / 32] = word;
   }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  blank = __any_sync(0xffffffffu, blank);
+  if (lane == 0) out.khull[w] = make_int4(lo, hi, blank, 0);
   if (lane < p.kv_splits) out.kcount[w * p.kv_splits + lane] = count;
   if (any || idle.dK == nullptr) return;
   // no row sees a key of the tile
