@@ -124,8 +124,8 @@ cudaError_t launch_scored_bwd_simt(const ScoredBwd& a);
 
 // bf16 on the tensor cores; tmQ, tmK, tmV with 128-row boxes
 cudaError_t launch_scored_fwd_bf16(const ScoredFwd& a);
-// bf16, at most 64 packed rows a key head; tmK, tmV with 64-row boxes
-constexpr int kScoredTokenRows = 64;
+// bf16, at most 32 packed rows a key head; tmK, tmV with 64-row boxes
+constexpr int kScoredTokenRows = 32;
 cudaError_t launch_scored_tokens_bf16(const ScoredFwd& a);
 cudaError_t launch_scored_bwd_bf16(const ScoredBwd& a);
 

@@ -1,5 +1,5 @@
 // bf16 scored attention of few query rows (single tokens) against a long
-// cache (d, dv <= 128, at most 64 packed rows per key head).
+// cache (d, dv <= 128, at most 32 packed rows per key head).
 //
 // Reads every seen key and value once: bound by memory. The keys that the
 // rows of a (batch entry, key head) see - the hull of their ranges - are cut
@@ -15,7 +15,10 @@
 // maximum, sum and accumulator of their own, joined at the end of the pair.
 // The products run on mma.m16n8k16: with 16 rows or fewer per key head the
 // tcgen05 tile of 128 rows would be mostly empty, and at this intensity (at
-// most 64 rows) the memory is what counts. Fragments are read as 16-byte
+// most 32 rows) the memory is what counts: 32 sequences of 32768 keys, H=32
+// Hkv=8 d=128, 2.6 GB, 365 us or 7.0 TB/s; 87 us of 79 with 16 rows at B=8
+// Hkv=8 Tk=16384. Four row tiles of 16 were tried too: 338 us there with 64
+// rows, where the 128-row tiles take 112. Fragments are read as 16-byte
 // vectors: the columns of Q and K are permuted alike, so that a thread's
 // fragments of K are 8 adjacent elements of a row; keys are numbered so that
 // the accumulator layout of S is the operand layout of P, and V's pairs are
@@ -610,7 +613,7 @@ cudaError_t launch(const ScoredFwd& a) {
 template <int HD>
 cudaError_t rows(const ScoredFwd& a) {
   if (a.p.R <= 16) return launch<HD, 1>(a);
-  return a.p.R <= 32 ? launch<HD, 2>(a) : launch<HD, 4>(a);
+  return launch<HD, 2>(a);
 }
 
 }  // namespace scored_tokens
