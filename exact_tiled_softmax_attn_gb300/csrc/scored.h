@@ -34,6 +34,7 @@ struct ScoredProblem {
 struct ScoredPlan {
   int4* rows;      // [B][rpad]: {key begin, key end, position, 0}; begin = INT_MAX, end = 0 for rows that see nothing
   int4* tiles;     // [B][n_rt]: {min begin, max end over the rows that see keys, max begin, min end over all rows}
+  int2* fine;      // [B][rpad / 32]: {min begin, max end} of 32 rows, (0, 0) where none sees a key (fp32 only), or null
   int* kcount;     // [B][n_kt][kv_splits]: row tiles of the part whose hull meets the key tile (backward only), or null
   int4* khull;     // [B][n_kt]: hull of the row tiles that meet the key tile, whether a row of theirs sees no key, 0; or null
   uint32_t* kbits; // [B][n_kt][n_words]: which they are, one bit each

@@ -102,12 +102,12 @@ void fwd_splits(const ScoredProblem& p, attn_dtype_t dt, int* S, int* keys) {
 bool fwd_tokens(const ScoredProblem& p, attn_dtype_t dt) { return dt == ATTN_BF16 && p.R <= kScoredTokenRows; }
 
 struct Layout {
-  size_t start, rows, tiles, counters, kcount, khull, kbits, even, slope2, D, NL, dkpart, dvpart, opart, lsepart, total;
+  size_t start, rows, tiles, fine, counters, kcount, khull, kbits, even, slope2, D, NL, dkpart, dvpart, opart, lsepart, total;
   int n_splits, split_keys;
 };
 
-// Forward: rows | tiles | counters | Opart | LSEpart, with few rows in bf16
-// start | Opart | LSEpart. Backward: rows | tiles |
+// Forward: rows | tiles | fine (fp32) | counters | Opart | LSEpart, with few rows in bf16
+// start | Opart | LSEpart. Backward: rows | tiles | fine |
 // counters | kcount | khull | kbits | even | slope2 | D | NL | dKpart | dVpart. Each part starts on 256 bytes.
 Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
   Layout L{};
@@ -133,6 +133,7 @@ Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
   }
   L.rows = take(B * rpad * sizeof(int4));
   L.tiles = take(B * p.n_rt * sizeof(int4));
+  if (dt == ATTN_F32) L.fine = take(B * rpad / 32 * sizeof(int2));
   L.counters = take(256);
   if (bwd) {
     L.kcount = take(B * p.n_kt * p.kv_splits * sizeof(int));
@@ -157,12 +158,13 @@ Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
   return L;
 }
 
-ScoredPlan plan_at(const Layout& L, void* ws, bool bwd, bool bias) {
+ScoredPlan plan_at(const Layout& L, void* ws, attn_dtype_t dt, bool bwd, bool bias) {
   uint8_t* w = static_cast<uint8_t*>(ws);
   ScoredPlan s{};
   s.rows = reinterpret_cast<int4*>(w + L.rows);
   s.tiles = reinterpret_cast<int4*>(w + L.tiles);
   s.counters = reinterpret_cast<uint32_t*>(w + L.counters);
+  if (dt == ATTN_F32) s.fine = reinterpret_cast<int2*>(w + L.fine);
   if (bwd) {
     s.kcount = reinterpret_cast<int*>(w + L.kcount);
     s.khull = reinterpret_cast<int4*>(w + L.khull);
@@ -250,7 +252,7 @@ attn_status_t attn_fwd_scored(const void* Q, const void* K, const void* V, void*
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
   }
   a.mask = ScoredMask{sc.q_pos, sc.key_begin, sc.key_end, sc.causal};
-  a.plan = plan_at(L, workspace, false, sc.slopes != nullptr);
+  a.plan = plan_at(L, workspace, dtype, false, sc.slopes != nullptr);
   a.Q = Q;
   a.K = K;
   a.V = V;
@@ -335,7 +337,7 @@ attn_status_t attn_bwd_scored(const void* Q, const void* K, const void* V, const
     for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = launch_zero(outs[i], out_bytes[i], st);
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
   }
-  a.plan = plan_at(L, workspace, true, sc.slopes != nullptr);
+  a.plan = plan_at(L, workspace, dtype, true, sc.slopes != nullptr);
   a.Q = Q;
   a.K = K;
   a.V = V;

@@ -52,6 +52,8 @@ __global__ void __launch_bounds__(kScoredTile) plan_rows_kernel(const ScoredProb
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = min(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
+  if (out.fine && (threadIdx.x & 31) == 0)
+    out.fine[n / 32] = v[1] < 0 ? make_int2(v[0], -v[1]) : make_int2(0, 0);
   __shared__ int s[4][4];
   __shared__ int hull;
   if ((threadIdx.x & 31) == 0)
