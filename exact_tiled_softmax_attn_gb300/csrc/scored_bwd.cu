@@ -214,25 +214,24 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     // ------------------------------------------------------------ MMA issuer
     ptx::WaitCtx w{abort_flag, P.status, 6u};
     const uint32_t aR = ptx::smem_u32(ring);
-    auto kmaj = [](uint32_t base, int kk) {
-      return ptx::sdesc_advance(ptx::sdesc_sw128(base, 16, 1024), (kk >> 2) * BOX_BYTES + (kk & 3) * 32);
-    };
-    auto mnmaj = [](uint32_t base, int kk) {
-      return ptx::sdesc_advance(ptx::sdesc_sw128(base, BOX_BYTES, 1024), kk * 2048);
-    };
+    auto kmaj = [](uint64_t base, int kk) { return ptx::sdesc_advance(base, (kk >> 2) * BOX_BYTES + (kk & 3) * 32); };
+    auto mnmaj = [](uint64_t base, int kk) { return ptx::sdesc_advance(base, kk * 2048); };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, w));
     };
-    auto mma_s = [&](uint32_t ik) {
+    // K-major and M/N-major descriptors of the tile of ring item i
+    auto kdesc = [&](uint32_t i) { return scored::formed(ptx::sdesc_sw128(aR + slot(i) * C::TILE, 16, 1024)); };
+    auto mdesc = [&](uint32_t i) { return scored::formed(ptx::sdesc_sw128(aR + slot(i) * C::TILE, BOX_BYTES, 1024)); };
+    auto mma_s = [&](uint64_t k) {
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk)
-        ptx::mma_ts(tmem + C::T_S, tmem + C::T_Q + 8 * kk, kmaj(aR + slot(ik) * C::TILE, kk), C::IDESC_S, kk > 0);
+        ptx::mma_ts(tmem + C::T_S, tmem + C::T_Q + 8 * kk, kmaj(k, kk), C::IDESC_S, kk > 0);
       ptx::mma_commit(s_full);
     };
-    auto mma_dp = [&](uint32_t iv) {
+    auto mma_dp = [&](uint64_t v, uint32_t iv) {
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk)
-        ptx::mma_ts(tmem + C::T_DP, tmem + C::T_DO + 8 * kk, kmaj(aR + slot(iv) * C::TILE, kk), C::IDESC_S, kk > 0);
+        ptx::mma_ts(tmem + C::T_DP, tmem + C::T_DO + 8 * kk, kmaj(v, kk), C::IDESC_S, kk > 0);
       ptx::mma_commit(dp_full);
       ptx::mma_commit(empty + slot(iv));
     };
@@ -251,6 +250,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     bool ok = nk >= 0;
     while (ok && nk > 0) {
       const uint32_t i0 = item;
+      const uint64_t k0 = kdesc(i0 + 3), v0 = kdesc(i0 + 4);
       // Q and dO are in TMEM: the three staging slots go back to the ring
       if (!(ok = wait(qd_ready, u_it & 1u))) break;
       if (lane == 0)
@@ -260,14 +260,14 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
         moved |= lane != 0;
-        mma_s(i0 + 3);
+        mma_s(k0);
       }
       __syncwarp();
       if (!(ok = wait(full + slot(i0 + 4), par(i0 + 4)))) break;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
         moved |= lane != 0;
-        mma_dp(i0 + 4);
+        mma_dp(v0, i0 + 4);
       }
       __syncwarp();
       if (nk > 1 && !(ok = wait(full + slot(i0 + 5), par(i0 + 5)))) break;
@@ -278,12 +278,13 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
           if (!ok) break;
         }
         const uint32_t ik = i0 + 3 + 2 * j;   // K_j; V_{j+1} = ik + 3, K_{j+1} = ik + 2, K_{j+2} = ik + 4
+        const uint64_t k = mdesc(ik), kn = kdesc(ik + 2), vn = kdesc(ik + 3);
         if (j + 1 < nk) {
           if (!(ok = wait(s_free, sp & 1u))) break;
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
             moved |= lane != 0;
-            mma_s(ik + 2);
+            mma_s(kn);
           }
           __syncwarp();
         }
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
           moved |= lane != 0;
 #pragma unroll
           for (int kk = 0; kk < BT / 16; ++kk)
-            ptx::mma_ts(tmem + C::T_DQ, tmem + C::T_DP + packed_col(kk), mnmaj(aR + slot(ik) * C::TILE, kk),
+            ptx::mma_ts(tmem + C::T_DQ, tmem + C::T_DP + packed_col(kk), mnmaj(k, kk),
                         C::IDESC_DQ, (j > 0 || kk > 0) ? 1u : 0u);
           ptx::mma_commit(empty + slot(ik));
         }
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
             moved |= lane != 0;
-            mma_dp(ik + 3);
+            mma_dp(vn, ik + 3);
           }
           __syncwarp();
         }
@@ -855,22 +856,26 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
       // ---------------------------------------------------------- MMA issuer
       ptx::WaitCtx w{abort_flag, P.status, 2u};
       const uint32_t aK = ptx::smem_u32(sK), aV = ptx::smem_u32(sV), aQ = ptx::smem_u32(sQ), adO = ptx::smem_u32(sdO);
-      auto kmaj = [](uint32_t base, int kk) {
-        return ptx::sdesc_advance(ptx::sdesc_sw128(base, 16, 1024), (kk >> 2) * BOX_BYTES + (kk & 3) * 32);
-      };
-      auto mnmaj = [](uint32_t base, int kk) {
-        return ptx::sdesc_advance(ptx::sdesc_sw128(base, BOX_BYTES, 1024), kk * 2048);
-      };
-      auto mma_st = [&](uint32_t n) {   // S^T = K Q^T
-#pragma unroll
+      auto kmaj = [](uint64_t base, int kk) { return ptx::sdesc_advance(base, (kk >> 2) * BOX_BYTES + (kk & 3) * 32); };
+      auto mnmaj = [](uint64_t base, int kk) { return ptx::sdesc_advance(base, kk * 2048); };
+      const uint64_t k_desc = scored::formed(ptx::sdesc_sw128(aK, 16, 1024));
+      const uint64_t v_desc = scored::formed(ptx::sdesc_sw128(aV, 16, 1024));
+      // K-major and M/N-major descriptors of row tile n's Q and dO
+      auto q_k = [&](uint32_t n) { return scored::formed(ptx::sdesc_sw128(aQ + qslot(n) * C::TILE, 16, 1024)); };
+      auto q_m = [&](uint32_t n) { return scored::formed(ptx::sdesc_sw128(aQ + qslot(n) * C::TILE, BOX_BYTES, 1024)); };
+      auto o_k = [&](uint32_t n) { return scored::formed(ptx::sdesc_sw128(adO + oslot(n) * C::TILE, 16, 1024)); };
+      auto o_m = [&](uint32_t n) { return scored::formed(ptx::sdesc_sw128(adO + oslot(n) * C::TILE, BOX_BYTES, 1024)); };
+      // (products unrolled by 4: see the forward)
+      auto mma_st = [&](uint64_t q) {   // S^T = K Q^T
+#pragma unroll 4
         for (int kk = 0; kk < HD / 16; ++kk)
-          ptx::mma_ss(tmem + T_ST, kmaj(aK, kk), kmaj(aQ + qslot(n) * C::TILE, kk), C::IDESC_S, kk > 0);
+          ptx::mma_ss(tmem + T_ST, kmaj(k_desc, kk), kmaj(q, kk), C::IDESC_S, kk > 0);
         ptx::mma_commit(s_full);
       };
-      auto mma_dpt = [&](uint32_t n) {   // dP^T = V dO^T
-#pragma unroll
+      auto mma_dpt = [&](uint64_t o) {   // dP^T = V dO^T
+#pragma unroll 4
         for (int kk = 0; kk < HD / 16; ++kk)
-          ptx::mma_ss(tmem + T_DP, kmaj(aV, kk), kmaj(adO + oslot(n) * C::TILE, kk), C::IDESC_S, kk > 0);
+          ptx::mma_ss(tmem + T_DP, kmaj(v_desc, kk), kmaj(o, kk), C::IDESC_S, kk > 0);
         ptx::mma_commit(dp_full);
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -890,19 +895,20 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
       int nq = next_unit(), nq_next = 0;
       bool ok = nq >= 0;
       while (ok && nq > 0) {
+        const uint64_t q0 = q_k(q_it), o0 = o_k(q_it);
         if (!(ok = wait(kv_full, u_it & 1u))) break;
         if (!(ok = wait(q_full + qslot(q_it), qpar(q_it)))) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           moved |= lane != 0;
-          mma_st(q_it);
+          mma_st(q0);
         }
         __syncwarp();
         if (!(ok = wait(o_full + oslot(q_it), opar(q_it)))) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           moved |= lane != 0;
-          mma_dpt(q_it);
+          mma_dpt(o0);
           // K and V are read by no later MMA of a one-tile unit
           if (nq == 1) ptx::mma_commit(kv_empty);
         }
@@ -916,6 +922,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
           }
           const uint32_t it = q_it + ii;
           const bool more = ii + 1 < nq;
+          const uint64_t om = o_m(it), qm = q_m(it), qn = q_k(it + 1), on = o_k(it + 1);
           // dV += P^T dO, then the next S^T (which overwrites P^T). A unit's
           // first dV (dK) overwrites the accumulator: the epilogue must have
           // read the previous unit's.
@@ -924,12 +931,12 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
             moved |= lane != 0;
-#pragma unroll
+#pragma unroll 4
             for (int kk = 0; kk < BT / 16; ++kk)
-              ptx::mma_ts(tmem + T_DV, tmem + T_ST + packed_col(kk), mnmaj(adO + oslot(it) * C::TILE, kk),
+              ptx::mma_ts(tmem + T_DV, tmem + T_ST + packed_col(kk), mnmaj(om, kk),
                           C::IDESC_ACC, (ii > 0 || kk > 0) ? 1u : 0u);
             ptx::mma_commit(o_empty + oslot(it));
-            if (more) mma_st(it + 1);
+            if (more) mma_st(qn);
           }
           __syncwarp();
           if (ii == 0 && !(ok = wait(dk_free, (u_it & 1u) ^ 1u))) break;
@@ -938,9 +945,9 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
             moved |= lane != 0;
-#pragma unroll
+#pragma unroll 4
             for (int kk = 0; kk < BT / 16; ++kk)
-              ptx::mma_ts(tmem + T_DK, tmem + T_DP + packed_col(kk), mnmaj(aQ + qslot(it) * C::TILE, kk),
+              ptx::mma_ts(tmem + T_DK, tmem + T_DP + packed_col(kk), mnmaj(qm, kk),
                           C::IDESC_ACC, (ii > 0 || kk > 0) ? 1u : 0u);
             ptx::mma_commit(q_empty + qslot(it));
           }
@@ -950,7 +957,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
             ptx::tc_fence_after();
             if (ptx::elect_one()) {
               moved |= lane != 0;
-              mma_dpt(it + 1);
+              mma_dpt(on);
               if (ii + 2 == nq) ptx::mma_commit(kv_empty);   // the unit's last product of K or V
             }
             __syncwarp();

@@ -225,24 +225,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // 0) issues the MMAs and commits (see fwd_bf16.cu).
       ptx::WaitCtx w{abort_flag, P.status, 3u};
       const uint32_t sQa = ptx::smem_u32(sQ), sKVa = ptx::smem_u32(sKV);
-      auto mma_S = [&](int t, int sl) {
+      const uint64_t q_desc[2] = {scored::formed(ptx::sdesc_sw128(sQa, 16, 1024)),
+                                  scored::formed(ptx::sdesc_sw128(sQa + C::TILE, 16, 1024))};
+      auto k_desc = [&](int sl) { return scored::formed(ptx::sdesc_sw128(sKVa + sl * C::TILE, 16, 1024)); };
+      auto v_desc = [&](int sl) { return scored::formed(ptx::sdesc_sw128(sKVa + sl * C::TILE, BOX_BYTES, 1024)); };
+      // (unrolled by 4: whole, the eight products of each call fill the
+      // instruction cache, 141 in place of 138 us at B=2 H=16 T=4096 d=128
+      // with a cap; one at a time, the loop holds them up, 149)
+      auto mma_S = [&](int t, uint64_t k) {
         const uint32_t d = tmem + t * 256;
-#pragma unroll
+#pragma unroll 4
         for (int kk = 0; kk < HD / 16; ++kk) {
           const uint32_t off = (kk >> 2) * BOX_BYTES + (kk & 3) * 32;
-          const uint64_t a = ptx::sdesc_advance(ptx::sdesc_sw128(sQa + t * C::TILE, 16, 1024), off);
-          const uint64_t b = ptx::sdesc_advance(ptx::sdesc_sw128(sKVa + sl * C::TILE, 16, 1024), off);
-          ptx::mma_ss(d, a, b, C::IDESC_S, kk > 0 ? 1u : 0u);
+          ptx::mma_ss(d, ptx::sdesc_advance(q_desc[t], off), ptx::sdesc_advance(k, off), C::IDESC_S, kk > 0 ? 1u : 0u);
         }
         ptx::mma_commit(s_full + t);
       };
-      auto mma_PV = [&](int t, int sl, bool acc) {
+      auto mma_PV = [&](int t, uint64_t v, bool acc) {
         const uint32_t d = tmem + t * 256 + 128, a = tmem + t * 256;
-#pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk) {
-          const uint64_t b = ptx::sdesc_advance(ptx::sdesc_sw128(sKVa + sl * C::TILE, BOX_BYTES, 1024), kk * 2048);
-          ptx::mma_ts(d, a + kk * 8, b, C::IDESC_PV, (acc || kk > 0) ? 1u : 0u);
-        }
+#pragma unroll 4
+        for (int kk = 0; kk < BN / 16; ++kk)
+          ptx::mma_ts(d, a + kk * 8, ptx::sdesc_advance(v, kk * 2048), C::IDESC_PV, (acc || kk > 0) ? 1u : 0u);
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, w));
@@ -260,14 +263,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool ok = next_unit(&u);
       while (ok && u.bh >= 0) {
         const int n = u.e0 - u.s0;
+        const uint64_t k0 = k_desc(slot(item));
         if (!(ok = wait(q_full, u_it & 1u))) break;
         if (!(ok = wait(kv_full + slot(item), par(item)))) break;
         ptx::tc_fence_after();
         // (selects by constant index keep pp, s and e in registers)
         if (ptx::elect_one()) {
           moved |= lane != 0;
-          if (u.s[0] == u.s0 && u.e[0] > u.s[0]) mma_S(0, slot(item));
-          if (u.s[1] == u.s0 && u.e[1] > u.s[1]) mma_S(1, slot(item));
+          if (u.s[0] == u.s0 && u.e[0] > u.s[0]) mma_S(0, k0);
+          if (u.s[1] == u.s0 && u.e[1] > u.s[1]) mma_S(1, k0);
           ptx::mma_commit(kv_empty + slot(item));
           if (n == 1) ptx::mma_commit(q_empty);   // no later MMA reads Q: the next unit's may load
         }
@@ -278,6 +282,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int j = u.s0; j < u.e0; ++j, item += 2) {
           if (j + 1 == u.e0 && !(ok = next_unit(&un))) break;
           const uint32_t iv = item + 1, ikn = item + 2;   // V_j, K_{j+1}: resident
+          const uint64_t v = v_desc(slot(iv)), k = k_desc(slot(ikn));
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const bool act = j >= u.s[t] && j < u.e[t];
@@ -289,8 +294,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             if (ptx::elect_one()) {
               moved |= lane != 0;
-              if (act) mma_PV(t, slot(iv), j > u.s[t]);
-              if (next) mma_S(t, slot(ikn));
+              if (act) mma_PV(t, v, j > u.s[t]);
+              if (next) mma_S(t, k);
               if (act && !next) ptx::mma_commit(o_full + t);
               if (t == 1) {
                 ptx::mma_commit(kv_empty + slot(iv));

@@ -77,6 +77,13 @@ __device__ __forceinline__ int packed_block(int i, int n_padded, int G) {
   return (i % G) * per + i / G;
 }
 
+// A descriptor that exists from here on: the compiler would otherwise form it
+// behind the wait before the product that uses it, where its latency counts.
+__device__ __forceinline__ uint64_t formed(uint64_t desc) {
+  asm volatile("" : "+l"(desc));
+  return desc;
+}
+
 // Zeroes row r of a swizzled box of 64 bf16 columns in shared memory. The
 // swizzle moves 16-byte pieces within a row only; taken in its order, eight
 // rows' pieces are in different banks.
