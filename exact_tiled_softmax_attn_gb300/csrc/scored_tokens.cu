@@ -16,7 +16,7 @@
 // The products run on mma.m16n8k16: with 16 rows or fewer per key head the
 // tcgen05 tile of 128 rows would be mostly empty, and at this intensity (at
 // most 32 rows) the memory is what counts: 32 sequences of 32768 keys, H=32
-// Hkv=8 d=128, 2.6 GB, 365 us or 7.0 TB/s; 87 us of 79 with 16 rows at B=8
+// Hkv=8 d=128, 2.6 GB, 357 us or 7.2 TB/s; 87 us of 79 with 16 rows at B=8
 // Hkv=8 Tk=16384. Four row tiles of 16 were tried too: 338 us there with 64
 // rows, where the 128-row tiles take 112. Fragments are read as 16-byte
 // vectors: the columns of Q and K are permuted alike, so that a thread's
