@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           mx = -CUDART_INF_F;
           auto value = [&](float x) {
             if constexpr (CAP)
-              return x == -CUDART_INF_F ? x : scored::cap_any(x, P.cap);
+              return x == -CUDART_INF_F ? x : scored::cap_rough(x, P.cap);
             else
               return x * sc2;
           };
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         } else {
           mx = all_max();
           if constexpr (CAP)
-            mx = mx == -CUDART_INF_F ? mx : scored::cap_any(mx, P.cap);   // the cap is monotone
+            mx = mx == -CUDART_INF_F ? mx : scored::cap_rough(mx, P.cap);   // the cap is monotone
           else
             mx *= sc2;
         }

@@ -16,44 +16,59 @@ constexpr float kLog2e = 1.4426950408889634f;
 // y = cap2 * tanh(k s), s the raw product q.k, k = scale / softcap, cap2 =
 // softcap * log2(e). Three forms, chosen per warp and tile by the largest
 // |k s|: s times a polynomial in s^2 that has k and cap2 in its coefficients,
-// of degree 2 up to 0.25 and of degree 4 up to 0.6, and beyond (or where k^8
-// leaves fp32's range) the formula 1 - 2 / (1 + e^(2x)). The polynomials are
-// fits of tanh(x) / x in x^2 (least squares with Lawson's reweighting): |x *
-// poly - tanh(x)| <= 4.9e-8 and 2.0e-8, below 1e-7 as evaluated in fp32, the
-// size of fp32's own rounding. Per pair of scores they cost 4 and 6 two-lane
-// FMA-pipe instructions (2 issue cycles each); the formula costs 2
+// of degree 2 up to 0.25 and of degree 4 up to 0.6, and beyond cap_any, which
+// chooses per score: that polynomial of degree 4 in (k s)^2 up to 0.6, else
+// the formula 1 - 2 / (1 + e^(2x)). The formula alone would be off by a few
+// 2^-24 of the cap, whatever the score: 0.1 at a cap of 10^6. A form is left
+// out where a coefficient of it leaves fp32's range (degree 4 from a cap of
+// about 2000 on at d = 128; degree 2 only for scales far from 1/sqrt(d)). The
+// polynomials are fits of tanh(x) / x in x^2 (least squares with Lawson's
+// reweighting) in the relative error, 4.0e-7 and 7.4e-8 at most, which is what
+// scores far inside the cap need. Per pair of scores they cost 4 and 6
+// two-lane FMA-pipe instructions (2 issue cycles each); the formula costs 2
 // special-function instructions a score more than the uncapped exponential.
 // Scores of a trained layer lie well inside the cap.
+constexpr float kCapLimit2 = 0.25f, kCapLimit4 = 0.6f;
+constexpr double kCapPoly2Fit[3] = {0.9999996043350667, -0.33321908145397344, 0.12841612166110375};
+constexpr double kCapPoly4Fit[5] = {0.9999999268660169, -0.3333230996151517, 0.13310173509714307,
+                                    -0.05210147391716534, 0.015475418969482619};
 struct Cap {
-  float k2;        // 2 k log2(e): e^(2 k s) = 2^(k2 s)
+  float k;         // scale / softcap
   float cap2;      // softcap * log2(e)
   float ninv2;     // -1 / cap2^2
   float limit2;    // |s| up to which the polynomial of degree 2 holds, or -1
   float limit4;    // and that of degree 4
   float c2[3];     // polynomials in s^2
   float c4[5];
+  float n4[5];     // that of degree 4 in (k s)^2
 };
 
 inline Cap make_cap(float scale, float softcap) {
   Cap r{};
   if (!(softcap > 0.f)) return r;
-  const double c2[3] = {0.9999986329868529, -0.3331570156541373, 0.12762232173572735};
-  const double c4[5] = {0.9999996274092242, -0.333312085910721, 0.13299210221337304, -0.05169674295522158,
-                        0.014976960081731636};
+  constexpr double kLeast = 1.2e-38, kMost = 1e38;   // within fp32's normal numbers
   const double k = static_cast<double>(scale) / softcap, cap2 = softcap * 1.4426950408889634;
-  const double k2 = 2.0 * k * 1.4426950408889634;
-  r.k2 = k2 < 1e30 ? static_cast<float>(k2) : 1e30f;   // (any score but 0 is at the cap there)
+  const double sc2 = scale * 1.4426950408889634;
+  r.k = k < 1e30 ? static_cast<float>(k) : 1e30f;   // (any score but 0 is at the cap there)
   r.cap2 = static_cast<float>(cap2);
   r.ninv2 = static_cast<float>(-1.0 / (cap2 * cap2));
-  const double k8 = k * k * k * k * k * k * k * k;
-  const bool fits = k8 > 1e-30 && k8 < 1e30;
-  r.limit2 = fits ? static_cast<float>(0.25 / k) : -1.f;
-  r.limit4 = fits ? static_cast<float>(0.6 / k) : -1.f;
-  double kk = k * cap2;
-  for (int i = 0; i < 5; ++i, kk *= k * k) {
-    if (i < 3) r.c2[i] = static_cast<float>(c2[i] * kk);
-    r.c4[i] = static_cast<float>(c4[i] * kk);
+  bool fits2 = kCapLimit2 < k * 1e19, fits4 = kCapLimit4 < k * 1e19;   // (s^2 within range)
+  double p = sc2;
+  for (int i = 0; i < 5; ++i, p *= k * k) {
+    const double a4 = kCapPoly4Fit[i] * p, size4 = a4 < 0 ? -a4 : a4;
+    fits4 = fits4 && size4 > kLeast && size4 < kMost;
+    r.c4[i] = static_cast<float>(a4);
+    const double n4 = kCapPoly4Fit[i] * sc2;
+    r.n4[i] = static_cast<float>(n4 > kMost ? kMost : n4 < -kMost ? -kMost : n4);
+    if (i > 2) continue;
+    const double a2 = kCapPoly2Fit[i] * p, size2 = a2 < 0 ? -a2 : a2;
+    fits2 = fits2 && size2 > kLeast && size2 < kMost;
+    r.c2[i] = static_cast<float>(a2);
   }
+  r.limit2 = fits2 ? static_cast<float>(kCapLimit2 / k) : -1.f;
+  r.limit4 = fits4 ? static_cast<float>(kCapLimit4 / k) : r.limit2;
+  if (!fits4)   // where a kernel takes degree 4 for degree 2's range
+    for (int i = 0; i < 5; ++i) r.c4[i] = i < 3 ? r.c2[i] : 0.f;
   return r;
 }
 
@@ -181,13 +196,24 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// cap2 * tanh(k s) for any s: -cap2 and cap2 at the infinities.
+// cap2 * tanh(k s) to within a few 2^-24 of cap2: enough for the references
+// that exponentials and sums share.
+__device__ __forceinline__ float cap_rough(float s, const Cap& c) {
+  return fmaf(-2.f * c.cap2, rcp_approx(1.f + ptx::ex2(s * c.k * (2.f * kLog2e))), c.cap2);
+}
+// cap2 * tanh(k s) for any s: -cap2 and cap2 at the infinities. (Two-lane FMAs
+// would hold the coefficients in registers, and the kernels' frequent forms
+// would spill for it: 569 in place of 560 us for a training step of B=2 H=16
+// T=4096 d=128 whose scores stay far inside the cap.)
 __device__ __forceinline__ float cap_any(float s, const Cap& c) {
-  return fmaf(-2.f * c.cap2, rcp_approx(1.f + ptx::ex2(s * c.k2)), c.cap2);
+  const float x = s * c.k, u = x * x;
+  float g = fmaf(c.n4[4], u, c.n4[3]);
+#pragma unroll
+  for (int i = 2; i >= 0; --i) g = fmaf(g, u, c.n4[i]);
+  const float far = fmaf(-2.f * c.cap2, rcp_approx(1.f + ptx::ex2(x * (2.f * kLog2e))), c.cap2);
+  return fabsf(x) <= kCapLimit4 ? s * g : far;
 }
-__device__ __forceinline__ F2 cap_any(F2 s, const Cap& c) {
-  return f2(cap_any(s.x, c), cap_any(s.y, c));
-}
+__device__ __forceinline__ F2 cap_any(F2 s, const Cap& c) { return f2(cap_any(s.x, c), cap_any(s.y, c)); }
 
 }  // namespace scored
 }  // namespace attn

@@ -321,14 +321,40 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::THREADS, Cfg<HD, RT>::CTAS)
           }
         }
         // changed and masked scores, in log2 units; x[i][2 r + e] is row g + 8 r, key 8 i + (e ? k_hi : k_lo)
+        if (P.p.softcap > 0.f) {   // the cap's form by the warp's scores; degree 4 holds where degree 2 does
+          float top = 0.f;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[i][e]));
+          if (__all_sync(0xffffffffu, !(top > P.cap.limit4))) {
+            const scored::CapPoly<scored::kCapPoly4> poly(P.cap);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const scored::F2 v = scored::f2(x[i][e], x[i][e + 1]), y = scored::mul2(v, poly(v));
+                x[i][e] = y.x, x[i][e + 1] = y.y;
+              }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[i][e] = scored::cap_any(x[i][e], P.cap);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i][e] *= P.sc2;
+        }
         float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int r = e >> 1, key = key0 + 8 * i + ((e & 1) ? k_hi : k_lo);
-            float y = P.p.softcap > 0.f ? scored::cap_any(x[i][e], P.cap) : x[i][e] * P.sc2;
-            y = fmaf(-slope2[r], fabsf(static_cast<float>(key - pos[r])), y);
+            const float y = fmaf(-slope2[r], fabsf(static_cast<float>(key - pos[r])), x[i][e]);
             x[i][e] = key >= lo[r] && key < hi[r] ? y : -CUDART_INF_F;
             mx[r] = fmaxf(mx[r], x[i][e]);
           }

@@ -1,0 +1,119 @@
+"""Scored attention at the ends of what it accepts: caps far above the scores.
+
+Tolerances are those of the other bf16 tests of the scored attention: with a
+cap of any size a score is off by a few 2^-24 of itself, below 1e-4 for the
+scores of these inputs (up to 50).
+"""
+import math
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import exact_tiled_softmax_attn_gb300 as B
+from oracle import scored as ref
+
+from parity import check_o, np64
+from test_scored import check_grad, check_lse, how_of, magnitudes, make, run_case
+
+CSRC = os.path.join(os.path.dirname(os.path.abspath(B.__file__)), "csrc")
+
+
+# ------------------------------------------------------------------ the cap
+
+def relative_fit(degree, top):
+    """The polynomial of tanh(x) / x in x^2 on (0, top] with the least largest relative error: (error, coefficients).
+
+    Least squares, reweighted by the errors until the largest are equal (Lawson)."""
+    x = top * np.sin(np.linspace(0.0, np.pi / 2, 4001))[1:]
+    want = np.tanh(x) / x
+    a = np.vander((x / top) ** 2, degree + 1, increasing=True)
+    w = np.full(len(x), 1.0 / len(x))
+    best = (1.0, None)
+    for _ in range(400):
+        s = np.sqrt(w) / want
+        c = np.linalg.lstsq(a * s[:, None], want * s, rcond=None)[0]
+        e = np.abs(a @ c / want - 1.0)
+        if e.max() < best[0]:
+            best = (e.max(), c / top ** (2 * np.arange(degree + 1)))
+        w = w * e
+        w /= w.sum()
+    return best
+
+
+@pytest.mark.parametrize("degree,top,bound", [(2, 0.25, 4.0e-7), (4, 0.6, 7.4e-8)])
+def test_the_caps_polynomials_are_their_fits(degree, top, bound):
+    text = open(os.path.join(CSRC, "scored_math.cuh")).read()
+    assert "kCapLimit%d = %gf" % (degree, top) in text
+    held = [float(t) for t in re.search(r"kCapPoly%dFit\[%d\] = \{([^}]*)\}" % (degree, degree + 1),
+                                        text).group(1).split(",")]
+    x = np.linspace(0.0, top, 20001)[1:]
+    assert np.abs(np.polyval(held[::-1], x * x) * x / np.tanh(x) - 1.0).max() <= bound
+    best, c = relative_fit(degree, top)
+    assert best <= bound <= 1.02 * best
+    assert np.abs(np.polyval((np.array(held) - c)[::-1], x * x)).max() <= 1e-9
+
+
+CAPS = [(1e3, None), (5.5e3, None), (1e4, None), (1e5, None), (1e6, None), (50.0, 1.0 / 128), (1e6, 1.0 / 128),
+        (1e-4, None), (3.0, 40.0)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap,scale", CAPS)
+@pytest.mark.parametrize("shape,mask,bias", [((1, 4, 2, 300, 300, 128, 128), "causal", False),
+                                             ((2, 4, 4, 260, 300, 64, 64), "docs", True),
+                                             ((1, 8, 1, 300, 260, 64, 64), "wild", False)])
+def test_caps_of_any_size(shape, mask, bias, cap, scale):
+    if scale != 40.0:
+        run_case(shape, mask, cap, bias, torch.bfloat16, grad=True, scale=scale)
+        return
+    # Scores of a spread of 200 caps: T = 1 - (t / cap)^2 leaves a row two or three of its keys, and where those have
+    # most of its weight, dP - D is small beside D. The O in D is rounded, by half a step of each element, so dS is off
+    # by up to P T 2^-8 |dO| |O|, however small dP - D is: no bound in the norm of dQ, which T makes small too. The
+    # bound by terms instead: dS rounded and D's O rounded (2 half steps of P (|dO| |V| + |dO| |O|)), for dK P T too,
+    # and the result; T and P off by what the score is off, d roundings of its product, over the cap.
+    run_case(shape, mask, cap, bias, torch.bfloat16, grad=False, scale=scale)
+    Bn, H, Hkv, Tq, Tk, d, dv = shape
+    x, how = make(*shape, torch.bfloat16, seed=Tq + 3 * Tk + d), how_of(mask, cap, bias, Bn, H, Tq, Tk)
+    o, lse = B.forward_scored(*x[:3], scale=scale, **how)
+    g = B.backward_scored(*x[:3], o, lse, x[3], scale=scale, **how)
+    flat = dict(how, slopes=torch.zeros(H)) if how["slopes"] is None else how
+    r, size = ref.scored(*x, scale=scale, **how), magnitudes(x, flat, scale)
+    rel = 3 * 2.0 ** -8 + 2 * d * 2.0 ** -24 * size["score"] / cap + 1e-5
+    for t, name in zip(g, ("dQ", "dK", "dV")):
+        assert (np.abs(np64(t) - r[name]) <= rel * size[name] + 2.0 ** -8 * np.abs(r[name]) + 1e-6).all(), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap,scale", CAPS)
+@pytest.mark.parametrize("shape,mask,bias", [((1, 8, 8, 1, 3000, 128, 128), "causal", False),
+                                             ((3, 16, 2, 2, 700, 64, 64), "window", True),
+                                             ((2, 4, 1, 7, 300, 128, 64), "wild", False)])
+def test_caps_of_any_size_with_few_rows(shape, mask, bias, cap, scale):
+    run_case(shape, mask, cap, bias, torch.bfloat16, grad=False, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap", [30.0, 1e3, 1e5, 1e6])
+@pytest.mark.parametrize("Tq", [5, 200])
+def test_a_rows_scores_do_not_suffer_from_its_neighbours(Tq, cap):
+    """One row's scores reach the cap, and so would those of keys that no row sees; the other rows' stay small."""
+    Bn, H, Hkv, Tk, d = 1, 2, 2, 500, 64
+    x = make(Bn, H, Hkv, Tq, Tk, d, d, torch.bfloat16, 61)
+    x[0][:, :, 3] *= cap / 8
+    x[1][:, :, Tk - 40:] *= cap / 8
+    how = dict(softcap=cap, key_end=torch.full((Bn, Tq), Tk - 40, dtype=torch.int32, device="cuda"))
+    o, lse = B.forward_scored(*x[:3], **how)
+    dq, dk, dv = B.backward_scored(*x[:3], o, lse, x[3], **how)
+    assert B.attn_device_status() == B.ATTN_OK
+    r = ref.scored(*x, scale=1.0 / math.sqrt(d), **how)
+    check_o(o, r["O"], torch.bfloat16)
+    rest = [i for i in range(Tq) if i != 3]
+    check_lse(lse[:, :, rest], r["LSE"][:, :, rest], torch.bfloat16)
+    # beyond 0.6 of the cap: 3e-7 of the cap from the formula, and the sum of products' own rounding
+    assert np.abs(np64(lse)[:, :, 3] - r["LSE"][:, :, 3]).max() <= 1e-4 + 2e-6 * cap
+    check_grad(dq[:, :, rest], r["dQ"][:, :, rest], torch.bfloat16, "dQ")
+    check_grad(dv, r["dV"], torch.bfloat16, "dV")
+    assert not dk[:, :, Tk - 40:].any() and not dv[:, :, Tk - 40:].any()
