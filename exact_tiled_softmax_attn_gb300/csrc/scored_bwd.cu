@@ -555,6 +555,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         uint32_t v[32];
         ptx::tmem_ld32(tDQ + c * 32, v);
         ptx::tmem_ld_wait(v);
+        if (ri.y == 0) {   // sees no key (0 times what other rows see may be NaN)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
         uint4 pk[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {

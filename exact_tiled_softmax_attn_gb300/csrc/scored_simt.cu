@@ -146,6 +146,12 @@ __device__ __forceinline__ void acc_cols(float (&acc)[4][4 * NC], const float* w
   }
 }
 
+template <int N>
+__device__ __forceinline__ void zero_row(float (&acc)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) acc[e] = 0.f;
+}
+
 template <int NC>
 __device__ __forceinline__ void store_row(float* row, const float (&acc)[4 * NC], float mul, int d) {
   const int tx = threadIdx.x & 15;
@@ -273,6 +279,7 @@ __global__ void __launch_bounds__(NT) fwd_kernel(const ScoredProblem p, const Sc
     const bool none = l[i] == 0.f;   // no key seen (a NaN among the row's scores goes through)
     const float inv = none ? 0.f : 1.f / l[i];
     const float lse = none ? -CUDART_INF_F : m[i] + logf(l[i]);
+    if (none) zero_row(acc[i]);   // (0 times what other rows see may be NaN)
     if (n_splits > 1) {
       store_row<NCV>(Opart + (split * rows + row) * p.dv, acc[i], inv, p.dv);
       if (tx == 0) LSEpart[split * rows + row] = lse;
@@ -347,6 +354,7 @@ __global__ void __launch_bounds__(NT) dq_kernel(const ScoredProblem p, const Sco
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = r0 + 4 * ty + i;
+    if (ri.hi[i] == 0) zero_row(acc[i]);   // (as in the forward)
     if (r < p.R)
       store_row<NCK>(dQ + (static_cast<long long>(bh) * p.R + r) * p.d, acc[i], p.scale, p.d);
   }
@@ -381,6 +389,7 @@ __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const S
 #pragma unroll
     for (int e = 0; e < 4 * NCV; ++e) av[i][e] = 0.f;
   }
+  const int4 hull = plan.khull[static_cast<long long>(b) * p.n_kt + k0 / kScoredTile];
   const uint32_t* list = plan.kbits + (static_cast<long long>(b) * p.n_kt + k0 / kScoredTile) * p.n_words();
   const int rows = p.kv_split_tiles * kScoredTile, part = blockIdx.y;
   for (int r0 = part * rows; r0 < min(p.R, (part + 1) * rows); r0 += KM) {
@@ -433,6 +442,10 @@ __global__ void __launch_bounds__(NT) dkdv_kernel(const ScoredProblem p, const S
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int key = k0 + 4 * ky + i;
+    if (key < hull.x || key >= hull.y) {   // seen by no row
+      zero_row(ak[i]);
+      zero_row(av[i]);
+    }
     if (key < p.Tk) {
       const long long at = (static_cast<long long>(part) * p.B * p.Hkv + bh) * p.Tk + key;
       store_row<NCK>(dK + at * p.d, ak[i], p.scale, p.d);

@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::THREADS, Cfg<HD, RT>::CTAS)
       for (int r = 0; r < 2; ++r) {
         if (row[r] >= R) continue;
         const bool none = l[r] == 0.f;   // no key seen (a NaN among the row's scores goes through)
-        const float inv = none ? 0.f : 1.f / l[r];
+        const float inv = 1.f / l[r];
         const float lse = none ? -CUDART_INF_F : (m[r] + log2f(l[r])) * 0.69314718055994530942f;
         const long long at = whole ? static_cast<long long>(bh) * R + row[r]
                                    : (static_cast<long long>(blockIdx.x) * 2 + part) * R + row[r];
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::THREADS, Cfg<HD, RT>::CTAS)
             if (col >= dv) continue;
             float f[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = o[8 * c + i][2 * r + e] * inv;
+            for (int i = 0; i < 8; ++i) f[i] = none ? 0.f : o[8 * c + i][2 * r + e] * inv;
             if (whole) {
               *reinterpret_cast<uint4*>(P.O + at * dv + col) =
                   make_uint4(ptx::pack_bf16(f[0], f[1]), ptx::pack_bf16(f[2], f[3]), ptx::pack_bf16(f[4], f[5]),

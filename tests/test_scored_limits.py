@@ -117,3 +117,38 @@ def test_a_rows_scores_do_not_suffer_from_its_neighbours(Tq, cap):
     check_grad(dq[:, :, rest], r["dQ"][:, :, rest], torch.bfloat16, "dQ")
     check_grad(dv, r["dV"], torch.bfloat16, "dV")
     assert not dk[:, :, Tk - 40:].any() and not dv[:, :, Tk - 40:].any()
+
+
+# ------------------------------------------------------------------ rows and keys that nothing concerns
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (4.0, True)])
+@pytest.mark.parametrize("shape", [(1, 2, 2, 3, 300, 64, 64), (1, 8, 1, 4, 2000, 128, 40), (2, 4, 2, 150, 300, 128, 64),
+                                   (1, 1, 1, 300, 2100, 64, 64), (1, 8, 1, 300, 260, 64, 64)])
+def test_zeros_beside_infinities_that_others_see(shape, cap, bias, dtype):
+    """Rows that see no key give O = 0, LSE = -inf and dQ = 0, and keys before and behind every range dK = dV = 0,
+    whatever the rows and keys of others hold: infinite V and K in their ranges, NaN in their dO."""
+    Bn, H, Hkv, Tq, Tk, d, dv = shape
+    x = make(*shape, dtype, 67)
+    how = how_of("none", cap, bias, Bn, H, Tq, Tk)
+    empty = torch.arange(Tq) % 3 == 1
+    how["key_begin"] = torch.full((Bn, Tq), 2, dtype=torch.int32, device="cuda")
+    how["key_end"] = torch.where(empty, 0, Tk - 3).to(torch.int32).expand(Bn, Tq).contiguous().cuda()
+    at = empty.nonzero()[:, 0].cuda()
+
+    def check():
+        o, lse = B.forward_scored(*x[:3], **how)
+        assert not o[:, :, at].any() and torch.isneginf(lse[:, :, at]).all()
+        dq, dk, dv_ = B.backward_scored(*x[:3], o, lse, x[3], **how)
+        assert B.attn_device_status() == B.ATTN_OK
+        assert not dq[:, :, at].any()
+        for t in (dk, dv_):
+            assert not t[:, :, :2].any() and not t[:, :, Tk - 3:].any()
+    check()
+    x[2][:, :, Tk // 2] = float("inf")
+    check()
+    x[3][:, :, 0] = float("nan")
+    check()
+    x[1][:, :, 5] = float("inf")
+    check()
