@@ -200,12 +200,13 @@ __global__ void __launch_bounds__(256) merge_kernel(const ScoredProblem p, const
   const float ref = mx == -CUDART_INF_F ? 0.f : mx;
 #pragma unroll 4
   for (int s = first; s <= last; ++s) {
-    const float w = expf(LSEpart[s * rows + r] - ref);   // 0 for a range without keys
+    // 0 for a range without keys, whose row is zeros; where the weight of one with keys underflows, a NaN in it shows
+    const float w = expf(LSEpart[s * rows + r] - ref);
     wsum += w;
     const float* o = Opart + (s * rows + r) * p.dv;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (lane + 32 * c < p.dv && w != 0.f) acc[c] = fmaf(w, o[lane + 32 * c], acc[c]);
+      if (lane + 32 * c < p.dv) acc[c] = fmaf(w, o[lane + 32 * c], acc[c]);
   }
   if (wsum != 0.f) {   // (NaN too)
     const float inv = 1.0f / wsum;

@@ -561,12 +561,15 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
   const int col = 4 * lane;
   for (int i0 = w; i0 < parts; i0 += 32 * WPR) {   // lane k: the weight of part i0 + k WPR
     const int mine = i0 + lane * WPR;
-    const float weight = mine < parts ? expf(lse_of(mine) - ref) : 0.f;
+    const float lse = mine < parts ? lse_of(mine) : -CUDART_INF_F;
+    const float weight = expf(lse - ref);
+    // parts whose CTA wrote them; the weight of one may underflow, and a NaN in it still shows
+    const unsigned written = __ballot_sync(0xffffffffu, lse != -CUDART_INF_F);
     const int count = min(32, (parts - i0 + WPR - 1) / WPR);
 #pragma unroll 4
     for (int k = 0; k < count; ++k) {
       const float x = __shfl_sync(0xffffffffu, weight, k);
-      if (x != 0.f && col < dv) {
+      if ((written >> k & 1u) && col < dv) {
         const float4 v = *reinterpret_cast<const float4*>(P.Opart + at(i0 + k * WPR) * dv + col);
         acc.x = fmaf(x, v.x, acc.x);
         acc.y = fmaf(x, v.y, acc.y);

@@ -323,8 +323,9 @@ typedef struct {
  * else ATTN_ERR_UNSUPPORTED. Tq, Tk <= 2^30, and H / Hkv * Tq too.
  * What no query reads may hold anything, NaN included: K and V rows that lie
  * before every range or behind every range of their batch entry (unused
- * capacity of a cache), and Q rows whose range is empty (padding). A NaN that
- * a row does see makes its O and LSE NaN.
+ * capacity of a cache), and Q rows whose range is empty (padding). A NaN among
+ * the scores that a row sees makes its O and LSE NaN; one in a value that it
+ * sees makes that element of its O NaN, whatever the weight.
  * `workspace`: as in attn_fwd_splitkv (256-byte aligned, at least
  * attn_fwd_scored_workspace_size bytes, not overlapping any argument), else
  * ATTN_ERR_WORKSPACE; it is scratch, overwritten by each call, so calls that

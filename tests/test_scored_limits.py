@@ -152,3 +152,25 @@ def test_zeros_beside_infinities_that_others_see(shape, cap, bias, dtype):
     check()
     x[1][:, :, 5] = float("inf")
     check()
+
+
+# ------------------------------------------------------------------ what a row does see
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 2, 2, 1, 3000, 64, 64), (1, 8, 1, 4, 2000, 128, 40), (2, 4, 2, 150, 300, 128, 64),
+                                   (1, 2, 1, 300, 3000, 64, 64)])
+def test_a_nan_among_the_values_shows_whatever_its_weight(shape, dtype):
+    """A steep bias leaves far keys weights below fp32's range, in ranges of keys of their own too; a NaN in one
+    element of such a key's value is a NaN in that column of O, and nowhere else."""
+    Bn, H, Hkv, Tq, Tk, d, dv = shape
+    x = make(*shape, dtype, 71, grad=False)
+    how = dict(slopes=torch.full((H,), 2.0, device="cuda"),
+               q_pos=torch.full((Bn, Tq), Tk, dtype=torch.int32, device="cuda"))
+    want = B.forward_scored(*x, **how)
+    x[2][:, :, 17, 3] = float("nan")
+    o, lse = B.forward_scored(*x, **how)
+    assert B.attn_device_status() == B.ATTN_OK
+    assert o[..., 3].isnan().all()
+    o[..., 3] = want[0][..., 3]
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
