@@ -20,15 +20,12 @@
 
 #include "attn.h"
 #include "host.h"
+#include "views.h"
 
 namespace attn {
 namespace rope {
 
 constexpr int NT = 256;
-
-struct View {   // element strides of batch, head, token
-  long long b, h, t;
-};
 
 struct Params {
   attn_rope_t plan;
@@ -160,46 +157,6 @@ __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ Params
   }
 }
 
-// Elements past a view's first one to its last one plus one.
-long long extent(const View& s, int B, int H, int T, int d) {
-  return (B - 1) * s.b + (H - 1) * s.h + (T - 1) * s.t + d;
-}
-
-// Whether no two elements of the view share an address: its dimensions, from
-// the smallest stride up, must each step over what lies below.
-bool distinct(const View& s, int B, int H, int T, int d) {
-  long long st[3] = {s.b, s.h, s.t};
-  long long n[3] = {B, H, T};
-  long long span = d;
-  for (int i = 0; i < 3; ++i) {
-    int m = i;
-    for (int j = i + 1; j < 3; ++j)
-      if (st[j] < st[m]) m = j;
-    const long long a = st[m], c = n[m];
-    st[m] = st[i], n[m] = n[i];
-    if (c <= 1) continue;
-    if (a < span) return false;
-    span += (c - 1) * a;
-  }
-  return true;
-}
-
-// Whether two views are known to share no address: their extents are apart,
-// or both step by the same batch and token strides and lie beside each other
-// within a token (the queries and keys of one projection's rows).
-bool apart(const void* pa, const View& a, int Ha, const void* pb, const View& b, int Hb, int B, int T, int d,
-           size_t es) {
-  if (!overlap(range(pa, extent(a, B, Ha, T, d) * es), range(pb, extent(b, B, Hb, T, d) * es))) return true;
-  if (a.t != b.t || a.t <= 0 || (B > 1 && (a.b != b.b || a.b % a.t))) return false;
-  const long long delta = static_cast<long long>(reinterpret_cast<uintptr_t>(pb)) -
-                          static_cast<long long>(reinterpret_cast<uintptr_t>(pa));
-  const long long step = a.t * static_cast<long long>(es);
-  const long long off = ((delta % step) + step) % step;
-  const long long la = ((Ha - 1) * a.h + d) * static_cast<long long>(es),
-                  lb = ((Hb - 1) * b.h + d) * static_cast<long long>(es);
-  return off >= la && off + lb <= step;
-}
-
 template <typename T, int V>
 cudaError_t launch(Params& P, cudaStream_t st, int num_sms) {
   const long long tokens = static_cast<long long>(P.B) * P.T;
@@ -276,10 +233,11 @@ attn_status_t attn_rope(const attn_rope_t* plan, const void* Q, void* Qout, cons
   rope::Params P{};
   bool wide = true;   // 16-byte accesses everywhere
   const int V = 16 / static_cast<int>(es);
+  Rows from[2], to[2];
   for (int k = 0; k < 2; ++k) {
     const long long* s = strides + 6 * k;
-    P.xs[k] = rope::View{s[0], s[1], s[2]};
-    P.ys[k] = rope::View{s[3], s[4], s[5]};
+    P.xs[k] = View{s[0], s[1], s[2]};
+    P.ys[k] = View{s[3], s[4], s[5]};
     P.heads[k] = some ? heads[k] : 0;
     if (P.heads[k] == 0) continue;
     for (int i = 0; i < 6; ++i) {
@@ -294,7 +252,9 @@ attn_status_t attn_rope(const attn_rope_t* plan, const void* Q, void* Qout, cons
     if (static_cast<double>(s[0]) * B + static_cast<double>(s[1]) * heads[k] + static_cast<double>(s[2]) * T > 9e15 ||
         static_cast<double>(s[3]) * B + static_cast<double>(s[4]) * heads[k] + static_cast<double>(s[5]) * T > 9e15)
       return ATTN_ERR_INVALID_ARG;
-    if (!rope::distinct(P.ys[k], B, heads[k], T, d)) return ATTN_ERR_INVALID_ARG;
+    from[k] = rows_of(in[k], P.xs[k], B, heads[k], T, d, es);
+    to[k] = rows_of(out[k], P.ys[k], B, heads[k], T, d, es);
+    if (!distinct(to[k])) return ATTN_ERR_INVALID_ARG;
     P.x[k] = in[k];
     P.y[k] = out[k];
   }
@@ -302,15 +262,13 @@ attn_status_t attn_rope(const attn_rope_t* plan, const void* Q, void* Qout, cons
     if (P.heads[k] == 0) continue;
     for (int j = 0; j < 2; ++j) {
       if (P.heads[j] == 0) continue;
-      const rope::View &y = P.ys[k], &x = P.xs[j];
-      const bool in_place = j == k && in[k] == out[k] && y.b == x.b && y.h == x.h && y.t == x.t;
-      if (!in_place && !rope::apart(out[k], y, heads[k], in[j], x, heads[j], B, T, d, es)) return ATTN_ERR_INVALID_ARG;
-      if (j > k && !rope::apart(out[k], y, heads[k], out[j], P.ys[j], heads[j], B, T, d, es))
-        return ATTN_ERR_INVALID_ARG;
+      // in place: the same rows (a stride of a single row does not count)
+      bool in_place = j == k && in[k] == out[k];
+      for (int i = 0; i < 3; ++i) in_place = in_place && (to[k].n[i] <= 1 || to[k].step[i] == from[k].step[i]);
+      if (!in_place && !apart(to[k], from[j])) return ATTN_ERR_INVALID_ARG;
+      if (j > k && !apart(to[k], to[j])) return ATTN_ERR_INVALID_ARG;
     }
-    if (pos && overlap(range(out[k], rope::extent(P.ys[k], B, heads[k], T, d) * es),
-                       range(pos, static_cast<size_t>(B) * T * 4)))
-      return ATTN_ERR_INVALID_ARG;
+    if (pos && !apart(to[k], Rows{reinterpret_cast<uintptr_t>(pos), 4LL * B * T, {}, {}})) return ATTN_ERR_INVALID_ARG;
   }
   if (!some || (H == 0 && Hkv == 0)) return ATTN_OK;
   DeviceInfo* di;

@@ -404,8 +404,10 @@ ATTN_API attn_status_t attn_rope_init(attn_rope_t* plan, int rot, int interleave
  * strides: 12 element strides, those of batch, head and token for Q, Qout, K
  * and Kout in this order; rows of d elements are contiguous. Strides are >=
  * 0; Qout and Kout must place no two elements at one address. In place (Qout
- * == Q with equal strides) is allowed; any other overlap between an output
- * and an input or the other output is refused. pos: int32 [B,T] device
+ * == Q with equal strides) is allowed; otherwise a call is refused where a row
+ * of an output shares a byte with a row of an input, of the other output or
+ * with pos. Slices and permutations of one tensor are told apart; views so
+ * tangled that 16384 steps do not decide are refused. pos: int32 [B,T] device
  * positions of any sign, or NULL: token t is at position t. rot <= d <= 256.
  * Pointers aligned to the element size. cos, sin and the products are fp32,
  * rounded once to the type. Errors: ATTN_ERR_INVALID_ARG,
