@@ -1,8 +1,9 @@
 // Rotary positions of queries and keys.
 //
 // Pair (u, v) of a token at position p is turned by p * f_i. The plan holds
-// f_i / (2 pi) as F_i * 2^-64, so that p * F_i modulo 2^64 is the angle as a
-// fraction of a turn, exact at any position: its upper 32 bits, as a signed
+// f_i / (2 pi), rounded to F_i * 2^-64, so that p * F_i modulo 2^64 is the
+// angle as a fraction of a turn, off by |p| * 2^-65 at most; an int32 position
+// leaves its upper 32 bits right, to one of them. They, as a signed
 // number, times 2^-31 is the angle in half turns within [-1, 1), which
 // sincospi takes. (An fp32 product p * f_i would be off by 0.03 radians at p
 // = 10^6.) One thread does one chunk of pairs of one token for several heads
@@ -157,6 +158,41 @@ __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ Params
   }
 }
 
+// Sums of two doubles, x + y with |y| at most half a step of x (Dekker;
+// Knuth): some 100 bits for the plan, whose entries have 64 behind the point.
+struct Two {
+  double x, y;
+};
+Two sum(double a, double b) {
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+Two operator+(Two a, Two b) {
+  const Two s = sum(a.x, b.x), t = sum(a.y, b.y);
+  const Two u = sum(s.x, s.y + t.x);
+  return sum(u.x, u.y + t.y);
+}
+Two operator*(Two a, Two b) {
+  const double p = a.x * b.x;
+  return sum(p, fma(a.x, b.x, -p) + (a.x * b.y + a.y * b.x));
+}
+Two operator-(Two a) { return {-a.x, -a.y}; }
+Two operator/(Two a, Two b) {
+  const double q = a.x / b.x;
+  const Two r = a + -(Two{q, 0.0} * b);
+  return sum(q, r.x / b.x);
+}
+
+// theta^(-1/n): the double nearest to it, or nearly, corrected by one step of
+// Newton's method on theta * f^n = 1.
+Two root(double theta, int n) {
+  const double f = pow(theta, -1.0 / n);
+  Two r{theta, 0.0};
+  for (int i = 0; i < n; ++i) r = r * Two{f, 0.0};
+  const Two off = r + Two{-1.0, 0.0};
+  return sum(f, -f * off.x / n);
+}
+
 template <typename T, int V>
 cudaError_t launch(Params& P, cudaStream_t st, int num_sms) {
   const long long tokens = static_cast<long long>(P.B) * P.T;
@@ -195,20 +231,26 @@ attn_status_t attn_rope_init(attn_rope_t* plan, int rot, int interleaved, double
     return ATTN_ERR_INVALID_ARG;
   if (!(mscale > 0.0) || !isfinite(static_cast<float>(mscale)) || !(static_cast<float>(mscale) > 0.f))
     return ATTN_ERR_INVALID_ARG;
-  const double two_pi = 6.283185307179586476925;
   *plan = attn_rope_t{};
   plan->rot = rot;
   plan->interleaved = interleaved;
   plan->mscale = static_cast<float>(mscale);
-  for (int i = 0; i < rot / 2; ++i) {
-    const double f = pow(theta, -2.0 * i / rot);
-    double keep = 0.0;   // the share of f that is not divided by the factor
+  // f_i = f_1^i, as turns: f_i / (2 pi)
+  using rope::Two;
+  const Two per_turn{0.15915494309189535, -9.839338337591243e-18};   // 1 / (2 pi)
+  const Two f1 = rope::root(theta, rot / 2), one{1.0, 0.0};
+  Two f = one;
+  for (int i = 0; i < rot / 2; ++i, f = f * f1) {
+    const Two t = f * per_turn;
+    Two keep{0.0, 0.0};   // the share of f_i that is not divided by the factor
     if (original_length > 0.0) {
-      keep = (original_length * f / two_pi - low_turns) / (high_turns - low_turns);
-      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+      keep = (Two{original_length, 0.0} * t + Two{-low_turns, 0.0}) / rope::sum(high_turns, -low_turns);
+      keep = keep.x < 0.0 ? Two{0.0, 0.0} : keep.x >= 1.0 ? one : keep;
     }
-    const double g = f * keep + f / factor * (1.0 - keep);
-    plan->turns[i] = static_cast<unsigned long long>(rint(ldexp(g / two_pi, 64)));   // g <= 1: below 2^62
+    const Two g = t * keep + t / Two{factor, 0.0} * (one + -keep);
+    const double units = ldexp(g.x, 64), whole = rint(units);   // below 2^62
+    plan->turns[i] = static_cast<unsigned long long>(static_cast<long long>(whole) +
+                                                     static_cast<long long>(rint(units - whole + ldexp(g.y, 64))));
   }
   return ATTN_OK;
 }
