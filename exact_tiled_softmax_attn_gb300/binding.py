@@ -409,6 +409,12 @@ def _scored_args(q, k, v, causal, scale, softcap, slopes, q_pos, key_begin, key_
     return shape, 1.0 / math.sqrt(d) if scale is None else scale, score, _dtype_code(q), dev
 
 
+def _check_workspace(given, dev):
+    # (its address and size go to the library as they are: a view that repeats memory, or host memory, would be written)
+    if given is not None and (given.dtype != torch.uint8 or not given.is_contiguous() or given.get_device() != dev):
+        raise ValueError("workspace must be a contiguous uint8 tensor on Q's device")
+
+
 def _workspace(given, nbytes, device):
     return torch.empty(nbytes or 1, dtype=torch.uint8, device=device) if given is None else given
 
@@ -422,6 +428,7 @@ def forward_scored(q, k, v, causal: bool = False, scale: Optional[float] = None,
     (int32 [B, Tq], shared by the heads) and, with causal, to keys at or before q_pos (default: the row index).
     Allocates O, LSE and, unless given, the workspace (uint8, attn_fwd_scored_workspace_size bytes)."""
     shape, scale, score, dt, dev = _scored_args(q, k, v, causal, scale, softcap, slopes, q_pos, key_begin, key_end)
+    _check_workspace(workspace, dev)
     B, H, _, Tq, _, _, dv = shape
 
     def call(handle):
@@ -440,6 +447,7 @@ def backward_scored(q, k, v, o, lse, do, causal: bool = False, scale: Optional[f
                     slopes=None, q_pos=None, key_begin=None, key_end=None, stream=None, workspace=None):
     """dQ, dK, dV of forward_scored's O (same arguments; dK and dV summed over the heads that share them)."""
     shape, scale, score, dt, dev = _scored_args(q, k, v, causal, scale, softcap, slopes, q_pos, key_begin, key_end)
+    _check_workspace(workspace, dev)
     B, H, _, Tq, _, _, dv = shape
     for name, t, want, dtype in (("O", o, (B, H, Tq, dv), q.dtype), ("dO", do, (B, H, Tq, dv), q.dtype),
                                  ("LSE", lse, (B, H, Tq), torch.float32)):

@@ -174,3 +174,32 @@ def test_a_nan_among_the_values_shows_whatever_its_weight(shape, dtype):
     assert o[..., 3].isnan().all()
     o[..., 3] = want[0][..., 3]
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+# ------------------------------------------------------------------ what is handed in beside the inputs
+
+@pytest.mark.parametrize("workspace", [torch.zeros(1 << 20), torch.zeros(1, dtype=torch.uint8).expand(1 << 20),
+                                       torch.zeros(1 << 21, dtype=torch.uint8)[::2]], ids=["f32", "repeated", "strided"])
+def test_a_workspace_of_another_kind_is_refused(workspace):
+    q, k = torch.zeros(1, 4, 8, 64), torch.zeros(1, 2, 8, 64)
+    with pytest.raises(ValueError, match="workspace"):
+        B.forward_scored(q, k, k, workspace=workspace)
+    with pytest.raises(ValueError, match="workspace"):
+        B.backward_scored(q, k, k, q, q[..., 0].contiguous(), q, workspace=workspace)
+
+
+@pytest.mark.gpu
+def test_a_workspace_of_the_host_is_refused_and_one_of_the_device_serves():
+    x = make(1, 4, 2, 300, 300, 64, 64, torch.bfloat16, 73)
+    n = [f(1, 4, 2, 300, 300, 64, 64, B.ATTN_BF16) for f in (B.attn_fwd_scored_workspace_size,
+                                                            B.attn_bwd_scored_workspace_size)]
+    with pytest.raises(ValueError, match="workspace"):
+        B.forward_scored(*x[:3], workspace=torch.zeros(n[0], dtype=torch.uint8))
+    o, lse = B.forward_scored(*x[:3], workspace=torch.empty(n[0], dtype=torch.uint8, device="cuda"))
+    ws = torch.empty(n[1], dtype=torch.uint8, device="cuda")
+    g = B.backward_scored(*x[:3], o, lse, x[3], workspace=ws)
+    want = B.forward_scored(*x[:3])
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert all(torch.equal(a, b) for a, b in zip(g, B.backward_scored(*x[:3], *want, x[3])))
+    with pytest.raises(B.AttnError):
+        B.backward_scored(*x[:3], o, lse, x[3], workspace=ws[:-1])
