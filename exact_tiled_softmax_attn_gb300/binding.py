@@ -364,6 +364,8 @@ def _call_on(index, stream, call, *args):
             return call(_raw_stream(index), *args)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=index)
+    elif stream.device.index != index:
+        raise ValueError("the stream must be one of the tensors' device")
     with torch.cuda.device(index), torch.cuda.stream(stream):
         return call(stream.cuda_stream, *args)
 

@@ -7,12 +7,14 @@ scores of these inputs (up to 50).
 import math
 import os
 import re
+import types
 
 import numpy as np
 import pytest
 import torch
 
 import exact_tiled_softmax_attn_gb300 as B
+from exact_tiled_softmax_attn_gb300 import binding
 from oracle import scored as ref
 
 from parity import check_o, np64
@@ -203,3 +205,23 @@ def test_a_workspace_of_the_host_is_refused_and_one_of_the_device_serves():
     assert all(torch.equal(a, b) for a, b in zip(g, B.backward_scored(*x[:3], *want, x[3])))
     with pytest.raises(B.AttnError):
         B.backward_scored(*x[:3], o, lse, x[3], workspace=ws[:-1])
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Before anything is made current or launched: the kernels would run on the stream's device."""
+    def call(*a):
+        raise AssertionError("called")
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    with pytest.raises(ValueError, match="stream"):
+        binding._call_on(0, other, call)
+
+
+@pytest.mark.gpu
+def test_streams_of_the_tensors_device_serve():
+    x = make(1, 4, 2, 70, 90, 64, 64, torch.bfloat16, 79, grad=False)
+    want = B.forward_scored(*x)
+    torch.cuda.synchronize()
+    for s in (torch.cuda.Stream(), torch.cuda.default_stream(), torch.cuda.current_stream()):
+        o, lse = B.forward_scored(*x, stream=s)
+        s.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
