@@ -18,6 +18,7 @@
 // bias are applied per row (dq) and per column (dkdv).
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <limits.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -45,6 +46,10 @@ using scored::f2;
 using scored::F2;
 using scored::fma2;
 using scored::mul2;
+
+// The dK/dV kernel works on 2^kLift P: what it keeps of P T between its passes
+// is fp16, and from 4e-9 on that holds P T in 11 bits.
+constexpr float kLift = 14.f, kLower = 0x1p-14f;
 
 struct Params {
   ScoredProblem p;
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       const F2 ndd = dup(-dd);
       if (g == 0) {   // for every row of the padded tile: the dK/dV kernel reads whole 128-row slices
         P.D[static_cast<long long>(u.bh) * rpad + row] = dd;
-        P.NL[static_cast<long long>(u.bh) * rpad + row] = nlse2;
+        P.NL[static_cast<long long>(u.bh) * rpad + row] = nlse2 + kLift;
       }
       for (int j = 0; j < u.n; ++j, ++sp) {
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full, sp & 1u, w)))) break;
@@ -1101,8 +1106,9 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         ptx::tc_fence_after();
         // pass 1: P^T, packed bf16 (the product's type) over the first half of
         // this group's S^T columns; P^T T stays in registers for pass 2, as
-        // bf16 too: as fp32 it would take 64 of 168 registers. With dS's and
-        // the result's rounding dK is off by 0.0030 of its norm, 0.0024 without.
+        // fp16: as fp32 it would take 64 of 168 registers. (As bf16 it would be
+        // a rounding as large as dS's: dK off by 0.0030 of its norm, 0.0025
+        // so.)
         uint32_t keep[2][16];
         {
           uint32_t rs[2][32];
@@ -1170,10 +1176,8 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
                   if constexpr (decltype(masked)::value)
                     p = f2(seen[c] & (1u << a) ? p.x : 0.f, seen[c] & (2u << a) ? p.y : 0.f);
                   pk[i + q] = scored::pack_bf16(p);
-                  if constexpr (kForm != 0)
-                    keep[c][i + q] = scored::pack_bf16(mul2(p, grad));
-                  else
-                    keep[c][i + q] = pk[i + q];
+                  if constexpr (kForm != 0) p = mul2(p, grad);
+                  keep[c][i + q] = ptx::pack_f16_sat(p.x, p.y);
                 }
               }
               ptx::tmem_st16(tST + c * 16, pk);
@@ -1229,8 +1233,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
               const float4 d4 = ptx::lds128(dd + c * 32 + 2 * i);
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                // P T as two floats: a bf16 is the upper half of a float
-                const F2 pt = f2(__uint_as_float(keep[c][i + q] << 16), __uint_as_float(keep[c][i + q] & 0xffff0000u));
+                const F2 pt = __half22float2(*reinterpret_cast<const __half2*>(&keep[c][i + q]));
                 const F2 e = fma2(q ? f2(d4.z, d4.w) : f2(d4.x, d4.y), neg1,
                                   f2(__uint_as_float(rd[c][2 * (i + q)]), __uint_as_float(rd[c][2 * (i + q) + 1])));
                 pk[i + q] = scored::pack_bf16(mul2(pt, e));
@@ -1283,7 +1286,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         const uint32_t tcol = tmem + lane_off + (acc ? T_DK : T_DV);
         const int width = acc ? P.p.d : P.p.dv;
         const int key4 = key & ~3;   // (see scored::quad_transpose)
-        const float mul = acc ? scale : 1.0f;
+        const float mul = acc ? scale * kLower : kLower;
 #pragma unroll 1
         for (int c = 0; c < HD / 32; ++c) {
           uint32_t v[32];

@@ -17,7 +17,7 @@ import exact_tiled_softmax_attn_gb300 as B
 from exact_tiled_softmax_attn_gb300 import binding
 from oracle import scored as ref
 
-from parity import check_o, np64
+from parity import check_o, frob_rel, np64
 from test_scored import check_grad, check_lse, how_of, magnitudes, make, run_case
 
 CSRC = os.path.join(os.path.dirname(os.path.abspath(B.__file__)), "csrc")
@@ -225,3 +225,44 @@ def test_streams_of_the_tensors_device_serve():
         o, lse = B.forward_scored(*x, stream=s)
         s.synchronize()
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+# ------------------------------------------------------------------ how often a gradient is rounded
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap", [0.0, 8.0])
+@pytest.mark.parametrize("H,Hkv,T", [(2, 2, 700), (8, 1, 400)])   # (the second in parts of row tiles)
+def test_roundings_of_the_gradients(H, Hkv, T, cap):
+    """dQ and dK: dS and the result are rounded to bf16, and the O in D is; dV: P and the result. Nothing else.
+
+    A rounding to bf16 moves a tensor of these gradients by r = 0.00166 of its norm (measured on the results, in
+    float64); roundings of independent terms of a sum of independent terms move the sum by as much; independent errors
+    add in squares. What the rounded O does to D is formed from the formula. One rounding more would be at least a
+    sixth more."""
+    d = 128
+    x = make(1, H, Hkv, T, T, d, d, torch.bfloat16, 83)
+    o, lse = B.forward_scored(*x[:3], causal=True, softcap=cap)
+    g = B.backward_scored(*x[:3], o, lse, x[3], causal=True, softcap=cap)
+    how = dict(scale=1.0 / math.sqrt(d), causal=True, softcap=cap)
+    r = ref.scored(*x, **how)
+    # the formula with the rounded O in D: D enters dS linearly, so its error's share is that of dO o (O - O')
+    q, k, _, do = (np64(t)[0] for t in x)
+    extra = (do * (np64(o)[0] - r["O"][0])).sum(-1)
+    dq, dk = np.zeros_like(q), np.zeros_like(k)
+    for h in range(H):
+        s = how["scale"] * q[h] @ k[h * Hkv // H].T
+        t = 1.0
+        if cap:
+            s = cap * np.tanh(s / cap)
+            t = 1.0 - (s / cap) ** 2
+        p = np.where(np.tri(T, dtype=bool), np.exp(s - r["LSE"][0, h][:, None]), 0.0)
+        ds = -p * extra[h][:, None] * t * how["scale"]
+        dq[h] = ds @ k[h * Hkv // H]
+        dk[h * Hkv // H] += ds.T @ q[h]
+    for t, name, off in zip(g, ("dQ", "dK", "dV"), (dq, dk, 0.0)):
+        want = r[name]
+        once = frob_rel(torch.from_numpy(want).to(torch.bfloat16), want)
+        assert 0.0015 < once < 0.0018
+        bound = math.sqrt(2 * once ** 2 + (np.linalg.norm(off) / np.linalg.norm(want)) ** 2)
+        err = frob_rel(t, want)
+        assert err <= 1.08 * bound, (name, err, bound)
