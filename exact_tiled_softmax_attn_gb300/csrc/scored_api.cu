@@ -34,7 +34,7 @@ attn_status_t check_scored(int B, int H, int Hkv, int Tq, int Tk, int d, int dv,
   return ATTN_OK;
 }
 
-attn_status_t check_score(const attn_score_t& sc, int B, int H, int Tq, float scale) {
+attn_status_t check_score(const attn_score_t& sc, float scale) {
   if (!(scale > 0.f) || !isfinite(scale)) return ATTN_ERR_INVALID_ARG;
   if (sc.softcap != 0.f && !(sc.softcap >= 1e-4f && sc.softcap <= 1e6f)) return ATTN_ERR_INVALID_ARG;
   if (sc.causal != 0 && sc.causal != 1) return ATTN_ERR_INVALID_ARG;
@@ -214,7 +214,7 @@ attn_status_t attn_fwd_scored(const void* Q, const void* K, const void* V, void*
                               attn_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
   attn_status_t s = check_scored(B, H, Hkv, Tq, Tk, d, dv, dtype);
   const attn_score_t sc = score ? *score : attn_score_t{};
-  if (s == ATTN_OK) s = check_score(sc, B, H, Tq, scale);
+  if (s == ATTN_OK) s = check_score(sc, scale);
   if (s != ATTN_OK) return s;
   const bool bf16 = dtype == ATTN_BF16;
   const size_t es = elem_size(dtype), align = bf16 ? 16 : 4;
@@ -295,7 +295,7 @@ attn_status_t attn_bwd_scored(const void* Q, const void* K, const void* V, const
                               void* workspace, size_t workspace_bytes, void* stream) {
   attn_status_t s = check_scored(B, H, Hkv, Tq, Tk, d, dv, dtype);
   const attn_score_t sc = score ? *score : attn_score_t{};
-  if (s == ATTN_OK) s = check_score(sc, B, H, Tq, scale);
+  if (s == ATTN_OK) s = check_score(sc, scale);
   if (s != ATTN_OK) return s;
   const bool bf16 = dtype == ATTN_BF16;
   const size_t es = elem_size(dtype), align = bf16 ? 16 : 4;

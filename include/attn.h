@@ -298,12 +298,12 @@ ATTN_API attn_status_t attn_bwd_noalloc(const void* Q, const void* K, const void
  *   S_ij = -inf unless key_begin[b,i] <= j < key_end[b,i], and, with
  *          causal = 1, j <= q_pos[b,i]
  * and O, LSE as above. Causal, document (rows see their own document's keys),
- * prefix (rows see a prefix and what precedes them), sliding-window and
- * padding masks are all of this form. A row whose range is empty gives O = 0,
- * LSE = -inf and zero gradients. The three arrays are shared by the heads of
- * a batch entry; ranges are clamped to [0, Tk] and positions to +-2^30 on the
- * device, so any values are safe. The struct is read during the call; the
- * arrays it points to are device memory read by the enqueued kernels.
+ * prefix (rows see a prefix and what precedes them), sliding-window and padding
+ * masks are all of this form. A row whose range is empty gives O = 0, LSE =
+ * -inf and zero gradients, whatever other rows see. The three arrays are shared
+ * by the heads of a batch entry; ranges are clamped to [0, Tk] and positions to
+ * +-2^30 on the device, so any values are safe. The struct is read during the
+ * call; the arrays it points to are device memory read by the enqueued kernels.
  */
 typedef struct {
   float softcap;        /* 0: none; otherwise from 1e-4 to 1e6 */
@@ -323,7 +323,10 @@ typedef struct {
  * else ATTN_ERR_UNSUPPORTED. Tq, Tk <= 2^30, and H / Hkv * Tq too.
  * What no query reads may hold anything, NaN included: K and V rows that lie
  * before every range or behind every range of their batch entry (unused
- * capacity of a cache), and Q rows whose range is empty (padding). A NaN among
+ * capacity of a cache), and Q rows whose range is empty (padding); K and V rows
+ * in gaps between ranges have to be finite. (ATTN_BF16 with a cap: scores near
+ * by, seen or not, decide which of several forms of tanh, equal to a few 2^-24
+ * of a score, a row's scores go through, and so may its last bits.) A NaN among
  * the scores that a row sees makes its O and LSE NaN; one in a value that it
  * sees makes that element of its O NaN, whatever the weight.
  * `workspace`: as in attn_fwd_splitkv (256-byte aligned, at least
@@ -349,13 +352,13 @@ ATTN_API size_t attn_fwd_scored_workspace_size(int B, int H, int Hkv, int Tq, in
  * key head. With T_ij = 1 - (t_ij / softcap)^2 (1 without a cap):
  *   P = exp(S - LSE),  D = rowsum(dO o O),  dV = P^T dO,
  *   dS = P o (dO V^T - D) o T,  dQ = scale * dS K,  dK = scale * dS^T Q
- * (the bias and the ranges have no gradient). `O` and `LSE` must be the
- * outputs of attn_fwd_scored on the same inputs, scale and score. Shapes as
- * attn_fwd_scored. What no query reads may hold anything here too: K and V
- * rows outside every range of their batch entry, and Q, O and dO rows whose
- * range is empty; their gradients are 0. Sums run in a fixed order: equal
- * calls give bitwise equal results. Workspace and errors as attn_fwd_scored,
- * with attn_bwd_scored_workspace_size.
+ * (the bias and the ranges have no gradient). `O` and `LSE` must be the outputs
+ * of attn_fwd_scored on the same inputs, scale and score. Shapes as
+ * attn_fwd_scored. What no query reads may hold anything here too: K and V rows
+ * before every range or behind every range of their batch entry, and Q, O and
+ * dO rows whose range is empty; their gradients are 0. Sums run in a fixed
+ * order: equal calls give bitwise equal results. Workspace and errors as
+ * attn_fwd_scored, with attn_bwd_scored_workspace_size.
  */
 ATTN_API attn_status_t attn_bwd_scored(const void* Q, const void* K, const void* V, const void* O, const float* LSE,
                                        const void* dO, void* dQ, void* dK, void* dV, int B, int H, int Hkv, int Tq,
