@@ -5,8 +5,8 @@
 // with T = 1 - (capped score / cap)^2, or 1 without a cap. Two kernels, with
 // the pipelines of the plain backward (bwd_bf16.cu):
 //   - dq_kernel: a unit is one 128-row tile of packed rows; Q and dO stay in
-//     tensor memory as A operands, dQ accumulates there over the key tiles
-//     the rows see, and D and -LSE log2(e) go to the workspace;
+//     shared memory, dQ accumulates in tensor memory over the key tiles the
+//     rows see, and D and -LSE log2(e) go to the workspace;
 //   - dkdv_kernel: a unit is one 128-key tile; K and V stay in shared memory,
 //     and dK and dV accumulate in tensor memory over the row tiles that see
 //     a key of it (a bit list from the plan), which with packed rows sums
@@ -14,8 +14,8 @@
 // Both sum in a fixed order. Differences from the plain kernels: the units'
 // tile lists come from the plan and are claimed at run time; the factor P T,
 // which dS needs, takes the place of P in the registers between the two
-// passes over a tile, so the cap costs arithmetic but no storage; ranges and
-// bias are applied per row (dq) and per column (dkdv).
+// passes over a tile (the dQ kernel keeps P too, in 11 bits, where there is a
+// cap); ranges and bias are applied per row (dq) and per column (dkdv).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -90,23 +90,29 @@ template <int HD>
 struct CfgQ {
   static constexpr int KB = HD / 64;
   static constexpr int TILE = BT * HD * 2;
-  static constexpr int DPART_BYTES = 2 * 2 * BT * 4;   // [unit parity][row group][128] fp32 partial D
-  static constexpr int NSLOT_FIT = (227 * 1024 - DPART_BYTES - 256) / TILE;
-  static constexpr int NSLOT = NSLOT_FIT < 16 ? NSLOT_FIT : 16;
-  static constexpr int OFF_RING = 0;
-  static constexpr int OFF_DPART = OFF_RING + NSLOT * TILE;
-  static constexpr int OFF_BAR = OFF_DPART + DPART_BYTES;
-  // full[NSLOT], empty[NSLOT], qd_ready, s_full, s_free, dp_full, ds_full, dq_full, drain, dpart_full, unit queue
-  static constexpr int NBAR = 2 * NSLOT + 8 + 2 * RingQ::N;
+  static constexpr int SUMS_BYTES = 2 * BT * 8;   // [row group][128]: sums of P (dP - D) and of P
+  static constexpr int NSLOT_FIT = (227 * 1024 - 2 * TILE - SUMS_BYTES - 512) / TILE;
+  static constexpr int NSLOT = NSLOT_FIT < 12 ? NSLOT_FIT : 12;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_DO = OFF_Q + TILE;
+  static constexpr int OFF_RING = OFF_DO + TILE;
+  static constexpr int OFF_SUMS = OFF_RING + NSLOT * TILE;
+  static constexpr int OFF_BAR = OFF_SUMS + SUMS_BYTES;
+  // full[NSLOT], empty[NSLOT], q_full, q_empty, o_read, s_full, s_free, dp_full, ds_full, dq_full, sums_full, drain,
+  // unit queue
+  static constexpr int NBAR = 2 * NSLOT + 10 + 2 * RingQ::N;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16 + RingQ::BYTES;
   static constexpr int READERS = 1 + 256;
   static constexpr uint32_t IDESC_S = ptx::idesc_bf16(BT, BT, false, false);
   static constexpr uint32_t IDESC_DQ = ptx::idesc_bf16(BT, HD, false, true);
-  // Q and dO as packed bf16, the S and dP tiles, the dQ accumulator
-  static constexpr uint32_t T_Q = 0, T_DO = 64, T_S = 128, T_DP = 256, T_DQ = 384;
+  // two tiles, of alternate key tiles: S, then dP, then dS and P T; the
+  // accumulators of dS K and of P T K
+  static constexpr uint32_t T_X = 0, T_DQ = 256, T_PK = 384;
 };
-constexpr int DQ_THREADS = 320;
+constexpr int DQ_THREADS = 384;
+constexpr int DQ_REG_CTRL = 96, DQ_REG_ROWS = 200;
+constexpr float kWhole = 0x1p-10f;   // how near 1 a row's sum of P is where the call holds all its keys
 
 __device__ __forceinline__ UnitQ load_unit_q(const Params& P, int x) {
   UnitQ u;
@@ -120,8 +126,30 @@ __device__ __forceinline__ UnitQ load_unit_q(const Params& P, int x) {
   return u;
 }
 
-// Warps: 0 producer, 1 MMA, 2-5 and 6-9 two row groups of a thread per query
+// Warps: 0 producer, 1 MMA, 4-7 and 8-11 two row groups of a thread per query
 // row; group g works on key columns [64 g, 64 g + 64) of every row.
+//
+// D enters dS linearly, and rowsum(dO o O) with the rounded O is off by enough
+// to show: where a row's weight lies on few keys, dP - D is small beside D, and
+// dQ and dK were off by 0.0026 of their norm over long rows, 0.0035 over
+// documents of 16 tokens and up to 0.02 where rows see two to four keys. So that
+// D is only a first estimate; the difference to the exact one,
+//   rowsum P o (dP - D) = rowsum(P o dP) - D   (the rows of P sum to 1),
+// is summed in fp32 along the way, a fourth product accumulates P T K, and at
+// the end dQ = dS K - difference * P T K. The dK/dV kernel reads the exact D.
+// dQ and dK are now off by 0.0024, what the roundings of dS and of the result
+// make. Where a row's P does not sum to 1 (a call on a part of its keys, with O
+// and LSE of them all) the difference is something else, and the estimate stays.
+// It costs this kernel 176 -> 221 us at B=2 H=16 T=4096 d=128 causal with a cap,
+// 83 -> 95 at B=4 H=16 T=2048 d=64 with a bias: a product more, at d = 128 Q and
+// dO in shared memory for its accumulator's sake, and a quarter more arithmetic.
+//
+// dP_j goes where S_j was, dS_j and P_j T_j where dP_j was, and the next tile's
+// S into the other place, so that the products run in the order dQ_j-1, dP_j,
+// (P T K)_j-1, S_j+1 and both products of K fall behind what the threads wait
+// for. (dP first: 617 in place of 611 us for a step over documents, H=32 Hkv=8
+// T=8192 d=128; P T over S and the products of K together before the next S:
+// 604 there, 622 in place of 610 with the cap.)
 template <int HD, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(DQ_THREADS, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -135,36 +163,42 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     if (threadIdx.x == 0) atomicOr(P.status, ATTN_DEV_BAD_SMEM);
     return;
   }
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sdO = smem + C::OFF_DO;
   uint8_t* ring = smem + C::OFF_RING;
+  float2* sums = reinterpret_cast<float2*>(smem + C::OFF_SUMS);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* full = bars;
   uint64_t* empty = full + C::NSLOT;
-  uint64_t* qd_ready = empty + C::NSLOT;   // the row threads staged a unit's Q and dO (and read its O)
-  uint64_t* s_full = qd_ready + 1;
-  uint64_t* s_free = qd_ready + 2;
-  uint64_t* dp_full = qd_ready + 3;
-  uint64_t* ds_full = qd_ready + 4;
-  uint64_t* dq_full = qd_ready + 5;
-  uint64_t* drain = qd_ready + 6;
-  uint64_t* dpart_full = qd_ready + 7;
-  float* dpart = reinterpret_cast<float*>(smem + C::OFF_DPART);
+  uint64_t* q_full = empty + C::NSLOT;   // Q and dO
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* o_read = q_full + 2;         // the row threads have read a unit's dO and O
+  uint64_t* s_full = q_full + 3;
+  uint64_t* s_free = q_full + 4;
+  uint64_t* dp_full = q_full + 5;
+  uint64_t* ds_full = q_full + 6;
+  uint64_t* dq_full = q_full + 7;
+  uint64_t* sums_full = q_full + 8;
+  uint64_t* drain = q_full + 9;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 4);
-  const RingQ units{reinterpret_cast<UnitQ*>(smem + C::OFF_MISC + 16), qd_ready + 8, qd_ready + 8 + RingQ::N};
+  const RingQ units{reinterpret_cast<UnitQ*>(smem + C::OFF_MISC + 16), q_full + 10, q_full + 10 + RingQ::N};
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NSLOT; ++s) {
       ptx::mbar_init(full + s, 1);
       ptx::mbar_init(empty + s, 1);
     }
     units.init(C::READERS);
-    ptx::mbar_init(qd_ready, 256);
+    ptx::mbar_init(q_full, 1);
+    ptx::mbar_init(q_empty, 1);
+    ptx::mbar_init(o_read, 256);
     ptx::mbar_init(s_full, 1);
     ptx::mbar_init(s_free, 256);
     ptx::mbar_init(dp_full, 1);
     ptx::mbar_init(ds_full, 256);
     ptx::mbar_init(dq_full, 1);
+    ptx::mbar_init(sums_full, 256);
     ptx::mbar_init(drain, 1);
-    ptx::mbar_init(dpart_full, 256);
     *abort_flag = 0u;
     ptx::fence_mbar_init();
   }
@@ -176,222 +210,216 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // Ring item i sits in slot i % NSLOT. A unit whose first item is i0 has Q,
-  // dO, O at i0 .. i0 + 2 and K_j, V_j at i0 + 3 + 2 j and i0 + 4 + 2 j.
+  // Ring item i sits in slot i % NSLOT. A unit whose first item is i0 has O at
+  // i0 and K_j, V_j at i0 + 1 + 2 j and i0 + 2 + 2 j; its Q and dO have tiles
+  // of their own.
   auto slot = [](uint32_t i) { return static_cast<int>(i % C::NSLOT); };
   auto par = [](uint32_t i) { return (i / C::NSLOT) & 1u; };
 
-  if (warp == 0 && lane == 0) {
-    // ------------------------------------------------------------ producer
-    ptx::WaitCtx w{abort_flag, P.status, 5u};
-    ptx::tma_prefetch_desc(&tmQ);
-    ptx::tma_prefetch_desc(&tmK);
-    ptx::tma_prefetch_desc(&tmV);
-    ptx::tma_prefetch_desc(&tmdO);
-    ptx::tma_prefetch_desc(&tmO);
-    uint32_t item = 0, pu = 0;
-    auto load = [&](const CUtensorMap* map, int row, int bh) {
-      const int s = slot(item);
-      if (!ptx::mbar_wait(empty + s, par(item) ^ 1u, w)) return false;
-      ptx::mbar_arrive_expect_tx(full + s, C::TILE);
-      for (int c = 0; c < C::KB; ++c)
-        ptx::tma_load_3d(ring + s * C::TILE + c * BOX_BYTES, map, full + s, c * 64, row, bh);
-      ++item;
-      return true;
-    };
-    auto look = [&](int x) { return load_unit_q(P, x); };
-    auto work = [](const UnitQ& u) { return u.n > 0; };
-    scored::NextUnit<UnitQ> cur{}, next{};
-    bool ok = cur.first(P.counter, P.total, look, work, units, &pu, w);
-    for (; ok && cur.u.bh >= 0; cur = next) {
-      const UnitQ& u = cur.u;
-      ok = load(&tmQ, u.rt * BT, u.bh) && load(&tmdO, u.rt * BT, u.bh) && load(&tmO, u.rt * BT, u.bh);
-      for (int j = 0; ok && j < u.n; ++j) {
-        if (!(ok = next.step(j, u.n, P.counter, P.total, look, work, units, &pu, w))) break;
-        ok = load(&tmK, (u.j0 + j) * BT, u.bh) && load(&tmV, (u.j0 + j) * BT, u.bh);
-      }
-    }
-    if (!ok) {
-      for (uint32_t n = (item > static_cast<uint32_t>(C::NSLOT) ? item - C::NSLOT : 0u); n < item; ++n)
-        ptx::mbar_wait_drain(full + slot(n), par(n));
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    ptx::WaitCtx w{abort_flag, P.status, 6u};
-    const uint32_t aR = ptx::smem_u32(ring);
-    auto kmaj = [](uint64_t base, int kk) { return ptx::sdesc_advance(base, (kk >> 2) * BOX_BYTES + (kk & 3) * 32); };
-    auto mnmaj = [](uint64_t base, int kk) { return ptx::sdesc_advance(base, kk * 2048); };
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, w));
-    };
-    // K-major and M/N-major descriptors of the tile of ring item i
-    auto kdesc = [&](uint32_t i) { return scored::formed(ptx::sdesc_sw128(aR + slot(i) * C::TILE, 16, 1024)); };
-    auto mdesc = [&](uint32_t i) { return scored::formed(ptx::sdesc_sw128(aR + slot(i) * C::TILE, BOX_BYTES, 1024)); };
-    auto mma_s = [&](uint64_t k) {
-#pragma unroll
-      for (int kk = 0; kk < HD / 16; ++kk)
-        ptx::mma_ts(tmem + C::T_S, tmem + C::T_Q + 8 * kk, kmaj(k, kk), C::IDESC_S, kk > 0);
-      ptx::mma_commit(s_full);
-    };
-    auto mma_dp = [&](uint64_t v, uint32_t iv) {
-#pragma unroll
-      for (int kk = 0; kk < HD / 16; ++kk)
-        ptx::mma_ts(tmem + C::T_DP, tmem + C::T_DO + 8 * kk, kmaj(v, kk), C::IDESC_S, kk > 0);
-      ptx::mma_commit(dp_full);
-      ptx::mma_commit(empty + slot(iv));
-    };
-    uint32_t item = 0, u_it = 0, sp = 0, ru = 0;
-    bool moved = false;
-    // key tiles of the next unit, 0 at the end, -1 on a timeout
-    auto next_unit = [&]() {
-      UnitQ u;
-      if (!units.read(ru, &u, w)) return -1;
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(units.empty + ru % RingQ::N);
-      ++ru;
-      return u.bh < 0 ? 0 : u.n;
-    };
-    int nk = next_unit(), nk_next = 0;
-    bool ok = nk >= 0;
-    while (ok && nk > 0) {
-      const uint32_t i0 = item;
-      const uint64_t k0 = kdesc(i0 + 3), v0 = kdesc(i0 + 4);
-      // Q and dO are in TMEM: the three staging slots go back to the ring
-      if (!(ok = wait(qd_ready, u_it & 1u))) break;
-      if (lane == 0)
-        for (int k = 0; k < 3; ++k) ptx::mbar_arrive(empty + slot(i0 + k));
-      __syncwarp();
-      if (!(ok = wait(full + slot(i0 + 3), par(i0 + 3)))) break;
-      ptx::tc_fence_after();
-      if (ptx::elect_one()) {
-        moved |= lane != 0;
-        mma_s(k0);
-      }
-      __syncwarp();
-      if (!(ok = wait(full + slot(i0 + 4), par(i0 + 4)))) break;
-      ptx::tc_fence_after();
-      if (ptx::elect_one()) {
-        moved |= lane != 0;
-        mma_dp(v0, i0 + 4);
-      }
-      __syncwarp();
-      if (nk > 1 && !(ok = wait(full + slot(i0 + 5), par(i0 + 5)))) break;
-      for (int j = 0; j < nk; ++j, ++sp) {
-        if (j + 1 == nk) {
-          nk_next = next_unit();
-          ok = nk_next >= 0;
-          if (!ok) break;
+  const int wg = warp >> 2;
+  if (wg == 0) {
+    ptx::reg_release<DQ_REG_CTRL>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer
+      ptx::WaitCtx w{abort_flag, P.status, 5u};
+      ptx::tma_prefetch_desc(&tmQ);
+      ptx::tma_prefetch_desc(&tmK);
+      ptx::tma_prefetch_desc(&tmV);
+      ptx::tma_prefetch_desc(&tmdO);
+      ptx::tma_prefetch_desc(&tmO);
+      uint32_t item = 0, u_it = 0, pu = 0;
+      auto load = [&](const CUtensorMap* map, int row, int bh) {
+        const int s = slot(item);
+        if (!ptx::mbar_wait(empty + s, par(item) ^ 1u, w)) return false;
+        ptx::mbar_arrive_expect_tx(full + s, C::TILE);
+        for (int c = 0; c < C::KB; ++c)
+          ptx::tma_load_3d(ring + s * C::TILE + c * BOX_BYTES, map, full + s, c * 64, row, bh);
+        ++item;
+        return true;
+      };
+      // Q and dO, when the unit before needs its own no more
+      auto load_rows = [&](int row, int bh) {
+        if (!ptx::mbar_wait(q_empty, (u_it & 1u) ^ 1u, w)) return false;
+        ptx::mbar_arrive_expect_tx(q_full, 2 * C::TILE);
+        for (int c = 0; c < C::KB; ++c) {
+          ptx::tma_load_3d(sQ + c * BOX_BYTES, &tmQ, q_full, c * 64, row, bh);
+          ptx::tma_load_3d(sdO + c * BOX_BYTES, &tmdO, q_full, c * 64, row, bh);
         }
-        const uint32_t ik = i0 + 3 + 2 * j;   // K_j; V_{j+1} = ik + 3, K_{j+1} = ik + 2, K_{j+2} = ik + 4
-        const uint64_t k = mdesc(ik), kn = kdesc(ik + 2), vn = kdesc(ik + 3);
-        if (j + 1 < nk) {
-          if (!(ok = wait(s_free, sp & 1u))) break;
-          ptx::tc_fence_after();
-          if (ptx::elect_one()) {
-            moved |= lane != 0;
-            mma_s(kn);
-          }
-          __syncwarp();
+        ++u_it;
+        return true;
+      };
+      auto look = [&](int x) { return load_unit_q(P, x); };
+      auto work = [](const UnitQ& u) { return u.n > 0; };
+      scored::NextUnit<UnitQ> cur{}, next{};
+      bool ok = cur.first(P.counter, P.total, look, work, units, &pu, w);
+      for (; ok && cur.u.bh >= 0; cur = next) {
+        const UnitQ& u = cur.u;
+        ok = load(&tmO, u.rt * BT, u.bh);
+        for (int j = 0; ok && j < u.n; ++j) {
+          if (!(ok = next.step(j, u.n, P.counter, P.total, look, work, units, &pu, w))) break;
+          ok = load(&tmK, (u.j0 + j) * BT, u.bh) && load(&tmV, (u.j0 + j) * BT, u.bh) &&
+               (j > 0 || load_rows(u.rt * BT, u.bh));
         }
-        if (!(ok = wait(ds_full, sp & 1u))) break;
+      }
+      if (!ok) {
+        // let the copies in flight land before the CTA exits
+        for (uint32_t n = (item > static_cast<uint32_t>(C::NSLOT) ? item - C::NSLOT : 0u); n < item; ++n)
+          ptx::mbar_wait_drain(full + slot(n), par(n));
+        if (u_it > 0) ptx::mbar_wait_drain(q_full, (u_it - 1) & 1u);
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      ptx::WaitCtx w{abort_flag, P.status, 6u};
+      const uint32_t aR = ptx::smem_u32(ring);
+      auto kmaj = [](uint64_t base, int kk) { return ptx::sdesc_advance(base, (kk >> 2) * BOX_BYTES + (kk & 3) * 32); };
+      auto mnmaj = [](uint64_t base, int kk) { return ptx::sdesc_advance(base, kk * 2048); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, w));
+      };
+      const uint64_t q_desc = scored::formed(ptx::sdesc_sw128(ptx::smem_u32(sQ), 16, 1024));
+      const uint64_t do_desc = scored::formed(ptx::sdesc_sw128(ptx::smem_u32(sdO), 16, 1024));
+      // K-major and M/N-major descriptors of the tile of ring item i
+      auto kdesc = [&](uint32_t i) { return scored::formed(ptx::sdesc_sw128(aR + slot(i) * C::TILE, 16, 1024)); };
+      auto mdesc = [&](uint32_t i) { return scored::formed(ptx::sdesc_sw128(aR + slot(i) * C::TILE, BOX_BYTES, 1024)); };
+      // (unrolled whole: the issue is on the way of every product)
+      auto mma_s = [&](uint32_t x, uint64_t k) {
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          ptx::mma_ss(x, kmaj(q_desc, kk), kmaj(k, kk), C::IDESC_S, kk > 0);
+        ptx::mma_commit(s_full);
+      };
+      auto mma_dp = [&](uint32_t x, uint64_t v, uint32_t iv) {
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          ptx::mma_ss(x, kmaj(do_desc, kk), kmaj(v, kk), C::IDESC_S, kk > 0);
+        ptx::mma_commit(dp_full);
+        ptx::mma_commit(empty + slot(iv));
+      };
+      // dS (at 0) or P T (at 16) times K: the row threads put 16 columns of
+      // each, packed, in the place of 32 keys of dP
+      auto mma_k = [&](uint32_t acc, uint32_t x, uint64_t k, bool add) {
+#pragma unroll
+        for (int kk = 0; kk < BT / 16; ++kk)
+          ptx::mma_ts(tmem + acc, x + (kk >> 1) * 32 + (kk & 1) * 8, mnmaj(k, kk), C::IDESC_DQ,
+                      (add || kk > 0) ? 1u : 0u);
+      };
+      auto place = [&](uint32_t t) { return tmem + C::T_X + 128 * (t & 1u); };
+      uint32_t item = 0, u_it = 0, sp = 0, ru = 0;
+      bool moved = false;
+      // key tiles of the next unit, 0 at the end, -1 on a timeout
+      auto next_unit = [&]() {
+        UnitQ u;
+        if (!units.read(ru, &u, w)) return -1;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(units.empty + ru % RingQ::N);
+        ++ru;
+        return u.bh < 0 ? 0 : u.n;
+      };
+      int nk = next_unit(), nk_next = 0;
+      bool ok = nk >= 0;
+      while (ok && nk > 0) {
+        const uint32_t i0 = item;
+        const uint64_t k0 = kdesc(i0 + 1);
+        // (the products that read what this one overwrites have been issued: they run in order)
+        if (!(ok = wait(q_full, u_it & 1u))) break;
+        if (!(ok = wait(full + slot(i0 + 1), par(i0 + 1)))) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           moved |= lane != 0;
-#pragma unroll
-          for (int kk = 0; kk < BT / 16; ++kk)
-            ptx::mma_ts(tmem + C::T_DQ, tmem + C::T_DP + packed_col(kk), mnmaj(k, kk),
-                        C::IDESC_DQ, (j > 0 || kk > 0) ? 1u : 0u);
-          ptx::mma_commit(empty + slot(ik));
+          mma_s(place(sp), k0);
         }
         __syncwarp();
-        if (j + 1 < nk) {
-          if (!(ok = wait(full + slot(ik + 3), par(ik + 3)))) break;
+        for (int j = 0; j < nk; ++j, ++sp) {
+          if (j + 1 == nk) {
+            nk_next = next_unit();
+            ok = nk_next >= 0;
+            if (!ok) break;
+          }
+          const uint32_t ik = i0 + 1 + 2 * j, x = place(sp), y = place(sp + 1);   // K_j; V_j = ik + 1, K_{j+1} = ik + 2
+          const uint64_t v = kdesc(ik + 1), kn = kdesc(ik + 2), kl = mdesc(ik - 2), k = mdesc(ik);
+          if (!(ok = wait(full + slot(ik + 1), par(ik + 1)))) break;
+          if (!(ok = wait(s_free, sp & 1u))) break;
+          if (j == 0) {   // O goes back to the ring
+            if (!(ok = wait(o_read, u_it & 1u))) break;
+            if (lane == 0) ptx::mbar_arrive(empty + slot(i0));
+            __syncwarp();
+          }
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
             moved |= lane != 0;
-            mma_dp(vn, ik + 3);
+            mma_dp(x, v, ik + 1);
+            if (j + 1 == nk) ptx::mma_commit(q_empty);   // the last product of Q and dO
+            if (j > 0) {
+              mma_k(C::T_PK, y + 16, kl, j > 1);
+              ptx::mma_commit(empty + slot(ik - 2));
+            }
+          }
+          __syncwarp();
+          if (j + 1 < nk) {
+            if (!(ok = wait(full + slot(ik + 2), par(ik + 2)))) break;
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+              moved |= lane != 0;
+              mma_s(y, kn);
+            }
+            __syncwarp();
+          }
+          if (!(ok = wait(ds_full, sp & 1u))) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            moved |= lane != 0;
+            mma_k(C::T_DQ, x, k, j > 0);
+            if (j + 1 == nk) {
+              mma_k(C::T_PK, x + 16, k, j > 0);
+              ptx::mma_commit(empty + slot(ik));
+              ptx::mma_commit(dq_full);
+            }
           }
           __syncwarp();
         }
-        if (j + 2 < nk && !(ok = wait(full + slot(ik + 4), par(ik + 4)))) break;
+        if (!ok) break;
+        item = i0 + 1 + 2 * nk;
+        ++u_it;
+        nk = nk_next;
       }
-      if (!ok) break;
-      if (ptx::elect_one()) {
-        moved |= lane != 0;
-        ptx::mma_commit(dq_full);
+      if (!ok) {
+        if (ptx::elect_one()) ptx::mma_commit(drain);
+        __syncwarp();
+        ptx::mbar_wait_drain(drain, 0u);
       }
-      __syncwarp();
-      item = i0 + 3 + 2 * nk;
-      ++u_it;
-      nk = nk_next;
+      if (__any_sync(0xffffffffu, moved) && lane == 0) atomicOr(P.status, ATTN_DEV_ISSUER);
     }
-    if (!ok) {
-      if (ptx::elect_one()) ptx::mma_commit(drain);
-      __syncwarp();
-      ptx::mbar_wait_drain(drain, 0u);
-    }
-    if (__any_sync(0xffffffffu, moved) && lane == 0) atomicOr(P.status, ATTN_DEV_ISSUER);
-  } else if (warp >= 2) {
+  } else {
+    ptx::reg_acquire<DQ_REG_ROWS>();
     // ------------------------------------------------------------ row groups
-    const int g = (warp - 2) >> 2;
+    const int g = wg - 1;
     const int quad = warp & 3;
     const int r = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t tS = tmem + lane_off + C::T_S + 64 * g, tDP = tmem + lane_off + C::T_DP + 64 * g;
-    const uint32_t tDQ = tmem + lane_off + C::T_DQ + (HD / 2) * g;
-    const uint32_t tQ = tmem + lane_off + C::T_Q + (HD / 4) * g, tDO = tmem + lane_off + C::T_DO + (HD / 4) * g;
+    const uint32_t tX = tmem + lane_off + C::T_X + 64 * g;
+    const uint32_t tDQ = tmem + lane_off + C::T_DQ + (HD / 2) * g, tPK = tmem + lane_off + C::T_PK + (HD / 2) * g;
     ptx::WaitCtx w{abort_flag, P.status, 7u + g};
     const float sc2 = P.sc2, scale = P.p.scale;
     const F2 sc2v = dup(sc2), ninv2 = dup(P.cap.ninv2), one = dup(1.f);
     const int R = P.p.R, d = P.p.d, rpad = P.p.rpad();
-    // Stage a unit: this group's half of row r of Q and dO into TMEM, its
-    // half of D_r into dpart. Rows past R load as zeros.
-    auto stage = [&](uint32_t i0, uint32_t u) {
-      for (int k = 0; k < 3; ++k)
-        if (!__all_sync(0xffffffffu, ptx::mbar_wait(full + slot(i0 + k), par(i0 + k), w))) return false;
-      const uint8_t* sq = ring + slot(i0) * C::TILE;
-      const uint8_t* sdo = ring + slot(i0 + 1) * C::TILE;
-      const uint8_t* so = ring + slot(i0 + 2) * C::TILE;
-      {
-        uint32_t v[HD / 4];
+    // rowsum(dO o O) of this thread's row. Rows past R load as zeros.
+    auto estimate = [&](uint32_t i0, uint32_t u, float* sum) {
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait(q_full, u & 1u, w))) return false;
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait(full + slot(i0), par(i0), w))) return false;
+      const uint8_t* so = ring + slot(i0) * C::TILE;
+      F2 part = dup(0.f);
+#pragma unroll 4
+      for (int k = 0; k < HD / 8; ++k) {
+        const uint32_t off = sw128_offset(r, 8 * k);
+        const uint4 x = *reinterpret_cast<const uint4*>(sdO + off);
+        const uint4 o = *reinterpret_cast<const uint4*>(so + off);
+        const __nv_bfloat162* dov = reinterpret_cast<const __nv_bfloat162*>(&x);
+        const __nv_bfloat162* ov = reinterpret_cast<const __nv_bfloat162*>(&o);
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const uint4 x = *reinterpret_cast<const uint4*>(sq + sw128_offset(r, (HD / 2) * g + 8 * k));
-          v[4 * k] = x.x;
-          v[4 * k + 1] = x.y;
-          v[4 * k + 2] = x.z;
-          v[4 * k + 3] = x.w;
-        }
-        if constexpr (HD == 128) ptx::tmem_st32(tQ, v); else ptx::tmem_st16(tQ, v);
+        for (int e = 0; e < 4; ++e) part = fma2(__bfloat1622float2(ov[e]), __bfloat1622float2(dov[e]), part);
       }
-      float part = 0.f;
-      {
-        uint32_t v[HD / 4];
-#pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const uint32_t off = sw128_offset(r, (HD / 2) * g + 8 * k);
-          const uint4 x = *reinterpret_cast<const uint4*>(sdo + off);
-          const uint4 o = *reinterpret_cast<const uint4*>(so + off);
-          v[4 * k] = x.x;
-          v[4 * k + 1] = x.y;
-          v[4 * k + 2] = x.z;
-          v[4 * k + 3] = x.w;
-          const __nv_bfloat162* dov = reinterpret_cast<const __nv_bfloat162*>(&x);
-          const __nv_bfloat162* ov = reinterpret_cast<const __nv_bfloat162*>(&o);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = __bfloat1622float2(ov[e]), b = __bfloat1622float2(dov[e]);
-            part = fmaf(a.x, b.x, part);
-            part = fmaf(a.y, b.y, part);
-          }
-        }
-        if constexpr (HD == 128) ptx::tmem_st32(tDO, v); else ptx::tmem_st16(tDO, v);
-      }
-      dpart[((u & 1u) * 2 + g) * BT + r] = part;
-      ptx::mbar_arrive(dpart_full);
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(qd_ready);
+      *sum = part.x + part.y;
+      ptx::mbar_arrive(o_read);
       return true;
     };
     // the next unit: 1, 0 at the end, -1 on a timeout (with what this
@@ -419,35 +447,36 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     Mine me{}, nx{};
     const int first = next_unit(&me);
     bool have = first == 1;
-    bool ok = first >= 0 && (!have || stage(0u, 0u));
+    bool ok = first >= 0;
     while (ok && have) {
       const UnitQ& u = me.u;
       const int row = u.rt * BT + r;
       const int4 ri = me.row;
       const float lse = me.lse, slope2 = me.slope2;
       bool have_next = false;
-      const float nlse2 = (lse == -CUDART_INF_F) ? -CUDART_INF_F : -lse * scored::kLog2e;
+      const float nlse2 = (lse == -CUDART_INF_F) ? -CUDART_INF_F : fmaf(-lse, scored::kLog2e, kLift);
       const F2 nlv = dup(nlse2);
-      if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dpart_full, u_it & 1u, w)))) break;
-      const float* dpu = dpart + (u_it & 1u) * 2 * BT;
-      const float dd = ri.y > 0 ? dpu[r] + dpu[BT + r] : 0.f;   // (rows that see no key may hold anything)
+      float dd;
+      if (!(ok = estimate(item, u_it, &dd))) break;
+      if (ri.y == 0) dd = 0.f;   // (rows that see no key may hold anything)
       const F2 ndd = dup(-dd);
-      if (g == 0) {   // for every row of the padded tile: the dK/dV kernel reads whole 128-row slices
-        P.D[static_cast<long long>(u.bh) * rpad + row] = dd;
-        P.NL[static_cast<long long>(u.bh) * rpad + row] = nlse2 + kLift;
-      }
+      F2 rest = dup(0.f), weight = dup(0.f);   // sums of P (dP - D) and of P
       for (int j = 0; j < u.n; ++j, ++sp) {
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full, sp & 1u, w)))) break;
         ptx::tc_fence_after();
-        float f[64];   // P T
+        const uint32_t tx = tX + 128 * (sp & 1u);
+        float f[64];                      // P T
+        uint32_t whole[CAP ? 2 : 1][16];  // P where T is not 1, as fp16: for the sums
         const int kv0 = (u.j0 + j) * BT + 64 * g;   // key of this thread's first column
+        // a key of the group's that some row does not see
+        const bool partial = kv0 < u.tile.z || kv0 + 64 > u.tile.w;
         {
           uint32_t v[2][32];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) ptx::tmem_ld32(tS + c * 32, v[c]);
+          for (int c = 0; c < 2; ++c) ptx::tmem_ld32(tx + c * 32, v[c]);
 #pragma unroll
           for (int c = 0; c < 2; ++c) ptx::tmem_ld_wait(v[c]);
-          // S is in registers: the next S product may overwrite it
+          // S is in registers: the dP product may overwrite it
           ptx::tc_fence_before();
           ptx::mbar_arrive(s_free);
           const float* s = reinterpret_cast<const float*>(&v[0][0]);
@@ -488,7 +517,9 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                   y = mul2(t, cap_poly(t));
                 else
                   y = scored::cap_any(t, P.cap);
-                p = mul2(scored::ex2(add2(y, add)), fma2(mul2(y, y), ninv2, one));
+                p = scored::ex2(add2(y, add));
+                whole[i / 32][i / 2 % 16] = ptx::pack_f16_sat(p.x, p.y);
+                p = mul2(p, fma2(mul2(y, y), ninv2, one));
               }
               f[i] = p.x;
               f[i + 1] = p.y;
@@ -504,14 +535,25 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             }
           }
         }
-        // Keys that no row of the tile sees may hold anything, which a dS of 0
-        // would not hold back: their K is zeroed, now that the S product has
+        uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+        if (partial) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            seen[c] = scored::bit_range(ri.x - kv0 - 32 * c, ri.y - kv0 - 32 * c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(seen[c] & (1u << i))) f[32 * c + i] = 0.f;
+            if constexpr (CAP) mask_pairs(whole[c], seen[c]);
+          }
+        }
+        // Keys that no row of the tile sees may hold anything, which a weight of
+        // 0 would not hold back: their K is zeroed, now that the S product has
         // read it (each group a box of 64 columns).
         const int k0 = kv0 - 64 * g;
         if (k0 < u.tile.x || k0 + BT > u.tile.y) {
           if (k0 + r < u.tile.x || k0 + r >= u.tile.y)
             for (int c = g; c < C::KB; c += 2)
-              scored::zero_box_row(ring + slot(item + 3 + 2 * j) * C::TILE + c * BOX_BYTES, r);
+              scored::zero_box_row(ring + slot(item + 1 + 2 * j) * C::TILE + c * BOX_BYTES, r);
           ptx::fence_proxy_async_smem();
         }
         if (j + 1 == u.n) {
@@ -522,55 +564,75 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         }
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dp_full, sp & 1u, w)))) break;
         ptx::tc_fence_after();
-        uint32_t v[2][32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) ptx::tmem_ld32(tDP + c * 32, v[c]);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32], pk[32];
+          ptx::tmem_ld32(tx + c * 32, v);
+          ptx::tmem_ld_wait(v);
+          if (partial) {   // (what the row does not see may hold anything)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) ptx::tmem_ld_wait(v[c]);
-        uint32_t pk[2][16];
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
+            for (int i = 0; i < 32; ++i)
+              if (!(seen[c] & (1u << i))) v[i] = __float_as_uint(dd);
+          }
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const F2 e = add2(f2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])), ndd);
-            pk[c][i] = scored::pack_bf16(mul2(f2(f[c * 32 + 2 * i], f[c * 32 + 2 * i + 1]), e));
+            const F2 pt = f2(f[c * 32 + 2 * i], f[c * 32 + 2 * i + 1]);
+            const F2 e = add2(f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ndd);
+            const F2 ds = mul2(pt, e);
+            pk[i] = scored::pack_bf16(ds);
+            pk[16 + i] = scored::pack_bf16(pt);
+            if constexpr (CAP) {
+              const F2 p = __half22float2(*reinterpret_cast<const __half2*>(&whole[c][i]));
+              rest = fma2(p, e, rest);
+              weight = add2(weight, p);
+            } else {
+              rest = add2(rest, ds);
+              weight = add2(weight, pt);
+            }
           }
-        // (the product, not a factor of it: what the row does not see may hold anything)
-        if (kv0 < u.tile.z || kv0 + 64 > u.tile.w) {
-          mask_pairs(pk[0], scored::bit_range(ri.x - kv0, ri.y - kv0));
-          mask_pairs(pk[1], scored::bit_range(ri.x - kv0 - 32, ri.y - kv0 - 32));
+          ptx::tmem_st32(tx + c * 32, pk);   // over the columns just read
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) ptx::tmem_st16(tDP + c * 16, pk[c]);   // over this group's own first columns (already read)
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(ds_full);
       }
       if (!ok) break;
-      // the next unit's Q and dO go into TMEM now: the products that read
-      // this unit's have completed (their results were consumed above)
-      const uint32_t i_next = item + 3 + 2 * u.n;
-      if (have_next && !(ok = stage(i_next, u_it + 1))) break;
       if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(dq_full, u_it & 1u, w)))) break;
       ptx::tc_fence_after();
+      // The two groups' sums. (Every thread has read the last unit's: dq_full
+      // came after its first dS of this one.)
+      sums[g * BT + r] = f2(rest.x + rest.y, weight.x + weight.y);
+      ptx::mbar_arrive(sums_full);
+      if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(sums_full, u_it & 1u, w)))) break;
+      const F2 sum = mul2(add2(sums[r], sums[BT + r]), dup(kLower));
+      const float off = fabsf(sum.y - 1.f) <= kWhole ? sum.x : 0.f;
+      if (g == 0) {   // for every row of the padded tile: the dK/dV kernel reads whole 128-row slices
+        P.D[static_cast<long long>(u.bh) * rpad + row] = ri.y > 0 ? dd + off : 0.f;
+        P.NL[static_cast<long long>(u.bh) * rpad + row] = nlse2;
+      }
+      const float mul = scale * kLower;
+      const F2 mulv = dup(mul), offv = dup(-off * mul);
       const int row4 = row & ~3;   // (see scored::quad_transpose)
       __nv_bfloat16* out = P.dQ + (static_cast<long long>(u.bh) * R + row4) * d;
 #pragma unroll 1
       for (int c = 0; c < HD / 64; ++c) {
-        uint32_t v[32];
+        uint32_t v[32], k[32];
         ptx::tmem_ld32(tDQ + c * 32, v);
+        ptx::tmem_ld32(tPK + c * 32, k);
         ptx::tmem_ld_wait(v);
-        if (ri.y == 0) {   // sees no key (0 times what other rows see may be NaN)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
-        }
+        ptx::tmem_ld_wait(k);
         uint4 pk[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          pk[e].x = ptx::pack_bf16(__uint_as_float(v[8 * e + 0]) * scale, __uint_as_float(v[8 * e + 1]) * scale);
-          pk[e].y = ptx::pack_bf16(__uint_as_float(v[8 * e + 2]) * scale, __uint_as_float(v[8 * e + 3]) * scale);
-          pk[e].z = ptx::pack_bf16(__uint_as_float(v[8 * e + 4]) * scale, __uint_as_float(v[8 * e + 5]) * scale);
-          pk[e].w = ptx::pack_bf16(__uint_as_float(v[8 * e + 6]) * scale, __uint_as_float(v[8 * e + 7]) * scale);
+          uint32_t x[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int i = 8 * e + 2 * q;
+            const F2 y = fma2(f2(__uint_as_float(k[i]), __uint_as_float(k[i + 1])), offv,
+                              mul2(f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), mulv));
+            x[q] = ri.y == 0 ? 0u : scored::pack_bf16(y);   // sees no key: 0 times what others see may be NaN
+          }
+          pk[e] = make_uint4(x[0], x[1], x[2], x[3]);
         }
         scored::quad_transpose(pk, lane);
         const int col = (HD / 2) * g + c * 32 + 8 * (lane & 3);
@@ -578,10 +640,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         for (int i = 0; i < 4; ++i)
           if (row4 + i < R && col < d) *reinterpret_cast<uint4*>(out + static_cast<long long>(i) * d + col) = pk[i];
       }
-      // (the next unit's first dQ product, which overwrites the accumulator,
-      // waits for this group's first dS of that unit, issued after this)
+      // (the next unit's first products into the accumulators wait for this
+      // group's first dS of that unit, stored after this)
       ptx::tc_fence_before();
-      item = i_next;
+      item += 1 + 2 * u.n;
       ++u_it;
       have = have_next;
       me = nx;
@@ -1377,8 +1439,11 @@ cudaError_t launch(const ScoredBwd& a) {
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgKV<HD>::SMEM);
   if (e != cudaSuccess) return e;
-  // the register split must fit the launch allocation (see ptx::reg_acquire)
+  // the register splits must fit the launch allocations (see ptx::reg_acquire)
   cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, kq)) != cudaSuccess) return e;
+  if (fa.numRegs < DQ_REG_CTRL || fa.numRegs > DQ_REG_ROWS || 3 * fa.numRegs < DQ_REG_CTRL + 2 * DQ_REG_ROWS)
+    return cudaErrorInvalidConfiguration;
   if ((e = cudaFuncGetAttributes(&fa, kk)) != cudaSuccess) return e;
   if (fa.numRegs != KV_REG_LAUNCH) return cudaErrorInvalidConfiguration;
   P.n_blocks = scored::packed_blocks(p.n_rt, p.G);

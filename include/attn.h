@@ -353,12 +353,15 @@ ATTN_API size_t attn_fwd_scored_workspace_size(int B, int H, int Hkv, int Tq, in
  *   P = exp(S - LSE),  D = rowsum(dO o O),  dV = P^T dO,
  *   dS = P o (dO V^T - D) o T,  dQ = scale * dS K,  dK = scale * dS^T Q
  * (the bias and the ranges have no gradient). `O` and `LSE` must be the outputs
- * of attn_fwd_scored on the same inputs, scale and score. Shapes as
- * attn_fwd_scored. What no query reads may hold anything here too: K and V rows
- * before every range or behind every range of their batch entry, and Q, O and
- * dO rows whose range is empty; their gradients are 0. Sums run in a fixed
- * order: equal calls give bitwise equal results. Workspace and errors as
- * attn_fwd_scored, with attn_bwd_scored_workspace_size.
+ * of attn_fwd_scored on the same inputs, scale and score. (Those of a row over
+ * more keys than the call holds give that row's share of the gradients.)
+ * ATTN_BF16: D is formed from the rounded O and corrected by rowsum(P o dP),
+ * which it equals, where a row's P sums to 1. Shapes as attn_fwd_scored. What
+ * no query reads may hold anything here too: K and V rows before every range or
+ * behind every range of their batch entry, and Q, O and dO rows whose range is
+ * empty; their gradients are 0. Sums run in a fixed order: equal calls give
+ * bitwise equal results. Workspace and errors as attn_fwd_scored, with
+ * attn_bwd_scored_workspace_size.
  */
 ATTN_API attn_status_t attn_bwd_scored(const void* Q, const void* K, const void* V, const void* O, const float* LSE,
                                        const void* dO, void* dQ, void* dK, void* dV, int B, int H, int Hkv, int Tq,

@@ -266,3 +266,76 @@ def test_roundings_of_the_gradients(H, Hkv, T, cap):
         bound = math.sqrt(2 * once ** 2 + (np.linalg.norm(off) / np.linalg.norm(want)) ** 2)
         err = frob_rel(t, want)
         assert err <= 1.08 * bound, (name, err, bound)
+
+
+# ------------------------------------------------------------------ rows whose weight lies on a few keys
+
+FEW = [  # B, H, Hkv, Tq, Tk, d, dv
+    ((1, 5, 1, 54, 2, 40, 64), "window", 0.5, True),
+    ((2, 2, 1, 59, 3, 40, 8), "window", 0.0, True),
+    ((1, 15, 3, 4, 4, 8, 80), "docs", 0.0, True),
+    ((3, 9, 3, 330, 2, 128, 8), "prefix", 0.0, False),
+    ((1, 3, 1, 7, 3, 72, 128), "causal", 700.0, False),
+    ((2, 6, 2, 24, 2, 16, 80), "causal", 1e5, False),
+    ((2, 4, 2, 574, 2, 64, 64), "wild", 1e5, False),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,mask,cap,bias", FEW)
+def test_gradients_of_rows_that_see_few_keys(shape, mask, cap, bias):
+    """dP - D is small beside D there: a D formed from the rounded O alone put dQ off by up to 0.02 of its norm."""
+    run_case(shape, mask, cap, bias, torch.bfloat16, grad=True)
+
+
+def short_documents(T, longest, seed):
+    g = np.random.default_rng(seed)
+    edge = [0]
+    while edge[-1] < T:
+        edge.append(min(T, edge[-1] + int(g.integers(2, longest + 1))))
+    begin = np.concatenate([np.full(b - a, a) for a, b in zip(edge, edge[1:])])
+    return begin.astype(np.int32)[None], np.concatenate([np.full(b - a, b) for a, b in zip(edge, edge[1:])]).astype(np.int32)[None]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("longest", [3, 12, 60])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (8.0, False), (0.0, True), (8.0, True)])
+@pytest.mark.parametrize("H,Hkv,d", [(4, 2, 64), (2, 2, 128)])
+def test_gradients_over_short_documents_are_rounded_twice(H, Hkv, d, cap, bias, longest):
+    """dS and the result are rounded to bf16, nothing else: sqrt(2) of what rounding the exact gradients is (see
+    test_roundings_of_the_gradients), and a tenth for what is left of the rounding of O in D (a fifth of it at most,
+    where P goes into its correction in 11 bits) and for the spread of a few hundred rows."""
+    T = 700
+    x = make(1, H, Hkv, T, T, d, d, torch.bfloat16, 89)
+    begin, end = short_documents(T, longest, 90)
+    how = dict(softcap=cap, key_begin=torch.from_numpy(begin).cuda(), key_end=torch.from_numpy(end).cuda(),
+               slopes=torch.exp2(-torch.arange(1.0, H + 1)).cuda() if bias else None)
+    o, lse = B.forward_scored(*x[:3], **how)
+    g = B.backward_scored(*x[:3], o, lse, x[3], **how)
+    assert B.attn_device_status() == B.ATTN_OK
+    r = ref.scored(*x, scale=1.0 / math.sqrt(d), **how)
+    for t, name in zip(g, ("dQ", "dK", "dV")):
+        once = frob_rel(torch.from_numpy(r[name]).to(torch.bfloat16), r[name])
+        assert frob_rel(t, r[name]) <= 1.1 * math.sqrt(2) * once, name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (6.0, True)])
+def test_the_backward_on_parts_of_the_keys(cap, bias, dtype):
+    """With O and LSE of all keys, the gradients of the keys' parts are the formula's: dQ in two shares, dK and dV by
+    rows. (D is not the sum of P dP over a part.)"""
+    Bn, H, Hkv, Tq, Tk, d = 1, 4, 2, 300, 560, 64
+    x = make(Bn, H, Hkv, Tq, Tk, d, d, dtype, 97)
+    how = how_of("none", cap, bias, Bn, H, Tq, Tk)
+    o, lse = B.forward_scored(*x[:3], **how)
+    r = ref.scored(*x, scale=1.0 / math.sqrt(d), **how)
+    cut, dq = 250, 0.0
+    for a, b in ((0, cut), (cut, Tk)):
+        part = dict(how, q_pos=how["q_pos"] - a)
+        k, v = (t[:, :, a:b].contiguous() for t in x[1:3])
+        g = B.backward_scored(x[0], k, v, o, lse, x[3], **part)
+        dq = dq + g[0].double()
+        check_grad(g[1], r["dK"][:, :, a:b], dtype, "dK")
+        check_grad(g[2], r["dV"][:, :, a:b], dtype, "dV")
+    check_grad(dq, r["dQ"], dtype, "dQ")
