@@ -1168,9 +1168,8 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         ptx::tc_fence_after();
         // pass 1: P^T, packed bf16 (the product's type) over the first half of
         // this group's S^T columns; P^T T stays in registers for pass 2, as
-        // fp16: as fp32 it would take 64 of 168 registers. (As bf16 it would be
-        // a rounding as large as dS's: dK off by 0.0030 of its norm, 0.0025
-        // so.)
+        // fp16: as fp32 it would take 64 of 168 registers, and as bf16 it would
+        // be a third rounding of dK, as large as dS's and the result's.
         uint32_t keep[2][16];
         {
           uint32_t rs[2][32];
