@@ -78,7 +78,8 @@ struct ScoredFwd {
   const void* V;
   void* O;
   float* LSE;
-  int* start;         // few-row kernel: [B + 1], and n_splits is its grid
+  int* start;         // few-row kernel: [B + 1]
+  int grid;           // few-row kernel: its CTAs
   int n_splits;       // key ranges of split_keys keys (a multiple of 128) each, as units of their own
   int split_keys;
   float* Opart;       // [n_splits][B * Hkv * R][dv] fp32, n_splits > 1

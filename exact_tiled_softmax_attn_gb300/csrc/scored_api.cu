@@ -103,7 +103,7 @@ bool fwd_tokens(const ScoredProblem& p, attn_dtype_t dt) { return dt == ATTN_BF1
 
 struct Layout {
   size_t start, rows, tiles, fine, counters, kcount, khull, kbits, even, slope2, D, NL, dkpart, dvpart, opart, lsepart, total;
-  int n_splits, split_keys;
+  int n_splits, split_keys, grid;
 };
 
 // Forward: rows | tiles | fine (fp32) | counters | Opart | LSEpart, with few rows in bf16
@@ -124,10 +124,10 @@ Layout layout(const ScoredProblem& p, attn_dtype_t dt, bool bwd) {
   if (!bwd && fwd_tokens(p, dt)) {
     // one CTA per SM, two where 16 rows are enough, and at least a 64-key stage each
     const long long stages = static_cast<long long>(heads) * ((p.Tk + 63) / 64), want = p.R <= 16 ? 2 * kSms : kSms;
-    L.n_splits = static_cast<int>(stages < want ? stages : want);
+    L.grid = static_cast<int>(stages < want ? stages : want);
     L.start = take((B + 1) * sizeof(int));
-    L.opart = take(static_cast<size_t>(L.n_splits) * 2 * p.R * p.dv * sizeof(float));
-    L.lsepart = take(static_cast<size_t>(L.n_splits) * 2 * p.R * sizeof(float));
+    L.opart = take(static_cast<size_t>(L.grid) * 2 * p.R * p.dv * sizeof(float));
+    L.lsepart = take(static_cast<size_t>(L.grid) * 2 * p.R * sizeof(float));
     L.total = off;
     return L;
   }
@@ -259,6 +259,7 @@ attn_status_t attn_fwd_scored(const void* Q, const void* K, const void* V, void*
   a.O = O;
   a.LSE = LSE;
   a.n_splits = L.n_splits;
+  a.grid = L.grid;
   a.split_keys = L.split_keys;
   a.Opart = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.opart);
   a.LSEpart = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.lsepart);

@@ -606,7 +606,7 @@ template <int HD, int RT>
 cudaError_t launch(const ScoredFwd& a) {
   using C = Cfg<HD, RT>;
   static_assert(C::NST >= 2 && C::SMEM <= 227 * 1024, "shared memory");
-  if (a.n_splits > MAX_GRID) return cudaErrorInvalidValue;
+  if (a.grid > MAX_GRID) return cudaErrorInvalidValue;
   Params P;
   P.p = a.p;
   P.mask = a.mask;
@@ -622,11 +622,11 @@ cudaError_t launch(const ScoredFwd& a) {
   auto kern = tokens_kernel<HD, RT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<a.n_splits, C::THREADS, C::SMEM, a.stream>>>(*a.tmK, *a.tmV, P);
+  kern<<<a.grid, C::THREADS, C::SMEM, a.stream>>>(*a.tmK, *a.tmV, P);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // (rows fit int: the host checks)
   const int rows = a.p.B * a.p.Hkv * a.p.R;
-  const bool few = a.n_splits <= 8 * a.p.B * a.p.Hkv;   // parts of a row, on average
+  const bool few = a.grid <= 8 * a.p.B * a.p.Hkv;   // parts of a row, on average
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = few ? (rows + JOIN_WARPS - 1) / JOIN_WARPS : rows;
   cfg.blockDim = JOIN_THREADS;
@@ -636,7 +636,7 @@ cudaError_t launch(const ScoredFwd& a) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few ? join_kernel<1> : join_kernel<JOIN_WARPS>, P, a.n_splits);
+  return cudaLaunchKernelEx(&cfg, few ? join_kernel<1> : join_kernel<JOIN_WARPS>, P, a.grid);
 }
 
 template <int HD>
