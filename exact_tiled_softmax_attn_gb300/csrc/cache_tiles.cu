@@ -20,6 +20,19 @@
 // the scores, and the value scale's logarithm is added to them, as in
 // cache_tokens.cu; stages, shares and the join are cache_walk.cuh's.
 //
+// Weights are p vs as fp16, relative to the largest of the row, so a page of
+// zeros (or of tokens that no row sees) whose scale is 2^30 times the others'
+// must not set what they are relative to. A warp looks over the scales of a run
+// ahead of it. Where they lie more than 2^8 apart, or a page is none, it steps
+// between the producer of V and the converter: it finds the largest code that is
+// seen of every 16 keys, multiplies their codes by the power of two that brings
+// it above 224 - exact, codes have no more bits - and divides the scale by it.
+// Weights are then relative to the largest of what keys add to O, whatever the
+// scales. That costs other runs 6 % (57 -> 60.5 us with 64 rows, 78 -> 84 with
+// 128, by the code's size: the roles' loops together just fit the instruction
+// cache); a factor on the converted values instead 16 %, a product per band of
+// scales 30 %.
+//
 // Order of the tensor core's work, tile i: S(i + 1) is issued before O += P V
 // of tile i, so that the softmax of the next tile need not wait for it. S(i)
 // goes over P(i - 2), which the product before it in the queue has read by
@@ -27,8 +40,8 @@
 // tile i go, which is also when it may rescale O.
 // TMEM: S and P of even tiles at column 0, of odd ones at 128, O at 256.
 //
-// 16 sequences of up to 12000 keys, Hkv=4 d=128: 64 rows a key head 57 us (113
-// by groups of 32 rows in cache_tokens.cu), 128 rows 90. A tile of 128 keys
+// 16 sequences of up to 12000 keys, Hkv=4 d=128: 64 rows a key head 60 us (113
+// by groups of 32 rows in cache_tokens.cu), 128 rows 84. A tile of 128 keys
 // takes about 2300 cycles with 64 rows: the products 1260, shared memory 1750
 // (the codes in and out, the converted tiles in and out, Q), a converter 1150, a
 // softmax thread 1350; they wait for one another in turn.
@@ -37,6 +50,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "cache.h"
 #include "cache_walk.cuh"
@@ -58,6 +72,7 @@ using scored::fma2;
 constexpr int BM = 128, BN = 128;
 constexpr int BOX = 128 * 64 * 2;      // 128 rows of 64 fp16
 constexpr float TAU = 8.0f, SHIFT = 7.0f;   // weights up to 2^(TAU + SHIFT)
+constexpr float kWide = 256.0f;      // value scales further apart than this: a wide run
 constexpr int THREADS = 512;
 constexpr int REG_CTRL = 88, REG_CONVERT = 88, REG_SOFTMAX = 240;
 constexpr int NSC = 8;   // tiles whose scales are held (see the producer)
@@ -79,8 +94,8 @@ struct Cfg {
   static constexpr int OFF_V = OFF_K + 2 * TILE;   // two of K: the next is converted while S is formed from one
   static constexpr int OFF_RAW = OFF_V + TILE;
   // raw_full[NRAW], raw_empty[NRAW], k_full[2], k_empty[2], v_full, v_empty, s_full[2], p_full[2], pv_done, q_full, drain,
-  // sc_full[NSC], unit_full[2]
-  static constexpr int NBAR = 2 * NRAW + 15 + NSC;
+  // sc_full[NSC], unit_full[2], run_full[2], run_empty[2], wide_full[NRAW]
+  static constexpr int NBAR = 3 * NRAW + 19 + NSC;
   static constexpr int OFF_SUMS = OFF_RAW + NRAW * RAW;   // [2][RP][32] fp32: columns that a copy hands to the other
   static constexpr int OFF_BAR = OFF_SUMS + (CP > 1 ? 2 * RP * 128 : 0);
   static constexpr int OFF_NONE = OFF_BAR + (NBAR * 8 + 15) / 16 * 16;   // [NRAW]: 16-key groups of a slot that hold nothing
@@ -145,9 +160,13 @@ __global__ void __launch_bounds__(THREADS, 1) tiles_kernel(const __grid_constant
   uint64_t* drain = q_full + 1;
   uint64_t* sc_full = drain + 1;
   uint64_t* unit_full = sc_full + NSC;
+  uint64_t* run_full = unit_full + 2;    // whether a run is wide
+  uint64_t* run_empty = run_full + 2;
+  uint64_t* wide_full = run_empty + 2;   // values of wide runs, before they are raw_full
   float* units = reinterpret_cast<float*>(smem + C::OFF_UNIT);
   float4* scales = reinterpret_cast<float4*>(smem + C::OFF_SCALE);   // of 16-key groups: ks, log2 vs, 1 / vs
   volatile uint32_t* none_of = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_NONE);
+  volatile uint32_t* run_wide = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 8);   // [2]
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 4);
   int* found = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);
@@ -170,7 +189,12 @@ __global__ void __launch_bounds__(THREADS, 1) tiles_kernel(const __grid_constant
     ptx::mbar_init(q_full, 128);
     ptx::mbar_init(drain, 1);
     for (int k = 0; k < NSC; ++k) ptx::mbar_init(sc_full + k, 1);
-    for (int k = 0; k < 2; ++k) ptx::mbar_init(unit_full + k, 128);
+    for (int k = 0; k < 2; ++k) {
+      ptx::mbar_init(unit_full + k, 128);
+      ptx::mbar_init(run_full + k, 1);
+      ptx::mbar_init(run_empty + k, 2);
+    }
+    for (int k = 0; k < C::NRAW; ++k) ptx::mbar_init(wide_full + k, 1);
     *abort_flag = 0u;
     ptx::fence_mbar_init();
   }
@@ -200,61 +224,73 @@ __global__ void __launch_bounds__(THREADS, 1) tiles_kernel(const __grid_constant
   const int wg = warp >> 2;
   if (wg == 0) {
     ptx::reg_release<REG_CTRL>();
+    const int shift = P.c.shift, rows = 1 << shift, nb = BN >> shift;   // nb boxes of a tile, of `rows` keys each
+    // box `box` of the run: its plane of the pool, or -1
+    auto find = [&](int box, bool* seen) {
+      const int key = wk.key0(wk.s0) + box * rows;
+      *seen = box < wk.run * nb && key < wk.hull.y && key + rows > wk.hull.x;
+      const int at = *seen ? cache::page_of(P.c, wk.e / P.groups, key >> shift) : -1;
+      return at >= 0 ? at * P.p.Hkv + wk.h : -1;
+    };
     if ((warp == 0 || warp == 2) && last > first) {
       // ------------------------------------------------------------ producers, of K (and the scales) and of V
       const int side = warp >> 1;
       ptx::WaitCtx w{abort_flag, P.status, 1u};
-      const int shift = P.c.shift, rows = 1 << shift, nb = BN >> shift;   // boxes of a tile, of `rows` keys each
       const uint32_t bytes = static_cast<uint32_t>(rows * (side ? P.p.dv : P.p.d));   // of a box
-      uint32_t item = side;
-      bool ok = true;
+      uint32_t item = side, runs = 0;
+      bool ok = true, seen;
       do {
-        const int b = wk.e / P.groups;
-        const int key_s0 = wk.key0(wk.s0), n_box = wk.run * nb;
+        const int n_box = wk.run * nb;
+        bool wide = false;
         // lane i looks up box i of the next 32
-        auto find = [&](int box) {
-          const int key = key_s0 + box * rows;
-          const bool seen = box < n_box && key < wk.hull.y && key + rows > wk.hull.x;
-          const int at = seen ? cache::page_of(P.c, b, key >> shift) : -1;
-          return at >= 0 ? at * P.p.Hkv + wk.h : -1;
-        };
-        int plane = find(lane);
+        int plane = find(lane, &seen);
         for (int box0 = 0; ok && box0 < n_box; box0 += 32) {
           float ks = 1.f, vs = 1.f;
           if (side == 0 && plane >= 0) {
             ks = __ldg(P.c.scale[0] + plane);
             vs = __ldg(P.c.scale[1] + plane);
           }
-          const int next = find(box0 + 32 + lane);
+          const int next = find(box0 + 32 + lane, &seen);
           const int boxes = min(32, n_box - box0);
           for (int j = 0; ok && j < boxes; j += nb) {
             const int at = __shfl_sync(0xffffffffu, plane, (j + lane) & 31);
             const bool there = lane < nb && at >= 0;
             const unsigned got = __ballot_sync(0xffffffffu, there);
-            uint32_t none = 0;   // 16-key groups of the boxes that are not there
-            for (int i = 0; i < nb; ++i)
-              if (!(got >> i & 1u)) none |= ((1u << (rows / 16)) - 1u) << (i * (rows / 16));
+            const int from = j + ((16 * (lane & 7)) >> shift);   // box of 16-key group lane % 8
+            // 16-key groups of the boxes that are not there
+            const uint32_t none = 0xffu & ~__ballot_sync(0xffffffffu, __shfl_sync(0xffffffffu, plane, from) >= 0);
             const int sl = slot(item);
-            if (lane == 0) ok = ptx::mbar_wait(raw_empty + sl, par(item) ^ 1u, w);
+            if (lane == 0) {
+              ok = ptx::mbar_wait(raw_empty + sl, par(item) ^ 1u, w);
+              if (side && box0 + j == 0) ok = ok && ptx::mbar_wait(run_full + (runs & 1u), (runs >> 1) & 1u, w);
+            }
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             if (!ok) break;
+            if (side && box0 + j == 0) wide = run_wide[runs & 1u] != 0u;
+            uint64_t* full = (side && wide ? wide_full : raw_full) + sl;
             if (lane == 0) {
               none_of[sl] = none;
-              ptx::mbar_arrive_expect_tx(raw_full + sl, bytes * __popc(got));
+              ptx::mbar_arrive_expect_tx(full, bytes * __popc(got));
             }
             __syncwarp();
             if (there)
               ptx::bulk_load(smem + C::OFF_RAW + sl * C::RAW + lane * bytes,
                              static_cast<const uint8_t*>(P.c.pool[side]) + static_cast<long long>(at) * bytes, bytes,
-                             raw_full + sl);
+                             full);
             const uint32_t tile = item / 2;
             item += 2;
             if (side) continue;
+            if (box0 + j == 0) {
+              if (lane == 0) ok = ptx::mbar_wait(run_full + (runs & 1u), (runs >> 1) & 1u, w);
+              ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+              if (!ok) break;
+              wide = run_wide[runs & 1u] != 0u;
+            }
             // The scales of the tile j (of the CTA), behind its copies. They replace those of j - NSC, which the softmax
             // has done with: the ring had room for j's keys, so those of j - NRAW / 2 (j - 4 at least) were converted,
             // so S of the tile two before them (j - 6) was out, which is issued after the softmax of the one two before
-            // it (j - 8) was waited for.
-            const int from = j + ((16 * (lane & 7)) >> shift);
+            // it (j - 8) was waited for. (Of a wide run: below.)
+            if (wide) continue;
             const float k = cache::clamp_scale(__shfl_sync(0xffffffffu, ks, from));
             const float v = cache::clamp_scale(__shfl_sync(0xffffffffu, vs, from));
             if (lane < 8) scales[(tile % NSC) * 8 + lane] = make_float4(k, log2f(v), 1.f / v, 0.f);
@@ -263,10 +299,112 @@ __global__ void __launch_bounds__(THREADS, 1) tiles_kernel(const __grid_constant
           }
           plane = next;
         }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(run_empty + (runs & 1u));
+        ++runs;
       } while (ok && wk.next(P));
       if (!ok && lane == 0)   // let the copies in flight land before the CTA exits
         for (uint32_t n = item > static_cast<uint32_t>(C::NRAW) ? item - C::NRAW : side; n < item; n += 2)
           ptx::mbar_wait_drain(raw_full + slot(n), par(n));
+    } else if (warp == 3 && last > first) {
+      // ------------------------------------------------------------ value scales that lie far apart
+      ptx::WaitCtx w{abort_flag, P.status, 5u};
+      uint32_t runs = 0, tile = 0, phase = 0;   // phase: of wide_full, a bit each
+      bool ok = true, seen;
+      do {
+        float least = CUDART_INF_F, most = 0.f;
+        bool wide = false;
+        for (int box = lane; box < wk.run * nb; box += 4 * 32) {
+          int at[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            at[u] = find(box + 32 * u, &seen);
+            if (seen && at[u] < 0) wide = true;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (at[u] >= 0) {
+              const float v = cache::clamp_scale(P.c.scale[1][at[u]]);
+              least = fminf(least, v);
+              most = fmaxf(most, v);
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        }
+        wide = __any_sync(0xffffffffu, wide || most > kWide * least);
+        if (lane == 0 && (ok = ptx::mbar_wait(run_empty + (runs & 1u), ((runs >> 1) & 1u) ^ 1u, w))) {
+          run_wide[runs & 1u] = wide;
+          ptx::mbar_arrive(run_full + (runs & 1u));
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        ++runs;
+        if (wide) {
+          for (int j = 0; ok && j < wk.run; ++j, ++tile) {
+            // Four lanes a group of 16 keys: the rows that are seen, 16 codes at a time.
+            const int g = lane >> 2, box = j * nb + (16 * g >> shift), per = P.p.dv / 16;
+            const int plane = find(box, &seen);
+            const float ks = plane >= 0 ? cache::clamp_scale(P.c.scale[0][plane]) : 1.f;
+            const float vs = plane >= 0 ? cache::clamp_scale(P.c.scale[1][plane]) : 1.f;
+            const int key0 = wk.key0(wk.s0 + j) + 16 * g;
+            const int r0 = max(0, min(16, wk.hull.x - key0)), r1 = plane >= 0 ? max(0, min(16, wk.hull.y - key0)) : 0;
+            const int sl = slot(2 * tile + 1);
+            if (lane == 0) ok = ptx::mbar_wait(wide_full + sl, phase >> sl & 1u, w);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) {   // let the copies in flight land before the CTA exits
+              if (lane == 0) ptx::mbar_wait_drain(wide_full + sl, phase >> sl & 1u);
+              break;
+            }
+            phase ^= 1u << sl;
+            uint4* codes = reinterpret_cast<uint4*>(smem + C::OFF_RAW + sl * C::RAW) + 16 * g * per;
+            uint32_t m = 0;
+            for (int i = r0 * per + (lane & 3); i < r1 * per; i += 4) {
+              const uint4 u = codes[i];
+              constexpr uint32_t SIZE = 0x7f7f7f7fu;   // without the signs
+              m = __vmaxu4(m, __vmaxu4(__vmaxu4(u.x & SIZE, u.y & SIZE), __vmaxu4(u.z & SIZE, u.w & SIZE)));
+            }
+            uint32_t top = max(max(m & 255u, m >> 8 & 255u), max(m >> 16 & 255u, m >> 24));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float size = cache::half2_to_float2(cache::codes_to_half2(static_cast<uint16_t>(top))).x;
+            int up = 0;   // to 17
+            if (top > 0 && top < 0x7f) {   // (0x7f: NaN)
+              up = 8 - ilogbf(size);
+              if (ldexpf(size, up) > kCodeMost) --up;
+            }
+            if (up > 0) {
+              const float f = ldexpf(1.f, up);
+              for (int i = r0 * per + (lane & 3); i < r1 * per; i += 4) {
+                uint4 u = codes[i];
+                uint32_t* q = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 a = cache::half2_to_float2(cache::codes_to_half2(static_cast<uint16_t>(q[e])));
+                  const float2 c = cache::half2_to_float2(cache::codes_to_half2(static_cast<uint16_t>(q[e] >> 16)));
+                  q[e] = static_cast<uint32_t>(cache::float2_to_codes(a.x * f, a.y * f)) |
+                         static_cast<uint32_t>(cache::float2_to_codes(c.x * f, c.y * f)) << 16;
+                }
+                codes[i] = u;
+              }
+            }
+            ptx::fence_proxy_async_smem();   // (the slot's next copies come after these writes)
+            // Zeros: a scale below all others', 2^-40 2^-17. The place is free: the copies had room, so the values of the
+            // tile four before at least were converted, after the product of the one before that.
+            if ((lane & 3) == 0)
+              scales[(tile % NSC) * 8 + g] = make_float4(ks, top == 0 ? -60.f : log2f(vs) - static_cast<float>(up),
+                                                         top == 0 ? 0x1p60f : ldexpf(1.f / vs, up), 0.f);
+            __syncwarp();
+            if (lane == 0) {
+              ptx::mbar_arrive(raw_full + sl);
+              ptx::mbar_arrive(sc_full + tile % NSC);
+            }
+          }
+        } else {
+          tile += wk.run;
+        }
+      } while (ok && wk.next(P));
     } else if (warp == 1 && last > first) {
       // ------------------------------------------------------------ MMA issuer
       // The whole warp follows the schedule; the lane elect.sync picks issues.

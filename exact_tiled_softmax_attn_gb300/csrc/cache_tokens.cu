@@ -30,8 +30,20 @@
 // are their weights. The scales cost nothing per element: the key scale is part
 // of the factor that each score is multiplied by anyway, and the value scale
 // enters as its logarithm, added in the same instruction: weights are held as
-// p vs, relative to the largest of them, and the sum takes p = (p vs) / vs in
-// the FMA that adds it.
+// p vs, relative to a reference, and the sum takes p = (p vs) / vs in the FMA
+// that adds it.
+//
+// As fp16 the weights keep their 11 bits down to 2^-21 of that reference, so it
+// may not stand for a page of zeros, or of tokens that no row sees, whose scale
+// is 2^30 times the others'. Where the value scales since it was set are more
+// than 2^8 apart, it is set anew: to min(W, S vs), W the largest p vs and S the
+// largest p so far, vs the scale from here on, but no less than W 2^-72. A weight
+// is then in full as long as p is at least 2^-13 of the largest p, whatever the
+// scales (up to 2^72 apart; at 2^80, the most there is, 2^-5), and smaller ones
+// are off by 2^-32 of the reference. Sums and accumulators take the ratio of two
+// references in 32 bits: 2^15 of a weight, 448, 2^30 keys and 2^72 are below
+// 2^126. With scales within 2^8, which a layer's are, that costs a comparison per
+// step: 1 % with long caches, 3 % with one short one.
 //
 // Fragments are read as 16-byte vectors: the columns of Q and K are permuted
 // alike, so that a thread's fragments of K are 16 adjacent codes of a row; the
@@ -67,6 +79,9 @@ using cache_walk::Walk;
 
 constexpr int BK = 64;              // keys per stage
 constexpr float TAU = 8.0f;
+// The value scales that a reference stands for lie within 2^8 of one
+// another, and it is let down by at most 2^DEPTH (see the header).
+constexpr float SPREAD = 8.01f, DEPTH = 72.0f;   // (8, and the logarithms' rounding)
 
 // E: uint8_t (e4m3) or bf16; SPLIT: fp32 queries and results (e4m3 only); a
 // warp has 8 NT rows, and RT row tiles of 4 warps share the stages.
@@ -91,7 +106,8 @@ struct Cfg {
   static constexpr int OFF_SCALE = OFF_BAR + 2 * NST * 8;    // [NST][4] float4: of a stage's 16-key groups
   static constexpr int OFF_MISC = OFF_SCALE + NST * 64;
   static constexpr int OFF_HULL = OFF_MISC + 64 + 128;   // after the scan: [THREADS] hulls
-  static constexpr int SMEM = OFF_HULL + 8 * THREADS;
+  static constexpr int OFF_TOP = OFF_HULL + 8 * THREADS;     // [WARPS][RW] float2: log2 of W and S of a row
+  static constexpr int SMEM = OFF_TOP + (CODES ? 8 * WARPS * RW : 0);
 };
 
 template <bool F16>
@@ -259,6 +275,7 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
   const int krow = (g & 1) ? g ^ 4 : g;                 // key of fragment row g within 8
   const int k_lo = 2 * t, k_hi = (2 * t + 1) ^ 4;       // keys of operand elements 2t, 2t + 1 within 8
   constexpr float SHIFT = C::SHIFT;
+  float2* top = reinterpret_cast<float2*>(smem + C::OFF_TOP) + warp * C::RW + 2 * t;   // [8 n + e]
   uint32_t it = 0;
   bool ok = true;
   // The fragments of Q: row 8 n + g of the warp's. Codes: elements 64 c + 16 t + 4 j .. + 3 as words 2 (4 c + j) and the
@@ -365,6 +382,15 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
     }
+    float vs_lo = CUDART_INF_F, vs_hi = -CUDART_INF_F;   // log2 of the value scales since m was set
+    if (CODES) {
+      __syncwarp();   // (the last run's are read)
+      if (g == 0) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) top[8 * n] = top[8 * n + 1] = make_float2(-CUDART_INF_F, -CUDART_INF_F);
+      }
+      __syncwarp();
+    }
 
     for (int s = wk.s0; s < wk.s0 + wk.run; ++s, ++it) {
       const int st = it % C::NST;
@@ -468,6 +494,31 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
               const int key = key0 + krow + 8 * (e >> 1);
               x[n][e] = key >= lo[n][e & 1] && key < hi[n][e & 1] ? x[n][e] : -CUDART_INF_F;
             }
+        }
+        if constexpr (CODES) {
+          const float lo2 = fminf(vs_lo, sc.y), hi2 = fmaxf(vs_hi, sc.y);
+          if (hi2 - lo2 > SPREAD) {   // (the same in the whole warp) the references as these scales want them
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float2 ws = top[8 * n + e];
+                ws.x = fmaxf(ws.x, m[n][e]);
+                ws.y = fmaxf(ws.y, m[n][e] - vs_hi);
+                const float mn = fmaxf(fminf(ws.x, ws.y + sc.y), ws.x - DEPTH);
+                const float corr = m[n][e] == mn ? 1.f : ptx::ex2(m[n][e] - mn);
+                m[n][e] = mn;
+                l[n][e] *= corr;
+#pragma unroll
+                for (int i = 0; i < HD / 16; ++i) o[n][i][e] *= corr, o[n][i][2 + e] *= corr;
+                __syncwarp();
+                if (g == 0) top[8 * n + e] = ws;
+                __syncwarp();
+              }
+            vs_lo = vs_hi = sc.y;
+          } else {
+            vs_lo = lo2, vs_hi = hi2;
+          }
         }
         bool need = false;
 #pragma unroll
