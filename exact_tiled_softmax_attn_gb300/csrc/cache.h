@@ -58,7 +58,7 @@ __device__ __forceinline__ void row_range(const ScoredMask& m, long long at, int
   *hi = min(m.key_end ? __ldg(m.key_end + at) : len, min(len, Tk));
   if (m.causal) *hi = min(*hi, *pos + 1);
   if (window > 0) *lo = max(*lo, *pos - window + 1);
-  if (t >= n) *hi = 0;
+  *hi = t < n ? max(*hi, 0) : 0;   // (an end far below 0 less a key would wrap around)
 }
 
 // Two e4m3 codes as fp16 (exact), and two fp32 numbers as codes: to the

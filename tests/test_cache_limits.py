@@ -1,5 +1,5 @@
 """Attention over a paged 8-bit cache at the limits of its arguments: value
-scales that lie far apart.
+scales that lie far apart, ranges that end far below zero.
 
 Tolerances as test_cache.py's, row by row: bf16 rms 1e-2 of the row's, fp32
 1e-5 of the row's sum of P |V| (which is what the roundings of weights and
@@ -128,3 +128,19 @@ def test_scales_far_apart_in_long_sequences(Hkv, Tq):
     o, lse = compare(c, table, length, new, q, 12000)
     again = B.forward_cached(q, c, table, i32(length), new_len=i32(new), Tk=12000)
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq", [1, 6, 13, 30, 60, 100])
+def test_ranges_that_end_far_below_zero(Tq, dtype):
+    """A range's end may be any int32: one of -2^31 is an empty range, beside rows that see keys from every tile."""
+    shape = (2, 4, 2, Tq, 700, 64, 64, 32)
+    c, table, length, new, q = attention_case(shape, "e4m3", dtype, False, seed=11)
+    end = np.full((2, Tq), 700)
+    end[:, 1::3] = -2 ** 31
+    end[:, 2::6] = -2 ** 31 + 100
+    end[1, 0] = -2 ** 31
+    compare(c, table, length, new, q, 700, causal=False, key_end=end)
+    pos = np.where(end < 0, -2 ** 31, 650)
+    compare(c, table, length, new, q, 700, q_pos=pos)
