@@ -32,17 +32,28 @@ namespace cache {
 constexpr int kMostTokens = rope::kMostTokens;
 
 #ifdef __CUDACC__
+// An element of the call's arrays, by an ordinary load, as all that is read by
+// kernels launched over the end of the kernel before: that may write lengths,
+// table, scales, ranges or rows while they are resident, and a load through the
+// read-only path is right only for what nobody writes in a kernel's life.
+// (volatile: not moved before the wait for that kernel, and not made twice.)
+__device__ __forceinline__ int load(const int* p) {
+  int r;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
+}
+
 // Tokens of sequence b, and how many of them are the call's new ones (of T at most).
 __device__ __forceinline__ int tokens_of(const CacheView& c, int b) {
-  return min(max(__ldg(c.seq_len + b), 0), kMostTokens);
+  return min(max(load(c.seq_len + b), 0), kMostTokens);
 }
 __device__ __forceinline__ int new_of(const CacheView& c, int b, int T) {
-  return c.new_len ? min(max(__ldg(c.new_len + b), 0), T) : T;
+  return c.new_len ? min(max(load(c.new_len + b), 0), T) : T;
 }
 // The page that holds tokens [i * page, (i + 1) * page) of sequence b, or -1.
 __device__ __forceinline__ int page_of(const CacheView& c, int b, int i) {
   if (i < 0 || i >= c.max_pages) return -1;
-  const int at = __ldg(c.table + static_cast<long long>(b) * c.max_pages + i);
+  const int at = load(c.table + static_cast<long long>(b) * c.max_pages + i);
   return at >= 0 && at < c.pages ? at : -1;
 }
 // (a NaN reads as the least)
@@ -53,9 +64,9 @@ __device__ __forceinline__ float clamp_scale(float s) { return fminf(fmaxf(s, 0x
 // the last n of them new.
 __device__ __forceinline__ void row_range(const ScoredMask& m, long long at, int t, int len, int n, int Tk, int window,
                                           int* lo, int* hi, int* pos) {
-  *pos = m.q_pos ? min(max(__ldg(m.q_pos + at), -kMostTokens), kMostTokens) : len - n + t;
-  *lo = m.key_begin ? max(__ldg(m.key_begin + at), 0) : 0;
-  *hi = min(m.key_end ? __ldg(m.key_end + at) : len, min(len, Tk));
+  *pos = m.q_pos ? min(max(load(m.q_pos + at), -kMostTokens), kMostTokens) : len - n + t;
+  *lo = m.key_begin ? max(load(m.key_begin + at), 0) : 0;
+  *hi = min(m.key_end ? load(m.key_end + at) : len, min(len, Tk));
   if (m.causal) *hi = min(*hi, *pos + 1);
   if (window > 0) *lo = max(*lo, *pos - window + 1);
   *hi = t < n ? max(*hi, 0) : 0;   // (an end far below 0 less a key would wrap around)

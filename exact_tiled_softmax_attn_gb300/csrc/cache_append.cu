@@ -336,8 +336,8 @@ __global__ void __launch_bounds__(NT, 8 / NI) pages_kernel(const __grid_constant
     for (int i = 0; i < NI; ++i) {
       if (o0[i] < 0) continue;
       const T* p = src[i] + h * P.s[side].h;
-      raw[i][0] = __ldg(reinterpret_cast<const uint4*>(p));
-      raw[i][1] = __ldg(reinterpret_cast<const uint4*>(p + o1[i]));
+      raw[i][0] = *reinterpret_cast<const uint4*>(p);
+      raw[i][1] = *reinterpret_cast<const uint4*>(p + o1[i]);
     }
   };
   fetch(h0);

@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(THREADS, 1) tiles_kernel(const __grid_constant
         for (int box0 = 0; ok && box0 < n_box; box0 += 32) {
           float ks = 1.f, vs = 1.f;
           if (side == 0 && plane >= 0) {
-            ks = __ldg(P.c.scale[0] + plane);
-            vs = __ldg(P.c.scale[1] + plane);
+            ks = P.c.scale[0][plane];
+            vs = P.c.scale[1][plane];
           }
           const int next = find(box0 + 32 + lane, &seen);
           const int boxes = min(32, n_box - box0);
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(THREADS, 1) tiles_kernel(const __grid_constant
               const int r = (k0 + k) * ROWS + tid / LANES;
               raw[k] = make_uint4(0u, 0u, 0u, 0u);
               if (r < R && 8 * q < d)
-                raw[k] = __ldg(reinterpret_cast<const uint4*>(src + static_cast<long long>(r) * d + 8 * q));
+                raw[k] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(r) * d + 8 * q);
             }
 #pragma unroll
             for (int k = 0; k < N; ++k) {
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(THREADS, 1) tiles_kernel(const __grid_constant
           const int tok = (r0 + r) % Tq;
           cache::row_range(P.mask, static_cast<long long>(b) * Tq + tok, tok, cache::tokens_of(P.c, b),
                            cache::new_of(P.c, b, Tq), P.p.Tk, P.window, &from, &to, &pos);
-          if (bias) slope2 = __ldg(P.p.slopes + wk.h * P.p.G + (r0 + r) / Tq) * scored::kLog2e;
+          if (bias) slope2 = P.p.slopes[wk.h * P.p.G + (r0 + r) / Tq] * scored::kLog2e;
         }
         if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(unit_full + (runs & 1u), (runs >> 1) & 1u, w)))) {
           if constexpr (CP == 1) break;

@@ -225,8 +225,8 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
       for (int box0 = 0; ok && box0 < n_box; box0 += 32) {
         float ks = 1.f, vs = 1.f;
         if (CODES && plane >= 0) {
-          ks = __ldg(P.c.scale[0] + plane);
-          vs = __ldg(P.c.scale[1] + plane);
+          ks = P.c.scale[0][plane];
+          vs = P.c.scale[1][plane];
         }
         const int next = find(box0 + 32 + lane);
         ks = cache::clamp_scale(ks);
@@ -302,7 +302,7 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
           const int r = r0 + row, tok = r % Tq;
           cache::row_range(P.mask, static_cast<long long>(b) * Tq + tok, tok, len, n_new, P.p.Tk, P.window, &lo[n][e],
                            &hi[n][e], &pos[n][e]);
-          if (P.p.slopes) slope2[n][e] = __ldg(P.p.slopes + wk.h * P.p.G + r / Tq) * scored::kLog2e;
+          if (P.p.slopes) slope2[n][e] = P.p.slopes[wk.h * P.p.G + r / Tq] * scored::kLog2e;
           lo_all = max(lo_all, lo[n][e]);
           hi_all = min(hi_all, hi[n][e]);
         }
@@ -315,7 +315,7 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
         for (int c = 0; c < HD / 32; ++c) {
           const int col = 32 * c + 8 * t;
           const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(P.Q) + at + col;
-          const uint4 v = live && col < d ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 v = live && col < d ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
           q[0][n][4 * c] = v.x, q[0][n][4 * c + 1] = v.y, q[0][n][4 * c + 2] = v.z, q[0][n][4 * c + 3] = v.w;
         }
       } else {
@@ -329,7 +329,7 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(P.Q) + at + col);
-              const float4 v = there ? __ldg(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+              const float4 v = there ? src[j] : make_float4(0.f, 0.f, 0.f, 0.f);
               float* to = f + 16 * c + 4 * j;
               to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
             }
@@ -337,7 +337,7 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.Q) + at + col);
-              const uint4 v = there ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+              const uint4 v = there ? src[j] : make_uint4(0u, 0u, 0u, 0u);
               const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
