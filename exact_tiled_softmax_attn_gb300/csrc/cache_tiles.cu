@@ -49,7 +49,7 @@
 #include <math_constants.h>
 #include <stdint.h>
 
-#include <mutex>
+#include <atomic>
 #include <type_traits>
 
 #include "cache.h"
@@ -895,11 +895,14 @@ cudaError_t launch(const CacheTokens& a) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(kern, C::SMEM, done);
   if (e != cudaSuccess) return e;
-  static std::once_flag asked;
-  static cudaFuncAttributes fa;   // (those of the code, the same on every device)
-  std::call_once(asked, [&] { e = cudaFuncGetAttributes(&fa, kern); });
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs < REG_CONVERT || fa.numRegs > REG_SOFTMAX || 4 * fa.numRegs < REG_CTRL + 2 * REG_CONVERT + REG_SOFTMAX)
+  static std::atomic<int> regs{0};   // (of the code, the same on every device; a query that fails is made again)
+  int n = regs.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    regs.store(n = fa.numRegs, std::memory_order_relaxed);
+  }
+  if (n < REG_CONVERT || n > REG_SOFTMAX || 4 * n < REG_CTRL + 2 * REG_CONVERT + REG_SOFTMAX)
     return cudaErrorInvalidConfiguration;
   if ((e = launch_over(kern, a.grid, THREADS, C::SMEM, a.stream, P)) != cudaSuccess) return e;
   return cache_walk::launch_join<false>(P, a.grid, BM, a.stream);
