@@ -1,5 +1,7 @@
 """Attention over a paged 8-bit cache at the limits of its arguments: value
-scales that lie far apart, ranges that end far below zero.
+scales that lie far apart or are no powers of two, ranges that end far below
+zero, windows that decide how many blocks share a sequence; and appending with
+positions and a scaled rotation.
 
 Tolerances as test_cache.py's, row by row: bf16 rms 1e-2 of the row's, fp32
 1e-5 of the row's sum of P |V| (which is what the roundings of weights and
@@ -13,24 +15,28 @@ import torch
 
 import exact_tiled_softmax_attn_gb300 as B
 from oracle import cache as ref
+from oracle import scored as sref
 
 from parity import check_o, np64
-from test_cache import as_oracle, attention_case, i32
+from test_cache import F8, as_oracle, attention_case, clean, i32, pool_of, table_of
 from test_scored import check_lse
 
 
-def compare(c, table, length, new, q, Tk, **how):
-    """forward_cached against the oracle, row by row; every row that sees a key has a result to be wrong in."""
+def compare(c, table, length, new, q, Tk, keys=None, **how):
+    """forward_cached against the oracle, row by row; every row that sees a key has a result to be wrong in. keys: (K, V)
+    where they are not what the pages hold."""
     dtype, scale = q.dtype, 1.0 / math.sqrt(q.shape[3])
     arrays = {n: None if how.get(n) is None else i32(how[n]) for n in ("q_pos", "key_begin", "key_end")}
     o, lse = B.forward_cached(q, c, table, i32(length), new_len=i32(new), Tk=Tk, causal=how.get("causal", True),
                               window=how.get("window", 0), **arrays)
     torch.cuda.synchronize()
     assert B.attn_device_status() == B.ATTN_OK
-    k, v = as_oracle(c, table, length, Tk)
+    k, v = keys or as_oracle(c, table, length, Tk)
     r = ref.attend(q, k, v, length, new, scale, **how)
     assert np.abs(r["O"]).max(-1)[np.isfinite(r["LSE"])].all()
     check_lse(lse, r["LSE"], dtype)
+    with pytest.raises(AssertionError):   # (the bounds below would refuse zeros)
+        check_o(np.zeros_like(r["O"]), r["O"], dtype)
     if dtype == torch.bfloat16:
         check_o(o, r["O"], dtype)
     else:
@@ -144,3 +150,96 @@ def test_ranges_that_end_far_below_zero(Tq, dtype):
     compare(c, table, length, new, q, 700, causal=False, key_end=end)
     pos = np.where(end < 0, -2 ** 31, 650)
     compare(c, table, length, new, q, 700, q_pos=pos)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("page,d,dv", SHAPES)
+@pytest.mark.parametrize("Tq", [1, 6, 13, 30, 60, 100])
+def test_scales_that_are_no_powers_of_two(Tq, page, d, dv, dtype):
+    """Scales of any size and any bits, and ones outside the range that scales are read in. The path that reads the
+    pages into the workspace (more than 128 rows) rounds keys and values to the type: the oracle takes those."""
+    shape = (2, 4, 2, Tq, 700, d, dv, page)
+    c, table, length, new, q = attention_case(shape, "e4m3", dtype, True, seed=13)
+    g = torch.Generator().manual_seed(3)
+    c.k_scale.copy_(torch.exp2(torch.rand(c.k_scale.shape, generator=g) * 6 - 12))
+    c.v_scale.copy_(torch.exp2(torch.rand(c.v_scale.shape, generator=g) * 60 - 30))
+    c.v_scale[int(table[0, 2])], c.k_scale[int(table[0, 3])] = 0.0, 1e-30
+    keys = None
+    if 2 * Tq > 128 and dtype == torch.bfloat16:
+        keys = [np64(x) for x in B.cache_read(c, table, i32(length), Tk=700)]
+    compare(c, table, length, new, q, 700, keys=keys)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("store", ["e4m3", "plain"])
+@pytest.mark.parametrize("Tq,window", [(1, 300), (4, 100), (6, 1000), (8, 300)])
+def test_windows_in_long_sequences(Tq, window, store, dtype):
+    """A window that leaves so few keys that blocks share them without a workspace, although the sequences' bound asks
+    for one; with positions given, the bound decides."""
+    shape = (3, 8, 2, Tq, 20000, 64, 64, 64)
+    c, table, length, new, q = attention_case(shape, store, dtype, True, seed=15)
+    length = [20000, 7001, 90]
+    clean(c, table, length)
+    code = B.ATTN_CACHE_E4M3 if store == "e4m3" else B.ATTN_CACHE_PLAIN
+    size = B.attn_fwd_cached_workspace_size(3, 8, 2, Tq, 20000, 64, 64, code,
+                                            B.ATTN_BF16 if dtype == torch.bfloat16 else B.ATTN_F32)
+    assert size > 0
+    compare(c, table, length, new, q, 20000, window=window)
+    pos = np.array([[19990], [5000], [60]]) - 37 * np.arange(Tq)[None]
+    compare(c, table, length, new, q, 20000, window=window, q_pos=np.maximum(pos, 0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("store", ["e4m3", "plain"])
+@pytest.mark.parametrize("mscale", [1.0, 1.3, 0.37])
+@pytest.mark.parametrize("T,d,rot,inter,odd", [(1, 128, 128, False, 0), (3, 96, 64, True, 0), (70, 128, 64, False, 0),
+                                               (130, 64, 64, True, 0), (40, 80, 40, False, 0), (70, 64, 64, False, 1)])
+def test_append_with_positions_and_a_scaled_rotation(T, d, rot, inter, odd, mscale, store, dtype):
+    """pos in place of the tokens' indexes, of any sign, and mscale in the keys, the queries and the scale's bound.
+    Tolerances as test_cache.py's test_append, the rotation's times mscale."""
+    Bn, H, Hkv, dv, page = 2, 4, 2, 64, 32
+    store = F8 if store == "e4m3" else dtype
+    g = torch.Generator().manual_seed(T + d)
+    x = torch.randn(Bn, T, H * d + Hkv * (d + dv) + odd, generator=g).to(dtype).cuda()[:, :, odd:]
+    q = x[..., :H * d].view(Bn, T, H, d).transpose(1, 2)
+    k = x[..., H * d:(H + Hkv) * d].view(Bn, T, Hkv, d).transpose(1, 2)
+    v = x[..., (H + Hkv) * d:].view(Bn, T, Hkv, dv).transpose(1, 2)
+    held = [37, 0]
+    seq_len, new = i32([h + T for h in held]), [T, T]
+    per = (37 + T) // page + 1
+    table = table_of(Bn, per, 1, 3)
+    kp, ks = pool_of(Bn * per + 1, Hkv, page, d, store, 1)
+    vp, vs = pool_of(Bn * per + 1, Hkv, page, dv, store, 2)
+    c = B.KVCache(kp, vp, ks, vs)
+    clean(c, table, i32(held))
+    old, old_scale = np64(kp.float()), None if ks is None else np64(ks)
+    pos = np.random.default_rng(T).integers(-2 ** 20, 2 ** 20, (Bn, T))
+    got = B.cache_append(c, k, v, table, seq_len, plan=B.rope_plan(rot, interleaved=inter, mscale=mscale), q=q, pos=i32(pos))
+    torch.cuda.synchronize()
+    m = float(np.float32(mscale))
+    freq = sref.rope_frequencies(rot)
+    step = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+
+    def near(a):     # |u| + |v| of the pair of every element (0 where nothing is turned)
+        a = np.abs(np64(a))
+        i = np.arange(rot)
+        z = np.zeros_like(a)
+        z[..., :rot] = a[..., i] + a[..., i ^ 1 if inter else (i + rot // 2) % rot]
+        return z * m * 8 * 2.0 ** -24
+    want = ref.rotated(q, pos, freq, inter, m)
+    assert (np.abs(np64(got) - want) <= near(q) + step * np.abs(want)).all()
+    kr = ref.rotated(k, pos, freq, inter, m)
+    size = ref.key_size(np64(k), rot, m).astype(np.float32).max(-1)
+    _, want_scale, fresh = ref.append(old, old_scale, table.cpu().numpy(), np64(seq_len), new, kr, size, page)
+    exact, _, _ = ref.append(old, None, table.cpu().numpy(), np64(seq_len), new, kr, size, page)
+    slack, _, _ = ref.append(old, None, table.cpu().numpy(), np64(seq_len), new, near(k), size, page)
+    if ks is None:
+        assert (np.abs(np64(kp) - exact) <= slack + step * np.abs(exact))[fresh].all()
+    else:
+        assert np.array_equal(np64(ks), want_scale)
+        s = want_scale[:, :, None, None]
+        off = np.abs(np64(kp.float()) * s - exact)
+        assert (off <= slack + np.maximum(2.0 ** -4 * np.abs(exact), 2.0 ** -10 * s))[fresh].all()
