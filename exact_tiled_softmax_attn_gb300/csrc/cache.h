@@ -142,7 +142,7 @@ struct CacheAppend {
   View s[2];
   const int* pos;
   int B, Hkv, T, w[2];   // w: d, dv
-  bool q_wide, wide;     // 16-byte accesses of the queries, and of K and V
+  bool wide;             // 16-byte accesses of the queries, K and V
   bool bf16;
   int num_sms;
   cudaStream_t stream;
@@ -178,7 +178,7 @@ struct CacheRows {
 cudaError_t launch_cache_rows(const CacheRows& a);
 
 // Attention of few rows, which reads the pages where they lie: bf16 over any
-// pages, fp32 over e4m3; tmK, tmV by cache_map.
+// pages, fp32 over e4m3; tmK, tmV by make_map_bytes.
 constexpr int kCacheTokenRows = 128;   // packed rows of a key head, at most
 inline int cache_token_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }   // of a group
 // CTAs of an SM, by the rows of a group: as many as registers and shared memory hold.

@@ -151,7 +151,7 @@ Few few_layout(Way way, int B, int H, int Hkv, int Tq, int Tk, int dv, int type)
   Few f{};
   if (B == 0 || H == 0 || Tq == 0) return f;
   const int R = H / Hkv * Tq, rows = way == kTiles ? kCacheTileRows : cache_token_rows(R);
-  f.groups = way == kTiles ? (R + kCacheTileRows - 1) / kCacheTileRows : cache_token_groups(R);
+  f.groups = way == kTiles ? 1 : cache_token_groups(R);   // (a tile holds all of kCacheTokenRows)
   const size_t entries = static_cast<size_t>(B) * f.groups;
   // All the CTAs that are resident at a time, and at least two stages each in
   // the few-row kernel: 8 pairs of 4096 keys, us with two and with one (fewer

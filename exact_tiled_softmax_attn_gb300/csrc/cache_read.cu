@@ -78,41 +78,39 @@ __global__ void __launch_bounds__(NT) read_kernel(const __grid_constant__ CacheR
     from = max(from, hull.x);
     to = min(to, hull.y);
   }
-  const int step = NT / per > 0 ? NT / per : 1;
+  const int step = NT / per;   // (rows have at most NT pieces)
   const int lane = threadIdx.x / per;
   if (lane >= step) return;
-  const int c = (static_cast<int>(threadIdx.x) - lane * per) * V, mask = (1 << P.c.shift) - 1;
+  const int col = (static_cast<int>(threadIdx.x) - lane * per) * V, mask = (1 << P.c.shift) - 1;
   T* out = static_cast<T*>(P.out[side]) + static_cast<long long>(bh) * P.Tk * w;
   const bool one = reinterpret_cast<uintptr_t>(out) % 32 == 0;   // (rows are whole 32 bytes)
-  for (int col = c; col < w; col += NT * V) {   // (a single round but for rows of more than NT pieces)
-    for (int r0 = from + lane; r0 < to; r0 += U * step) {
-      uint4 x[CODES ? U : 1];
-      In y[CODES ? 1 : U];
-      float s[U];
+  for (int r0 = from + lane; r0 < to; r0 += U * step) {
+    uint4 x[CODES ? U : 1];
+    In y[CODES ? 1 : U];
+    float s[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = r0 + u * step;
-        const int at = t < to && t < last ? page_of(P.c, b, t >> P.c.shift) : -1;
-        const long long head = static_cast<long long>(at) * P.Hkv + h;
-        const long long row = ((head << P.c.shift) + (t & mask)) * w + col;
-        if constexpr (CODES) {
-          x[u] = at >= 0 ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(P.c.pool[side]) + row)
-                         : make_uint4(0u, 0u, 0u, 0u);
-          s[u] = at >= 0 ? clamp_scale(__ldg(P.c.scale[side] + head)) : 1.f;
-        } else {
-          y[u] = at >= 0 ? *reinterpret_cast<const In*>(static_cast<const T*>(P.c.pool[side]) + row) : In{};
-        }
+    for (int u = 0; u < U; ++u) {
+      const int t = r0 + u * step;
+      const int at = t < to && t < last ? page_of(P.c, b, t >> P.c.shift) : -1;
+      const long long head = static_cast<long long>(at) * P.Hkv + h;
+      const long long row = ((head << P.c.shift) + (t & mask)) * w + col;
+      if constexpr (CODES) {
+        x[u] = at >= 0 ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(P.c.pool[side]) + row)
+                       : make_uint4(0u, 0u, 0u, 0u);
+        s[u] = at >= 0 ? clamp_scale(__ldg(P.c.scale[side] + head)) : 1.f;
+      } else {
+        y[u] = at >= 0 ? *reinterpret_cast<const In*>(static_cast<const T*>(P.c.pool[side]) + row) : In{};
       }
+    }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = r0 + u * step;
-        if (t >= to) break;
-        T* p = out + static_cast<long long>(t) * w + col;
-        if constexpr (CODES)
-          put16(p, x[u], s[u], one);
-        else
-          *reinterpret_cast<In*>(p) = y[u];
-      }
+    for (int u = 0; u < U; ++u) {
+      const int t = r0 + u * step;
+      if (t >= to) break;
+      T* p = out + static_cast<long long>(t) * w + col;
+      if constexpr (CODES)
+        put16(p, x[u], s[u], one);
+      else
+        *reinterpret_cast<In*>(p) = y[u];
     }
   }
 }

@@ -83,7 +83,6 @@ constexpr int NSC = 8;   // tiles whose scales are held (see the producer)
 template <int HD, int CP>
 struct Cfg {
   static constexpr int RP = BM / CP, KEYS = BN / CP;
-  static constexpr int KB = HD / 64;
   static constexpr int TILE = BN * HD * 2;     // fp16
   static constexpr int RAW = BN * HD;          // codes of a tile of keys or of values
   // Even: a place of the ring is then always keys' or always values', and its converters see every phase of its barriers.
