@@ -42,8 +42,7 @@
 // scales (up to 2^72 apart; at 2^80, the most there is, 2^-5), and smaller ones
 // are off by 2^-32 of the reference. Sums and accumulators take the ratio of two
 // references in 32 bits: 2^15 of a weight, 448, 2^30 keys and 2^72 are below
-// 2^126. With scales within 2^8, which a layer's are, that costs a comparison per
-// step: 1 % with long caches, 3 % with one short one.
+// 2^126. The producer compares the scales, of all that a CTA takes on.
 //
 // Fragments are read as 16-byte vectors: the columns of Q and K are permuted
 // alike, so that a thread's fragments of K are 16 adjacent codes of a row; the
@@ -82,6 +81,8 @@ constexpr float TAU = 8.0f;
 // The value scales that a reference stands for lie within 2^8 of one
 // another, and it is let down by at most 2^DEPTH (see the header).
 constexpr float SPREAD = 8.01f, DEPTH = 72.0f;   // (8, and the logarithms' rounding)
+// Where they do not, a stage's scales come with the largest of those before plus APART (log2), else with 0.
+constexpr float APART = 256.0f;
 
 // E: uint8_t (e4m3) or bf16; SPLIT: fp32 queries and results (e4m3 only); a
 // warp has 8 NT rows, and RT row tiles of 4 warps share the stages.
@@ -212,6 +213,7 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
     const int rows = shift < 6 ? 1 << shift : 64;
     const int planes = P.c.pages * P.p.Hkv;                   // (a plane past the last reads as zeros)
     do {
+      float vs_lo = CUDART_INF_F, vs_hi = -CUDART_INF_F;   // log2 of the value scales since the references were set
       const int b = wk.e / P.groups;
       const int key_s0 = wk.key0(wk.s0), n_box = wk.run * nb;
       // lane i looks up box i of the next 32: its plane, and its scales
@@ -250,9 +252,23 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
                              full + st, col * 64, key & ((1 << shift) - 1), at >= 0 ? at : planes);
           }
           if constexpr (CODES) {
-            const int from = j + (shift < 6 ? (16 * (lane & 3)) >> shift : 0);   // box of 16-key group `lane`
-            const float4 s = make_float4(__shfl_sync(0xffffffffu, ks, from), __shfl_sync(0xffffffffu, lv, from),
-                                         __shfl_sync(0xffffffffu, iv, from), 0.f);
+            const int from = j + (shift < 6 ? (16 * (lane & 3)) >> shift : 0);   // box of 16-key group lane % 4
+            float4 s = make_float4(__shfl_sync(0xffffffffu, ks, from), __shfl_sync(0xffffffffu, lv, from),
+                                   __shfl_sync(0xffffffffu, iv, from), 0.f);
+            const bool is = __shfl_sync(0xffffffffu, plane, from) >= 0;
+            float lo = is ? s.y : CUDART_INF_F, hi = is ? s.y : -CUDART_INF_F;
+#pragma unroll
+            for (int o = 1; o < 4; o *= 2) {
+              lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+              hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            }
+            const bool apart = vs_hi >= vs_lo && hi >= lo && fmaxf(hi, vs_hi) - fminf(lo, vs_lo) > SPREAD;
+            if (apart) s.w = vs_hi + APART;
+            vs_lo = apart ? lo : fminf(lo, vs_lo), vs_hi = apart ? hi : fmaxf(hi, vs_hi);
+            if (!is) {   // zeros: any scale, before the first page a small one
+              s.y = vs_lo < CUDART_INF_F ? vs_lo : -60.f;
+              s.z = exp2f(-s.y);
+            }
             if (lane < 4) scales[st * 4 + lane] = s;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(full + st);
@@ -382,7 +398,6 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
     }
-    float vs_lo = CUDART_INF_F, vs_hi = -CUDART_INF_F;   // log2 of the value scales since m was set
     if (CODES) {
       __syncwarp();   // (the last run's are read)
       if (g == 0) {
@@ -399,7 +414,7 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
       if (key0 < wk.hull.y && key0 + 16 > wk.hull.x && R > 0) {
         const uint8_t* sK = smem + st * C::STAGE + 16 * kg * (C::BOX / BK);
         const uint8_t* sV = sK + C::KB * C::BOX;
-        float4 sc = make_float4(1.f, 0.f, 1.f, 0.f);   // key scale, log2 of the value scale, 1 / value scale
+        float4 sc = make_float4(1.f, 0.f, 1.f, 0.f);   // key scale, log2 of the value scale, 1 / value scale, see APART
         if constexpr (CODES) sc = scales[st * 4 + kg];
         // x[n][2 h + e]: key krow + 8 h, row 8 n + 2 t + e; two chains of products where a warp has eight rows
         constexpr int CH = NT == 1 ? 2 : 1;
@@ -496,15 +511,14 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
             }
         }
         if constexpr (CODES) {
-          const float lo2 = fminf(vs_lo, sc.y), hi2 = fmaxf(vs_hi, sc.y);
-          if (hi2 - lo2 > SPREAD) {   // (the same in the whole warp) the references as these scales want them
+          if (sc.w != 0.f) {   // the references as these scales want them
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 float2 ws = top[8 * n + e];
                 ws.x = fmaxf(ws.x, m[n][e]);
-                ws.y = fmaxf(ws.y, m[n][e] - vs_hi);
+                ws.y = fmaxf(ws.y, m[n][e] - (sc.w - APART));
                 const float mn = fmaxf(fminf(ws.x, ws.y + sc.y), ws.x - DEPTH);
                 const float corr = m[n][e] == mn ? 1.f : ptx::ex2(m[n][e] - mn);
                 m[n][e] = mn;
@@ -515,9 +529,6 @@ __device__ __forceinline__ void attend(const CUtensorMap& tmK, const CUtensorMap
                 if (g == 0) top[8 * n + e] = ws;
                 __syncwarp();
               }
-            vs_lo = vs_hi = sc.y;
-          } else {
-            vs_lo = lo2, vs_hi = hi2;
           }
         }
         bool need = false;
