@@ -719,8 +719,10 @@ def forward_cached(q, cache: KVCache, table, seq_len, new_len=None, causal: bool
 
     table, seq_len and new_len as in cache_append, which has put the same tokens' keys there; row i is at position
     seq_len - new_len + i unless q_pos gives another. window > 0: a row sees its last `window` positions only. Tk: a
-    bound of the lengths, which sizes the work (default: all that the table has room for). The rest as forward_scored
-    (but causal by default); the workspace has attn_fwd_cached_workspace_size bytes."""
+    bound of the lengths, which sizes the work (default: all that the table has room for) and, with more than 128 rows a
+    key head or fp32 pages, a workspace of B * Hkv * Tk keys and values: give it where the table has room for more than
+    the sequences hold. The rest as forward_scored (but causal by default); the workspace has
+    attn_fwd_cached_workspace_size bytes."""
     qs, dtype = q.shape, q.dtype
     c, B, Hkv, d, dv, room, dev = _cache_args(cache, table, seq_len, new_len, dtype)
     if len(qs) != 4 or qs[0] != B or qs[3] != d:

@@ -16,9 +16,13 @@ constexpr int kMostRows = 1 << 29;   // tokens of a call
 // Workspace sizes are rules of the shapes alone, so counts that aim at
 // filling the GPU use GB300's SM count.
 constexpr int kSms = 152;
-// Packed rows of a key head above which the 128-row tiles take over: 16
-// sequences of up to 12000 keys, Hkv=4 d=128, 32 rows 66 us by the few-row
-// kernel and 87 by the tiles, 64 rows 113 and 64.
+// Packed rows of a key head above which the 128-row tiles take over. us by the
+// few-row kernel and by the tiles, Hkv=4 d=128: 16 sequences of up to 12000 keys,
+// 24 rows 65 and 58, 32 rows 66 and 58 (d=64: 45 and 43), 64 rows 113 and 60; 32
+// rows of 8 pairs of 1024 keys 10 and 16, of 4096 15 and 20, of 64 pairs of 1024
+// 16 and 16, of 4096 34 and 33, of 16384 86 and 70. Up to 32 rows it is the
+// number of keys that decides: short sequences have clusters in the few-row
+// kernel only, and they are what this limit is right for.
 constexpr int kTilesFrom = 32;
 
 // Sizes, widths and the pool's pointers; fills the view.

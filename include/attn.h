@@ -476,7 +476,8 @@ typedef struct {
  * whose first token is new takes that scale; one that holds tokens keeps the
  * larger of the two, and where that is the new one, the tokens that it holds
  * are requantised. Elements are rounded once, to the nearest (ties to even; the
- * largest is 448). Those that are not finite do not count towards a and are
+ * largest is 448; by a kept scale that is no power of two after the quotient's
+ * own rounding to fp32). Those that are not finite do not count towards a and are
  * stored as NaN.
  * A page may be appended to for one sequence of a call only; where two append
  * to it, what it then holds is unspecified.
@@ -513,8 +514,10 @@ ATTN_API attn_status_t attn_cache_read(const attn_cache_t* cache, void* K, void*
  * Up to 128 packed rows a key head (H / Hkv * Tq) the pages are read where they
  * lie (with ATTN_F32, where they hold e4m3); with more rows the seen tokens are
  * read into the workspace first, as by attn_cache_read, so that scales that are
- * no powers of two cost a rounding to dtype. Q and O aligned to 16 bytes
- * (ATTN_CACHE_PLAIN with ATTN_F32: 4).
+ * no powers of two cost a rounding to dtype; it then grows with B * Hkv * Tk. Q
+ * and O aligned to 16 bytes (ATTN_CACHE_PLAIN with ATTN_F32: 4). Scales may lie
+ * as far apart as they like: a page of zeros, or of tokens that no row sees,
+ * does not cost the others' values their bits.
  * Workspace as attn_fwd_scored, with attn_fwd_cached_workspace_size: a rule of
  * the shapes and types only (0 is possible). Other errors as attn_cache_append and
  * attn_fwd_scored; asynchronous on `stream`; equal calls give bitwise equal
