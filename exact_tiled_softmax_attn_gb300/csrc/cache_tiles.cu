@@ -259,13 +259,13 @@ __global__ void __launch_bounds__(THREADS, 1) tiles_kernel(const __grid_constant
             // 16-key groups of the boxes that are not there
             const uint32_t none = 0xffu & ~__ballot_sync(0xffffffffu, __shfl_sync(0xffffffffu, plane, from) >= 0);
             const int sl = slot(item);
-            if (lane == 0) {
-              ok = ptx::mbar_wait(raw_empty + sl, par(item) ^ 1u, w);
-              if (side && box0 + j == 0) ok = ok && ptx::mbar_wait(run_full + (runs & 1u), (runs >> 1) & 1u, w);
-            }
+            if (lane == 0) ok = ptx::mbar_wait(raw_empty + sl, par(item) ^ 1u, w);
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             if (!ok) break;
-            if (side && box0 + j == 0) wide = run_wide[runs & 1u] != 0u;
+            if (side && box0 + j == 0) {
+              if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(run_full + (runs & 1u), (runs >> 1) & 1u, w)))) break;
+              wide = run_wide[runs & 1u] != 0u;
+            }
             uint64_t* full = (side && wide ? wide_full : raw_full) + sl;
             if (lane == 0) {
               none_of[sl] = none;
@@ -280,9 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1) tiles_kernel(const __grid_constant
             item += 2;
             if (side) continue;
             if (box0 + j == 0) {
-              if (lane == 0) ok = ptx::mbar_wait(run_full + (runs & 1u), (runs >> 1) & 1u, w);
-              ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-              if (!ok) break;
+              if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(run_full + (runs & 1u), (runs >> 1) & 1u, w)))) break;
               wide = run_wide[runs & 1u] != 0u;
             }
             // The scales of the tile j (of the CTA), behind its copies. They replace those of j - NSC, which the softmax
@@ -302,7 +300,7 @@ __global__ void __launch_bounds__(THREADS, 1) tiles_kernel(const __grid_constant
         if (lane == 0) ptx::mbar_arrive(run_empty + (runs & 1u));
         ++runs;
       } while (ok && wk.next(P));
-      if (!ok && lane == 0)   // let the copies in flight land before the CTA exits
+      if (!ok && lane == 0)   // let the copies in flight land before the CTA exits (a wide run's: while this wait runs out)
         for (uint32_t n = item > static_cast<uint32_t>(C::NRAW) ? item - C::NRAW : side; n < item; n += 2)
           ptx::mbar_wait_drain(raw_full + slot(n), par(n));
     } else if (warp == 3 && last > first) {
@@ -350,9 +348,8 @@ __global__ void __launch_bounds__(THREADS, 1) tiles_kernel(const __grid_constant
             const int key0 = wk.key0(wk.s0 + j) + 16 * g;
             const int r0 = max(0, min(16, wk.hull.x - key0)), r1 = plane >= 0 ? max(0, min(16, wk.hull.y - key0)) : 0;
             const int sl = slot(2 * tile + 1);
-            if (lane == 0) ok = ptx::mbar_wait(wide_full + sl, phase >> sl & 1u, w);
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (!ok) {   // let the copies in flight land before the CTA exits
+            // (every lane reads what was copied)
+            if (!(ok = __all_sync(0xffffffffu, ptx::mbar_wait(wide_full + sl, phase >> sl & 1u, w)))) {   // let the copies in flight land before the CTA exits
               if (lane == 0) ptx::mbar_wait_drain(wide_full + sl, phase >> sl & 1u);
               break;
             }
