@@ -243,3 +243,31 @@ def test_append_with_positions_and_a_scaled_rotation(T, d, rot, inter, odd, msca
         s = want_scale[:, :, None, None]
         off = np.abs(np64(kp.float()) * s - exact)
         assert (off <= slack + np.maximum(2.0 ** -4 * np.abs(exact), 2.0 ** -10 * s))[fresh].all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("page,d,dv", SHAPES)
+@pytest.mark.parametrize("Tq", [1, 6, 13, 30, 60, 100])
+def test_nan_beside_scales_far_apart(Tq, page, d, dv, dtype):
+    """NaN behind the length changes nothing; a NaN in a value that rows see makes that element of their O NaN and leaves
+    the others as they are."""
+    shape = (2, 4, 2, Tq, 1290, d, dv, page)
+    c, table, length, new, q = attention_case(shape, "e4m3", dtype, True, seed=17)
+    n = table.shape[1]
+    i = np.arange(n)
+    for b in range(2):
+        set_pages(c, table, b, np.where(i % 3 == 1, 2.0 ** 30, 2.0 ** -8), i % 3 == 1)
+    how = dict(new_len=i32(new), Tk=1290, causal=False)
+    o, lse = compare(c, table, length, new, q, 1290, causal=False)
+    for b in range(2):
+        for p in c[:2]:
+            p.view(torch.uint8)[int(table[b, length[b] // page]), :, length[b] % page:] = 0x7f
+    o2, lse2 = B.forward_cached(q, c, table, i32(length), **how)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    c.v.view(torch.uint8)[int(table[0, 0]), 1, 3, 7] = 0xff
+    o3, lse3 = B.forward_cached(q, c, table, i32(length), **how)
+    assert torch.isnan(o3[0, 2:, :new[0], 7]).all() and torch.equal(lse, lse3)
+    o3[0, 2:, :, 7] = o[0, 2:, :, 7]
+    # (a group with a NaN keeps its codes as they are, where others are brought up: the last bits of weights)
+    assert (o3.float() - o.float()).abs().max() <= (2e-2 if dtype == torch.bfloat16 else 1e-5) * o.float().abs().max()
