@@ -24,8 +24,8 @@
 // zeros (or of tokens that no row sees) whose scale is 2^30 times the others'
 // must not set what they are relative to. A warp looks over the scales of a run
 // ahead of it. Where they lie more than 2^8 apart, or a page is none, it steps
-// between the producer of V and the converter: it finds the largest code that is
-// seen of every 16 keys, multiplies their codes by the power of two that brings
+// between the producer of V and the converter: it finds the largest code (but
+// NaN) that is seen of every 16 keys, multiplies their codes by the power of two that brings
 // it above 224 - exact, codes have no more bits - and divides the scale by it.
 // Weights are then relative to the largest of what keys add to O, whatever the
 // scales. That costs other runs 6 % (57 -> 60.5 us with 64 rows, 78 -> 84 with
@@ -358,15 +358,16 @@ __global__ void __launch_bounds__(THREADS, 1) tiles_kernel(const __grid_constant
             uint32_t m = 0;
             for (int i = r0 * per + (lane & 3); i < r1 * per; i += 4) {
               const uint4 u = codes[i];
-              constexpr uint32_t SIZE = 0x7f7f7f7fu;   // without the signs
-              m = __vmaxu4(m, __vmaxu4(__vmaxu4(u.x & SIZE, u.y & SIZE), __vmaxu4(u.z & SIZE, u.w & SIZE)));
+              constexpr uint32_t SIZE = 0x7f7f7f7fu;   // without the signs; four NaN
+              auto larger = [&](uint32_t x) { m = __vmaxu4(m, x & SIZE & ~__vcmpeq4(x & SIZE, SIZE)); };
+              larger(u.x), larger(u.y), larger(u.z), larger(u.w);
             }
             uint32_t top = max(max(m & 255u, m >> 8 & 255u), max(m >> 16 & 255u, m >> 24));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const float size = cache::half2_to_float2(cache::codes_to_half2(static_cast<uint16_t>(top))).x;
             int up = 0;   // to 17
-            if (top > 0 && top < 0x7f) {   // (0x7f: NaN)
+            if (top > 0) {
               up = 8 - ilogbf(size);
               if (ldexpf(size, up) > kCodeMost) --up;
             }
